@@ -149,7 +149,7 @@ def _inputs(case, seed):
              loss=torch.empty(N, device=dev, dtype=torch.float32),
              dlogits=torch.empty(N, V + case["pad"], device=dev, dtype=dt)[:, :V])
     if op == "pair":
-        s["stats"] = torch.empty(N, 4, device=dev, dtype=torch.float32)
+        s["stats"] = torch.empty(N, 8, device=dev, dtype=torch.float32)
     return s
 
 
