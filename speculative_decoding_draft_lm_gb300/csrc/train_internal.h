@@ -1,0 +1,55 @@
+// Host-side launch interface of the draft-head training operators.
+#pragma once
+
+#include "internal.h"
+
+#include "domino_train.h"
+
+struct domino_train_ctx {
+    domino_train_config cfg;
+    int device;
+    int num_sms;
+    int last_launches;
+    int* err;             // device error word
+    // embed_grad workspace (max_tokens > 0)
+    uint32_t* keys[2];    // [max_tokens] tokens between the passes of the sort
+    int32_t* pos[2];      // [max_tokens] their positions
+    unsigned* hist;       // [tiles][kSortMaxBins] digit counts of the sort's tiles
+    void* ws_base;
+};
+
+namespace domino {
+namespace train {
+
+constexpr int kSortTile = 4096;      // tokens per tile of the sort
+constexpr int kSortMaxBins = 1024;   // two digits cover tokens up to DOMINO_TRAIN_MAX_V
+
+struct DistillArgs {
+    const void* x;          // [n, V] student logits
+    long long ld;
+    int n, V;
+    const int32_t* ids;     // [n, K]
+    const float* top;       // [n, K]
+    const float* rest;      // [n] or null
+    int K;
+    float temperature;
+    const float* weight;    // [n] gradient by each row's loss (null: forward only)
+    float* loss;            // [n] or null
+    float* stats;           // [n, DOMINO_TRAIN_STATS], written by the forward, read by the backward
+    void* dx;               // [n, V]
+    long long ld_d;
+    int* err;
+};
+
+cudaError_t launch_top(domino_train_ctx* c, const void* x, int dtype, long long ld, int n, int K, float temperature,
+                       int32_t* ids, float* top, float* rest, cudaStream_t st);
+cudaError_t launch_distill_forward(domino_train_ctx* c, const DistillArgs& a, cudaStream_t st);
+cudaError_t launch_distill_backward(domino_train_ctx* c, const DistillArgs& a, cudaStream_t st);
+cudaError_t launch_distill_step(domino_train_ctx* c, const DistillArgs& a, cudaStream_t st);
+cudaError_t launch_embed(domino_train_ctx* c, const void* table, const int32_t* tokens, int n, float scale, void* out,
+                         long long ld, cudaStream_t st);
+cudaError_t launch_embed_grad(domino_train_ctx* c, const void* dout, long long ld, const int32_t* tokens, int n,
+                              float scale, void* dtable, int grad_dtype, bool accumulate, cudaStream_t st);
+
+}  // namespace train
+}  // namespace domino

@@ -1,0 +1,290 @@
+"""Python binding of the draft-head training operators in
+``include/domino_train.h`` (ctypes): argument marshalling only, like
+``rollout.py``.  ``DominoTrain`` takes torch CUDA tensors and the current torch
+stream; ``distill_loss`` and ``embedding`` are the operators as torch autograd
+functions.  There is no CPU fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import rollout as _r
+from .rollout import DOMINO_DTYPE_BF16, DOMINO_DTYPE_FP32, DOMINO_OK, DominoError, _check
+
+DOMINO_TRAIN_MAX_V = 524288
+DOMINO_TRAIN_MAX_K = 8192
+DOMINO_TRAIN_STATS = 8
+
+# every symbol the header declares
+EXPORTED = (
+    "domino_train_init", "domino_train_top_logits", "domino_train_distill_forward", "domino_train_distill_backward",
+    "domino_train_distill_step", "domino_train_embed", "domino_train_embed_grad", "domino_train_status",
+    "domino_train_last_launch_count", "domino_train_destroy",
+)
+
+
+class domino_train_config(ctypes.Structure):
+    _fields_ = [("V", ctypes.c_int), ("E", ctypes.c_int), ("max_tokens", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+_lib = None
+
+
+def load_library() -> ctypes.CDLL:
+    """The rollout's library with the training entry points declared."""
+    global _lib
+    if _lib is not None:
+        return _lib
+    lib = _r.load_library()
+    vp, i, ll, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
+    lib.domino_train_init.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(domino_train_config), i]
+    lib.domino_train_top_logits.argtypes = [vp, vp, i, ll, i, i, f, vp, vp, vp, vp]
+    lib.domino_train_distill_forward.argtypes = [vp, vp, ll, i, vp, vp, vp, i, f, vp, vp, vp]
+    lib.domino_train_distill_backward.argtypes = [vp, vp, ll, i, vp, vp, vp, i, f, vp, vp, vp, ll, vp]
+    lib.domino_train_distill_step.argtypes = [vp, vp, ll, i, vp, vp, vp, i, f, vp, vp, vp, ll, vp]
+    lib.domino_train_embed.argtypes = [vp, vp, vp, i, f, vp, ll, vp]
+    lib.domino_train_embed_grad.argtypes = [vp, vp, ll, vp, i, f, vp, i, i, vp]
+    lib.domino_train_status.argtypes = [vp, vp]
+    lib.domino_train_last_launch_count.argtypes = [vp]
+    lib.domino_train_destroy.argtypes = [vp]
+    for name in EXPORTED:
+        getattr(lib, name).restype = ctypes.c_int
+    lib.domino_train_destroy.restype = None
+    _lib = lib
+    return lib
+
+
+class DominoTrain:
+    """Owns one training context (see the header for the formulas).
+
+    V vocabulary, E embedding width (0: no embedding calls), max_tokens the
+    most tokens of one ``embed_grad`` call, dtype "bf16" or "fp32".
+
+    Tensors are on the context's device; rows may be strided (last dimension
+    contiguous).  Every method takes ``out``, the tensors to write, and
+    ``stream`` (a torch stream or raw handle; default: the current one).  With a
+    stream other than the current one the caller orders the two, as for any
+    kernel, and gives ``out``.
+    """
+
+    def __init__(self, V, E=0, max_tokens=0, dtype="bf16", device=0):
+        import torch
+        if dtype not in ("bf16", "fp32"):
+            raise ValueError(f"dtype: want 'bf16' or 'fp32', got {dtype!r}")
+        self._lib = load_library()
+        self.V, self.E, self.max_tokens, self.dtype = V, E, max_tokens, dtype
+        self.device = torch.device("cuda", device)
+        self.torch_dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
+        cfg = domino_train_config(V, E, max_tokens, DOMINO_DTYPE_BF16 if dtype == "bf16" else DOMINO_DTYPE_FP32)
+        self.ctx = ctypes.c_void_p()
+        _check(self._lib.domino_train_init(ctypes.byref(self.ctx), ctypes.byref(cfg), device), "domino_train_init")
+
+    # -- checks ----------------------------------------------------------------
+
+    def _rows(self, t, cols, name, dtype=None, n=None):
+        """Row stride of a [n, cols] tensor whose rows are contiguous."""
+        dtype = self.torch_dtype if dtype is None else dtype
+        if (t.dim() != 2 or t.shape[1] != cols or t.dtype != dtype or t.device != self.device
+                or (n is not None and t.shape[0] != n) or (cols > 1 and t.stride(1) != 1)
+                or (t.shape[0] > 1 and t.stride(0) < cols)):
+            raise ValueError(f"{name}: want CUDA [{'n' if n is None else n}, {cols}] {dtype} with contiguous rows on "
+                             f"{self.device}, got {tuple(t.shape)} {t.dtype} strides {t.stride()} on {t.device}")
+        return max(t.stride(0), cols)
+
+    def _flat(self, t, shape, dtype, name):
+        """A contiguous tensor of exactly this shape and type."""
+        if t.shape != shape or t.dtype != dtype or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{name}: want contiguous CUDA {tuple(shape)} {dtype} on {self.device}, "
+                             f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+        return t.data_ptr()
+
+    def _stream(self, stream):
+        if stream is None:
+            import torch
+            return torch.cuda.current_stream(self.device).cuda_stream
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
+    def _record(self, ids, top, rest, n):
+        import torch
+        if ids.dim() != 2:
+            raise ValueError(f"ids: want [n, K], got {tuple(ids.shape)}")
+        shape = (n, ids.shape[1])
+        return (self._flat(ids, shape, torch.int32, "ids"), self._flat(top, shape, torch.float32, "top"),
+                None if rest is None else self._flat(rest, (n,), torch.float32, "rest"), shape[1])
+
+    # -- operators ---------------------------------------------------------------
+
+    def top_logits(self, logits, K, temperature=1.0, out=None, stream=None):
+        """(ids [n, K] int32 ascending, top [n, K], rest [n]) of a teacher's
+        logits [n, V] (bf16 or fp32)."""
+        import torch
+        n = logits.shape[0]
+        if logits.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"logits: want bfloat16 or float32, got {logits.dtype}")
+        ld = self._rows(logits, self.V, "logits", logits.dtype)
+        if out is None:
+            out = (torch.empty((n, max(K, 0)), dtype=torch.int32, device=self.device),
+                   torch.empty((n, max(K, 0)), dtype=torch.float32, device=self.device),
+                   torch.empty((n,), dtype=torch.float32, device=self.device))
+        ids, top, rest = out
+        _check(self._lib.domino_train_top_logits(
+            self.ctx, logits.data_ptr(), DOMINO_DTYPE_BF16 if logits.dtype == torch.bfloat16 else DOMINO_DTYPE_FP32,
+            ld, n, K, temperature, self._flat(ids, (n, K), torch.int32, "ids"),
+            self._flat(top, (n, K), torch.float32, "top"), self._flat(rest, (n,), torch.float32, "rest"),
+            self._stream(stream)), "domino_train_top_logits")
+        return ids, top, rest
+
+    def distill_forward(self, logits, ids, top, rest=None, temperature=1.0, out=None, stream=None):
+        """(loss [n], stats [n, 8]) of student logits [n, V]; ``stats`` is for distill_backward."""
+        import torch
+        n = logits.shape[0]
+        ld = self._rows(logits, self.V, "logits")
+        pi, pt, pr, K = self._record(ids, top, rest, n)
+        if out is None:
+            out = (torch.empty((n,), dtype=torch.float32, device=self.device),
+                   torch.empty((n, DOMINO_TRAIN_STATS), dtype=torch.float32, device=self.device))
+        loss, stats = out
+        _check(self._lib.domino_train_distill_forward(
+            self.ctx, logits.data_ptr(), ld, n, pi, pt, pr, K, temperature,
+            self._flat(loss, (n,), torch.float32, "loss"),
+            self._flat(stats, (n, DOMINO_TRAIN_STATS), torch.float32, "stats"), self._stream(stream)),
+            "domino_train_distill_forward")
+        return loss, stats
+
+    def distill_backward(self, logits, ids, top, rest, stats, dloss, temperature=1.0, out=None, stream=None):
+        """dlogits [n, V] from the gradient dloss [n] by each row's loss."""
+        import torch
+        n = logits.shape[0]
+        ld = self._rows(logits, self.V, "logits")
+        pi, pt, pr, K = self._record(ids, top, rest, n)
+        if out is None:
+            out = torch.empty((n, self.V), dtype=self.torch_dtype, device=self.device)
+        ld_d = self._rows(out, self.V, "dlogits", n=n)
+        _check(self._lib.domino_train_distill_backward(
+            self.ctx, logits.data_ptr(), ld, n, pi, pt, pr, K, temperature,
+            self._flat(stats, (n, DOMINO_TRAIN_STATS), torch.float32, "stats"),
+            self._flat(dloss, (n,), torch.float32, "dloss"), out.data_ptr(), ld_d, self._stream(stream)),
+            "domino_train_distill_backward")
+        return out
+
+    def distill_step(self, logits, ids, top, rest, weight, temperature=1.0, out=None, stream=None):
+        """(loss [n], dlogits [n, V]) in one call; dlogits is the gradient of sum(weight * loss)."""
+        import torch
+        n = logits.shape[0]
+        ld = self._rows(logits, self.V, "logits")
+        pi, pt, pr, K = self._record(ids, top, rest, n)
+        if out is None:
+            out = (torch.empty((n,), dtype=torch.float32, device=self.device),
+                   torch.empty((n, self.V), dtype=self.torch_dtype, device=self.device))
+        loss, grad = out
+        ld_d = self._rows(grad, self.V, "dlogits", n=n)
+        _check(self._lib.domino_train_distill_step(
+            self.ctx, logits.data_ptr(), ld, n, pi, pt, pr, K, temperature,
+            self._flat(weight, (n,), torch.float32, "weight"), self._flat(loss, (n,), torch.float32, "loss"),
+            grad.data_ptr(), ld_d, self._stream(stream)), "domino_train_distill_step")
+        return loss, grad
+
+    def embed(self, table, tokens, scale=1.0, out=None, stream=None):
+        """scale * table[tokens] for tokens [n] int32 (-1: zeros)."""
+        import torch
+        n = tokens.shape[0]
+        if out is None:
+            out = torch.empty((n, self.E), dtype=self.torch_dtype, device=self.device)
+        ld = self._rows(out, self.E, "out", n=n)
+        _check(self._lib.domino_train_embed(
+            self.ctx, self._flat(table, (self.V, self.E), self.torch_dtype, "table"),
+            self._flat(tokens, (n,), torch.int32, "tokens"), n, scale, out.data_ptr(), ld, self._stream(stream)),
+            "domino_train_embed")
+        return out
+
+    def embed_grad(self, dout, tokens, scale=1.0, out=None, grad_dtype=None, accumulate=False, stream=None):
+        """dtable [V, E] (fp32 unless ``grad_dtype`` or ``out`` says bfloat16) from dout [n, E];
+        ``accumulate`` adds to ``out``."""
+        import torch
+        n = tokens.shape[0]
+        ld = self._rows(dout, self.E, "dout", n=n)
+        if out is None:
+            if accumulate:
+                raise ValueError("accumulate needs out")
+            out = torch.empty((self.V, self.E), dtype=grad_dtype or torch.float32, device=self.device)
+        if out.dtype not in (torch.bfloat16, torch.float32) or grad_dtype not in (None, out.dtype):
+            raise ValueError(f"dtable: want bfloat16 or float32 (grad_dtype {grad_dtype}), got {out.dtype}")
+        _check(self._lib.domino_train_embed_grad(
+            self.ctx, dout.data_ptr(), ld, self._flat(tokens, (n,), torch.int32, "tokens"), n, scale,
+            self._flat(out, (self.V, self.E), out.dtype, "dtable"),
+            DOMINO_DTYPE_BF16 if out.dtype == torch.bfloat16 else DOMINO_DTYPE_FP32, int(bool(accumulate)),
+            self._stream(stream)), "domino_train_embed_grad")
+        return out
+
+    # -- context -------------------------------------------------------------------
+
+    def status(self, stream=None) -> int:
+        """Synchronise the stream; return and clear the device's error word as a status code."""
+        return self._lib.domino_train_status(self.ctx, self._stream(stream))
+
+    def last_launch_count(self) -> int:
+        return self._lib.domino_train_last_launch_count(self.ctx)
+
+    def close(self):
+        if getattr(self, "ctx", None) is not None and self.ctx.value:
+            self._lib.domino_train_destroy(self.ctx)
+            self.ctx = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ---- autograd ------------------------------------------------------------------
+
+def distill_loss(train: DominoTrain, logits, ids, top, rest=None, temperature=1.0):
+    """Loss [n] of student logits [n, V], differentiable by the logits."""
+    return _functions()[0].apply(logits, train, ids, top, rest, temperature)
+
+
+def embedding(train: DominoTrain, table, tokens, scale=1.0):
+    """scale * table[tokens] [n, E], differentiable by the table (whose gradient
+    comes in the table's type)."""
+    return _functions()[1].apply(table, train, tokens, scale)
+
+
+_autograd = None
+
+
+def _functions():
+    global _autograd
+    if _autograd is None:
+        import torch
+
+        class Distill(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, logits, train, ids, top, rest, temperature):
+                loss, stats = train.distill_forward(logits, ids, top, rest, temperature)
+                ctx.save_for_backward(logits, ids, top, rest, stats)
+                ctx.train, ctx.temperature = train, temperature
+                return loss
+
+            @staticmethod
+            def backward(ctx, dloss):
+                logits, ids, top, rest, stats = ctx.saved_tensors
+                grad = ctx.train.distill_backward(logits, ids, top, rest, stats, dloss.contiguous(), ctx.temperature)
+                return grad, None, None, None, None, None
+
+        class Embedding(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, table, train, tokens, scale):
+                ctx.save_for_backward(tokens)
+                ctx.train, ctx.scale = train, scale
+                return train.embed(table, tokens, scale)
+
+            @staticmethod
+            def backward(ctx, dout):
+                (tokens,) = ctx.saved_tensors
+                if dout.stride(1) != 1 or dout.stride(0) < dout.shape[1]:
+                    dout = dout.contiguous()
+                return ctx.train.embed_grad(dout, tokens, ctx.scale, grad_dtype=ctx.train.torch_dtype), None, None, None
+
+        _autograd = (Distill, Embedding)
+    return _autograd
