@@ -84,7 +84,9 @@ int domino_train_init(domino_train_ctx** out, const domino_train_config* cfg, in
         o_keys[i] = take(n * 4);
         o_pos[i] = take(n * 4);
     }
-    const size_t o_hist = take(tiles * train::kSortMaxBins * 4);
+    const size_t o_hist = take(tiles > train::kSortMaxCluster ? tiles * train::kSortMaxBins * 4 : 0);
+    const size_t units = n > 0 ? train::max_sum_units((int)n, c->num_sms) : 0;
+    const size_t o_part = take(units * 2 * cfg->E * sizeof(float));
     if (cudaMalloc(&c->ws_base, off) != cudaSuccess) {
         cudaGetLastError();
         free(c);
@@ -97,7 +99,9 @@ int domino_train_init(domino_train_ctx** out, const domino_train_config* cfg, in
         c->pos[i] = (int32_t*)(base + o_pos[i]);
     }
     c->hist = (unsigned*)(base + o_hist);
-    if (cudaMemset(c->err, 0, sizeof(int)) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+    c->part = (float*)(base + o_part);
+    if (cudaMemset(c->err, 0, sizeof(int)) != cudaSuccess || train::prepare_embed_kernels() != cudaSuccess ||
+        cudaDeviceSynchronize() != cudaSuccess) {
         cudaFree(c->ws_base);
         free(c);
         return DOMINO_ERR_CUDA;

@@ -1,193 +1,676 @@
 // Scaled embedding lookup and the gradient of its table.
 //
-// The gradient sums the rows of dout that share a token.  The tokens are sorted
-// first (stable, least significant digit first, with their positions), so that
-// every sum has one owner and one order: no atomics on the gradient, the same
-// bits every time.
+//   lookup:    out[i] = scale * table[tok_i]
+//   gradient:  dtable[v] = scale * sum_{i: tok_i = v} dout[i]
+//
+// Both only move rows, so both are bound by HBM.  The gradient writes the whole
+// table and touches few of its rows (1024 tokens: under 1 % of 151,936), so most
+// of its time is the zeros, and the rest must not wait in front of them.
+//
+// The gradient sorts the tokens with their positions (stable), so that every
+// row's sum has one owner and one order: no atomics on the gradient, the same
+// bits every time.  Four launches:
+//   k_sort_cluster  one cluster sorts all tokens through distributed shared
+//                   memory (up to 16 x 8192; more take the tiled passes);
+//   k_fill          meanwhile writes zeros to the rows that no token names;
+//   k_sum_runs      every group of threads sums `unit` consecutive sorted places,
+//                   so that a frequent token's thousands of rows are spread over
+//                   the chip; a run of equal tokens that lies inside a unit goes
+//                   straight to its row, one that crosses a unit's edge leaves
+//                   a partial row;
+//   k_join_runs     adds a crossing run's partial rows in their order.
+#include <cooperative_groups.h>
+
 #include "train_internal.h"
 #include "train_math.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace domino {
 namespace train {
 
 namespace {
 
-constexpr int kSortThreads = 512;
-constexpr int kSortWarps = kSortThreads / 32;
+// ---- vectors of four elements ------------------------------------------------
 
+template <typename T, int VEC>
+struct Vec;
 template <typename T>
-__global__ void __launch_bounds__(256) k_embed(const T* __restrict__ table, const int32_t* __restrict__ tokens, int n,
-                                               int V, int E, float scale, T* __restrict__ out, long long ld, int* err) {
-    const int i = blockIdx.x;
-    const int tok = tokens[i];
-    const bool in = (unsigned)tok < (unsigned)V;
-    if (!in && tok != -1 && threadIdx.x == 0) atomicOr(err, kErrBadToken);
-    const T* src = table + (size_t)(in ? tok : 0) * E;
-    for (int e = threadIdx.x; e < E; e += 256)
-        out[(size_t)i * ld + e] = from_f32<T>(in ? scale * to_f32(src[e]) : 0.f);
+struct Vec<T, 1> {
+    T raw;
+    __device__ __forceinline__ void load(const T* p) { raw = *p; }
+    __device__ __forceinline__ void get(float* f) const { f[0] = to_f32(raw); }
+};
+template <>
+struct Vec<float, 4> {
+    float4 raw;
+    __device__ __forceinline__ void load(const float* p) { raw = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ void get(float* f) const { f[0] = raw.x; f[1] = raw.y; f[2] = raw.z; f[3] = raw.w; }
+};
+template <>
+struct Vec<__nv_bfloat16, 4> {
+    uint2 raw;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { raw = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ void get(float* f) const {
+        bf16x2_to_f32(raw.x, f[0], f[1]);
+        bf16x2_to_f32(raw.y, f[2], f[3]);
+    }
+};
+template <>
+struct Vec<__nv_bfloat16, 8> {
+    uint4 raw;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { raw = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void get(float* f) const {
+        bf16x2_to_f32(raw.x, f[0], f[1]);
+        bf16x2_to_f32(raw.y, f[2], f[3]);
+        bf16x2_to_f32(raw.z, f[4], f[5]);
+        bf16x2_to_f32(raw.w, f[6], f[7]);
+    }
+};
+__device__ __forceinline__ unsigned pack2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const unsigned*>(&v);
+}
+template <int VEC>
+__device__ __forceinline__ void store(float* p, const float* f) {
+    if constexpr (VEC == 4)
+        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    else
+        *p = f[0];
+}
+template <int VEC>
+__device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
+    if constexpr (VEC == 8)
+        *reinterpret_cast<uint4*>(p) =
+            make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+    else if constexpr (VEC == 4)
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+    else
+        *p = __float2bfloat16_rn(f[0]);
 }
 
-// Digit counts of each tile.  The first pass reads the tokens themselves (an
-// id outside [0, V) becomes V, which sorts last).
+// rows of `e`-byte elements can be moved `vec` elements at a time
+inline bool by_vec(const void* p, long long ld, int E, int e, int vec) {
+    return E % vec == 0 && ld % vec == 0 && (uintptr_t)p % (uintptr_t)(vec * e) == 0;
+}
+
+// Threads over the columns of rows of `cols` vectors, and rows per block.
+inline void row_block(int cols, int threads, dim3* block, int* col_blocks) {
+    int tx = 1;
+    while (tx < cols && tx < 32) tx *= 2;
+    *col_blocks = (cols + threads - 1) / threads;
+    if (cols > 32) tx = ((cols + *col_blocks - 1) / *col_blocks + 31) / 32 * 32;  // equal blocks of whole warps
+    *block = dim3(tx, threads / tx);
+}
+
+// ---- lookup ------------------------------------------------------------------
+
+constexpr int kEmbedThreads = 256;
+
+// Threads over a row's 16-byte vectors; each thread moves ROWS tokens' vectors
+// at once.
+template <typename T, int VEC, int ROWS>
+__global__ void __launch_bounds__(kEmbedThreads) k_embed(const T* __restrict__ table,
+                                                         const int32_t* __restrict__ tokens, int n, int V, int E,
+                                                         float scale, T* __restrict__ out, long long ld, int* err) {
+    const int col = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
+    const int i0 = (blockIdx.x * blockDim.y + threadIdx.y) * ROWS;
+    if (col >= E) return;
+    Vec<T, VEC> v[ROWS];
+    bool in[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int tok = i0 + r < n ? tokens[i0 + r] : -1;
+        in[r] = (unsigned)tok < (unsigned)V;
+        if (in[r]) v[r].load(table + (size_t)tok * E + col);
+        else if (tok != -1 && col == 0) atomicOr(err, kErrBadToken);
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        if (i0 + r >= n) break;
+        float f[VEC];
+        v[r].get(f);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) f[k] = in[r] ? scale * f[k] : 0.f;
+        store<VEC>(out + (size_t)(i0 + r) * ld + col, f);
+    }
+}
+
+// ---- sort --------------------------------------------------------------------
+//
+// Two passes of a stable counting sort, low digit first.  A tile's tokens are
+// split into 32-token steps in their order, a warp's steps adjacent; a token's
+// place is (smaller digits) + (its digit in the tiles before) + (in the warps
+// before) + (in its warp before it), the last from a warp-wide match.  Tokens
+// outside [0, V) sort last, as V.
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortSteps = kSortTile / kSortThreads;  // tokens per thread
+static_assert(kSortTile % kSortThreads == 0 && kSortMaxBins <= kSortThreads, "one bin per thread");
+
+struct SortShared {
+    uint16_t warp[kSortWarps][kSortMaxBins];  // a warp's counts, then the tile's counts in the warps before it
+    unsigned total[kSortMaxBins];             // the tile's count
+    unsigned base[kSortMaxBins];              // first place of the tile's tokens of a digit
+    unsigned sums[kSortWarps];
+};
+struct SortClusterShared {
+    SortShared s;
+    uint32_t key[kSortTile];
+    int32_t pos[kSortTile];
+};
+
+__device__ __forceinline__ uint32_t token_key(int tok, int V, int* err) {
+    if ((unsigned)tok < (unsigned)V) return (uint32_t)tok;
+    if (tok != -1) atomicOr(err, kErrBadToken);
+    return (uint32_t)V;
+}
+
+// Counts the digits of this tile: rank[j] = this thread's j-th token's place
+// among its warp's tokens of that digit; s.warp and s.total as above.
+__device__ void tile_count(SortShared& s, const uint32_t* key, unsigned* rank, int count, int shift, int bins) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int b = lane; b < bins; b += 32) s.warp[warp][b] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kSortSteps; ++j) {
+        const bool in = warp * (32 * kSortSteps) + j * 32 + lane < count;
+        const unsigned d = in ? key[j] >> shift & (unsigned)(bins - 1) : (unsigned)bins;
+        const unsigned peers = __match_any_sync(0xffffffffu, d);
+        const unsigned below = __popc(peers & ((1u << lane) - 1u));
+        if (in) rank[j] = s.warp[warp][d] + below;
+        __syncwarp();
+        if (in && below == 0) s.warp[warp][d] += (uint16_t)__popc(peers);
+        __syncwarp();
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < bins) {
+        unsigned run = 0;
+        for (int w = 0; w < kSortWarps; ++w) {
+            const unsigned c = s.warp[w][threadIdx.x];
+            s.warp[w][threadIdx.x] = (uint16_t)run;
+            run += c;
+        }
+        s.total[threadIdx.x] = run;
+    }
+}
+
+// s.base from this thread's digit's count in the tiles before and in all tiles.
+__device__ void tile_base(SortShared& s, unsigned before, unsigned all, int bins) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned incl = all;
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) s.sums[warp] = incl;
+    __syncthreads();
+    unsigned w = s.sums[lane], wi = w;
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, wi, o);
+        if (lane >= o) wi += y;
+    }
+    const unsigned smaller = __shfl_sync(0xffffffffu, wi - w, warp) + incl - all;
+    if ((int)threadIdx.x < bins) s.base[threadIdx.x] = smaller + before;
+    __syncthreads();
+}
+
+// All tokens in one cluster: a tile per CTA, exchanged through distributed
+// shared memory.  151,936 ids, 65,536 tokens: ??? us alone, hidden behind k_fill.
+__global__ void __launch_bounds__(kSortThreads) k_sort_cluster(const int32_t* __restrict__ tokens, int n, int V,
+                                                               int digit, uint32_t* __restrict__ keys_out,
+                                                               int32_t* __restrict__ pos_out, int* err) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    SortClusterShared& S = *reinterpret_cast<SortClusterShared*>(smem);
+    pdl_trigger();  // k_fill writes nothing that this kernel or one before it reads
+    cg::cluster_group cluster = cg::this_cluster();
+    const int tiles = (int)cluster.num_blocks(), tile = (int)cluster.block_rank();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = 1 << digit;
+    const int first = warp * (32 * kSortSteps) + lane;  // this thread's tokens of the tile: first + 32 j
+    const int count = max(0, min(kSortTile, n - tile * kSortTile));
+    uint32_t key[kSortSteps];
+    int32_t pos[kSortSteps];
+    unsigned rank[kSortSteps];
+#pragma unroll
+    for (int j = 0; j < kSortSteps; ++j) {
+        const int i = first + 32 * j;
+        key[j] = i < count ? token_key(tokens[tile * kSortTile + i], V, err) : 0u;
+        pos[j] = tile * kSortTile + i;
+    }
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        const int shift = pass * digit;
+        tile_count(S.s, key, rank, count, shift, bins);
+        cluster.sync();
+        unsigned before = 0, all = 0;
+        if ((int)threadIdx.x < bins)
+            for (int t = 0; t < tiles; ++t) {
+                const unsigned c = cluster.map_shared_rank(S.s.total, t)[threadIdx.x];
+                if (t < tile) before += c;
+                all += c;
+            }
+        tile_base(S.s, before, all, bins);
+#pragma unroll
+        for (int j = 0; j < kSortSteps; ++j)
+            if (first + 32 * j < count) {
+                const unsigned d = key[j] >> shift & (unsigned)(bins - 1);
+                const unsigned at = S.s.base[d] + S.s.warp[warp][d] + rank[j];
+                if (pass == 0) {
+                    cluster.map_shared_rank(S.key, at / kSortTile)[at % kSortTile] = key[j];
+                    cluster.map_shared_rank(S.pos, at / kSortTile)[at % kSortTile] = pos[j];
+                } else {
+                    keys_out[at] = key[j];
+                    pos_out[at] = pos[j];
+                }
+            }
+        cluster.sync();  // the tile's new tokens are here; nobody reads these counts any more
+        if (pass == 0) {
+#pragma unroll
+            for (int j = 0; j < kSortSteps; ++j)
+                if (first + 32 * j < count) {
+                    key[j] = S.key[first + 32 * j];
+                    pos[j] = S.pos[first + 32 * j];
+                }
+        }
+    }
+}
+
+// The same passes for more tokens than a cluster holds: digit counts of every
+// tile, then the tiles' tokens to their places.  tokens is null in pass 2.
+__device__ __forceinline__ void load_tile(const int32_t* tokens, const uint32_t* keys, const int32_t* pos, int V,
+                                          int count, uint32_t* key, int32_t* at, int* err) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const size_t lo = (size_t)blockIdx.x * kSortTile;
+#pragma unroll
+    for (int j = 0; j < kSortSteps; ++j) {
+        const int i = warp * (32 * kSortSteps) + j * 32 + lane;
+        key[j] = 0;
+        if (i < count) {
+            key[j] = tokens ? token_key(tokens[lo + i], V, err) : keys[lo + i];
+            if (at) at[j] = tokens ? (int32_t)(lo + i) : pos[lo + i];
+        }
+    }
+}
 __global__ void __launch_bounds__(kSortThreads) k_sort_count(const int32_t* __restrict__ tokens,
                                                              const uint32_t* __restrict__ keys, int n, int V,
                                                              int shift, int bins, unsigned* __restrict__ hist,
                                                              int* err) {
-    __shared__ unsigned h[kSortMaxBins];
-    for (int b = threadIdx.x; b < bins; b += kSortThreads) h[b] = 0;
-    __syncthreads();
-    const int lo = blockIdx.x * kSortTile, hi = min(n, lo + kSortTile);
-    for (int i = lo + threadIdx.x; i < hi; i += kSortThreads) {
-        uint32_t k;
-        if (tokens) {
-            const int t = tokens[i];
-            k = (unsigned)t < (unsigned)V ? (uint32_t)t : (uint32_t)V;
-            if (k == (uint32_t)V && t != -1) atomicOr(err, kErrBadToken);
-        } else {
-            k = keys[i];
-        }
-        atomicAdd(&h[k >> shift & (unsigned)(bins - 1)], 1u);
-    }
-    __syncthreads();
-    for (int b = threadIdx.x; b < bins; b += kSortThreads) hist[(size_t)blockIdx.x * kSortMaxBins + b] = h[b];
+    extern __shared__ __align__(16) uint8_t smem[];
+    SortShared& s = *reinterpret_cast<SortShared*>(smem);
+    const int count = min(kSortTile, n - (int)blockIdx.x * kSortTile);
+    uint32_t key[kSortSteps];
+    unsigned rank[kSortSteps];
+    load_tile(tokens, keys, nullptr, V, count, key, nullptr, err);
+    tile_count(s, key, rank, count, shift, bins);
+    if ((int)threadIdx.x < bins) hist[(size_t)blockIdx.x * kSortMaxBins + threadIdx.x] = s.total[threadIdx.x];
 }
-
-// Moves each tile's tokens to their places.  A bin's first place is the count
-// of all smaller bins plus this bin's count in the tiles before.
 __global__ void __launch_bounds__(kSortThreads) k_sort_place(const int32_t* __restrict__ tokens,
                                                              const uint32_t* __restrict__ keys_in,
                                                              const int32_t* __restrict__ pos_in, int n, int V,
                                                              int shift, int bins, const unsigned* __restrict__ hist,
                                                              uint32_t* __restrict__ keys_out,
-                                                             int32_t* __restrict__ pos_out) {
-    __shared__ unsigned base[kSortMaxBins], total[kSortMaxBins];
-    for (int b = threadIdx.x; b < bins; b += kSortThreads) {
-        unsigned before = 0, all = 0;
+                                                             int32_t* __restrict__ pos_out, int* err) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    SortShared& s = *reinterpret_cast<SortShared*>(smem);
+    const int count = min(kSortTile, n - (int)blockIdx.x * kSortTile);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t key[kSortSteps];
+    int32_t pos[kSortSteps];
+    unsigned rank[kSortSteps];
+    load_tile(tokens, keys_in, pos_in, V, count, key, pos, err);
+    tile_count(s, key, rank, count, shift, bins);
+    unsigned before = 0, all = 0;
+    if ((int)threadIdx.x < bins)
         for (int t = 0; t < (int)gridDim.x; ++t) {
-            const unsigned v = hist[(size_t)t * kSortMaxBins + b];
-            if (t < (int)blockIdx.x) before += v;
-            all += v;
+            const unsigned c = hist[(size_t)t * kSortMaxBins + threadIdx.x];
+            if (t < (int)blockIdx.x) before += c;
+            all += c;
         }
-        base[b] = before;
-        total[b] = all;
-    }
+    tile_base(s, before, all, bins);
+#pragma unroll
+    for (int j = 0; j < kSortSteps; ++j)
+        if (warp * (32 * kSortSteps) + j * 32 + lane < count) {
+            const unsigned d = key[j] >> shift & (unsigned)(bins - 1);
+            const unsigned at = s.base[d] + s.warp[warp][d] + rank[j];
+            keys_out[at] = key[j];
+            pos_out[at] = pos[j];
+        }
+}
+
+// ---- zeros ---------------------------------------------------------------------
+
+constexpr int kFillThreads = 512;
+
+// Zeros to the rows of this block's slice of the vocabulary that no token
+// names: a bit per row from a scan of all tokens (which stay in L2), then a warp
+// per row.  It may start while the sort is running and ends only after it, so
+// that what waits for this kernel has waited for both.
+template <typename G, bool VEC16>
+__global__ void __launch_bounds__(kFillThreads) k_fill(const int32_t* __restrict__ tokens, int n, int V, int E,
+                                                       int rows, G* __restrict__ dtable) {
+    extern __shared__ unsigned named[];
+    const int v0 = blockIdx.x * rows, count = min(rows, V - v0);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i = threadIdx.x; i < (rows + 31) / 32; i += kFillThreads) named[i] = 0;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        unsigned run = 0;
-        for (int b = 0; b < bins; ++b) {
-            base[b] += run;
-            run += total[b];
+    auto mark = [&](int tok) {
+        const unsigned r = (unsigned)tok - (unsigned)v0;  // a token outside the slice wraps past it
+        if (tok >= 0 && r < (unsigned)count) atomicOr(&named[r >> 5], 1u << (r & 31));
+    };
+    const int head = min(n, (int)((16 - ((uintptr_t)tokens & 15)) & 15) / 4), quads = (n - head) / 4;
+    const int4* t4 = reinterpret_cast<const int4*>(tokens + head);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < quads; i += kFillThreads) {
+        const int4 t = t4[i];
+        mark(t.x);
+        mark(t.y);
+        mark(t.z);
+        mark(t.w);
+    }
+    if ((int)threadIdx.x < head) mark(tokens[threadIdx.x]);
+    if ((int)threadIdx.x < n - head - 4 * quads) mark(tokens[head + 4 * quads + threadIdx.x]);
+    __syncthreads();
+    for (int r = warp; r < count; r += kFillThreads / 32) {
+        if (named[r >> 5] >> (r & 31) & 1u) continue;
+        G* row = dtable + (size_t)(v0 + r) * E;
+        if constexpr (VEC16) {
+            uint4* p = reinterpret_cast<uint4*>(row);
+            const int quad = E * (int)sizeof(G) / 16;
+            for (int i = lane; i < quad; i += 32) p[i] = make_uint4(0, 0, 0, 0);
+        } else {
+            for (int e = lane; e < E; e += 32) row[e] = from_f32<G>(0.f);
         }
     }
-    __syncthreads();
-    // one warp walks the tile 32 tokens at a time
-    const int lo = blockIdx.x * kSortTile, hi = min(n, lo + kSortTile);
-    if (threadIdx.x >= 32) return;
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-        const int i = i0 + (int)threadIdx.x;
-        const bool in = i < hi;
-        uint32_t k = 0;
-        int32_t p = 0;
-        if (in) {
-            if (tokens) {
-                const int t = tokens[i];
-                k = (unsigned)t < (unsigned)V ? (uint32_t)t : (uint32_t)V;
-                p = i;
-            } else {
-                k = keys_in[i];
-                p = pos_in[i];
+    pdl_wait();
+}
+
+// ---- sums ----------------------------------------------------------------------
+
+constexpr int kSumThreads = 256;
+constexpr int kSumAhead = 8;  // rows in flight per thread
+
+struct SumArgs {
+    const void* dout;
+    long long ld;
+    const uint32_t* keys;
+    const int32_t* pos;
+    int n, V, E;
+    int unit;       // sorted places per group of threads
+    float scale;
+    void* dtable;
+    bool accumulate;
+    float* part;    // [units][2][E]: the sums of a unit's first run, begun before it, and of its last run, not ended in it
+};
+
+template <typename G, int VEC>
+__device__ __forceinline__ void write_row(const SumArgs& p, uint32_t key, int col, const float* acc) {
+    G* to = static_cast<G*>(p.dtable) + (size_t)key * p.E + col;
+    float f[VEC];
+    if (p.accumulate) {
+        Vec<G, VEC> old;
+        old.load(to);
+        old.get(f);
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] = p.accumulate ? f[j] + p.scale * acc[j] : p.scale * acc[j];
+    store<VEC>(to, f);
+}
+
+template <typename T, typename G, int VEC>
+__global__ void __launch_bounds__(kSumThreads) k_sum_runs(SumArgs p) {
+    pdl_wait();
+    const int unit = blockIdx.x * blockDim.y + threadIdx.y;
+    const int col = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
+    const size_t lo64 = (size_t)unit * p.unit;
+    if (lo64 >= (size_t)p.n || col >= p.E) return;
+    const int lo = (int)lo64, hi = min(p.n, lo + p.unit);
+    const uint32_t none = 0xFFFFFFFFu, V = (uint32_t)p.V;
+    const uint32_t key_before = lo > 0 ? p.keys[lo - 1] : none, key_after = hi < p.n ? p.keys[hi] : none;
+    const T* dout = static_cast<const T*>(p.dout) + col;
+    float* part = p.part + ((size_t)unit * 2) * p.E + col;
+    float acc[VEC] = {};
+    uint32_t run = none;
+    int begun = lo;
+    auto end_run = [&](int end) {  // the run [begun, end) of token `run` is summed
+        if (run >= V) return;
+        if (begun == lo && run == key_before)
+            store<VEC>(part, acc);
+        else if (end == hi && run == key_after)
+            store<VEC>(part + p.E, acc);
+        else
+            write_row<G, VEC>(p, run, col, acc);
+    };
+    for (int i0 = lo; i0 < hi; i0 += kSumAhead) {
+        uint32_t key[kSumAhead];
+        Vec<T, VEC> row[kSumAhead];
+#pragma unroll
+        for (int j = 0; j < kSumAhead; ++j) {
+            key[j] = i0 + j < hi ? p.keys[i0 + j] : none;
+            if (key[j] < V) row[j].load(dout + (size_t)p.pos[i0 + j] * p.ld);
+        }
+#pragma unroll
+        for (int j = 0; j < kSumAhead; ++j) {
+            if (i0 + j < hi) {
+                if (key[j] != run) {
+                    end_run(i0 + j);
+                    run = key[j];
+                    begun = i0 + j;
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+                }
+                if (key[j] < V) {
+                    float f[VEC];
+                    row[j].get(f);
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) acc[k] += f[k];
+                }
             }
         }
-        const unsigned active = __ballot_sync(0xffffffffu, in);
-        if (in) {
-            const unsigned d = k >> shift & (unsigned)(bins - 1);
-            const unsigned peers = __match_any_sync(active, d);
-            const unsigned rank = __popc(peers & ((1u << threadIdx.x) - 1u));
-            const unsigned at = base[d] + rank;
-            __syncwarp(active);
-            if (rank == 0) base[d] += __popc(peers);
-            keys_out[at] = k;
-            pos_out[at] = p;
-        }
-        __syncwarp();
     }
+    end_run(hi);
+}
+
+// The unit in which a crossing run begins adds up its parts: its own last sum,
+// then the first sums of the units after it that the run reaches.
+template <typename G, int VEC>
+__global__ void __launch_bounds__(kSumThreads) k_join_runs(SumArgs p, int units) {
+    pdl_wait();
+    const int unit = blockIdx.x * blockDim.y + threadIdx.y;
+    const int col = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
+    if (unit + 1 >= units || col >= p.E) return;
+    const size_t lo = (size_t)unit * p.unit, hi = lo + p.unit;  // hi < n: it is not the last unit
+    const uint32_t run = p.keys[hi];
+    if (run >= (uint32_t)p.V || p.keys[hi - 1] != run) return;           // nothing crosses this edge
+    if (lo > 0 && p.keys[lo] == run && p.keys[lo - 1] == run) return;     // begun in an earlier unit
+    const float* part = p.part + col;
+    float acc[VEC];
+    Vec<float, VEC> v;
+    v.load(part + ((size_t)unit * 2 + 1) * p.E);
+    v.get(acc);
+    bool on = true;
+    for (int u0 = unit + 1; u0 < units && on; u0 += kSumAhead) {
+        Vec<float, VEC> row[kSumAhead];
+        bool in[kSumAhead];
+#pragma unroll
+        for (int j = 0; j < kSumAhead; ++j) {
+            in[j] = u0 + j < units && p.keys[(size_t)(u0 + j) * p.unit] == run;
+            if (in[j]) row[j].load(part + (size_t)(u0 + j) * 2 * p.E);
+        }
+#pragma unroll
+        for (int j = 0; j < kSumAhead; ++j) {
+            on = on && in[j];
+            if (on) {
+                float f[VEC];
+                row[j].get(f);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) acc[k] += f[k];
+            }
+        }
+    }
+    write_row<G, VEC>(p, run, col, acc);
+}
+
+// A unit's edges cost two partial rows, so units are as long as leaves
+// kUnitsPerSm groups of threads per SM, and no longer than kMaxUnit.
+constexpr int kUnitsPerSm = 8, kMinUnit = 4, kMaxUnit = 64;
+int sum_unit(int n, int num_sms) {
+    int unit = kMinUnit;
+    while (unit < kMaxUnit && (long long)unit * num_sms * kUnitsPerSm < n) unit *= 2;
+    return unit;
+}
+
+// ---- launches --------------------------------------------------------------------
+
+cudaError_t launch_sort(domino_train_ctx* c, const int32_t* tokens, int n, cudaStream_t st) {
+    const int V = c->cfg.V;
+    int bits = 1;
+    while ((V >> bits) != 0) ++bits;  // keys 0..V
+    const int digit = (bits + 1) / 2, bins = 1 << digit, tiles = (n + kSortTile - 1) / kSortTile;
+    if (tiles <= kSortMaxCluster) {
+        int size = 1;
+        while (size < tiles) size *= 2;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(size);
+        cfg.blockDim = dim3(kSortThreads);
+        cfg.dynamicSmemBytes = sizeof(SortClusterShared);
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = size;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        c->last_launches += 1;
+        return cudaLaunchKernelEx(&cfg, k_sort_cluster, tokens, n, V, digit, c->keys[0], c->pos[0], c->err);
+    }
+    for (int pass = 0; pass < 2; ++pass) {
+        const int32_t* tok = pass == 0 ? tokens : nullptr;
+        const int from = pass, to = 1 - pass, shift = pass * digit;
+        k_sort_count<<<tiles, kSortThreads, sizeof(SortShared), st>>>(tok, c->keys[from], n, V, shift, bins, c->hist,
+                                                                      c->err);
+        k_sort_place<<<tiles, kSortThreads, sizeof(SortShared), st>>>(tok, c->keys[from], c->pos[from], n, V, shift,
+                                                                      bins, c->hist, c->keys[to], c->pos[to], c->err);
+        c->last_launches += 2;
+    }
+    return cudaGetLastError();
+}
+
+// A launch that may start before the one in front of it ends, if there is one.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_after(bool after, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                         Args&&... args) {
+    if (after) return launch_pdl(kern, grid, block, smem, st, std::forward<Args>(args)...);
+    kern<<<grid, block, smem, st>>>(std::forward<Args>(args)...);
+    return cudaGetLastError();
 }
 
 template <typename G>
-__global__ void __launch_bounds__(256) k_zero(G* __restrict__ p, size_t n) {
-    for (size_t i = blockIdx.x * (size_t)256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) p[i] = from_f32<G>(0.f);
-}
-
-// One block per sorted place; the first place of a token sums its whole run.
-template <typename T, typename G>
-__global__ void __launch_bounds__(256) k_sum_runs(const T* __restrict__ dout, long long ld,
-                                                  const uint32_t* __restrict__ keys, const int32_t* __restrict__ pos,
-                                                  int n, int V, int E, float scale, G* __restrict__ dtable,
-                                                  bool accumulate) {
-    const int i = blockIdx.x;
-    const uint32_t k = keys[i];
-    if (k >= (uint32_t)V || (i > 0 && keys[i - 1] == k)) return;
-    for (int e = threadIdx.x; e < E; e += 256) {
-        float s = 0.f;
-        for (int j = i; j < n && keys[j] == k; ++j) s += to_f32(dout[(size_t)pos[j] * ld + e]);
-        G* to = dtable + (size_t)k * E + e;
-        *to = from_f32<G>(accumulate ? to_f32(*to) + scale * s : scale * s);
-    }
-}
-
-template <typename T, typename G>
-cudaError_t sum_runs(domino_train_ctx* c, const void* dout, long long ld, int n, float scale, void* dtable,
-                     bool accumulate, cudaStream_t st) {
+cudaError_t launch_fill(domino_train_ctx* c, const int32_t* tokens, int n, bool after, G* dtable, cudaStream_t st) {
     const int V = c->cfg.V, E = c->cfg.E;
-    if (!accumulate) {
-        k_zero<G><<<c->num_sms * 8, 256, 0, st>>>(static_cast<G*>(dtable), (size_t)V * E);
-        c->last_launches += 1;
-    }
-    if (n > 0) {
-        k_sum_runs<T, G><<<n, 256, 0, st>>>(static_cast<const T*>(dout), ld, c->keys[0], c->pos[0], n, V, E, scale,
-                                            static_cast<G*>(dtable), accumulate);
-        c->last_launches += 1;
-    }
-    return cudaGetLastError();
+    const int rows = (V + c->num_sms * 4 - 1) / (c->num_sms * 4), blocks = (V + rows - 1) / rows;
+    const bool vec = ((uintptr_t)dtable & 15) == 0 && (size_t)E * sizeof(G) % 16 == 0;
+    const size_t smem = (size_t)(rows + 31) / 32 * 4;
+    c->last_launches += 1;
+    return vec ? launch_after(after, k_fill<G, true>, blocks, kFillThreads, smem, st, tokens, n, V, E, rows, dtable)
+               : launch_after(after, k_fill<G, false>, blocks, kFillThreads, smem, st, tokens, n, V, E, rows, dtable);
+}
+
+template <typename T, typename G, int VEC>
+cudaError_t launch_sums(domino_train_ctx* c, const SumArgs& p, cudaStream_t st) {
+    const int cols = (p.E + VEC - 1) / VEC, units = (p.n + p.unit - 1) / p.unit;
+    dim3 block;
+    int col_blocks;
+    row_block(cols, kSumThreads, &block, &col_blocks);
+    const dim3 grid((units + block.y - 1) / block.y, col_blocks);
+    cudaError_t e = launch_pdl(k_sum_runs<T, G, VEC>, grid, block, 0, st, p);
+    if (e == cudaSuccess) e = launch_pdl(k_join_runs<G, VEC>, grid, block, 0, st, p, units);
+    c->last_launches += 2;
+    return e;
+}
+
+template <typename T, typename G>
+cudaError_t launch_grad(domino_train_ctx* c, SumArgs p, const int32_t* tokens, cudaStream_t st) {
+    cudaError_t e = cudaSuccess;
+    if (p.n > 0) e = launch_sort(c, tokens, p.n, st);
+    if (e == cudaSuccess && !p.accumulate) e = launch_fill(c, tokens, p.n, p.n > 0, static_cast<G*>(p.dtable), st);
+    if (e != cudaSuccess || p.n == 0) return e;
+    const bool four = by_vec(p.dout, p.ld, p.E, sizeof(T), 4) && by_vec(p.dtable, p.E, p.E, sizeof(G), 4);
+    return four ? launch_sums<T, G, 4>(c, p, st) : launch_sums<T, G, 1>(c, p, st);
 }
 
 }  // namespace
 
-cudaError_t launch_embed(domino_train_ctx* c, const void* table, const int32_t* tokens, int n, float scale, void* out,
-                         long long ld, cudaStream_t st) {
+int max_sum_units(int max_tokens, int num_sms) {
+    // calls that a unit of less than kMaxUnit suffices for have at most
+    // kUnitsPerSm * num_sms units, the others fewer than their tokens / kMaxUnit
+    const int a = kUnitsPerSm * num_sms, b = (max_tokens + kMaxUnit - 1) / kMaxUnit;
+    return a > b ? a : b;
+}
+
+cudaError_t prepare_embed_kernels() {
+    cudaError_t e = cudaFuncSetAttribute(k_sort_cluster, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sizeof(SortClusterShared));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_sort_cluster, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_sort_count, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SortShared));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_sort_place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SortShared));
+    return e;
+}
+
+namespace {
+template <typename T, int VEC>
+cudaError_t embed(domino_train_ctx* c, const void* table, const int32_t* tokens, int n, float scale, void* out,
+                  long long ld, cudaStream_t st) {
     const int V = c->cfg.V, E = c->cfg.E;
-    if (c->cfg.dtype == DOMINO_DTYPE_BF16)
-        k_embed<<<n, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(table), tokens, n, V, E, scale,
-                                   static_cast<__nv_bfloat16*>(out), ld, c->err);
-    else
-        k_embed<<<n, 256, 0, st>>>(static_cast<const float*>(table), tokens, n, V, E, scale, static_cast<float*>(out),
-                                   ld, c->err);
+    dim3 block;
+    int col_blocks;
+    row_block((E + VEC - 1) / VEC, kEmbedThreads, &block, &col_blocks);
+    // several rows a thread once that still fills the chip
+    const bool many = (long long)n * col_blocks >= (long long)c->num_sms * 32 * (int)block.y;
+    const int rows = (many ? 4 : 1) * (int)block.y;
+    const dim3 grid((n + rows - 1) / rows, col_blocks);
+    auto kern = many ? k_embed<T, VEC, 4> : k_embed<T, VEC, 1>;
+    kern<<<grid, block, 0, st>>>(static_cast<const T*>(table), tokens, n, V, E, scale, static_cast<T*>(out), ld,
+                                 c->err);
     c->last_launches = 1;
     return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_embed(domino_train_ctx* c, const void* table, const int32_t* tokens, int n, float scale, void* out,
+                         long long ld, cudaStream_t st) {
+    const int E = c->cfg.E;
+    if (c->cfg.dtype == DOMINO_DTYPE_BF16)
+        return by_vec(table, E, E, 2, 8) && by_vec(out, ld, E, 2, 8)
+                   ? embed<__nv_bfloat16, 8>(c, table, tokens, n, scale, out, ld, st)
+                   : embed<__nv_bfloat16, 1>(c, table, tokens, n, scale, out, ld, st);
+    return by_vec(table, E, E, 4, 4) && by_vec(out, ld, E, 4, 4)
+               ? embed<float, 4>(c, table, tokens, n, scale, out, ld, st)
+               : embed<float, 1>(c, table, tokens, n, scale, out, ld, st);
 }
 
 cudaError_t launch_embed_grad(domino_train_ctx* c, const void* dout, long long ld, const int32_t* tokens, int n,
                               float scale, void* dtable, int grad_dtype, bool accumulate, cudaStream_t st) {
-    const int V = c->cfg.V;
-    if (n > 0) {
-        int bits = 1;
-        while ((V >> bits) != 0) ++bits;  // keys 0..V
-        const int digit = (bits + 1) / 2, bins = 1 << digit, tiles = (n + kSortTile - 1) / kSortTile;
-        for (int pass = 0; pass < 2; ++pass) {
-            const int32_t* tok = pass == 0 ? tokens : nullptr;
-            const int from = pass, to = 1 - pass, shift = pass * digit;
-            k_sort_count<<<tiles, kSortThreads, 0, st>>>(tok, c->keys[from], n, V, shift, bins, c->hist, c->err);
-            k_sort_place<<<tiles, kSortThreads, 0, st>>>(tok, c->keys[from], c->pos[from], n, V, shift, bins, c->hist,
-                                                        c->keys[to], c->pos[to]);
-            c->last_launches += 2;
-        }
-    }
+    SumArgs p = {};
+    p.dout = dout;
+    p.ld = ld;
+    p.keys = c->keys[0];
+    p.pos = c->pos[0];
+    p.n = n;
+    p.V = c->cfg.V;
+    p.E = c->cfg.E;
+    p.unit = sum_unit(n, c->num_sms);
+    p.scale = scale;
+    p.dtable = dtable;
+    p.accumulate = accumulate;
+    p.part = c->part;
     const bool in16 = c->cfg.dtype == DOMINO_DTYPE_BF16, out16 = grad_dtype == DOMINO_DTYPE_BF16;
     if (in16)
-        return out16 ? sum_runs<__nv_bfloat16, __nv_bfloat16>(c, dout, ld, n, scale, dtable, accumulate, st)
-                     : sum_runs<__nv_bfloat16, float>(c, dout, ld, n, scale, dtable, accumulate, st);
-    return out16 ? sum_runs<float, __nv_bfloat16>(c, dout, ld, n, scale, dtable, accumulate, st)
-                 : sum_runs<float, float>(c, dout, ld, n, scale, dtable, accumulate, st);
+        return out16 ? launch_grad<__nv_bfloat16, __nv_bfloat16>(c, p, tokens, st)
+                     : launch_grad<__nv_bfloat16, float>(c, p, tokens, st);
+    return out16 ? launch_grad<float, __nv_bfloat16>(c, p, tokens, st) : launch_grad<float, float>(c, p, tokens, st);
 }
 
 }  // namespace train

@@ -14,14 +14,16 @@ struct domino_train_ctx {
     // embed_grad workspace (max_tokens > 0)
     uint32_t* keys[2];    // [max_tokens] tokens between the passes of the sort
     int32_t* pos[2];      // [max_tokens] their positions
-    unsigned* hist;       // [tiles][kSortMaxBins] digit counts of the sort's tiles
+    unsigned* hist;       // [tiles][kSortMaxBins] digit counts of the sort's tiles (more tokens than a cluster sorts)
+    float* part;          // [units][2][E] partial sums of the runs that cross a unit's edge
     void* ws_base;
 };
 
 namespace domino {
 namespace train {
 
-constexpr int kSortTile = 4096;      // tokens per tile of the sort
+constexpr int kSortTile = 8192;      // tokens per tile of the sort
+constexpr int kSortMaxCluster = 16;  // tiles that one cluster sorts
 constexpr int kSortMaxBins = 1024;   // two digits cover tokens up to DOMINO_TRAIN_MAX_V
 
 struct DistillArgs {
@@ -46,6 +48,8 @@ cudaError_t launch_top(domino_train_ctx* c, const void* x, int dtype, long long 
 cudaError_t launch_distill_forward(domino_train_ctx* c, const DistillArgs& a, cudaStream_t st);
 cudaError_t launch_distill_backward(domino_train_ctx* c, const DistillArgs& a, cudaStream_t st);
 cudaError_t launch_distill_step(domino_train_ctx* c, const DistillArgs& a, cudaStream_t st);
+cudaError_t prepare_embed_kernels();
+int max_sum_units(int max_tokens, int num_sms);  // most groups of threads that sum runs in any call
 cudaError_t launch_embed(domino_train_ctx* c, const void* table, const int32_t* tokens, int n, float scale, void* out,
                          long long ld, cudaStream_t st);
 cudaError_t launch_embed_grad(domino_train_ctx* c, const void* dout, long long ld, const int32_t* tokens, int n,

@@ -90,6 +90,13 @@ def test_embed_grad_many_tokens(n, kind):
     check_grad(n, 3000, 24, kind, "bf16", "fp32")
 
 
+@pytest.mark.parametrize("n", [8191, 8192, 8193, 16385, 40000, 131072, 131073, 140001])
+@pytest.mark.parametrize("kind", ["uniform", "frequent", "padded"])
+def test_embed_grad_tile_edges(n, kind):
+    """Token counts at and beside the sort's tiles and the most that one cluster sorts."""
+    check_grad(n, 5000, 8, kind, "bf16", "fp32")
+
+
 @pytest.mark.parametrize("V", [2, 3, 255, 256, 257, 1023, 1024, 1025, 65535, 65536, 151936, 524288])
 def test_embed_grad_vocabulary_edges(V):
     """The sort's digits: vocabularies at and beside powers of two, first and last ids."""
