@@ -87,6 +87,7 @@ int domino_train_init(domino_train_ctx** out, const domino_train_config* cfg, in
     const size_t o_hist = take(tiles > train::kSortMaxCluster ? tiles * train::kSortMaxBins * 4 : 0);
     const size_t units = n > 0 ? train::max_sum_units((int)n, c->num_sms) : 0;
     const size_t o_part = take(units * 2 * cfg->E * sizeof(float));
+    const size_t o_named = take(cfg->E > 0 ? ((size_t)cfg->V + 31) / 32 * 4 : 0), o_claim = take(sizeof(unsigned));
     if (cudaMalloc(&c->ws_base, off) != cudaSuccess) {
         cudaGetLastError();
         free(c);
@@ -100,6 +101,8 @@ int domino_train_init(domino_train_ctx** out, const domino_train_config* cfg, in
     }
     c->hist = (unsigned*)(base + o_hist);
     c->part = (float*)(base + o_part);
+    c->named = (unsigned*)(base + o_named);
+    c->claim = (unsigned*)(base + o_claim);
     if (cudaMemset(c->err, 0, sizeof(int)) != cudaSuccess || train::prepare_embed_kernels() != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
         cudaFree(c->ws_base);

@@ -5,14 +5,15 @@
 //
 // Both only move rows, so both are bound by HBM.  The gradient writes the whole
 // table and touches few of its rows (1024 tokens: under 1 % of 151,936), so most
-// of its time is the zeros, and the rest must not wait in front of them.
+// of its time is the zeros, and nothing must wait in front of them.
 //
 // The gradient sorts the tokens with their positions (stable), so that every
 // row's sum has one owner and one order: no atomics on the gradient, the same
-// bits every time.  Four launches:
-//   k_sort_cluster  one cluster sorts all tokens through distributed shared
-//                   memory (up to 16 x 8192; more take the tiled passes);
-//   k_fill          meanwhile writes zeros to the rows that no token names;
+// bits every time.  Launches:
+//   k_mark          finds the rows that tokens name;
+//   k_fill          writes zeros to the others;
+//   k_sort_cluster  beside it, one cluster sorts all tokens through distributed
+//                   shared memory (up to 16 x 8192; more take the tiled passes);
 //   k_sum_runs      every group of threads sums `unit` consecutive sorted places,
 //                   so that a frequent token's thousands of rows are spread over
 //                   the chip; a run of equal tokens that lies inside a unit goes
@@ -167,15 +168,23 @@ __device__ __forceinline__ uint32_t token_key(int tok, int V, int* err) {
     return (uint32_t)V;
 }
 
+// The tile's tokens by thread: step j of this thread's warp.  A tile that is not
+// full spreads over all warps.
+__device__ __forceinline__ int tile_steps(int count) { return (count + kSortThreads - 1) / kSortThreads; }
+__device__ __forceinline__ int tile_place(int j, int steps) {
+    return ((int)(threadIdx.x >> 5) * steps + j) * 32 + (int)(threadIdx.x & 31);
+}
+
 // Counts the digits of this tile: rank[j] = this thread's j-th token's place
 // among its warp's tokens of that digit; s.warp and s.total as above.
 __device__ void tile_count(SortShared& s, const uint32_t* key, unsigned* rank, int count, int shift, int bins) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, steps = tile_steps(count);
     for (int b = lane; b < bins; b += 32) s.warp[warp][b] = 0;
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < kSortSteps; ++j) {
-        const bool in = warp * (32 * kSortSteps) + j * 32 + lane < count;
+        if (j >= steps) break;
+        const bool in = tile_place(j, steps) < count;
         const unsigned d = in ? key[j] >> shift & (unsigned)(bins - 1) : (unsigned)bins;
         const unsigned peers = __match_any_sync(0xffffffffu, d);
         const unsigned below = __popc(peers & ((1u << lane) - 1u));
@@ -223,19 +232,17 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_cluster(const int32_t* __
                                                                int32_t* __restrict__ pos_out, int* err) {
     extern __shared__ __align__(16) uint8_t smem[];
     SortClusterShared& S = *reinterpret_cast<SortClusterShared*>(smem);
-    pdl_trigger();  // k_fill writes nothing that this kernel or one before it reads
     cg::cluster_group cluster = cg::this_cluster();
     const int tiles = (int)cluster.num_blocks(), tile = (int)cluster.block_rank();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = 1 << digit;
-    const int first = warp * (32 * kSortSteps) + lane;  // this thread's tokens of the tile: first + 32 j
-    const int count = max(0, min(kSortTile, n - tile * kSortTile));
+    const int warp = threadIdx.x >> 5, bins = 1 << digit;
+    const int count = max(0, min(kSortTile, n - tile * kSortTile)), steps = tile_steps(count);
     uint32_t key[kSortSteps];
     int32_t pos[kSortSteps];
     unsigned rank[kSortSteps];
 #pragma unroll
     for (int j = 0; j < kSortSteps; ++j) {
-        const int i = first + 32 * j;
-        key[j] = i < count ? token_key(tokens[tile * kSortTile + i], V, err) : 0u;
+        const int i = tile_place(j, steps);
+        key[j] = j < steps && i < count ? token_key(tokens[tile * kSortTile + i], V, err) : 0u;
         pos[j] = tile * kSortTile + i;
     }
 #pragma unroll 1
@@ -245,15 +252,16 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_cluster(const int32_t* __
         cluster.sync();
         unsigned before = 0, all = 0;
         if ((int)threadIdx.x < bins)
-            for (int t = 0; t < tiles; ++t) {
-                const unsigned c = cluster.map_shared_rank(S.s.total, t)[threadIdx.x];
+#pragma unroll
+            for (int t = 0; t < kSortMaxCluster; ++t) {
+                const unsigned c = t < tiles ? cluster.map_shared_rank(S.s.total, t)[threadIdx.x] : 0u;
                 if (t < tile) before += c;
                 all += c;
             }
         tile_base(S.s, before, all, bins);
 #pragma unroll
         for (int j = 0; j < kSortSteps; ++j)
-            if (first + 32 * j < count) {
+            if (j < steps && tile_place(j, steps) < count) {
                 const unsigned d = key[j] >> shift & (unsigned)(bins - 1);
                 const unsigned at = S.s.base[d] + S.s.warp[warp][d] + rank[j];
                 if (pass == 0) {
@@ -268,25 +276,28 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_cluster(const int32_t* __
         if (pass == 0) {
 #pragma unroll
             for (int j = 0; j < kSortSteps; ++j)
-                if (first + 32 * j < count) {
-                    key[j] = S.key[first + 32 * j];
-                    pos[j] = S.pos[first + 32 * j];
+                if (j < steps && tile_place(j, steps) < count) {
+                    key[j] = S.key[tile_place(j, steps)];
+                    pos[j] = S.pos[tile_place(j, steps)];
                 }
         }
     }
+    // launched beside k_fill (whose kernels before it are done and write nothing
+    // read here): end after it, so that what waits for this kernel has waited for both
+    pdl_wait();
 }
 
 // The same passes for more tokens than a cluster holds: digit counts of every
 // tile, then the tiles' tokens to their places.  tokens is null in pass 2.
 __device__ __forceinline__ void load_tile(const int32_t* tokens, const uint32_t* keys, const int32_t* pos, int V,
                                           int count, uint32_t* key, int32_t* at, int* err) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int steps = tile_steps(count);
     const size_t lo = (size_t)blockIdx.x * kSortTile;
 #pragma unroll
     for (int j = 0; j < kSortSteps; ++j) {
-        const int i = warp * (32 * kSortSteps) + j * 32 + lane;
+        const int i = tile_place(j, steps);
         key[j] = 0;
-        if (i < count) {
+        if (j < steps && i < count) {
             key[j] = tokens ? token_key(tokens[lo + i], V, err) : keys[lo + i];
             if (at) at[j] = tokens ? (int32_t)(lo + i) : pos[lo + i];
         }
@@ -314,7 +325,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_place(const int32_t* __re
     extern __shared__ __align__(16) uint8_t smem[];
     SortShared& s = *reinterpret_cast<SortShared*>(smem);
     const int count = min(kSortTile, n - (int)blockIdx.x * kSortTile);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5, steps = tile_steps(count);
     uint32_t key[kSortSteps];
     int32_t pos[kSortSteps];
     unsigned rank[kSortSteps];
@@ -330,7 +341,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_place(const int32_t* __re
     tile_base(s, before, all, bins);
 #pragma unroll
     for (int j = 0; j < kSortSteps; ++j)
-        if (warp * (32 * kSortSteps) + j * 32 + lane < count) {
+        if (j < steps && tile_place(j, steps) < count) {
             const unsigned d = key[j] >> shift & (unsigned)(bins - 1);
             const unsigned at = s.base[d] + s.warp[warp][d] + rank[j];
             keys_out[at] = key[j];
@@ -340,28 +351,34 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_place(const int32_t* __re
 
 // ---- zeros ---------------------------------------------------------------------
 
+constexpr int kMarkThreads = 1024;
+constexpr int kMarkBlocks = 16;   // slices of the vocabulary
 constexpr int kFillThreads = 512;
+constexpr int kFillBlocksPerSm = 2;  // half of an SM's threads: the sort needs the others
+constexpr int kFillRows = 32;     // rows per claim: one word of the bits
 
-// Zeros to the rows of this block's slice of the vocabulary that no token
-// names: a bit per row from a scan of all tokens (which stay in L2), then a warp
-// per row.  It may start while the sort is running and ends only after it, so
-// that what waits for this kernel has waited for both.
-template <typename G, bool VEC16>
-__global__ void __launch_bounds__(kFillThreads) k_fill(const int32_t* __restrict__ tokens, int n, int V, int E,
-                                                       int rows, G* __restrict__ dtable) {
-    extern __shared__ unsigned named[];
-    const int v0 = blockIdx.x * rows, count = min(rows, V - v0);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < (rows + 31) / 32; i += kFillThreads) named[i] = 0;
+// A bit per row of the table that some token names (a block per slice of the
+// vocabulary, each scanning all tokens), and the claim counter of k_fill.
+__global__ void __launch_bounds__(kMarkThreads) k_mark(const int32_t* __restrict__ tokens, int n, int V, int words,
+                                                       unsigned* __restrict__ named, unsigned* __restrict__ claim) {
+    extern __shared__ unsigned bits[];
+    pdl_trigger();
+    const int w0 = blockIdx.x * words, count = max(0, min(words, (V + 31) / 32 - w0));
+    const int v0 = w0 * 32;
+    for (int i = threadIdx.x; i < count; i += kMarkThreads) bits[i] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *claim = 0;
     __syncthreads();
     auto mark = [&](int tok) {
-        const unsigned r = (unsigned)tok - (unsigned)v0;  // a token outside the slice wraps past it
-        if (tok >= 0 && r < (unsigned)count) atomicOr(&named[r >> 5], 1u << (r & 31));
+        const unsigned r = (unsigned)tok - (unsigned)v0;  // a token below the slice wraps past it
+        if ((unsigned)tok >= (unsigned)V || r >= (unsigned)count * 32u) return;
+        const unsigned bit = 1u << (r & 31);
+        // look first: a frequent token's thousands of places would queue at its word
+        if (!(reinterpret_cast<volatile unsigned*>(bits)[r >> 5] & bit)) atomicOr(&bits[r >> 5], bit);
     };
     const int head = min(n, (int)((16 - ((uintptr_t)tokens & 15)) & 15) / 4), quads = (n - head) / 4;
     const int4* t4 = reinterpret_cast<const int4*>(tokens + head);
-#pragma unroll 4
-    for (int i = threadIdx.x; i < quads; i += kFillThreads) {
+#pragma unroll 8
+    for (int i = threadIdx.x; i < quads; i += kMarkThreads) {
         const int4 t = t4[i];
         mark(t.x);
         mark(t.y);
@@ -371,24 +388,46 @@ __global__ void __launch_bounds__(kFillThreads) k_fill(const int32_t* __restrict
     if ((int)threadIdx.x < head) mark(tokens[threadIdx.x]);
     if ((int)threadIdx.x < n - head - 4 * quads) mark(tokens[head + 4 * quads + threadIdx.x]);
     __syncthreads();
-    for (int r = warp; r < count; r += kFillThreads / 32) {
-        if (named[r >> 5] >> (r & 31) & 1u) continue;
-        G* row = dtable + (size_t)(v0 + r) * E;
-        if constexpr (VEC16) {
-            uint4* p = reinterpret_cast<uint4*>(row);
-            const int quad = E * (int)sizeof(G) / 16;
-            for (int i = lane; i < quad; i += 32) p[i] = make_uint4(0, 0, 0, 0);
-        } else {
-            for (int e = lane; e < E; e += 32) row[e] = from_f32<G>(0.f);
+    for (int i = threadIdx.x; i < count; i += kMarkThreads) named[w0 + i] = bits[i];
+}
+
+// Zeros to the rows that no token names.  One wave of blocks that claims 32
+// rows at a time: an SM that also sorts, or meets many named rows, takes fewer.
+template <typename G, bool VEC16>
+__global__ void __launch_bounds__(kFillThreads) k_fill(const unsigned* __restrict__ named, unsigned* __restrict__ claim,
+                                                       int V, int E, G* __restrict__ dtable) {
+    __shared__ unsigned next[2];
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, words = (V + 31) / 32;
+    for (int turn = 0;; turn ^= 1) {
+        if (threadIdx.x == 0) next[turn] = atomicAdd(claim, 1u);
+        __syncthreads();
+        const unsigned w = next[turn];
+        if (w >= (unsigned)words) return;
+        const unsigned bits = named[w];
+        for (int r = warp; r < kFillRows; r += kFillThreads / 32) {
+            const int v = (int)w * 32 + r;
+            if (v >= V || (bits >> r & 1u)) continue;
+            G* row = dtable + (size_t)v * E;
+            if constexpr (VEC16) {
+                uint4* p = reinterpret_cast<uint4*>(row);
+                const int quads = E * (int)sizeof(G) / 16;
+                for (int i = lane; i < quads; i += 32) p[i] = make_uint4(0, 0, 0, 0);
+            } else {
+                for (int e = lane; e < E; e += 32) row[e] = from_f32<G>(0.f);
+            }
         }
     }
-    pdl_wait();
 }
 
 // ---- sums ----------------------------------------------------------------------
 
 constexpr int kSumThreads = 256;
-constexpr int kSumAhead = 8;  // rows in flight per thread
+constexpr int kSumAhead = 4;    // rows in flight per thread, and as many being added
+constexpr int kJoinAhead = 8;   // parts in flight per thread
+constexpr int kMinUnit = 4, kMaxUnit = 64, kUnitsPerSm = 8;
+constexpr int kJoinThreads = 512;
 
 struct SumArgs {
     const void* dout;
@@ -419,101 +458,125 @@ __device__ __forceinline__ void write_row(const SumArgs& p, uint32_t key, int co
 
 template <typename T, typename G, int VEC>
 __global__ void __launch_bounds__(kSumThreads) k_sum_runs(SumArgs p) {
+    extern __shared__ uint32_t entries[];  // per group of threads: the unit's keys, then their positions
+    pdl_trigger();
     pdl_wait();
     const int unit = blockIdx.x * blockDim.y + threadIdx.y;
     const int col = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
-    const size_t lo64 = (size_t)unit * p.unit;
-    if (lo64 >= (size_t)p.n || col >= p.E) return;
-    const int lo = (int)lo64, hi = min(p.n, lo + p.unit);
+    const int lo = (int)min((size_t)unit * p.unit, (size_t)p.n), hi = min(p.n, lo + p.unit), count = hi - lo;
+    uint32_t* keys = entries + threadIdx.y * 2 * p.unit;
+    int32_t* pos = reinterpret_cast<int32_t*>(keys + p.unit);
+    for (int i = threadIdx.x; i < count; i += blockDim.x) {
+        keys[i] = p.keys[lo + i];
+        pos[i] = p.pos[lo + i];
+    }
     const uint32_t none = 0xFFFFFFFFu, V = (uint32_t)p.V;
     const uint32_t key_before = lo > 0 ? p.keys[lo - 1] : none, key_after = hi < p.n ? p.keys[hi] : none;
+    __syncthreads();
+    if (count == 0 || col >= p.E) return;
     const T* dout = static_cast<const T*>(p.dout) + col;
     float* part = p.part + ((size_t)unit * 2) * p.E + col;
     float acc[VEC] = {};
     uint32_t run = none;
-    int begun = lo;
+    int begun = 0;
     auto end_run = [&](int end) {  // the run [begun, end) of token `run` is summed
         if (run >= V) return;
-        if (begun == lo && run == key_before)
+        if (begun == 0 && run == key_before)
             store<VEC>(part, acc);
-        else if (end == hi && run == key_after)
+        else if (end == count && run == key_after)
             store<VEC>(part + p.E, acc);
         else
             write_row<G, VEC>(p, run, col, acc);
     };
-    for (int i0 = lo; i0 < hi; i0 += kSumAhead) {
-        uint32_t key[kSumAhead];
-        Vec<T, VEC> row[kSumAhead];
+    Vec<T, VEC> row[2][kSumAhead];
+    auto load = [&](Vec<T, VEC>* r, int i0) {
+#pragma unroll
+        for (int j = 0; j < kSumAhead; ++j)
+            if (i0 + j < count && keys[i0 + j] < V) r[j].load(dout + (size_t)pos[i0 + j] * p.ld);
+    };
+    auto sum = [&](const Vec<T, VEC>* r, int i0) {
 #pragma unroll
         for (int j = 0; j < kSumAhead; ++j) {
-            key[j] = i0 + j < hi ? p.keys[i0 + j] : none;
-            if (key[j] < V) row[j].load(dout + (size_t)p.pos[i0 + j] * p.ld);
+            if (i0 + j >= count) break;
+            const uint32_t key = keys[i0 + j];
+            if (key != run) {
+                end_run(i0 + j);
+                run = key;
+                begun = i0 + j;
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+            }
+            if (key < V) {
+                float f[VEC];
+                r[j].get(f);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) acc[k] += f[k];
+            }
         }
+    };
+    load(row[0], 0);
+    for (int i0 = 0; i0 < count; i0 += 2 * kSumAhead) {
+        load(row[1], i0 + kSumAhead);
+        sum(row[0], i0);
+        load(row[0], i0 + 2 * kSumAhead);
+        sum(row[1], i0 + kSumAhead);
+    }
+    end_run(count);
+}
+
+// The unit in which a crossing run begins adds up its parts: its own last sum,
+// then the first sums of the units after it that the run reaches.  One block
+// per unit and column block; the block's rows of threads take the parts in
+// turns and their sums are added in a fixed order, so that a run of thousands
+// of tokens costs a few round trips.
+template <typename G, int VEC>
+__global__ void __launch_bounds__(kJoinThreads) k_join_runs(SumArgs p, int units) {
+    __shared__ float sums[kJoinThreads * VEC];
+    pdl_wait();
+    const int unit = blockIdx.x, me = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
+    const size_t lo = (size_t)unit * p.unit, hi = lo + p.unit;  // hi < n: the grid leaves out the last unit
+    const uint32_t run = p.keys[hi];
+    if (run >= (uint32_t)p.V || p.keys[hi - 1] != run) return;        // nothing crosses this edge
+    if (lo > 0 && p.keys[lo] == run && p.keys[lo - 1] == run) return;  // begun in an earlier unit
+    // units after this one whose first place belongs to the run
+    int reached = 0;
+    for (int more = threads; more == threads; reached += more) {
+        const int u = unit + 1 + reached + me;
+        more = __syncthreads_count(u < units && p.keys[(size_t)u * p.unit] == run);
+    }
+    const int col = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
+    const float* part = p.part + ((size_t)unit * 2) * p.E + col;  // part r > 0 is 2 r rows on, part 0 one row on
+    float acc[VEC] = {};
+    if (col < p.E) {
+        for (int r0 = threadIdx.y; r0 <= reached; r0 += kJoinAhead * blockDim.y) {
+            Vec<float, VEC> row[kJoinAhead];
 #pragma unroll
-        for (int j = 0; j < kSumAhead; ++j) {
-            if (i0 + j < hi) {
-                if (key[j] != run) {
-                    end_run(i0 + j);
-                    run = key[j];
-                    begun = i0 + j;
+            for (int j = 0; j < kJoinAhead; ++j) {
+                const int r = r0 + j * blockDim.y;
+                if (r <= reached) row[j].load(part + (size_t)(r == 0 ? 1 : 2 * r) * p.E);
+            }
 #pragma unroll
-                    for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
-                }
-                if (key[j] < V) {
+            for (int j = 0; j < kJoinAhead; ++j)
+                if (r0 + j * blockDim.y <= reached) {
                     float f[VEC];
                     row[j].get(f);
 #pragma unroll
                     for (int k = 0; k < VEC; ++k) acc[k] += f[k];
                 }
-            }
         }
     }
-    end_run(hi);
-}
-
-// The unit in which a crossing run begins adds up its parts: its own last sum,
-// then the first sums of the units after it that the run reaches.
-template <typename G, int VEC>
-__global__ void __launch_bounds__(kSumThreads) k_join_runs(SumArgs p, int units) {
-    pdl_wait();
-    const int unit = blockIdx.x * blockDim.y + threadIdx.y;
-    const int col = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
-    if (unit + 1 >= units || col >= p.E) return;
-    const size_t lo = (size_t)unit * p.unit, hi = lo + p.unit;  // hi < n: it is not the last unit
-    const uint32_t run = p.keys[hi];
-    if (run >= (uint32_t)p.V || p.keys[hi - 1] != run) return;           // nothing crosses this edge
-    if (lo > 0 && p.keys[lo] == run && p.keys[lo - 1] == run) return;     // begun in an earlier unit
-    const float* part = p.part + col;
-    float acc[VEC];
-    Vec<float, VEC> v;
-    v.load(part + ((size_t)unit * 2 + 1) * p.E);
-    v.get(acc);
-    bool on = true;
-    for (int u0 = unit + 1; u0 < units && on; u0 += kSumAhead) {
-        Vec<float, VEC> row[kSumAhead];
-        bool in[kSumAhead];
 #pragma unroll
-        for (int j = 0; j < kSumAhead; ++j) {
-            in[j] = u0 + j < units && p.keys[(size_t)(u0 + j) * p.unit] == run;
-            if (in[j]) row[j].load(part + (size_t)(u0 + j) * 2 * p.E);
-        }
+    for (int k = 0; k < VEC; ++k) sums[me * VEC + k] = acc[k];
+    __syncthreads();
+    if (threadIdx.y != 0 || col >= p.E) return;
+    for (int y = 1; y < (int)blockDim.y; ++y)
 #pragma unroll
-        for (int j = 0; j < kSumAhead; ++j) {
-            on = on && in[j];
-            if (on) {
-                float f[VEC];
-                row[j].get(f);
-#pragma unroll
-                for (int k = 0; k < VEC; ++k) acc[k] += f[k];
-            }
-        }
-    }
+        for (int k = 0; k < VEC; ++k) acc[k] += sums[(y * blockDim.x + threadIdx.x) * VEC + k];
     write_row<G, VEC>(p, run, col, acc);
 }
 
 // A unit's edges cost two partial rows, so units are as long as leaves
 // kUnitsPerSm groups of threads per SM, and no longer than kMaxUnit.
-constexpr int kUnitsPerSm = 8, kMinUnit = 4, kMaxUnit = 64;
 int sum_unit(int n, int num_sms) {
     int unit = kMinUnit;
     while (unit < kMaxUnit && (long long)unit * num_sms * kUnitsPerSm < n) unit *= 2;
@@ -522,7 +585,8 @@ int sum_unit(int n, int num_sms) {
 
 // ---- launches --------------------------------------------------------------------
 
-cudaError_t launch_sort(domino_train_ctx* c, const int32_t* tokens, int n, cudaStream_t st) {
+// `beside`: it may start while the launch in front of it runs.
+cudaError_t launch_sort(domino_train_ctx* c, const int32_t* tokens, int n, bool beside, cudaStream_t st) {
     const int V = c->cfg.V;
     int bits = 1;
     while ((V >> bits) != 0) ++bits;  // keys 0..V
@@ -535,12 +599,14 @@ cudaError_t launch_sort(domino_train_ctx* c, const int32_t* tokens, int n, cudaS
         cfg.blockDim = dim3(kSortThreads);
         cfg.dynamicSmemBytes = sizeof(SortClusterShared);
         cfg.stream = st;
-        cudaLaunchAttribute attr[1];
+        cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = size;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = beside ? 2 : 1;
         c->last_launches += 1;
         return cudaLaunchKernelEx(&cfg, k_sort_cluster, tokens, n, V, digit, c->keys[0], c->pos[0], c->err);
     }
@@ -556,24 +622,18 @@ cudaError_t launch_sort(domino_train_ctx* c, const int32_t* tokens, int n, cudaS
     return cudaGetLastError();
 }
 
-// A launch that may start before the one in front of it ends, if there is one.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_after(bool after, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                         Args&&... args) {
-    if (after) return launch_pdl(kern, grid, block, smem, st, std::forward<Args>(args)...);
-    kern<<<grid, block, smem, st>>>(std::forward<Args>(args)...);
-    return cudaGetLastError();
-}
-
 template <typename G>
-cudaError_t launch_fill(domino_train_ctx* c, const int32_t* tokens, int n, bool after, G* dtable, cudaStream_t st) {
+cudaError_t launch_fill(domino_train_ctx* c, const int32_t* tokens, int n, G* dtable, cudaStream_t st) {
     const int V = c->cfg.V, E = c->cfg.E;
-    const int rows = (V + c->num_sms * 4 - 1) / (c->num_sms * 4), blocks = (V + rows - 1) / rows;
+    const int all = (V + 31) / 32, words = (all + kMarkBlocks - 1) / kMarkBlocks;
+    k_mark<<<kMarkBlocks, kMarkThreads, (size_t)words * 4, st>>>(tokens, n, V, words, c->named, c->claim);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int most = c->num_sms * kFillBlocksPerSm, blocks = all < most ? all : most;
     const bool vec = ((uintptr_t)dtable & 15) == 0 && (size_t)E * sizeof(G) % 16 == 0;
-    const size_t smem = (size_t)(rows + 31) / 32 * 4;
-    c->last_launches += 1;
-    return vec ? launch_after(after, k_fill<G, true>, blocks, kFillThreads, smem, st, tokens, n, V, E, rows, dtable)
-               : launch_after(after, k_fill<G, false>, blocks, kFillThreads, smem, st, tokens, n, V, E, rows, dtable);
+    c->last_launches += 2;
+    return launch_pdl(vec ? k_fill<G, true> : k_fill<G, false>, blocks, kFillThreads, 0, st,
+                      static_cast<const unsigned*>(c->named), c->claim, V, E, dtable);
 }
 
 template <typename T, typename G, int VEC>
@@ -582,18 +642,22 @@ cudaError_t launch_sums(domino_train_ctx* c, const SumArgs& p, cudaStream_t st) 
     dim3 block;
     int col_blocks;
     row_block(cols, kSumThreads, &block, &col_blocks);
+    if (block.y > 64) block.y = 64;  // their entries: 32 KB
     const dim3 grid((units + block.y - 1) / block.y, col_blocks);
-    cudaError_t e = launch_pdl(k_sum_runs<T, G, VEC>, grid, block, 0, st, p);
-    if (e == cudaSuccess) e = launch_pdl(k_join_runs<G, VEC>, grid, block, 0, st, p, units);
-    c->last_launches += 2;
-    return e;
+    cudaError_t e = launch_pdl(k_sum_runs<T, G, VEC>, grid, block, (size_t)block.y * 2 * p.unit * 4, st, p);
+    c->last_launches += 1;
+    if (e != cudaSuccess || units < 2) return e;
+    row_block(cols, 128, &block, &col_blocks);
+    block.y = kJoinThreads / block.x;
+    c->last_launches += 1;
+    return launch_pdl(k_join_runs<G, VEC>, dim3(units - 1, col_blocks), block, 0, st, p, units);
 }
 
 template <typename T, typename G>
 cudaError_t launch_grad(domino_train_ctx* c, SumArgs p, const int32_t* tokens, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
-    if (p.n > 0) e = launch_sort(c, tokens, p.n, st);
-    if (e == cudaSuccess && !p.accumulate) e = launch_fill(c, tokens, p.n, p.n > 0, static_cast<G*>(p.dtable), st);
+    if (!p.accumulate) e = launch_fill(c, tokens, p.n, static_cast<G*>(p.dtable), st);
+    if (e == cudaSuccess && p.n > 0) e = launch_sort(c, tokens, p.n, !p.accumulate, st);
     if (e != cudaSuccess || p.n == 0) return e;
     const bool four = by_vec(p.dout, p.ld, p.E, sizeof(T), 4) && by_vec(p.dtable, p.E, p.E, sizeof(G), 4);
     return four ? launch_sums<T, G, 4>(c, p, st) : launch_sums<T, G, 1>(c, p, st);

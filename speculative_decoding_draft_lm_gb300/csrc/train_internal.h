@@ -15,6 +15,8 @@ struct domino_train_ctx {
     uint32_t* keys[2];    // [max_tokens] tokens between the passes of the sort
     int32_t* pos[2];      // [max_tokens] their positions
     unsigned* hist;       // [tiles][kSortMaxBins] digit counts of the sort's tiles (more tokens than a cluster sorts)
+    unsigned* named;      // [ceil(V/32)] a bit per row of the table that a token of the call names
+    unsigned* claim;      // rows of zeros claimed so far
     float* part;          // [units][2][E] partial sums of the runs that cross a unit's edge
     void* ws_base;
 };
