@@ -128,7 +128,9 @@ DOMINO_API int domino_train_embed_grad(domino_train_ctx* ctx, const void* dout, 
                                        void* cuda_stream);
 
 /* Synchronise `cuda_stream`, then return and clear the device error word
- * (DOMINO_OK or DOMINO_ERR_BAD_TOKEN), or DOMINO_ERR_CUDA. */
+ * (DOMINO_OK, DOMINO_ERR_BAD_TOKEN, or DOMINO_ERR_TIMEOUT after a device-side
+ * wait ran out of time and left its row's results meaningless), or
+ * DOMINO_ERR_CUDA. */
 DOMINO_API int domino_train_status(domino_train_ctx* ctx, void* cuda_stream);
 
 /* Kernel launches the last successful operator call enqueued. */

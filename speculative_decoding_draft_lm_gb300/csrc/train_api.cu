@@ -104,6 +104,7 @@ int domino_train_init(domino_train_ctx** out, const domino_train_config* cfg, in
     c->named = (unsigned*)(base + o_named);
     c->claim = (unsigned*)(base + o_claim);
     if (cudaMemset(c->err, 0, sizeof(int)) != cudaSuccess || train::prepare_embed_kernels() != cudaSuccess ||
+        train::prepare_distill_kernels() != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
         cudaFree(c->ws_base);
         free(c);
@@ -223,6 +224,7 @@ int domino_train_status(domino_train_ctx* c, void* stream) {
     int word = 0;
     if (cudaMemcpy(&word, c->err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return DOMINO_ERR_CUDA;
     if (word && cudaMemset(c->err, 0, sizeof(int)) != cudaSuccess) return DOMINO_ERR_CUDA;
+    if (word & kErrTimeout) return DOMINO_ERR_TIMEOUT;
     return word & kErrBadToken ? DOMINO_ERR_BAD_TOKEN : DOMINO_OK;
 }
 

@@ -47,6 +47,7 @@ struct DistillArgs {
 
 cudaError_t launch_top(domino_train_ctx* c, const void* x, int dtype, long long ld, int n, int K, float temperature,
                        int32_t* ids, float* top, float* rest, cudaStream_t st);
+cudaError_t prepare_distill_kernels();
 cudaError_t launch_distill_forward(domino_train_ctx* c, const DistillArgs& a, cudaStream_t st);
 cudaError_t launch_distill_backward(domino_train_ctx* c, const DistillArgs& a, cudaStream_t st);
 cudaError_t launch_distill_step(domino_train_ctx* c, const DistillArgs& a, cudaStream_t st);

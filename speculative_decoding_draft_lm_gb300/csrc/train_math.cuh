@@ -42,6 +42,85 @@ __device__ __forceinline__ MaxSum join(const MaxSum& a, const MaxSum& b, float c
     return r;
 }
 
+// ---- two fp32 values in one 64-bit register, one instruction for both -----------
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 halves(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 ex2x2(F2 a) {
+    const float2 h = halves(a);
+    return f2(ex2(h.x), ex2(h.y));
+}
+
+// ---- sixteen bytes of a row --------------------------------------------------------
+template <typename T>
+struct Vec16;
+template <>
+struct Vec16<float> {
+    static constexpr int kElems = 4;
+    uint4 q;
+    __device__ __forceinline__ F2 pair(int i) const {
+        return i == 0 ? f2(__uint_as_float(q.x), __uint_as_float(q.y)) : f2(__uint_as_float(q.z), __uint_as_float(q.w));
+    }
+    // the largest value; NaN only if all are
+    __device__ __forceinline__ float top() const {
+        return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)), fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
+    }
+    __device__ __forceinline__ void set(int i, F2 v) {
+        const float2 h = halves(v);
+        if (i == 0) {
+            q.x = __float_as_uint(h.x);
+            q.y = __float_as_uint(h.y);
+        } else {
+            q.z = __float_as_uint(h.x);
+            q.w = __float_as_uint(h.y);
+        }
+    }
+};
+template <>
+struct Vec16<__nv_bfloat16> {
+    static constexpr int kElems = 8;
+    uint4 q;
+    __device__ __forceinline__ unsigned word(int i) const { return i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w; }
+    __device__ __forceinline__ F2 pair(int i) const {
+        const unsigned w = word(i);
+        return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    }
+    __device__ __forceinline__ float top() const {
+        auto h = [](unsigned w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+        const __nv_bfloat162 m = __hmax2(__hmax2(h(q.x), h(q.y)), __hmax2(h(q.z), h(q.w)));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    __device__ __forceinline__ void set(int i, F2 v) {
+        const float2 f = halves(v);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+        const unsigned w = *reinterpret_cast<const unsigned*>(&b);
+        if (i == 0) q.x = w;
+        else if (i == 1) q.y = w;
+        else if (i == 2) q.z = w;
+        else q.w = w;
+    }
+};
+
 template <typename T>
 __device__ __forceinline__ T from_f32(float x);
 template <>
