@@ -68,6 +68,29 @@ __device__ __forceinline__ Sums shuffled(const Sums& x, int mask) {
     return r;
 }
 
+// The warp's join of its lanes' sums: the maxima first, then one rescaling and
+// plain sums (a third of the exponentials and half of the latency of five
+// pairwise joins).  Every lane gets it.
+__device__ __forceinline__ float warp_max(float x) {
+    return unord_f32(__reduce_max_sync(0xffffffffu, ord_f32(x)));
+}
+__device__ __forceinline__ Sums warp_join(Sums u, float c) {
+    const float mt = warp_max(u.t.m), ms = warp_max(u.s.m), mo = warp_max(u.o.m);
+    const float ft = ex2((u.t.m - mt) * c);
+    u.t = {mt, u.t.s * ft};
+    u.a = rescaled(u.a, ft);
+    u.s = {ms, u.s.s * ex2((u.s.m - ms) * c)};
+    u.o = {mo, u.o.s * ex2((u.o.m - mo) * c)};
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        u.t.s += __shfl_xor_sync(0xffffffffu, u.t.s, o);
+        u.a += __shfl_xor_sync(0xffffffffu, u.a, o);
+        u.s.s += __shfl_xor_sync(0xffffffffu, u.s.s, o);
+        u.o.s += __shfl_xor_sync(0xffffffffu, u.o.s, o);
+    }
+    return u;
+}
+
 // The row's statistics and loss from its sums; rest = -inf where there is none.
 __device__ Stats finish(const Sums& u, float rest, float inv_t, float c, float* loss) {
     Stats st = {};
@@ -79,25 +102,25 @@ __device__ Stats finish(const Sums& u, float rest, float inv_t, float c, float* 
     if (rest != -INFINITY) {
         const float d = u.t.s == 0.f ? -INFINITY : fmaf(u.t.m, inv_t, -rest);
         if (d >= 0.f) {
-            part_r = expf(-d);
+            part_r = ex2(-d * kLog2e);
         } else {
-            part = expf(d);  // NaN stays NaN
+            part = ex2(d * kLog2e);  // NaN stays NaN
             part_r = 1.f;
             top = rest;
             top_is_t = false;
         }
     }
-    const float w = u.t.s * part + part_r;
-    const float pr = part_r / w;
+    const float w = u.t.s * part + part_r, inv_w = 1.f / w;
+    const float pr = part_r * inv_w;
     const MaxSum x = join(u.s, u.o, c);
     st.has = 1.f;
     st.mt = u.t.m;
-    st.pt = part / w;
+    st.pt = part * inv_w;
     st.mx = x.m;
     st.qx = 1.f / x.s;
     st.mo = u.o.m;
-    float l = rescaled(u.a, st.pt) + (top_is_t ? (x.m - u.t.m) * inv_t : fmaf(x.m, inv_t, -top)) + logf(x.s / w);
-    st.co = ex2((u.o.m - x.m) * c) / x.s;
+    float l = rescaled(u.a, st.pt) + (top_is_t ? (x.m - u.t.m) * inv_t : fmaf(x.m, inv_t, -top)) + logf(x.s * inv_w);
+    st.co = ex2((u.o.m - x.m) * c) * st.qx;
     if (pr != 0.f) {
         l -= pr * (fmaf(u.o.m, inv_t, -rest) + logf(u.o.s));
         st.co = u.o.s == 0.f ? 0.f : st.co - pr / u.o.s;
@@ -107,7 +130,7 @@ __device__ Stats finish(const Sums& u, float rest, float inv_t, float c, float* 
 }
 
 // Whether entry k of the record takes part: a valid id, and its first place.
-__device__ __forceinline__ bool takes_part(const int32_t* ids, int k, int id, int V, bool twice) {
+__device__ __noinline__ bool takes_part(const int32_t* ids, int k, int id, int V, bool twice) {
     if ((unsigned)id >= (unsigned)V) return false;
     if (twice)
         for (int j = 0; j < k; ++j)
@@ -128,15 +151,18 @@ __device__ __forceinline__ bool takes_part(const int32_t* ids, int k, int id, in
 // Entries of the record are taken out of the slice (set to -inf) once their
 // logits are read, so that the first pass is a plain sum over the outside.
 
-constexpr int kStepThreads = 256;
-constexpr int kStepWarps = kStepThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr int kSliceBytes = 40 * 1024;
-constexpr int kHeld = 4;  // record entries whose logits a thread keeps; later ones are read again
-
+#ifndef SLICE_KB
+#define SLICE_KB 40
+#define STEP_THREADS 256
+#define MINB 4
+#define UNR 4
+#endif
+constexpr int kSliceBytes = SLICE_KB * 1024;
+constexpr int kStepThreads = STEP_THREADS;
+constexpr int kStepWarps = kStepThreads / 32;
 struct StepShared {
-    Sums warp[kStepWarps];
-    Sums cta[kMaxCluster];
+    Sums part[2][kMaxCluster * kStepWarps];  // every warp of the row, by the row's parity
     Stats row;
     unsigned long long bar;
     int twice, abort;
@@ -165,7 +191,7 @@ struct Slice {
     }
     // fills what the copies leave of the first and last vectors: the row's own
     // elements, and -inf where there are none
-    __device__ void load_edges() {
+    __device__ void load_edges() const {
         const int first = (int)(data - reinterpret_cast<T*>(vec)), per = 16 / (int)sizeof(T);
         const int t = threadIdx.x;
         if (t < first) reinterpret_cast<T*>(vec)[t] = from_f32<T>(-INFINITY);
@@ -185,11 +211,18 @@ __device__ __forceinline__ void bulk_store_wait_read() {
     asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
+// Whole warps arrive and wait together: the per-thread forms let a warp that
+// branched just before meet the barrier in pieces, which cost 5000 cycles a row.
+__device__ __forceinline__ void cluster_barrier() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Adds the values of shared vectors to a set, four vectors of a thread at once:
 // one look at their maximum, then the exponentials.
 template <typename T>
 __device__ __forceinline__ MaxSum sum_vectors(const uint4* vec, int nvec, float c) {
-    constexpr int U = 4, P = Vec16<T>::kElems / 2;
+    constexpr int U = UNR, P = Vec16<T>::kElems / 2;
     const F2 cc = f2(c, c);
     MaxSum r = empty_set();
     F2 s = f2(0.f, 0.f);
@@ -222,144 +255,149 @@ __device__ __forceinline__ MaxSum sum_vectors(const uint4* vec, int nvec, float 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kStepThreads) k_step(DistillArgs p, int chunk) {
+__global__ void __launch_bounds__(kStepThreads, MINB) k_step(DistillArgs p, int chunk) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ StepShared S;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
-    const int n = blockIdx.x / size, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const float inv_t = 1.f / p.temperature, c = kLog2e / p.temperature;
-    const float weight = p.weight[n];
-    Slice<T> x(static_cast<const T*>(p.x) + (size_t)n * p.ld, p.V, chunk, rank, smem);
-    T* dx = static_cast<T*>(p.dx) + (size_t)n * p.ld_d + x.v0;
     unsigned* bits = reinterpret_cast<unsigned*>(smem + (size_t)chunk * sizeof(T) + 32);
-    const int32_t* ids = p.ids + (size_t)n * p.K;
-    const float* top = p.top + (size_t)n * p.K;
-    float w = 0.f;
-
-    if (weight != 0.f) {
-        const uint32_t bar = tc::smem_u32(&S.bar);
-        if (t == 0) {
-            tc::mbar_init(bar, 1);
-            S.twice = S.abort = 0;
-            tc::fence_barrier_init();
-            const uint32_t bytes = (uint32_t)x.body * sizeof(T);
-            tc::mbar_arrive_expect_tx(bar, bytes);
-            if (bytes) tc::bulk_load(tc::smem_u32(x.data + x.head), x.src + x.head, bytes, bar, tc::policy_evict_first());
-        }
-        cluster.sync();  // the barrier is up here, and every CTA of the row is running
-        for (int i = t; i < (x.n + 31) / 32; i += kStepThreads) bits[i] = 0;
-        x.load_edges();
-        __syncthreads();
-        for (int k = t; k < p.K; k += kStepThreads) {
-            const int id = ids[k];
-            const unsigned at = (unsigned)id - (unsigned)x.v0;
-            if (id >= 0 && at < (unsigned)x.n) {
-                const unsigned bit = 1u << (at & 31);
-                if (atomicOr(&bits[at >> 5], bit) & bit) S.twice = 1;
-            } else if (rank == 0 && id != -1 && (unsigned)id >= (unsigned)p.V) {
-                atomicOr(p.err, kErrBadToken);
+    const uint32_t bar = tc::smem_u32(&S.bar);
+    if (t == 0) {
+        tc::mbar_init(bar, 1);
+        S.twice = S.abort = 0;
+        tc::fence_barrier_init();
+    }
+    for (int i = t; i < chunk / 32; i += kStepThreads) bits[i] = 0;
+    cluster_barrier();  // every CTA of the cluster is running
+    uint32_t loaded = 0;  // parity of the next bulk load, and of the cluster's next exchange
+    for (int n = blockIdx.x / size; n < p.n; n += gridDim.x / size) {
+        const float weight = p.weight[n], rest = p.rest ? p.rest[n] : -INFINITY;
+        const Slice<T> x(static_cast<const T*>(p.x) + (size_t)n * p.ld, p.V, chunk, rank, smem);
+        T* dx = static_cast<T*>(p.dx) + (size_t)n * p.ld_d + x.v0;
+        float w = 0.f;
+        if (weight != 0.f) {
+            if (t == 0 && !S.abort) {
+                const uint32_t bytes = (uint32_t)x.body * sizeof(T);
+                tc::mbar_arrive_expect_tx(bar, bytes);
+                if (bytes)
+                    tc::bulk_load(tc::smem_u32(x.data + x.head), x.src + x.head, bytes, bar, tc::policy_evict_first());
             }
-        }
-        __syncthreads();
-        const bool twice = S.twice != 0;
-        tc::mbar_wait(bar, 0, &S.abort, p.err);
-
-        Sums u = {empty_set(), empty_set(), empty_set(), 0.f};
-        float held[kHeld];
-        int j = 0;
-        for (int k = t; k < p.K; k += kStepThreads, ++j) {
-            const int id = ids[k];
-            if ((unsigned)id - (unsigned)x.v0 >= (unsigned)x.n || !takes_part(ids, k, id, p.V, twice)) continue;
-            const float tk = top[k], v = to_f32(x.data[id - x.v0]);
-            x.data[id - x.v0] = from_f32<T>(-INFINITY);
-#pragma unroll
-            for (int h = 0; h < kHeld; ++h)
-                if (h == j) held[h] = v;
-            if (tk > u.t.m) {
-                const float m = clamp_max(u.t.m, tk), f = ex2((u.t.m - m) * c);
-                u.t.s *= f;
-                u.a = rescaled(u.a, f);
-                u.t.m = m;
+            const int32_t* ids = p.ids + (size_t)n * p.K;
+            const float* top = p.top + (size_t)n * p.K;
+            x.load_edges();
+#pragma unroll 1
+            for (int k = t; k < p.K; k += kStepThreads) {
+                const int id = ids[k];
+                const unsigned a = (unsigned)id - (unsigned)x.v0;
+                if (a < (unsigned)x.n) {
+                    const unsigned bit = 1u << (a & 31);
+                    if (atomicOr(&bits[a >> 5], bit) & bit) S.twice = 1;
+                } else if (rank == 0 && id != -1 && (unsigned)id >= (unsigned)p.V) {
+                    atomicOr(p.err, kErrBadToken);
+                }
             }
-            const float e = ex2((tk - u.t.m) * c);
-            u.t.s += e;
-            if (e != 0.f) u.a += e * (tk - v) * inv_t;
-            add(u.s, v, c);
-        }
-        __syncthreads();
-        u.o = sum_vectors<T>(x.vec, x.nvec, c);
-        for (int o = 16; o > 0; o >>= 1) u = join(u, shuffled(u, o), c);
-        if (lane == 0) S.warp[warp] = u;
-        __syncthreads();
-        if (t == 0) {
-            for (int i = 1; i < kStepWarps; ++i) u = join(u, S.warp[i], c);
-            for (int i = 0; i < size; ++i) *cluster.map_shared_rank(&S.cta[rank], i) = u;
-        }
-        cluster.sync();
-        if (t == 0) {
-            u = S.cta[0];
-            for (int i = 1; i < size; ++i) u = join(u, S.cta[i], c);
-            float loss;
-            S.row = finish(u, p.rest ? p.rest[n] : -INFINITY, inv_t, c, &loss);
-            if (rank == 0) p.loss[n] = loss;
-        }
-        __syncthreads();
-        const Stats st = S.row;
-        w = st.has == 0.f ? 0.f : weight * inv_t;
-        if (w != 0.f) {
-            constexpr int P = Vec16<T>::kElems / 2;
-            const float wc = w * st.co;
-            const F2 cc = f2(c, c), minus = f2(-st.mo, -st.mo), scale = f2(wc, wc);
-#pragma unroll 2
-            for (int i = t; i < x.nvec; i += kStepThreads) {
-                Vec16<T> v, g;
-                v.q = x.vec[i];
-#pragma unroll
-                for (int k = 0; k < P; ++k) g.set(k, mul2(scale, ex2x2(mul2(add2(v.pair(k), minus), cc))));
-                x.vec[i] = g.q;
+            if (t == 0) tc::mbar_wait(bar, loaded, &S.abort, p.err);
+            __syncthreads();
+            const bool twice = S.twice != 0;
+
+            Sums u = {empty_set(), empty_set(), empty_set(), 0.f};
+            float held = 0.f;  // the logit of this thread's first entry; later entries' are read again
+#pragma unroll 1
+            for (int k = t; k < p.K; k += kStepThreads) {
+                const int id = ids[k];
+                const unsigned a = (unsigned)id - (unsigned)x.v0;
+                if (a >= (unsigned)x.n || (twice && !takes_part(ids, k, id, p.V, true))) continue;
+                const float tv = top[k], v = to_f32(x.data[a]);
+                x.data[a] = from_f32<T>(-INFINITY);  // no part of the outside
+                bits[a >> 5] = 0;
+                if (k == t) held = v;
+                if (tv > u.t.m) {
+                    const float m = clamp_max(u.t.m, tv), f = ex2((u.t.m - m) * c);
+                    u.t.s *= f;
+                    u.a = rescaled(u.a, f);
+                    u.t.m = m;
+                }
+                const float e = ex2((tv - u.t.m) * c);
+                u.t.s += e;
+                if (e != 0.f) u.a += e * (tv - v) * inv_t;
+                add(u.s, v, c);
             }
             __syncthreads();
-            j = 0;
-            for (int k = t; k < p.K; k += kStepThreads, ++j) {
-                const int id = ids[k];
-                if ((unsigned)id - (unsigned)x.v0 >= (unsigned)x.n || !takes_part(ids, k, id, p.V, twice)) continue;
-                float v = 0.f;
-                if (j < kHeld) {
+            if (t == 0) S.twice = 0;
+            u.o = sum_vectors<T>(x.vec, x.nvec, c);
+            u = warp_join(u, c);
+            // every warp's sums to every CTA of the row
+            if (lane < size) *cluster.map_shared_rank(&S.part[loaded][rank * kStepWarps + warp], lane) = u;
+            cluster_barrier();
+            if (warp == 0) {
+                const Sums* part = S.part[loaded];
+                u = part[min(lane, size * kStepWarps - 1)];
+                if (lane >= size * kStepWarps) u = {empty_set(), empty_set(), empty_set(), 0.f};
+                for (int i = lane + 32; i < size * kStepWarps; i += 32) u = join(u, part[i], c);
+                u = warp_join(u, c);
+                float loss;
+                const Stats st = finish(u, rest, inv_t, c, &loss);
+                if (lane == 0) S.row = st;
+                if (rank == 0 && lane == 0) p.loss[n] = loss;
+            }
+            __syncthreads();
+            loaded ^= 1;
+            const Stats st = S.row;
+            w = st.has == 0.f ? 0.f : weight * inv_t;
+            if (w != 0.f) {
+                constexpr int P = Vec16<T>::kElems / 2;
+                const float wc = w * st.co;
+                const F2 cc = f2(c, c), minus = f2(-st.mo, -st.mo), scale = f2(wc, wc);
+#pragma unroll 2
+                for (int i = t; i < x.nvec; i += kStepThreads) {
+                    Vec16<T> v, g;
+                    v.q = x.vec[i];
 #pragma unroll
-                    for (int h = 0; h < kHeld; ++h)
-                        if (h == j) v = held[h];
-                } else {
-                    v = to_f32(x.src[id - x.v0]);
+                    for (int k = 0; k < P; ++k) g.set(k, mul2(scale, ex2x2(mul2(add2(v.pair(k), minus), cc))));
+                    x.vec[i] = g.q;
                 }
-                const float q = st.qx * ex2((v - st.mx) * c), pk = st.pt * ex2((top[k] - st.mt) * c);
-                x.data[id - x.v0] = from_f32<T>(w * (q - pk));
+                __syncthreads();
+#pragma unroll 1
+                for (int k = t; k < p.K; k += kStepThreads) {
+                    const int id = ids[k];
+                    const unsigned a = (unsigned)id - (unsigned)x.v0;
+                    if (a >= (unsigned)x.n || (twice && !takes_part(ids, k, id, p.V, true))) continue;
+                    const float v = k == t ? held : to_f32(x.src[a]);
+                    const float q = st.qx * ex2((v - st.mx) * c), pk = st.pt * ex2((top[k] - st.mt) * c);
+                    x.data[a] = from_f32<T>(w * (q - pk));
+                }
             }
+        } else if (rank == 0 && t == 0) {
+            p.loss[n] = 0.f;
         }
-        if (S.abort && t == 0) {  // the copies' wait ran out: give them a last chance to land before the CTA leaves
-            const unsigned long long t0 = tc::globaltimer();
-            while (!tc::mbar_try_wait(bar, 0) && tc::globaltimer() - t0 < 2000000ull) {
+        if (w == 0.f)
+            for (int i = t; i < x.nvec; i += kStepThreads) x.vec[i] = make_uint4(0, 0, 0, 0);
+        // out: whole vectors by bulk copy where the gradient's row starts at the same place modulo 16 bytes
+        const bool together = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x.src)) & 15) == 0;
+        tc::fence_proxy_async();
+        __syncthreads();
+        if (together) {
+            if (t < x.head) dx[t] = x.data[t];
+            const int tail = x.n - x.head - x.body;
+            if (t < tail) dx[x.head + x.body + t] = x.data[x.head + x.body + t];
+            if (t == 0 && x.body) {
+                bulk_store(dx + x.head, tc::smem_u32(x.data + x.head), (uint32_t)x.body * sizeof(T));
+                bulk_store_wait_read();
             }
+        } else {
+            for (int i = t; i < x.n; i += kStepThreads) dx[i] = x.data[i];
         }
-    } else if (rank == 0 && t == 0) {
-        p.loss[n] = 0.f;
+        __syncthreads();
     }
-    if (w == 0.f)
-        for (int i = t; i < x.nvec; i += kStepThreads) x.vec[i] = make_uint4(0, 0, 0, 0);
-    // out: whole vectors by bulk copy where the gradient's row starts at the same place modulo 16 bytes
-    const bool together = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x.src)) & 15) == 0;
-    tc::fence_proxy_async();
-    __syncthreads();
-    if (together) {
-        if (t < x.head) dx[t] = x.data[t];
-        const int tail = x.n - x.head - x.body;
-        if (t < tail) dx[x.head + x.body + t] = x.data[x.head + x.body + t];
-        if (t == 0 && x.body) {
-            bulk_store(dx + x.head, tc::smem_u32(x.data + x.head), (uint32_t)x.body * sizeof(T));
-            bulk_store_wait_read();
+    // A CTA whose copy never came goes on through its cluster's exchanges, with
+    // meaningless data and without further copies, and gives the lost one a last
+    // chance to land before it leaves.
+    if (S.abort && t == 0) {
+        const unsigned long long t0 = tc::globaltimer();
+        while (!tc::mbar_try_wait(bar, loaded ^ 1) && tc::globaltimer() - t0 < 2000000ull) {
         }
-    } else {
-        for (int i = t; i < x.n; i += kStepThreads) dx[i] = x.data[i];
     }
 }
 
@@ -485,7 +523,6 @@ cudaError_t launch_step(domino_train_ctx* ctx, const DistillArgs& a, cudaStream_
     cudaError_t e = cudaFuncSetAttribute(k_step<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.n * size);
     cfg.blockDim = dim3(kStepThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -495,6 +532,17 @@ cudaError_t launch_step(domino_train_ctx* ctx, const DistillArgs& a, cudaStream_
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    // one wave of clusters, each taking rows in turn; how many the GPU holds at
+    // once depends on how its SMs are grouped, so it is asked (once per context
+    // and cluster size)
+    int& most = ctx->step_clusters[size];
+    if (most == 0) {
+        cfg.gridDim = dim3(size);
+        e = cudaOccupancyMaxActiveClusters(&most, k_step<T>, &cfg);
+        if (e != cudaSuccess) return e;
+        if (most < 1) most = 1;
+    }
+    cfg.gridDim = dim3((unsigned)(a.n < most ? a.n : most) * size);
     ctx->last_launches = 1;
     return cudaLaunchKernelEx(&cfg, k_step<T>, a, chunk);
 }
