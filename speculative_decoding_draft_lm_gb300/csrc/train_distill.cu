@@ -26,8 +26,6 @@ namespace train {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 
 // What a row's loss and gradient go by; row layout of `stats`.
 struct Stats {
@@ -35,7 +33,7 @@ struct Stats {
     float mx, qx;   // record:  q = qx 2^((x - mx) c)
     float mt, pt;   //          p = pt 2^((t - mt) c)
     float has;      // 0: the record holds no mass
-    float pad;
+    float twice;    // an id occurs twice in the record
 };
 static_assert(sizeof(Stats) == DOMINO_TRAIN_STATS * sizeof(float), "stats row");
 
@@ -152,10 +150,17 @@ __device__ __noinline__ bool takes_part(const int32_t* ids, int k, int id, int V
 // logits are read, so that the first pass is a plain sum over the outside.
 
 constexpr int kMaxCluster = 16;
+#ifndef STREAM_KB
+#define STREAM_KB 320
+#define STREAM_THREADS 256
+#define STREAM_AHEAD 4
+#define STREAM_MINB 4
+#define STREAM_WAVES 4
+#endif
 #ifndef SLICE_KB
 #define SLICE_KB 40
-#define STEP_THREADS 256
-#define MINB 4
+#define STEP_THREADS 128
+#define MINB 5
 #define UNR 4
 #endif
 constexpr int kSliceBytes = SLICE_KB * 1024;
@@ -401,105 +406,291 @@ __global__ void __launch_bounds__(kStepThreads, MINB) k_step(DistillArgs p, int 
     }
 }
 
-// Marks the row's record in `bits` (one bit per id) and returns whether an id
-// occurs twice.  All threads.
-__device__ bool mark_record(const int32_t* ids, int K, int V, unsigned* bits, int* flag, int* err) {
-    if (threadIdx.x == 0) *flag = 0;
-    for (int i = threadIdx.x; i < (V + 31) / 32; i += kThreads) bits[i] = 0;
-    __syncthreads();
-    for (int k = threadIdx.x; k < K; k += kThreads) {
-        const int id = ids[k];
-        if ((unsigned)id < (unsigned)V) {
-            const unsigned bit = 1u << (id & 31);
-            if (atomicOr(&bits[id >> 5], bit) & bit) *flag = 1;
-        } else if (id != -1) {
-            atomicOr(err, kErrBadToken);
-        }
+// ---- forward and backward by themselves -------------------------------------------
+//
+// Every thread streams 16-byte vectors of its CTA's slice of the row, kAhead of
+// them in flight.  The forward skips the record's entries by a bit per element,
+// one byte (half a byte) of which covers a vector; the backward writes every
+// element as if it were outside the record and then, after a barrier, the
+// entries again.  A row is one CTA's, or a cluster's where there are few rows.
+
+constexpr int kThreads = STREAM_THREADS;
+constexpr int kWarps = kThreads / 32;
+constexpr int kAhead = STREAM_AHEAD;
+
+struct StreamShared {
+    Sums part[kMaxCluster * kWarps];
+    Stats row;
+    int twice;
+};
+
+// A slice of a row as whole 16-byte vectors [first, last) of memory and the
+// elements beside them; vector i covers the elements 8 i - phase + {0..7} (4 i
+// for fp32).
+template <typename T>
+struct Vectors {
+    static constexpr int kPer = 16 / (int)sizeof(T);
+    const T* src;
+    int n, phase, first, last;
+    __device__ Vectors(const T* src_, int n_) : src(src_), n(n_) {
+        phase = (int)(reinterpret_cast<uintptr_t>(src) & 15) / (int)sizeof(T);
+        first = phase ? 1 : 0;
+        last = (phase + n) / kPer;
+        if (last < first) last = first;
     }
-    __syncthreads();
-    return *flag != 0;
+    __device__ const uint4* vec() const { return reinterpret_cast<const uint4*>(src - phase); }
+    // element j of those before the first vector or behind the last: its place, or n
+    __device__ int beside(int j) const {
+        const int head = min(n, (kPer - phase) % kPer);
+        if (j < head) return j;
+        const int at = max(head, last * kPer - phase) + (j - head);
+        return j - head < kPer && at < n ? at : n;
+    }
+};
+
+__device__ __forceinline__ uint4 load_stream(const uint4* p) {
+    uint4 q;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                 : "l"(p));
+    return q;
+}
+
+// the record's entries among a vector's elements set to -inf
+__device__ __forceinline__ void strike(Vec16<float>& v, unsigned m) {
+    const unsigned inf = 0xFF800000u;
+    if (m & 1u) v.q.x = inf;
+    if (m & 2u) v.q.y = inf;
+    if (m & 4u) v.q.z = inf;
+    if (m & 8u) v.q.w = inf;
+}
+__device__ __forceinline__ void strike(Vec16<__nv_bfloat16>& v, unsigned m) {
+    auto word = [](unsigned w, unsigned two) {
+        if (two & 1u) w = (w & 0xFFFF0000u) | 0xFF80u;
+        if (two & 2u) w = (w & 0xFFFFu) | 0xFF800000u;
+        return w;
+    };
+    v.q.x = word(v.q.x, m);
+    v.q.y = word(v.q.y, m >> 2);
+    v.q.z = word(v.q.z, m >> 4);
+    v.q.w = word(v.q.w, m >> 6);
 }
 
 template <typename T, bool kForward, bool kBackward>
-__global__ void __launch_bounds__(kThreads) k_distill(DistillArgs p) {
+__global__ void __launch_bounds__(kThreads, STREAM_MINB) k_stream(DistillArgs p, int chunk) {
     extern __shared__ unsigned bits[];
-    __shared__ Sums part[kWarps];
-    __shared__ Stats row;
-    __shared__ int flag;
-    const int n = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ StreamShared S;
+    constexpr int P = Vec16<T>::kElems / 2, kPer = Vec16<T>::kElems;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
+    const int n = blockIdx.x / size, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const float inv_t = 1.f / p.temperature, c = kLog2e / p.temperature;
-    const T* x = static_cast<const T*>(p.x) + (size_t)n * p.ld;
-    T* dx = static_cast<T*>(p.dx) + (size_t)n * p.ld_d;
+    const float weight = kBackward ? p.weight[n] : 1.f, rest = kForward && p.rest ? p.rest[n] : -INFINITY;
+    const int v0 = min(p.V, rank * chunk);
+    const Vectors<T> x(static_cast<const T*>(p.x) + (size_t)n * p.ld + v0, min(p.V, v0 + chunk) - v0);
+    T* dx = static_cast<T*>(p.dx) + (size_t)n * p.ld_d + v0;
+    const bool together = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x.src)) & 15) == 0;
     const int32_t* ids = p.ids + (size_t)n * p.K;
     const float* top = p.top + (size_t)n * p.K;
     Stats st = {};
     if (!kForward) st = reinterpret_cast<const Stats*>(p.stats)[n];
-    if (kBackward) {
-        if (p.weight[n] == 0.f || (!kForward && st.has == 0.f)) {
-            for (int v = threadIdx.x; v < p.V; v += kThreads) dx[v] = from_f32<T>(0.f);
-            if (kForward && threadIdx.x == 0) p.loss[n] = 0.f;
-            return;
-        }
-    }
-    const bool twice = mark_record(ids, p.K, p.V, bits, &flag, p.err);
-    if (kForward) {
-        Sums u = {empty_set(), empty_set(), empty_set(), 0.f};
-        for (int k = threadIdx.x; k < p.K; k += kThreads) {
+    bool twice = st.twice != 0.f;
+    float w = !kForward && st.has == 0.f ? 0.f : weight * inv_t;
+
+    if (kForward && weight != 0.f) {
+        for (int i = t; i <= (x.phase + x.n) / 32; i += kThreads) bits[i] = 0;
+        if (t == 0) S.twice = 0;
+        if (size > 1) cluster_barrier();  // every CTA of the row is running
+        else __syncthreads();
+#pragma unroll 1
+        for (int k = t; k < p.K; k += kThreads) {
             const int id = ids[k];
-            if (!takes_part(ids, k, id, p.V, twice)) continue;
-            const float t = top[k], v = to_f32(x[id]);
-            if (t > u.t.m) {
-                const float m = clamp_max(u.t.m, t), f = ex2((u.t.m - m) * c);
+            const unsigned a = (unsigned)id - (unsigned)v0;
+            if (a < (unsigned)x.n) {
+                const unsigned b = a + x.phase, bit = 1u << (b & 31);
+                if (atomicOr(&bits[b >> 5], bit) & bit) S.twice = 1;
+            } else if (rank == 0 && id != -1 && (unsigned)id >= (unsigned)p.V) {
+                atomicOr(p.err, kErrBadToken);
+            }
+        }
+        __syncthreads();
+        twice = S.twice != 0;
+        Sums u = {empty_set(), empty_set(), empty_set(), 0.f};
+#pragma unroll 1
+        for (int k = t; k < p.K; k += kThreads) {
+            const int id = ids[k];
+            const unsigned a = (unsigned)id - (unsigned)v0;
+            if (a >= (unsigned)x.n || (twice && !takes_part(ids, k, id, p.V, true))) continue;
+            const float tv = top[k], v = to_f32(x.src[a]);
+            if (tv > u.t.m) {
+                const float m = clamp_max(u.t.m, tv), f = ex2((u.t.m - m) * c);
                 u.t.s *= f;
                 u.a = rescaled(u.a, f);
                 u.t.m = m;
             }
-            const float e = ex2((t - u.t.m) * c);
+            const float e = ex2((tv - u.t.m) * c);
             u.t.s += e;
-            if (e != 0.f) u.a += e * (t - v) * inv_t;
+            if (e != 0.f) u.a += e * (tv - v) * inv_t;
             add(u.s, v, c);
         }
-        for (int v = threadIdx.x; v < p.V; v += kThreads)
-            if (!(bits[v >> 5] >> (v & 31) & 1u)) add(u.o, to_f32(x[v]), c);
-        for (int o = 16; o > 0; o >>= 1) u = join(u, shuffled(u, o), c);
-        if (lane == 0) part[warp] = u;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int w = 1; w < kWarps; ++w) u = join(u, part[w], c);
-            float loss;
-            row = finish(u, p.rest ? p.rest[n] : -INFINITY, inv_t, c, &loss);
-            p.loss[n] = loss;
-            if (p.stats) reinterpret_cast<Stats*>(p.stats)[n] = row;
+        // the outside
+        const unsigned char* masks = reinterpret_cast<const unsigned char*>(bits);
+        const F2 cc = f2(c, c);
+        F2 s = f2(0.f, 0.f);
+        for (int i0 = x.first + t; i0 < x.last; i0 += kAhead * kThreads) {
+            Vec16<T> v[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (i0 + j * kThreads < x.last) v[j].q = load_stream(x.vec() + i0 + j * kThreads);
+            float most = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int i = i0 + j * kThreads;
+                if (i < x.last) {
+                    const unsigned m = kPer == 8 ? masks[i] : masks[i >> 1] >> (i & 1) * 4 & 15u;
+                    if (m) strike(v[j], m);
+                    most = fmaxf(most, v[j].top());
+                }
+            }
+            if (most > u.o.m) {
+                const float m = clamp_max(u.o.m, most), f = ex2((u.o.m - m) * c);
+                s = mul2(s, f2(f, f));
+                u.o.m = m;
+            }
+            const F2 minus = f2(-u.o.m, -u.o.m);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (i0 + j * kThreads < x.last)
+#pragma unroll
+                    for (int k = 0; k < P; ++k) s = add2(s, ex2x2(mul2(add2(v[j].pair(k), minus), cc)));
         }
-        __syncthreads();
-        st = row;
+        const float2 h = halves(s);
+        u.o.s = h.x + h.y;
+        const int side = t < 2 * kPer ? x.beside(t) : x.n;
+        if (side < x.n && !(bits[(side + x.phase) >> 5] >> ((side + x.phase) & 31) & 1u)) add(u.o, to_f32(x.src[side]), c);
+        u = warp_join(u, c);
+        // every warp's sums to every CTA of the row
+        if (size > 1) {
+            if (lane < size) *cluster.map_shared_rank(&S.part[rank * kWarps + warp], lane) = u;
+            cluster_barrier();
+        } else {
+            if (lane == 0) S.part[warp] = u;
+            __syncthreads();
+        }
+        if (warp == 0) {
+            const int parts = size * kWarps;
+            u = S.part[min(lane, parts - 1)];
+            if (lane >= parts) u = {empty_set(), empty_set(), empty_set(), 0.f};
+            for (int i = lane + 32; i < parts; i += 32) u = join(u, S.part[i], c);
+            u = warp_join(u, c);
+            float loss;
+            st = finish(u, rest, inv_t, c, &loss);
+            if (lane == 0) S.row = st;
+            if (rank == 0 && lane == 0) p.loss[n] = loss;
+        }
+        if (kBackward) {
+            __syncthreads();
+            st = S.row;
+            if (st.has == 0.f) w = 0.f;
+        } else {
+            // whether any CTA of the row saw an id twice
+            if (size > 1) {
+                if (t == 0 && twice) *cluster.map_shared_rank(&S.twice, 0) = 1;
+                cluster_barrier();
+            }
+            if (rank == 0 && t == 0) {
+                st.twice = S.twice ? 1.f : 0.f;
+                reinterpret_cast<Stats*>(p.stats)[n] = st;
+            }
+        }
+    } else if (kForward && rank == 0 && t == 0) {
+        p.loss[n] = 0.f;
     }
     if (kBackward) {
-        // a row without mass takes this path too: its factors are 0, but its
-        // logits may be infinite
-        const float w = st.has == 0.f ? 0.f : p.weight[n] * inv_t;
-        for (int v = threadIdx.x; v < p.V; v += kThreads)
-            if (!(bits[v >> 5] >> (v & 31) & 1u))
-                dx[v] = from_f32<T>(w == 0.f ? 0.f : w * st.co * ex2((to_f32(x[v]) - st.mo) * c));
-        for (int k = threadIdx.x; k < p.K; k += kThreads) {
+        const float wc = w * st.co;
+        const F2 cc = f2(c, c), minus = f2(-st.mo, -st.mo), scale = f2(wc, wc);
+        if (w == 0.f) {
+            if (together) {
+                uint4* out = reinterpret_cast<uint4*>(dx - x.phase);
+                for (int i = x.first + t; i < x.last; i += kThreads) out[i] = make_uint4(0, 0, 0, 0);
+                const int side = t < 2 * kPer ? x.beside(t) : x.n;
+                if (side < x.n) dx[side] = from_f32<T>(0.f);
+            } else {
+                for (int i = t; i < x.n; i += kThreads) dx[i] = from_f32<T>(0.f);
+            }
+            return;
+        }
+        if (together) {
+            uint4* out = reinterpret_cast<uint4*>(dx - x.phase);
+            for (int i0 = x.first + t; i0 < x.last; i0 += kAhead * kThreads) {
+                Vec16<T> v[kAhead];
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j)
+                    if (i0 + j * kThreads < x.last) v[j].q = load_stream(x.vec() + i0 + j * kThreads);
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j)
+                    if (i0 + j * kThreads < x.last) {
+                        Vec16<T> g;
+#pragma unroll
+                        for (int k = 0; k < P; ++k) g.set(k, mul2(scale, ex2x2(mul2(add2(v[j].pair(k), minus), cc))));
+                        out[i0 + j * kThreads] = g.q;
+                    }
+            }
+            const int side = t < 2 * kPer ? x.beside(t) : x.n;
+            if (side < x.n) dx[side] = from_f32<T>(wc * ex2((to_f32(x.src[side]) - st.mo) * c));
+        } else {
+            for (int i = t; i < x.n; i += kThreads) dx[i] = from_f32<T>(wc * ex2((to_f32(x.src[i]) - st.mo) * c));
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int k = t; k < p.K; k += kThreads) {
             const int id = ids[k];
-            if (!takes_part(ids, k, id, p.V, twice)) continue;
-            const float q = st.qx * ex2((to_f32(x[id]) - st.mx) * c), pk = st.pt * ex2((top[k] - st.mt) * c);
-            dx[id] = from_f32<T>(w == 0.f ? 0.f : w * (q - pk));
+            const unsigned a = (unsigned)id - (unsigned)v0;
+            if (a >= (unsigned)x.n || (twice && !takes_part(ids, k, id, p.V, true))) continue;
+            const float q = st.qx * ex2((to_f32(x.src[a]) - st.mx) * c), pk = st.pt * ex2((top[k] - st.mt) * c);
+            dx[a] = from_f32<T>(w * (q - pk));
         }
     }
 }
 
+// A launch in clusters of `size` CTAs.
+inline cudaLaunchConfig_t cluster_config(unsigned blocks, int threads, int size, size_t smem, cudaStream_t st,
+                                         cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = size;
+    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+template <typename T, bool kForward, bool kBackward>
+cudaError_t launch_stream(domino_train_ctx* ctx, const DistillArgs& a, cudaStream_t st) {
+    int size = 1;
+    auto slice = [&](int parts) { return ((a.V + parts - 1) / parts + 63) / 64 * 64; };
+    while (size < kMaxCluster && (long long)a.n * size < STREAM_WAVES * ctx->num_sms && slice(2 * size) >= 2048) size *= 2;
+    while (size < kMaxCluster && slice(size) * (int)sizeof(T) > STREAM_KB * 1024) size *= 2;
+    const int chunk = slice(size);
+    const size_t smem = kForward ? (size_t)chunk / 8 + 8 : 0;
+    auto kern = k_stream<T, kForward, kBackward>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = cluster_config((unsigned)a.n * size, kThreads, size, smem, st, &attr);
+    ctx->last_launches = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, chunk);
+}
+
 template <bool kForward, bool kBackward>
 cudaError_t launch(domino_train_ctx* ctx, const DistillArgs& a, cudaStream_t st) {
-    const size_t smem = (size_t)(a.V + 31) / 32 * 4;
-    auto kern = ctx->cfg.dtype == DOMINO_DTYPE_BF16 ? k_distill<__nv_bfloat16, kForward, kBackward>
-                                                    : k_distill<float, kForward, kBackward>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    kern<<<a.n, kThreads, smem, st>>>(a);
-    ctx->last_launches = 1;
-    return cudaGetLastError();
+    return ctx->cfg.dtype == DOMINO_DTYPE_BF16 ? launch_stream<__nv_bfloat16, kForward, kBackward>(ctx, a, st)
+                                               : launch_stream<float, kForward, kBackward>(ctx, a, st);
 }
 
 }  // namespace
@@ -556,6 +747,9 @@ cudaError_t prepare_distill_kernels() {
 }
 
 cudaError_t launch_distill_step(domino_train_ctx* c, const DistillArgs& a, cudaStream_t st) {
+#ifdef STEP_STREAM
+    return launch<true, true>(c, a, st);
+#endif
     return c->cfg.dtype == DOMINO_DTYPE_BF16 ? launch_step<__nv_bfloat16>(c, a, st) : launch_step<float>(c, a, st);
 }
 
