@@ -151,10 +151,11 @@ __device__ __noinline__ bool takes_part(const int32_t* ids, int k, int id, int V
 
 constexpr int kMaxCluster = 16;
 #ifndef STREAM_KB
-#define STREAM_KB 320
+#define STREAM_KB 160
 #define STREAM_THREADS 256
-#define STREAM_AHEAD 4
-#define STREAM_MINB 4
+#define STREAM_AHEAD 2
+#define STREAM_STAGES 3
+#define STREAM_MINB 5
 #define STREAM_WAVES 4
 #endif
 #ifndef SLICE_KB
@@ -417,6 +418,8 @@ __global__ void __launch_bounds__(kStepThreads, MINB) k_step(DistillArgs p, int 
 constexpr int kThreads = STREAM_THREADS;
 constexpr int kWarps = kThreads / 32;
 constexpr int kAhead = STREAM_AHEAD;
+constexpr int kStages = STREAM_STAGES;
+constexpr size_t kRingBytes = (size_t)kThreads * kAhead * kStages * 16;
 
 struct StreamShared {
     Sums part[kMaxCluster * kWarps];
@@ -448,12 +451,43 @@ struct Vectors {
     }
 };
 
-__device__ __forceinline__ uint4 load_stream(const uint4* p) {
-    uint4 q;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-                 : "l"(p));
-    return q;
+// Calls f(i, v) on the vectors [x.first, x.last) of this thread, kAhead
+// adjacent places of the thread at once (v.q is -inf in every element where i
+// is past the end).  The vectors pass through a ring in shared memory that no
+// other thread touches, filled by asynchronous copies kStages calls ahead: the
+// bytes in flight cost no registers, and nothing waits on a barrier.
+template <typename T, typename F>
+__device__ __forceinline__ void stream(const Vectors<T>& x, uint4* ring, F&& f) {
+    const int t = threadIdx.x, calls = (x.last - x.first + kAhead * kThreads - 1) / (kAhead * kThreads);
+    const unsigned inf = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
+    const uint4* src = x.vec();
+    auto fill = [&](int call) {
+        uint4* slot = ring + (call % kStages) * (kAhead * kThreads) + t;
+        int i = x.first + call * (kAhead * kThreads) + t;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j, i += kThreads, slot += kThreads) {
+            if (i < x.last)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(slot)), "l"(src + i) : "memory");
+            else
+                *slot = make_uint4(inf, inf, inf, inf);
+        }
+    };
+#pragma unroll
+    for (int g = 0; g < kStages; ++g) {
+        if (g < calls) fill(g);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+#pragma unroll 1
+    for (int g = 0; g < calls; ++g) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        const uint4* slot = ring + (g % kStages) * (kAhead * kThreads) + t;
+        Vec16<T> v[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) v[j].q = slot[j * kThreads];
+        f(x.first + g * (kAhead * kThreads) + t, v);
+        if (g + kStages < calls) fill(g + kStages);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
 }
 
 // the record's entries among a vector's elements set to -inf
@@ -478,8 +512,10 @@ __device__ __forceinline__ void strike(Vec16<__nv_bfloat16>& v, unsigned m) {
 
 template <typename T, bool kForward, bool kBackward>
 __global__ void __launch_bounds__(kThreads, STREAM_MINB) k_stream(DistillArgs p, int chunk) {
-    extern __shared__ unsigned bits[];
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ StreamShared S;
+    uint4* ring = reinterpret_cast<uint4*>(smem);
+    unsigned* bits = reinterpret_cast<unsigned*>(smem + kRingBytes);
     constexpr int P = Vec16<T>::kElems / 2, kPer = Vec16<T>::kElems;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
@@ -537,21 +573,21 @@ __global__ void __launch_bounds__(kThreads, STREAM_MINB) k_stream(DistillArgs p,
         const unsigned char* masks = reinterpret_cast<const unsigned char*>(bits);
         const F2 cc = f2(c, c);
         F2 s = f2(0.f, 0.f);
-        for (int i0 = x.first + t; i0 < x.last; i0 += kAhead * kThreads) {
-            Vec16<T> v[kAhead];
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-                if (i0 + j * kThreads < x.last) v[j].q = load_stream(x.vec() + i0 + j * kThreads);
-            float most = -INFINITY;
+        stream(x, ring, [&](int i0, Vec16<T>* v) {
+            unsigned m[kAhead], any = 0;
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
                 const int i = i0 + j * kThreads;
-                if (i < x.last) {
-                    const unsigned m = kPer == 8 ? masks[i] : masks[i >> 1] >> (i & 1) * 4 & 15u;
-                    if (m) strike(v[j], m);
-                    most = fmaxf(most, v[j].top());
-                }
+                m[j] = i < x.last ? (kPer == 8 ? masks[i] : masks[i >> 1] >> (i & 1) * 4 & 15u) : 0u;
+                any |= m[j];
             }
+            if (any) {
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) strike(v[j], m[j]);
+            }
+            float most = v[0].top();
+#pragma unroll
+            for (int j = 1; j < kAhead; ++j) most = fmaxf(most, v[j].top());
             if (most > u.o.m) {
                 const float m = clamp_max(u.o.m, most), f = ex2((u.o.m - m) * c);
                 s = mul2(s, f2(f, f));
@@ -560,10 +596,9 @@ __global__ void __launch_bounds__(kThreads, STREAM_MINB) k_stream(DistillArgs p,
             const F2 minus = f2(-u.o.m, -u.o.m);
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
-                if (i0 + j * kThreads < x.last)
 #pragma unroll
-                    for (int k = 0; k < P; ++k) s = add2(s, ex2x2(mul2(add2(v[j].pair(k), minus), cc)));
-        }
+                for (int k = 0; k < P; ++k) s = add2(s, ex2x2(mul2(add2(v[j].pair(k), minus), cc)));
+        });
         const float2 h = halves(s);
         u.o.s = h.x + h.y;
         const int side = t < 2 * kPer ? x.beside(t) : x.n;
@@ -622,20 +657,15 @@ __global__ void __launch_bounds__(kThreads, STREAM_MINB) k_stream(DistillArgs p,
         }
         if (together) {
             uint4* out = reinterpret_cast<uint4*>(dx - x.phase);
-            for (int i0 = x.first + t; i0 < x.last; i0 += kAhead * kThreads) {
-                Vec16<T> v[kAhead];
+            stream(x, ring, [&](int i0, Vec16<T>* v) {
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j)
-                    if (i0 + j * kThreads < x.last) v[j].q = load_stream(x.vec() + i0 + j * kThreads);
+                for (int j = 0; j < kAhead; ++j) {
+                    Vec16<T> g;
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j)
-                    if (i0 + j * kThreads < x.last) {
-                        Vec16<T> g;
-#pragma unroll
-                        for (int k = 0; k < P; ++k) g.set(k, mul2(scale, ex2x2(mul2(add2(v[j].pair(k), minus), cc))));
-                        out[i0 + j * kThreads] = g.q;
-                    }
-            }
+                    for (int k = 0; k < P; ++k) g.set(k, mul2(scale, ex2x2(mul2(add2(v[j].pair(k), minus), cc))));
+                    if (i0 + j * kThreads < x.last) out[i0 + j * kThreads] = g.q;
+                }
+            });
             const int side = t < 2 * kPer ? x.beside(t) : x.n;
             if (side < x.n) dx[side] = from_f32<T>(wc * ex2((to_f32(x.src[side]) - st.mo) * c));
         } else {
@@ -676,7 +706,7 @@ cudaError_t launch_stream(domino_train_ctx* ctx, const DistillArgs& a, cudaStrea
     while (size < kMaxCluster && (long long)a.n * size < STREAM_WAVES * ctx->num_sms && slice(2 * size) >= 2048) size *= 2;
     while (size < kMaxCluster && slice(size) * (int)sizeof(T) > STREAM_KB * 1024) size *= 2;
     const int chunk = slice(size);
-    const size_t smem = kForward ? (size_t)chunk / 8 + 8 : 0;
+    const size_t smem = kRingBytes + (kForward ? (size_t)chunk / 8 + 8 : 0);
     auto kern = k_stream<T, kForward, kBackward>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
