@@ -15,9 +15,8 @@
 // near convergence the record holds almost all of the mass.
 #include <cooperative_groups.h>
 
-#include "tc_common.cuh"
 #include "train_internal.h"
-#include "train_math.cuh"
+#include "train_stream.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -69,9 +68,6 @@ __device__ __forceinline__ Sums shuffled(const Sums& x, int mask) {
 // The warp's join of its lanes' sums: the maxima first, then one rescaling and
 // plain sums (a third of the exponentials and half of the latency of five
 // pairwise joins).  Every lane gets it.
-__device__ __forceinline__ float warp_max(float x) {
-    return unord_f32(__reduce_max_sync(0xffffffffu, ord_f32(x)));
-}
 __device__ __forceinline__ Sums warp_join(Sums u, float c) {
     const float mt = warp_max(u.t.m), ms = warp_max(u.s.m), mo = warp_max(u.o.m);
     const float ft = ex2((u.t.m - mt) * c);
@@ -149,7 +145,6 @@ __device__ __noinline__ bool takes_part(const int32_t* ids, int k, int id, int V
 // Entries of the record are taken out of the slice (set to -inf) once their
 // logits are read, so that the first pass is a plain sum over the outside.
 
-constexpr int kMaxCluster = 16;
 #ifndef STREAM_KB
 #define STREAM_KB 160
 #define STREAM_THREADS 256
@@ -215,13 +210,6 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
 }
 __device__ __forceinline__ void bulk_store_wait_read() {
     asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-
-// Whole warps arrive and wait together: the per-thread forms let a warp that
-// branched just before meet the barrier in pieces, which cost 5000 cycles a row.
-__device__ __forceinline__ void cluster_barrier() {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Adds the values of shared vectors to a set, four vectors of a thread at once:
@@ -427,89 +415,6 @@ struct StreamShared {
     int twice;
 };
 
-// A slice of a row as whole 16-byte vectors [first, last) of memory and the
-// elements beside them; vector i covers the elements 8 i - phase + {0..7} (4 i
-// for fp32).
-template <typename T>
-struct Vectors {
-    static constexpr int kPer = 16 / (int)sizeof(T);
-    const T* src;
-    int n, phase, first, last;
-    __device__ Vectors(const T* src_, int n_) : src(src_), n(n_) {
-        phase = (int)(reinterpret_cast<uintptr_t>(src) & 15) / (int)sizeof(T);
-        first = phase ? 1 : 0;
-        last = (phase + n) / kPer;
-        if (last < first) last = first;
-    }
-    __device__ const uint4* vec() const { return reinterpret_cast<const uint4*>(src - phase); }
-    // element j of those before the first vector or behind the last: its place, or n
-    __device__ int beside(int j) const {
-        const int head = min(n, (kPer - phase) % kPer);
-        if (j < head) return j;
-        const int at = max(head, last * kPer - phase) + (j - head);
-        return j - head < kPer && at < n ? at : n;
-    }
-};
-
-// Calls f(i, v) on the vectors [x.first, x.last) of this thread, kAhead
-// adjacent places of the thread at once (v.q is -inf in every element where i
-// is past the end).  The vectors pass through a ring in shared memory that no
-// other thread touches, filled by asynchronous copies kStages calls ahead: the
-// bytes in flight cost no registers, and nothing waits on a barrier.
-template <typename T, typename F>
-__device__ __forceinline__ void stream(const Vectors<T>& x, uint4* ring, F&& f) {
-    const int t = threadIdx.x, calls = (x.last - x.first + kAhead * kThreads - 1) / (kAhead * kThreads);
-    const unsigned inf = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
-    const uint4* src = x.vec();
-    auto fill = [&](int call) {
-        uint4* slot = ring + (call % kStages) * (kAhead * kThreads) + t;
-        int i = x.first + call * (kAhead * kThreads) + t;
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j, i += kThreads, slot += kThreads) {
-            if (i < x.last)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(slot)), "l"(src + i) : "memory");
-            else
-                *slot = make_uint4(inf, inf, inf, inf);
-        }
-    };
-#pragma unroll
-    for (int g = 0; g < kStages; ++g) {
-        if (g < calls) fill(g);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-#pragma unroll 1
-    for (int g = 0; g < calls; ++g) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-        const uint4* slot = ring + (g % kStages) * (kAhead * kThreads) + t;
-        Vec16<T> v[kAhead];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) v[j].q = slot[j * kThreads];
-        f(x.first + g * (kAhead * kThreads) + t, v);
-        if (g + kStages < calls) fill(g + kStages);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-}
-
-// the record's entries among a vector's elements set to -inf
-__device__ __forceinline__ void strike(Vec16<float>& v, unsigned m) {
-    const unsigned inf = 0xFF800000u;
-    if (m & 1u) v.q.x = inf;
-    if (m & 2u) v.q.y = inf;
-    if (m & 4u) v.q.z = inf;
-    if (m & 8u) v.q.w = inf;
-}
-__device__ __forceinline__ void strike(Vec16<__nv_bfloat16>& v, unsigned m) {
-    auto word = [](unsigned w, unsigned two) {
-        if (two & 1u) w = (w & 0xFFFF0000u) | 0xFF80u;
-        if (two & 2u) w = (w & 0xFFFFu) | 0xFF800000u;
-        return w;
-    };
-    v.q.x = word(v.q.x, m);
-    v.q.y = word(v.q.y, m >> 2);
-    v.q.z = word(v.q.z, m >> 4);
-    v.q.w = word(v.q.w, m >> 6);
-}
-
 template <typename T, bool kForward, bool kBackward>
 __global__ void __launch_bounds__(kThreads, STREAM_MINB) k_stream(DistillArgs p, int chunk) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -573,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, STREAM_MINB) k_stream(DistillArgs p,
         const unsigned char* masks = reinterpret_cast<const unsigned char*>(bits);
         const F2 cc = f2(c, c);
         F2 s = f2(0.f, 0.f);
-        stream(x, ring, [&](int i0, Vec16<T>* v) {
+        stream<kThreads, kAhead, kStages>(x, ring, [&](int i0, Vec16<T>* v) {
             unsigned m[kAhead], any = 0;
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
@@ -657,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, STREAM_MINB) k_stream(DistillArgs p,
         }
         if (together) {
             uint4* out = reinterpret_cast<uint4*>(dx - x.phase);
-            stream(x, ring, [&](int i0, Vec16<T>* v) {
+            stream<kThreads, kAhead, kStages>(x, ring, [&](int i0, Vec16<T>* v) {
 #pragma unroll
                 for (int j = 0; j < kAhead; ++j) {
                     Vec16<T> g;
@@ -681,22 +586,6 @@ __global__ void __launch_bounds__(kThreads, STREAM_MINB) k_stream(DistillArgs p,
             dx[a] = from_f32<T>(w * (q - pk));
         }
     }
-}
-
-// A launch in clusters of `size` CTAs.
-inline cudaLaunchConfig_t cluster_config(unsigned blocks, int threads, int size, size_t smem, cudaStream_t st,
-                                         cudaLaunchAttribute* attr) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    attr->id = cudaLaunchAttributeClusterDimension;
-    attr->val.clusterDim.x = size;
-    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cfg;
 }
 
 template <typename T, bool kForward, bool kBackward>

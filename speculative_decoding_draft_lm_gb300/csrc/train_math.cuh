@@ -85,6 +85,15 @@ struct Vec16<float> {
     __device__ __forceinline__ float top() const {
         return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)), fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
     }
+    // the largest value, NaN if any is
+    __device__ __forceinline__ float top_nan() const {
+        const float a = __uint_as_float(q.x), b = __uint_as_float(q.y), c = __uint_as_float(q.z), d = __uint_as_float(q.w);
+        float r;
+        asm("{\n .reg .f32 s, t;\n max.NaN.f32 s, %1, %2;\n max.NaN.f32 t, %3, %4;\n max.NaN.f32 %0, s, t;\n}"
+            : "=f"(r)
+            : "f"(a), "f"(b), "f"(c), "f"(d));
+        return r;
+    }
     __device__ __forceinline__ void set(int i, F2 v) {
         const float2 h = halves(v);
         if (i == 0) {
@@ -109,6 +118,13 @@ struct Vec16<__nv_bfloat16> {
         auto h = [](unsigned w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
         const __nv_bfloat162 m = __hmax2(__hmax2(h(q.x), h(q.y)), __hmax2(h(q.z), h(q.w)));
         return fmaxf(__low2float(m), __high2float(m));
+    }
+    __device__ __forceinline__ float top_nan() const {
+        auto h = [](unsigned w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+        const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(h(q.x), h(q.y)), __hmax2_nan(h(q.z), h(q.w)));
+        float r;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(__low2float(m)), "f"(__high2float(m)));
+        return r;
     }
     __device__ __forceinline__ void set(int i, F2 v) {
         const float2 f = halves(v);

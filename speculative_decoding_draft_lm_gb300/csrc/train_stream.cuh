@@ -1,0 +1,121 @@
+// Streaming of rows of any alignment through a CTA, and cluster helpers.
+#pragma once
+
+#include "tc_common.cuh"
+#include "train_math.cuh"
+
+namespace domino {
+namespace train {
+
+constexpr int kMaxCluster = 16;  // non-portable size
+
+// A slice of a row as whole 16-byte vectors [first, last) of memory and the
+// elements beside them; vector i covers the elements 8 i - phase + {0..7} (4 i
+// for fp32).
+template <typename T>
+struct Vectors {
+    static constexpr int kPer = 16 / (int)sizeof(T);
+    const T* src;
+    int n, phase, first, last;
+    __device__ Vectors(const T* src_, int n_) : src(src_), n(n_) {
+        phase = (int)(reinterpret_cast<uintptr_t>(src) & 15) / (int)sizeof(T);
+        first = phase ? 1 : 0;
+        last = (phase + n) / kPer;
+        if (last < first) last = first;
+    }
+    __device__ const uint4* vec() const { return reinterpret_cast<const uint4*>(src - phase); }
+    // element j of those before the first vector or behind the last: its place, or n
+    __device__ int beside(int j) const {
+        const int head = min(n, (kPer - phase) % kPer);
+        if (j < head) return j;
+        const int at = max(head, last * kPer - phase) + (j - head);
+        return j - head < kPer && at < n ? at : n;
+    }
+};
+
+// Calls f(i, v) on the vectors [x.first, x.last) of this thread, kAhead
+// adjacent places of the thread at once (v.q is -inf in every element where i
+// is past the end).  The vectors pass through a ring in shared memory that no
+// other thread touches, filled by asynchronous copies kStages calls ahead: the
+// bytes in flight cost no registers, and nothing waits on a barrier.
+template <int kThreads, int kAhead, int kStages, typename T, typename F>
+__device__ __forceinline__ void stream(const Vectors<T>& x, uint4* ring, F&& f) {
+    const int t = threadIdx.x, calls = (x.last - x.first + kAhead * kThreads - 1) / (kAhead * kThreads);
+    const unsigned inf = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
+    const uint4* src = x.vec();
+    auto fill = [&](int call) {
+        uint4* slot = ring + (call % kStages) * (kAhead * kThreads) + t;
+        int i = x.first + call * (kAhead * kThreads) + t;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j, i += kThreads, slot += kThreads) {
+            if (i < x.last)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(slot)), "l"(src + i) : "memory");
+            else
+                *slot = make_uint4(inf, inf, inf, inf);
+        }
+    };
+#pragma unroll
+    for (int g = 0; g < kStages; ++g) {
+        if (g < calls) fill(g);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+#pragma unroll 1
+    for (int g = 0; g < calls; ++g) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        const uint4* slot = ring + (g % kStages) * (kAhead * kThreads) + t;
+        Vec16<T> v[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) v[j].q = slot[j * kThreads];
+        f(x.first + g * (kAhead * kThreads) + t, v);
+        if (g + kStages < calls) fill(g + kStages);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+}
+
+// the elements of a vector that `m` names set to -inf
+__device__ __forceinline__ void strike(Vec16<float>& v, unsigned m) {
+    const unsigned inf = 0xFF800000u;
+    if (m & 1u) v.q.x = inf;
+    if (m & 2u) v.q.y = inf;
+    if (m & 4u) v.q.z = inf;
+    if (m & 8u) v.q.w = inf;
+}
+__device__ __forceinline__ void strike(Vec16<__nv_bfloat16>& v, unsigned m) {
+    auto word = [](unsigned w, unsigned two) {
+        if (two & 1u) w = (w & 0xFFFF0000u) | 0xFF80u;
+        if (two & 2u) w = (w & 0xFFFFu) | 0xFF800000u;
+        return w;
+    };
+    v.q.x = word(v.q.x, m);
+    v.q.y = word(v.q.y, m >> 2);
+    v.q.z = word(v.q.z, m >> 4);
+    v.q.w = word(v.q.w, m >> 6);
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+    return unord_f32(__reduce_max_sync(0xffffffffu, ord_f32(x)));
+}
+// All threads of the cluster, whole warps at a time.
+__device__ __forceinline__ void cluster_barrier() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A launch in clusters of `size` CTAs.
+inline cudaLaunchConfig_t cluster_config(unsigned blocks, int threads, int size, size_t smem, cudaStream_t st,
+                                         cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = size;
+    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+}  // namespace train
+}  // namespace domino
