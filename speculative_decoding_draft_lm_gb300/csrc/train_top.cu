@@ -5,22 +5,24 @@
 // two zeros equal; a 64-bit word, orderable logit over inverted id, has that
 // order.
 //
-// One pass over the row.  A CTA streams its slice and keeps the words that beat
-// a bound, the K-th best so far, in a buffer in shared memory; when the buffer
-// is full an exact radix select leaves the best K in it and raises the bound.
-// Ids only grow along the stream, so after a select an equal logit is too late:
-// the test of the stream is one comparison of a vector's maximum with the
-// bound.  In a row without order the j-th piece passes K / j words, so the
-// selects are few and most of the time goes into the exponentials of the
-// others, which are summed as they are turned away.  The rest is never formed
-// as a difference of sums: a peaked teacher leaves less in it than the
-// rounding of the whole.  Places in the buffer come from scans, not from
-// atomics, so that equal calls sum in equal order.
+// The row is read once.  A thread's two vectors of a step of the stream are a
+// group; the CTA keeps every group's largest key and the sum of its
+// exponentials in shared memory, so the stream itself has no barrier and no
+// branch on the data.  The K-th largest of the groups' maxima is then a bound
+// that K elements reach and few others: the groups below it are in the rest
+// with their sums, the others (about K of them) are read again, and of their
+// elements those that reach the bound become words in a buffer, of which an
+// exact radix select leaves K.  The rest is never formed as a difference of
+// sums: a peaked teacher leaves less in it than the rounding of the whole.
+// Places in lists come from scans, not from atomics, so that equal calls sum
+// in equal order.
 //
-// Few rows are spread over a cluster each: every CTA finds its slice's best K
-// and rank 0 takes the others' through distributed shared memory, in the order
-// of the slices.
+// Few rows, and rows whose groups do not fit one CTA, are spread over a cluster
+// each: every CTA finds its slice's best K and rank 0 takes the others' through
+// distributed shared memory.
 #include <cooperative_groups.h>
+
+#include <type_traits>
 
 #include "train_internal.h"
 #include "train_stream.cuh"
@@ -32,12 +34,15 @@ namespace train {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kAhead = 2;
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr size_t kRingBytes = (size_t)kThreads * kAhead * kStages * 16;
 constexpr int kBins = 2048;
+constexpr int kDue = 512;    // words beyond K that make a select due
+constexpr int kStep = 2048;  // words that are sure to fit then: four per thread
+constexpr size_t kMaxSmem = 224 * 1024;  // of a CTA, beside its static variables
 
 __device__ __forceinline__ unsigned top_key(float x) { return x != x ? 0xFFFFFFFFu : ord_f32(x); }
 __device__ __forceinline__ float key_logit(unsigned k) { return k == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : unord_f32(k); }
@@ -46,16 +51,21 @@ __device__ __forceinline__ unsigned long long word_of(unsigned key, unsigned id)
     return (unsigned long long)key << 32 | (unsigned)~id;
 }
 
-// elements of one call of the stream
 template <typename T>
-constexpr int call_elems() { return kThreads * kAhead * Vec16<T>::kElems; }
-// words that the buffer holds before a select is due (even: the ring behind the
-// buffer starts on 16 bytes)
-__host__ __device__ constexpr int due_words(int K) { return ((2 * K > K + 512 ? 2 * K : K + 512) + 1) & ~1; }
-static_assert(call_elems<float>() % 2 == 0 && call_elems<__nv_bfloat16>() % 2 == 0, "the ring's alignment");
+struct Group {
+    static constexpr int kElems = kAhead * Vec16<T>::kElems;
+};
+// a key without the bits that a logit of this type cannot have
+template <typename T>
+using Key = typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type;
+// The 16-bit keys drop a half of zeros, or of ones in negative numbers' and
+// NaN's keys: the order is the same, and a bound loses nothing by the zeros.
+template <typename T>
+__device__ __forceinline__ unsigned whole(Key<T> k) { return sizeof(T) == 2 ? (unsigned)k << 16 : (unsigned)k; }
+
+constexpr int kTile = 8;  // words per thread that a select moves at once
 
 struct TopShared {
-    unsigned hist[kBins];
     unsigned warp[kWarps];
     unsigned digit, need, in_bin;
     MaxSum part[kWarps];
@@ -86,236 +96,383 @@ __device__ __forceinline__ unsigned block_scan(unsigned x, unsigned* warp_tot, u
     return before + incl - x;
 }
 
-// A CTA's selection in progress.  `bound` is the key of the K-th best word once
-// K words were seen (0 before: every word passes, and so does the test `>`).
+__device__ __forceinline__ unsigned block_max(unsigned x, unsigned* warp_tot) {
+    x = __reduce_max_sync(0xffffffffu, x);
+    if ((threadIdx.x & 31) == 0) warp_tot[threadIdx.x >> 5] = x;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) x = max(x, warp_tot[w]);
+    __syncthreads();
+    return x;
+}
+
+// Shared memory of a slice of `elems` elements: its groups, in whole steps of
+// the stream; the ring, later the histogram and the list of groups; the groups'
+// sums and keys.  Behind them: the buffer of K + kDue + kStep words.
+template <typename T>
+__host__ __device__ constexpr int groups_of(int elems) {
+    return (elems / Group<T>::kElems + kThreads) / kThreads * kThreads;  // one vector more than elems if unaligned
+}
+__host__ __device__ constexpr size_t ring_bytes(int groups) {
+    const size_t later = (size_t)kBins * 4 + (size_t)groups * 2;
+    return kRingBytes > later ? kRingBytes : later;
+}
+template <typename T>
+__host__ __device__ constexpr size_t group_bytes(int groups) { return (size_t)groups * (4 + sizeof(Key<T>)); }
+
+// A CTA's selection in progress.  `bound` is the key that a new word has to
+// beat: the K-th best's once that is known, 0 before (every key beats 0).
+// kShort: logits with 16 significant bits.
+template <bool kShort>
 struct Selection {
     TopShared& S;
     unsigned long long* buf;
-    int K, due;
+    unsigned* hist;  // [kBins]
+    int K;
     float c;
     unsigned bound;
-    float bound_logit;
     int count;
-    MaxSum rest;  // this thread's share of what was turned away
+    unsigned most;  // largest key of this thread's words
+    MaxSum rest;    // this thread's share of what was turned away
 
-    __device__ Selection(TopShared& s, unsigned long long* b, int k, float scale)
-        : S(s), buf(b), K(k), due(due_words(k)), c(scale), bound(0), bound_logit(-INFINITY), count(0), rest(empty_set()) {}
+    __device__ Selection(TopShared& s, unsigned long long* b, unsigned* h, int k, float scale)
+        : S(s), buf(b), hist(h), K(k), c(scale), bound(0), count(0), most(0), rest(empty_set()) {}
 
-    // The digit of the `need`-th largest among the words that match prefix
-    // under mask, its count and what remains to be found in it.  All threads.
-    __device__ void pass(unsigned long long prefix, unsigned long long mask, int shift, int bins, unsigned need) {
-        for (int i = threadIdx.x; i < bins; i += kThreads) S.hist[i] = 0;
+    // The digit of the `need`-th largest among the words word(0..n-1) that match
+    // prefix under mask, its count and what remains to be found in it.  All threads.
+    template <typename F>
+    __device__ __forceinline__ void pass(F&& word, int n, unsigned long long prefix, unsigned long long mask, int shift,
+                                         int bins, unsigned need) {
+        const int t = threadIdx.x;
+        for (int i = t; i < bins; i += kThreads) hist[i] = 0;
         __syncthreads();
-        const int lane = threadIdx.x & 31;
-        for (int i0 = 0; i0 < count; i0 += kThreads) {
-            const int i = i0 + threadIdx.x;
-            const unsigned long long w = i < count ? buf[i] : 0;
-            const bool in = i < count && (w & mask) == prefix;
-            const unsigned act = __ballot_sync(0xffffffffu, in);
-            if (in) {
-                const unsigned d = (unsigned)(w >> shift) & (unsigned)(bins - 1);
-                const unsigned peers = __match_any_sync(act, d);
-                if (lane == __ffs(peers) - 1) atomicAdd(&S.hist[d], (unsigned)__popc(peers));
-            }
+#pragma unroll 4
+        for (int i = t; i < n; i += kThreads) {
+            const unsigned long long w = word(i);
+            if ((w & mask) == prefix) atomicAdd(&hist[(unsigned)(w >> shift) & (unsigned)(bins - 1)], 1u);
         }
         __syncthreads();
-        // thread t holds the bins from the top down: bins-1 - t*per ...
-        const int per = bins / kThreads;
-        unsigned mine = 0;
-        for (int j = 0; j < per; ++j) mine += S.hist[bins - 1 - (int)threadIdx.x * per - j];
-        unsigned all;
+        // thread t holds `per` bins, from the top down
+        const int per = bins > kThreads ? bins / kThreads : 1, first = bins - 1 - t * per;
+        unsigned mine = 0, all;
+        if (first >= 0)
+            for (int j = 0; j < per; ++j) mine += hist[first - j];
         unsigned above = block_scan(mine, S.warp, &all);
         if (above < need && above + mine >= need) {
-            int b = bins - 1 - (int)threadIdx.x * per;
-            while (above + S.hist[b] < need) above += S.hist[b--];
+            int b = first;
+            while (above + hist[b] < need) above += hist[b--];
             S.digit = (unsigned)b;
             S.need = need - above;
-            S.in_bin = S.hist[b];
+            S.in_bin = hist[b];
         }
         __syncthreads();
     }
 
-    // Leaves the best K words at the front of the buffer.  All threads.
-    template <bool kShort>  // keys with 16 significant bits
-    __device__ void select() {
-        if (count <= K) return;
-        unsigned long long prefix = 0, mask = 0;
+    // Where to look for the K-th of keys between `low` and the largest: the
+    // bits above `bit` are common to all.
+    __device__ void range(unsigned low, unsigned largest, int floor, int* bit, unsigned long long* prefix,
+                          unsigned long long* mask) {
+        *bit = max(floor, 32 - __clz((int)(largest ^ low)));
+        *mask = *bit == 32 ? 0ull : ~0ull << (32 + *bit);
+        *prefix = ((unsigned long long)largest << 32) & *mask;
+    }
+
+    // A bound for the K largest of n keys: the K-th largest, or a little less.
+    template <typename KeyT>
+    __device__ __noinline__ void bound_by(const KeyT* keys, int n, unsigned lowest, unsigned largest) {
+        constexpr int kFloor = sizeof(KeyT) == 2 ? 16 : 0;
+        int bit;
+        unsigned long long prefix, mask;
+        range(lowest, largest, kFloor, &bit, &prefix, &mask);
         unsigned need = (unsigned)K;
-        // logit: 11 + 11 + 10 bits; inverted id: 10 + 10 bits (the bits above are all ones)
-        const int shift[5] = {53, 42, 32, 10, 0};
-        const int bits[5] = {11, 11, 10, 10, 10};
-#pragma unroll 1
-        for (int p = 0; p < 5; ++p) {
-            if (p == 2 && kShort) {
-                // a 16-bit logit's key ends in ten zeros, or ten ones if negative or NaN
-                const bool ones = !(prefix >> 63) || prefix >> 42 == 0x3FFFFFull;
-                prefix |= ones ? 0x3FFull << 32 : 0ull;
-                mask |= 0x3FFull << 32;
-                continue;
-            }
-            if (p == 3) {
-                prefix |= 0xFFF00000ull;
-                mask |= 0xFFF00000ull;
-            }
-            pass(prefix, mask, shift[p], 1 << bits[p], need);
-            prefix |= (unsigned long long)S.digit << shift[p];
-            mask |= (unsigned long long)((1u << bits[p]) - 1) << shift[p];
+        while (bit > kFloor) {
+            const int bits = min(11, bit - kFloor);
+            bit -= bits;
+            pass([&](int i) { return (unsigned long long)keys[i] << (sizeof(KeyT) == 2 ? 48 : 32); }, n, prefix, mask,
+                 32 + bit, 1 << bits, need);
+            prefix |= (unsigned long long)S.digit << (32 + bit);
+            mask |= (unsigned long long)((1u << bits) - 1) << (32 + bit);
             need = S.need;
-            if (S.in_bin == need) break;  // the whole bin belongs: everything from `prefix` up
+            if (S.in_bin <= need + (unsigned)(K / 8)) break;  // few more than needed lie in the bin
         }
-        // words in the buffer from `prefix` up are exactly K
-        unsigned kept = 0;
-        unsigned low = 0xFFFFFFFFu;
-        for (int i0 = 0; i0 < count; i0 += kThreads) {
-            const int i = i0 + threadIdx.x;
-            const unsigned long long w = i < count ? buf[i] : 0;
-            const bool keep = i < count && w >= prefix;
-            if (i < count && !keep) add(rest, key_logit((unsigned)(w >> 32)), c);
-            if (keep) low = min(low, (unsigned)(w >> 32));
-            unsigned all;
-            const unsigned at = kept + block_scan(keep, S.warp, &all);  // its barriers part the reads from the writes
-            if (keep) buf[at] = w;
+        bound = (unsigned)(prefix >> 32);
+        __syncthreads();
+    }
+
+    // Leaves the best K words at the front of the buffer.  All threads, after a barrier.
+    __device__ __noinline__ void select() {
+        if (count <= K) return;
+        // every word lies between the bound and the largest: only the bits in
+        // which the two differ are searched, 11 at a time
+        const unsigned largest = block_max(most, S.warp);
+        constexpr int kFloor = kShort ? 16 : 0;
+        int bit;
+        unsigned long long prefix, mask;
+        range(bound, largest, kFloor, &bit, &prefix, &mask);
+        const auto word = [&](int i) { return buf[i]; };
+        unsigned need = (unsigned)K;
+        bool found = false;
+        while (bit > kFloor && !found) {
+            const int bits = min(11, bit - kFloor);
+            bit -= bits;
+            pass(word, count, prefix, mask, 32 + bit, 1 << bits, need);
+            prefix |= (unsigned long long)S.digit << (32 + bit);
+            mask |= (unsigned long long)((1u << bits) - 1) << (32 + bit);
+            need = S.need;
+            found = S.in_bin == need;  // the whole bin belongs: everything from `prefix` up
+        }
+        if (!found) {
+            // equal logits: the lowest ids, two digits of the inverted id (the bits above are all ones).  A 16-bit
+            // logit's key ends in zeros, or in ones if it is negative or NaN
+            if (kShort && (!(prefix >> 63) || prefix >> 48 == 0xFFFFull)) prefix |= 0xFFFFull << 32;
+            prefix |= 0xFFF00000ull;
+            mask = ~0ull << 20;
+            for (int shift = 10; shift >= 0 && !found; shift -= 10) {
+                pass(word, count, prefix, mask, shift, 1024, need);
+                prefix |= (unsigned long long)S.digit << shift;
+                mask |= 1023ull << shift;
+                need = S.need;
+                found = S.in_bin == need;
+            }
+        }
+        // the words from `prefix` up, exactly K, to the front; a thread's words
+        // of a tile are read before the scan's barriers and written after them
+        unsigned kept = 0, low = 0xFFFFFFFFu;
+        for (int i0 = 0; i0 < count; i0 += kTile * kThreads) {
+            unsigned long long w[kTile];
+            unsigned keep = 0, all;
+#pragma unroll
+            for (int j = 0; j < kTile; ++j) {
+                const int i = i0 + j * kThreads + (int)threadIdx.x;
+                if (i0 + j * kThreads >= count) break;
+                w[j] = i < count ? buf[i] : 0;
+                if (w[j] >= prefix) {
+                    keep |= 1u << j;
+                    low = min(low, (unsigned)(w[j] >> 32));
+                } else if (i < count) {
+                    add(rest, key_logit((unsigned)(w[j] >> 32)), c);
+                }
+            }
+            unsigned at = kept + block_scan((unsigned)__popc(keep), S.warp, &all);
+#pragma unroll
+            for (int j = 0; j < kTile; ++j) {
+                if (i0 + j * kThreads >= count) break;
+                if (keep >> j & 1u) buf[at++] = w[j];
+            }
             kept += all;
         }
-        low = __reduce_min_sync(0xffffffffu, low);
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) S.warp[threadIdx.x >> 5] = low;
-        __syncthreads();
-        for (int w = 0; w < kWarps; ++w) low = min(low, S.warp[w]);
-        __syncthreads();
+        low = ~block_max(~low, S.warp);
         count = K;
         bound = low;
-        bound_logit = key_logit(low);
     }
 
-    // Takes the words that `n` says this thread has.  All threads; room for one
-    // call's words is left below the buffer's end by the select.
-    template <bool kShort, typename F>
+    // Takes `n` words of this thread.  All threads; at most kStep in all, or as
+    // many as `fits` said.
+    template <typename F>
     __device__ __forceinline__ void take(unsigned n, F&& write) {
-        if (!__syncthreads_or((int)n)) return;
         unsigned all;
         const unsigned at = block_scan(n, S.warp, &all);
         if (n) write(buf + count + at);
         count += (int)all;
-        if (count > due) {
+        if (count > K + kDue) {
             __syncthreads();
-            select<kShort>();
+            select();
         }
     }
 
+    __device__ bool fits(int words) const { return count + words <= K + kDue + kStep; }
+
     // One logit per thread, or none.
-    template <bool kShort>
     __device__ void one(bool in, float x, unsigned id) {
         const unsigned k = in ? top_key(x) : 0u;
-        const bool pass = in && k > bound;
+        const bool pass = in && k >= bound;
         if (in && !pass) add(rest, x, c);
-        take<kShort>(pass, [&](unsigned long long* to) { *to = word_of(k, id); });
+        if (pass) most = max(most, k);
+        take(pass, [&](unsigned long long* to) { *to = word_of(k, id); });
     }
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_top(const T* __restrict__ logits, long long ld, int V, int K,
-                                                  float temperature, int32_t* __restrict__ ids,
-                                                  float* __restrict__ top, float* __restrict__ rest, int chunk) {
+__global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logits, long long ld, int V, int K,
+                                                     float temperature, int32_t* __restrict__ ids,
+                                                     float* __restrict__ top, float* __restrict__ rest, int chunk, int front) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ TopShared S;
     constexpr bool kShort = sizeof(T) == 2;
-    constexpr int kPer = Vec16<T>::kElems, P = kPer / 2;
+    constexpr int kPer = Vec16<T>::kElems, P = kPer / 2, kG = Group<T>::kElems;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
     const int n = blockIdx.x / size, t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    unsigned long long* buf = reinterpret_cast<unsigned long long*>(smem);
-    uint4* ring = reinterpret_cast<uint4*>(buf + due_words(K) + call_elems<T>());
+    // shared memory: the ring of the stream (then the list of groups and the
+    // histogram), the groups' sums and keys, the buffer of words
+    uint4* ring = reinterpret_cast<uint4*>(smem);
+    unsigned* hist = reinterpret_cast<unsigned*>(smem);
+    uint16_t* list = reinterpret_cast<uint16_t*>(hist + kBins);
+    const int most_groups = groups_of<T>(chunk);
+    float* sums = reinterpret_cast<float*>(smem + ring_bytes(most_groups));
+    Key<T>* keys = reinterpret_cast<Key<T>*>(sums + most_groups);
+    unsigned long long* buf = reinterpret_cast<unsigned long long*>(smem + front);
     const int v0 = min(V, rank * chunk);
     const Vectors<T> x(logits + (size_t)n * ld + v0, min(V, v0 + chunk) - v0);
-    Selection sel(S, buf, K, kLog2e / temperature);
+    const float c = kLog2e / temperature;
+    const F2 cc = f2(c, c);
+    Selection<kShort> sel(S, buf, hist, K, c);
 
-    // the elements in front of the first whole vector, the vectors, the elements behind the last
-    const int head = min(x.n, (kPer - x.phase) % kPer);
-    if (head) sel.one<kShort>(t < head, t < head ? to_f32(x.src[t]) : 0.f, (unsigned)(v0 + t));
+    // the groups: a thread's two vectors of each step
+    unsigned largest = 0, lowest = 0xFFFFFFFFu;
+    stream<kThreads, kAhead, kStages>(x, ring, [&](int i0, Vec16<T>* v) {
+        float m = v[0].top_nan();
+#pragma unroll
+        for (int j = 1; j < kAhead; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(v[j].top_nan()));
+        const int g = (i0 - t - x.first) / kAhead + t;  // kThreads groups a step
+        const unsigned k = i0 < x.last ? top_key(m) : 0u;
+        // exponentials on the group's own scale
+        const float at = clamp_max(-FLT_MAX, m);
+        const F2 minus = f2(-at, -at);
+        F2 s = f2(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+            for (int e = 0; e < P; ++e) s = add2(s, ex2x2(mul2(add2(v[j].pair(e), minus), cc)));
+        const float2 h = halves(s);
+        sums[g] = h.x + h.y;
+        keys[g] = (Key<T>)(kShort ? k >> 16 : k);
+        largest = max(largest, k);
+        if (k) lowest = min(lowest, k);
+    });
+    const int groups = (x.last - x.first + kAhead * kThreads - 1) / (kAhead * kThreads) * kThreads;
+    largest = block_max(largest, S.warp);
+    lowest = ~block_max(~lowest, S.warp);
+    // fewer groups than K: every group is read again
+    if (x.last - x.first >= K * kAhead) sel.bound_by(keys, groups, kShort ? lowest & 0xFFFF0000u : lowest, largest);
+
+    // the groups below the bound are in the rest; the others' list, a warp's share after another's
+    int listed;
     {
-        MaxSum r = sel.rest;
-        F2 s = f2(r.s, 0.f);
-        const F2 cc = f2(sel.c, sel.c);
-        sel.rest = empty_set();  // what selects turn away meanwhile
-        stream<kThreads, kAhead, kStages>(x, ring, [&](int i0, Vec16<T>* v) {
-            // a bit per element that beats the bound
-            unsigned pass = 0;
+        const int share = (groups / kThreads) * 32, g0 = warp * share;  // a multiple of 32 groups per warp
+        MaxSum r = empty_set();
+        int mine = 0;
+        for (int g = g0 + lane; g < g0 + share; g += 32) {
+            const unsigned k = whole<T>(keys[g]);
+            const bool in = k != 0 && k >= sel.bound;
+            mine += __popc(__ballot_sync(0xffffffffu, in));
+            if (!in && k != 0) {
+                // the group's maximum back from its key (its low half: see Key)
+                const unsigned full = kShort && !(k >> 31) ? k | 0xFFFFu : k;
+                r = join(r, MaxSum{clamp_max(-FLT_MAX, key_logit(full)), sums[g]}, c);
+            }
+        }
+        sel.rest = r;
+        unsigned all;
+        unsigned at = block_scan(lane == 0 ? (unsigned)mine : 0u, S.warp, &all);
+        at = __shfl_sync(0xffffffffu, at, 0);
+        listed = (int)all;
+        for (int g = g0 + lane; g < g0 + share; g += 32) {
+            const unsigned k = whole<T>(keys[g]);
+            const bool in = k != 0 && k >= sel.bound;
+            const unsigned who = __ballot_sync(0xffffffffu, in);
+            if (in) list[at + __popc(who & ((1u << lane) - 1u))] = (uint16_t)g;
+            at += __popc(who);
+        }
+    }
+    __syncthreads();
+    for (int l0 = 0; l0 < listed; l0 += kThreads) {
+        const bool in = l0 + t < listed;
+        Vec16<T> v[kAhead];
+        int at[kAhead];  // element of the slice at which the vector begins
+        unsigned pass = 0;
+        if (in) {
+            const int g = list[l0 + t], i0 = x.first + g / kThreads * (kAhead * kThreads) + g % kThreads;
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                if (!(v[j].top_nan() <= sel.bound_logit) || sel.bound == 0) {
-                    if (i0 + j * kThreads < x.last) {
+                const int i = i0 + j * kThreads;
+                at[j] = i * kPer - x.phase;
+                if (i < x.last) v[j].q = x.vec()[i];
+            }
 #pragma unroll
-                        for (int e = 0; e < kPer; ++e) {
-                            const float2 f = halves(v[j].pair(e / 2));
-                            if (top_key(e & 1 ? f.y : f.x) > sel.bound) pass |= 1u << (j * kPer + e);
+            for (int j = 0; j < kAhead; ++j)
+                if (i0 + j * kThreads < x.last)
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) {
+                        const float2 f = halves(v[j].pair(e / 2));
+                        const float y = e & 1 ? f.y : f.x;
+                        const unsigned k = top_key(y);
+                        if (k >= sel.bound) {
+                            pass |= 1u << (j * kPer + e);
+                            sel.most = max(sel.most, k);
+                        } else {
+                            add(sel.rest, y, c);
                         }
                     }
-                }
-            }
-            const unsigned count = (unsigned)__popc(pass);
-            Vec16<T> kept[kAhead];
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                kept[j] = v[j];
-                if (pass) strike(v[j], pass >> (j * kPer) & ((1u << kPer) - 1u));
-            }
-            // the others' exponentials
-            float most = v[0].top();
-#pragma unroll
-            for (int j = 1; j < kAhead; ++j) most = fmaxf(most, v[j].top());
-            if (most > r.m) {
-                const float m = clamp_max(r.m, most), f = ex2((r.m - m) * sel.c);
-                s = mul2(s, f2(f, f));
-                r.m = m;
-            }
-            const F2 minus = f2(-r.m, -r.m);
+        }
+        // the words of elements [lo, hi) of the groups
+        auto write = [&](unsigned long long* to, int lo, int hi) {
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
 #pragma unroll
-                for (int k = 0; k < P; ++k) s = add2(s, ex2x2(mul2(add2(v[j].pair(k), minus), cc)));
-            sel.take<kShort>(count, [&](unsigned long long* to) {
-#pragma unroll
-                for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-                    for (int e = 0; e < kPer; ++e)
-                        if (pass >> (j * kPer + e) & 1u) {
-                            const float2 f = halves(kept[j].pair(e / 2));
-                            const int at = (i0 + j * kThreads) * kPer - x.phase + e;
-                            *to++ = word_of(top_key(e & 1 ? f.y : f.x), (unsigned)(v0 + at));
-                        }
-            });
-        });
-        const float2 h = halves(s);
-        r.s = h.x + h.y;
-        sel.rest = join(sel.rest, r, sel.c);
+                for (int e = 0; e < kPer; ++e) {
+                    const int b = j * kPer + e;
+                    if (b >= lo && b < hi && (pass >> b & 1u)) {
+                        const float2 f = halves(v[j].pair(e / 2));
+                        *to++ = word_of(top_key(e & 1 ? f.y : f.x), (unsigned)(v0 + at[j] + e));
+                    }
+                }
+        };
+        // all at once where they are sure to fit, else four elements of each group at a time
+        const int takers = __syncthreads_count(pass != 0);
+        if (sel.fits(takers * kG)) {
+            sel.take((unsigned)__popc(pass), [&](unsigned long long* to) { write(to, 0, kG); });
+        } else {
+#pragma unroll 1
+            for (int b = 0; b < kG; b += kStep / kThreads) {
+                const unsigned some = pass >> b & ((1u << (kStep / kThreads)) - 1u);
+                sel.take((unsigned)__popc(some), [&](unsigned long long* to) { write(to, b, b + kStep / kThreads); });
+            }
+        }
     }
-    const int behind = max(head, x.last * kPer - x.phase);
-    if (behind < x.n) {
-        const int at = behind + t;
-        sel.one<kShort>(at < x.n, at < x.n ? to_f32(x.src[at]) : 0.f, (unsigned)(v0 + at));
+    {  // the elements beside the whole vectors
+        const int at = t < 2 * kPer ? x.beside(t) : x.n;
+        sel.one(at < x.n, at < x.n ? to_f32(x.src[at]) : 0.f, (unsigned)(v0 + at));
     }
     __syncthreads();
-    sel.select<kShort>();
+    sel.select();
 
     if (size > 1) {
         if (t == 0) S.count = sel.count;
         cluster_barrier();
         if (rank == 0) {
-            for (int r = 1; r < size; ++r) {
-                const unsigned long long* from = cluster.map_shared_rank(buf, r);
-                const int words = *cluster.map_shared_rank(&S.count, r);
-                for (int i0 = 0; i0 < words; i0 += kThreads) {
-                    const int i = i0 + t;
-                    const unsigned long long w = i < words ? from[i] : 0;
-                    const unsigned k = (unsigned)(w >> 32);
-                    const bool pass = i < words && k > sel.bound;
-                    if (i < words && !pass) add(sel.rest, key_logit(k), sel.c);
-                    sel.take<kShort>(pass, [&](unsigned long long* to) { *to = w; });
+            // the other slices' words, four per thread at once
+            constexpr int kWords = 4;
+            const int most = min(K, chunk), words = (size - 1) * most;
+            for (int i0 = 0; i0 < words; i0 += kWords * kThreads) {
+                unsigned long long w[kWords];
+                unsigned pass = 0;
+#pragma unroll
+                for (int j = 0; j < kWords; ++j) {
+                    const int i = i0 + j * kThreads + t, r = 1 + i / most;
+                    w[j] = 0;
+                    if (i < words && i % most < *cluster.map_shared_rank(&S.count, r))
+                        w[j] = cluster.map_shared_rank(buf, r)[i % most];
                 }
+#pragma unroll
+                for (int j = 0; j < kWords; ++j) {
+                    const unsigned k = (unsigned)(w[j] >> 32);  // 0: no word
+                    if (k == 0) continue;
+                    if (k >= sel.bound) {
+                        pass |= 1u << j;
+                        sel.most = max(sel.most, k);
+                    } else {
+                        add(sel.rest, key_logit(k), sel.c);
+                    }
+                }
+                sel.take((unsigned)__popc(pass), [&](unsigned long long* to) {
+#pragma unroll
+                    for (int j = 0; j < kWords; ++j)
+                        if (pass >> j & 1u) *to++ = w[j];
+                });
             }
             __syncthreads();
-            sel.select<kShort>();
+            sel.select();
         }
     }
     // the CTA's rest
@@ -344,8 +501,8 @@ __global__ void __launch_bounds__(kThreads) k_top(const T* __restrict__ logits, 
     if (t == 0) rest[n] = S.rest.s == 0.f ? -INFINITY : S.rest.m / temperature + logf(S.rest.s);
 
     // ascending ids: a bit per id, counted in front of each thread's words of bits
-    unsigned* bits = reinterpret_cast<unsigned*>(buf + K);  // what follows the record is free now
-    unsigned* before = S.hist;
+    unsigned* bits = hist + kBins;  // over the list and the groups
+    unsigned* before = hist;
     const int words = (V + 31) / 32, per = (words + kThreads - 1) / kThreads;
     for (int i = t; i < per * kThreads; i += kThreads) bits[i] = 0;
     __syncthreads();
@@ -376,9 +533,17 @@ cudaError_t launch(domino_train_ctx* c, const void* x, long long ld, int n, int 
     auto slice = [&](int parts) { return ((V + parts - 1) / parts + 63) / 64 * 64; };
     // few rows: spread them while the slices stay longer than what they keep
     while (size < kMaxCluster && (long long)n * size < 2 * c->num_sms && slice(2 * size) >= 2 * K + 2048) size *= 2;
-    const size_t bits = (size_t)((V + 31) / 32 + kThreads) * 4;
-    const size_t during = (size_t)(due_words(K) + call_elems<T>()) * 8 + kRingBytes, after = (size_t)K * 8 + bits;
-    const size_t smem = during > after ? during : after;
+    // in front of the words: what the stream and the selection use, later a bit per id
+    const size_t bits = (size_t)kBins * 4 + (size_t)((V + 31) / 32 + kThreads) * 4;
+    const size_t words = (size_t)(K + kDue + kStep) * 8;
+    size_t front;
+    for (;; size *= 2) {
+        const int groups = groups_of<T>(slice(size));
+        front = ring_bytes(groups) + group_bytes<T>(groups);
+        if (front < bits) front = (bits + 15) / 16 * 16;
+        if (size == kMaxCluster || front + words <= kMaxSmem) break;
+    }
+    const size_t smem = front + words;
     auto kern = k_top<T>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -386,7 +551,8 @@ cudaError_t launch(domino_train_ctx* c, const void* x, long long ld, int n, int 
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = cluster_config((unsigned)n * size, kThreads, size, smem, st, &attr);
     c->last_launches = 1;
-    return cudaLaunchKernelEx(&cfg, kern, static_cast<const T*>(x), ld, V, K, temperature, ids, top, rest, slice(size));
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<const T*>(x), ld, V, K, temperature, ids, top, rest, slice(size),
+                              (int)front);
 }
 
 }  // namespace
