@@ -40,6 +40,7 @@ constexpr int kAhead = 2;
 constexpr int kStages = 2;
 constexpr size_t kRingBytes = (size_t)kThreads * kAhead * kStages * 16;
 constexpr int kBins = 2048;
+constexpr int kFew = 256;    // a record whose ids are ordered by counting
 constexpr int kDue = 512;    // words beyond K that make a select due
 constexpr int kStep = 2048;  // words that are sure to fit then: four per thread
 constexpr size_t kMaxSmem = 224 * 1024;  // of a CTA, beside its static variables
@@ -68,6 +69,7 @@ constexpr int kTile = 8;  // words per thread that a select moves at once
 struct TopShared {
     unsigned warp[kWarps];
     unsigned digit, need, in_bin;
+    unsigned bound;
     MaxSum part[kWarps];
     MaxSum rest;   // the CTA's rest
     int count;     // the CTA's words
@@ -120,177 +122,140 @@ __host__ __device__ constexpr size_t ring_bytes(int groups) {
 template <typename T>
 __host__ __device__ constexpr size_t group_bytes(int groups) { return (size_t)groups * (4 + sizeof(Key<T>)); }
 
-// A CTA's selection in progress.  `bound` is the key that a new word has to
-// beat: the K-th best's once that is known, 0 before (every key beats 0).
-// kShort: logits with 16 significant bits.
-template <bool kShort>
-struct Selection {
-    TopShared& S;
-    unsigned long long* buf;
-    unsigned* hist;  // [kBins]
-    int K;
-    float c;
-    unsigned bound;
-    int count;
-    unsigned most;  // largest key of this thread's words
-    MaxSum rest;    // this thread's share of what was turned away
-
-    __device__ Selection(TopShared& s, unsigned long long* b, unsigned* h, int k, float scale)
-        : S(s), buf(b), hist(h), K(k), c(scale), bound(0), count(0), most(0), rest(empty_set()) {}
-
-    // The digit of the `need`-th largest among the words word(0..n-1) that match
-    // prefix under mask, its count and what remains to be found in it.  All threads.
-    template <typename F>
-    __device__ __forceinline__ void pass(F&& word, int n, unsigned long long prefix, unsigned long long mask, int shift,
-                                         int bins, unsigned need) {
-        const int t = threadIdx.x;
-        for (int i = t; i < bins; i += kThreads) hist[i] = 0;
-        __syncthreads();
+// The digit of the `need`-th largest among the words word(0..n-1) that match
+// prefix under mask, its count and what remains to be found in it, to S.  All
+// threads; hist is all zeros before and after.
+template <typename F>
+__device__ __forceinline__ void digit_pass(TopShared& S, unsigned* hist, F&& word, int n, unsigned long long prefix,
+                                           unsigned long long mask, int shift, int bins, unsigned need) {
+    const int t = threadIdx.x;
 #pragma unroll 4
-        for (int i = t; i < n; i += kThreads) {
-            const unsigned long long w = word(i);
-            if ((w & mask) == prefix) atomicAdd(&hist[(unsigned)(w >> shift) & (unsigned)(bins - 1)], 1u);
-        }
-        __syncthreads();
-        // thread t holds `per` bins, from the top down
-        const int per = bins > kThreads ? bins / kThreads : 1, first = bins - 1 - t * per;
-        unsigned mine = 0, all;
-        if (first >= 0)
-            for (int j = 0; j < per; ++j) mine += hist[first - j];
-        unsigned above = block_scan(mine, S.warp, &all);
-        if (above < need && above + mine >= need) {
-            int b = first;
-            while (above + hist[b] < need) above += hist[b--];
-            S.digit = (unsigned)b;
-            S.need = need - above;
-            S.in_bin = hist[b];
-        }
-        __syncthreads();
+    for (int i = t; i < n; i += kThreads) {
+        const unsigned long long w = word(i);
+        if ((w & mask) == prefix) atomicAdd(&hist[(unsigned)(w >> shift) & (unsigned)(bins - 1)], 1u);
     }
-
-    // Where to look for the K-th of keys between `low` and the largest: the
-    // bits above `bit` are common to all.
-    __device__ void range(unsigned low, unsigned largest, int floor, int* bit, unsigned long long* prefix,
-                          unsigned long long* mask) {
-        *bit = max(floor, 32 - __clz((int)(largest ^ low)));
-        *mask = *bit == 32 ? 0ull : ~0ull << (32 + *bit);
-        *prefix = ((unsigned long long)largest << 32) & *mask;
+    __syncthreads();
+    // thread t holds `per` bins, from the top down
+    const int per = bins > kThreads ? bins / kThreads : 1, first = bins - 1 - t * per;
+    unsigned mine = 0, all;
+    if (first >= 0)
+        for (int j = 0; j < per; ++j) mine += hist[first - j];
+    unsigned above = block_scan(mine, S.warp, &all);
+    if (above < need && above + mine >= need) {
+        int b = first;
+        while (above + hist[b] < need) above += hist[b--];
+        S.digit = (unsigned)b;
+        S.need = need - above;
+        S.in_bin = hist[b];
     }
+    if (first >= 0)
+        for (int j = 0; j < per; ++j) hist[first - j] = 0;
+    __syncthreads();
+}
 
-    // A bound for the K largest of n keys: the K-th largest, or a little less.
-    template <typename KeyT>
-    __device__ __noinline__ void bound_by(const KeyT* keys, int n, unsigned lowest, unsigned largest) {
-        constexpr int kFloor = sizeof(KeyT) == 2 ? 16 : 0;
-        int bit;
-        unsigned long long prefix, mask;
-        range(lowest, largest, kFloor, &bit, &prefix, &mask);
-        unsigned need = (unsigned)K;
-        while (bit > kFloor) {
-            const int bits = min(11, bit - kFloor);
-            bit -= bits;
-            pass([&](int i) { return (unsigned long long)keys[i] << (sizeof(KeyT) == 2 ? 48 : 32); }, n, prefix, mask,
-                 32 + bit, 1 << bits, need);
-            prefix |= (unsigned long long)S.digit << (32 + bit);
-            mask |= (unsigned long long)((1u << bits) - 1) << (32 + bit);
-            need = S.need;
-            if (S.in_bin <= need + (unsigned)(K / 8)) break;  // few more than needed lie in the bin
-        }
-        bound = (unsigned)(prefix >> 32);
-        __syncthreads();
+// Where to look for the K-th of keys between `low` and the largest: the bits
+// from `bit` up are common to all.
+__device__ __forceinline__ void search_range(unsigned low, unsigned largest, int floor, int* bit,
+                                             unsigned long long* prefix, unsigned long long* mask) {
+    *bit = max(floor, 32 - __clz((int)(largest ^ low)));
+    *mask = *bit == 32 ? 0ull : ~0ull << (32 + *bit);
+    *prefix = ((unsigned long long)largest << 32) & *mask;
+}
+
+// A bound for the K largest of n keys: the K-th largest, or a little less.
+template <typename KeyT>
+__device__ __noinline__ unsigned bound_by(TopShared& S, unsigned* hist, const KeyT* keys, int n, int K, unsigned lowest,
+                                          unsigned largest) {
+    constexpr int kFloor = sizeof(KeyT) == 2 ? 16 : 0;
+    int bit;
+    unsigned long long prefix, mask;
+    search_range(lowest, largest, kFloor, &bit, &prefix, &mask);
+    unsigned need = (unsigned)K;
+    while (bit > kFloor) {
+        const int bits = min(11, bit - kFloor);
+        bit -= bits;
+        digit_pass(S, hist, [&](int i) { return (unsigned long long)keys[i] << (sizeof(KeyT) == 2 ? 48 : 32); }, n,
+                   prefix, mask, 32 + bit, 1 << bits, need);
+        prefix |= (unsigned long long)S.digit << (32 + bit);
+        mask |= (unsigned long long)((1u << bits) - 1) << (32 + bit);
+        need = S.need;
+        if (S.in_bin <= need + (unsigned)(K / 8)) break;  // few more than needed lie in the bin
     }
+    return (unsigned)(prefix >> 32);
+}
 
-    // Leaves the best K words at the front of the buffer.  All threads, after a barrier.
-    __device__ __noinline__ void select() {
-        if (count <= K) return;
-        // every word lies between the bound and the largest: only the bits in
-        // which the two differ are searched, 11 at a time
-        const unsigned largest = block_max(most, S.warp);
-        constexpr int kFloor = kShort ? 16 : 0;
-        int bit;
-        unsigned long long prefix, mask;
-        range(bound, largest, kFloor, &bit, &prefix, &mask);
-        const auto word = [&](int i) { return buf[i]; };
-        unsigned need = (unsigned)K;
-        bool found = false;
-        while (bit > kFloor && !found) {
-            const int bits = min(11, bit - kFloor);
-            bit -= bits;
-            pass(word, count, prefix, mask, 32 + bit, 1 << bits, need);
-            prefix |= (unsigned long long)S.digit << (32 + bit);
-            mask |= (unsigned long long)((1u << bits) - 1) << (32 + bit);
-            need = S.need;
-            found = S.in_bin == need;  // the whole bin belongs: everything from `prefix` up
-        }
-        if (!found) {
-            // equal logits: the lowest ids, two digits of the inverted id (the bits above are all ones).  A 16-bit
-            // logit's key ends in zeros, or in ones if it is negative or NaN
-            if (kShort && (!(prefix >> 63) || prefix >> 48 == 0xFFFFull)) prefix |= 0xFFFFull << 32;
-            prefix |= 0xFFF00000ull;
-            mask = ~0ull << 20;
-            for (int shift = 10; shift >= 0 && !found; shift -= 10) {
-                pass(word, count, prefix, mask, shift, 1024, need);
-                prefix |= (unsigned long long)S.digit << shift;
-                mask |= 1023ull << shift;
-                need = S.need;
-                found = S.in_bin == need;
-            }
-        }
-        // the words from `prefix` up, exactly K, to the front; a thread's words
-        // of a tile are read before the scan's barriers and written after them
-        unsigned kept = 0, low = 0xFFFFFFFFu;
-        for (int i0 = 0; i0 < count; i0 += kTile * kThreads) {
-            unsigned long long w[kTile];
-            unsigned keep = 0, all;
-#pragma unroll
-            for (int j = 0; j < kTile; ++j) {
-                const int i = i0 + j * kThreads + (int)threadIdx.x;
-                if (i0 + j * kThreads >= count) break;
-                w[j] = i < count ? buf[i] : 0;
-                if (w[j] >= prefix) {
-                    keep |= 1u << j;
-                    low = min(low, (unsigned)(w[j] >> 32));
-                } else if (i < count) {
-                    add(rest, key_logit((unsigned)(w[j] >> 32)), c);
-                }
-            }
-            unsigned at = kept + block_scan((unsigned)__popc(keep), S.warp, &all);
-#pragma unroll
-            for (int j = 0; j < kTile; ++j) {
-                if (i0 + j * kThreads >= count) break;
-                if (keep >> j & 1u) buf[at++] = w[j];
-            }
-            kept += all;
-        }
-        low = ~block_max(~low, S.warp);
-        count = K;
-        bound = low;
-    }
-
-    // Takes `n` words of this thread.  All threads; at most kStep in all, or as
-    // many as `fits` said.
-    template <typename F>
-    __device__ __forceinline__ void take(unsigned n, F&& write) {
-        unsigned all;
-        const unsigned at = block_scan(n, S.warp, &all);
-        if (n) write(buf + count + at);
-        count += (int)all;
-        if (count > K + kDue) {
-            __syncthreads();
-            select();
-        }
-    }
-
-    __device__ bool fits(int words) const { return count + words <= K + kDue + kStep; }
-
-    // One logit per thread, or none.
-    __device__ void one(bool in, float x, unsigned id) {
-        const unsigned k = in ? top_key(x) : 0u;
-        const bool pass = in && k >= bound;
-        if (in && !pass) add(rest, x, c);
-        if (pass) most = max(most, k);
-        take(pass, [&](unsigned long long* to) { *to = word_of(k, id); });
-    }
+// What a select leaves beside the words: the bound (the K-th best key) and the
+// thread's share of the rest.
+struct Selected {
+    unsigned bound;
+    MaxSum rest;
 };
+
+// Leaves the best K of `count` words at the front of the buffer; every word's
+// key lies in [low, largest].  kShort: logits with 16 significant bits.  All
+// threads, after a barrier, count > K.
+template <bool kShort>
+__device__ __noinline__ Selected select(TopShared& S, unsigned long long* buf, unsigned* hist, int count, int K,
+                                        unsigned low, unsigned largest, MaxSum rest, float c) {
+    const int t = threadIdx.x;
+    constexpr int kFloor = kShort ? 16 : 0;
+    int bit;
+    unsigned long long prefix, mask;
+    search_range(low, largest, kFloor, &bit, &prefix, &mask);
+    const auto word = [&](int i) { return buf[i]; };
+    unsigned need = (unsigned)K;
+    bool found = false;
+    while (bit > kFloor && !found) {
+        const int bits = min(11, bit - kFloor);
+        bit -= bits;
+        digit_pass(S, hist, word, count, prefix, mask, 32 + bit, 1 << bits, need);
+        prefix |= (unsigned long long)S.digit << (32 + bit);
+        mask |= (unsigned long long)((1u << bits) - 1) << (32 + bit);
+        need = S.need;
+        found = S.in_bin == need;  // the whole bin belongs: everything from `prefix` up
+    }
+    if (!found) {
+        // equal logits: the lowest ids, two digits of the inverted id (the bits above are all ones).  A 16-bit
+        // logit's key ends in zeros, or in ones if it is negative or NaN
+        if (kShort && (!(prefix >> 63) || prefix >> 48 == 0xFFFFull)) prefix |= 0xFFFFull << 32;
+        prefix |= 0xFFF00000ull;
+        mask = ~0ull << 20;
+        for (int shift = 10; shift >= 0 && !found; shift -= 10) {
+            digit_pass(S, hist, word, count, prefix, mask, shift, 1024, need);
+            prefix |= (unsigned long long)S.digit << shift;
+            mask |= 1023ull << shift;
+            need = S.need;
+            found = S.in_bin == need;
+        }
+    }
+    // the words from `prefix` up, exactly K, to the front; a thread's words of a
+    // tile are read before the scan's barriers and written after them
+    unsigned kept = 0, least = 0xFFFFFFFFu;
+    for (int i0 = 0; i0 < count; i0 += kTile * kThreads) {
+        unsigned long long w[kTile];
+        unsigned keep = 0, all;
+#pragma unroll
+        for (int j = 0; j < kTile; ++j) {
+            const int i = i0 + j * kThreads + t;
+            if (i0 + j * kThreads >= count) break;
+            w[j] = i < count ? buf[i] : 0;
+            if (w[j] >= prefix) {
+                keep |= 1u << j;
+                least = min(least, (unsigned)(w[j] >> 32));
+            } else if (i < count) {
+                add(rest, key_logit((unsigned)(w[j] >> 32)), c);
+            }
+        }
+        unsigned at = kept + block_scan((unsigned)__popc(keep), S.warp, &all);
+#pragma unroll
+        for (int j = 0; j < kTile; ++j) {
+            if (i0 + j * kThreads >= count) break;
+            if (keep >> j & 1u) buf[at++] = w[j];
+        }
+        kept += all;
+    }
+    return {~block_max(~least, S.warp), rest};
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logits, long long ld, int V, int K,
@@ -316,8 +281,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
     const Vectors<T> x(logits + (size_t)n * ld + v0, min(V, v0 + chunk) - v0);
     const float c = kLog2e / temperature;
     const F2 cc = f2(c, c);
-    Selection<kShort> sel(S, buf, hist, K, c);
-
     // the groups: a thread's two vectors of each step
     unsigned largest = 0, lowest = 0xFFFFFFFFu;
     stream<kThreads, kAhead, kStages>(x, ring, [&](int i0, Vec16<T>* v) {
@@ -341,166 +304,235 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
         if (k) lowest = min(lowest, k);
     });
     const int groups = (x.last - x.first + kAhead * kThreads - 1) / (kAhead * kThreads) * kThreads;
-    largest = block_max(largest, S.warp);
-    lowest = ~block_max(~lowest, S.warp);
-    // fewer groups than K: every group is read again
-    if (x.last - x.first >= K * kAhead) sel.bound_by(keys, groups, kShort ? lowest & 0xFFFF0000u : lowest, largest);
+
+    // The bound.  For a K well below the number of threads the K-th largest of
+    // the threads' maxima does: K elements reach it, and in a row without order
+    // about -ln(1 - K / kThreads) kThreads do.  Else the K-th largest of the
+    // groups'; with fewer groups than K every group is read again.
+    unsigned bound = 0;
+    {
+        __syncthreads();  // the ring is free
+        for (int i = t; i < kBins; i += kThreads) hist[i] = 0;
+        unsigned* maxima = hist + kBins;
+        maxima[t] = largest;
+        const bool by_threads = K <= kThreads * 3 / 4;
+        lowest = ~block_max(by_threads ? ~largest : ~lowest, S.warp);
+        largest = block_max(largest, S.warp);
+        if (by_threads)
+            bound = bound_by(S, hist, maxima, kThreads, K, lowest, largest);
+        else if (x.last - x.first >= K * kAhead)
+            bound = bound_by(S, hist, keys, groups, K, kShort ? lowest & 0xFFFF0000u : lowest, largest);
+        if (kShort) bound &= 0xFFFF0000u;
+    }
 
     // the groups below the bound are in the rest; the others' list, a warp's share after another's
+    MaxSum r = empty_set();
     int listed;
     {
         const int share = (groups / kThreads) * 32, g0 = warp * share;  // a multiple of 32 groups per warp
-        MaxSum r = empty_set();
+        // a group's maximum from its key (its low half: see Key)
+        const auto maximum = [&](unsigned k) {
+            return clamp_max(-FLT_MAX, key_logit(kShort && !(k >> 31) ? k | 0xFFFFu : k));
+        };
         int mine = 0;
+        unsigned most = 0;
         for (int g = g0 + lane; g < g0 + share; g += 32) {
             const unsigned k = whole<T>(keys[g]);
-            const bool in = k != 0 && k >= sel.bound;
-            mine += __popc(__ballot_sync(0xffffffffu, in));
-            if (!in && k != 0) {
-                // the group's maximum back from its key (its low half: see Key)
-                const unsigned full = kShort && !(k >> 31) ? k | 0xFFFFu : k;
-                r = join(r, MaxSum{clamp_max(-FLT_MAX, key_logit(full)), sums[g]}, c);
-            }
+            const bool in = k != 0 && k >= bound;
+            mine += in;
+            if (!in) most = max(most, k);
         }
-        sel.rest = r;
-        unsigned all;
-        unsigned at = block_scan(lane == 0 ? (unsigned)mine : 0u, S.warp, &all);
-        at = __shfl_sync(0xffffffffu, at, 0);
+        unsigned all, at = block_scan((unsigned)mine, S.warp, &all);  // this thread's first place
         listed = (int)all;
+        r.m = most ? maximum(most) : -FLT_MAX;
         for (int g = g0 + lane; g < g0 + share; g += 32) {
             const unsigned k = whole<T>(keys[g]);
-            const bool in = k != 0 && k >= sel.bound;
-            const unsigned who = __ballot_sync(0xffffffffu, in);
-            if (in) list[at + __popc(who & ((1u << lane) - 1u))] = (uint16_t)g;
-            at += __popc(who);
+            if (k == 0) continue;
+            if (k >= bound) list[at++] = (uint16_t)g;
+            else r.s += sums[g] * ex2((maximum(k) - r.m) * c);
         }
     }
     __syncthreads();
+
+    unsigned most = 0;  // largest key of this thread's words
+    int count = 0;      // words in the buffer
+    const auto reduce = [&] {  // the buffer's best K
+        if (count <= K) return;
+        const unsigned top_key_seen = block_max(most, S.warp);
+        const Selected got = select<kShort>(S, buf, hist, count, K, bound, top_key_seen, r, c);
+        bound = got.bound;
+        r = got.rest;
+        count = K;
+    };
+    // Takes `n` words of this thread: kStep in all, or as many as `fits` said.
+    const auto fits = [&](int words) { return count + words <= K + kDue + kStep; };
+    const auto take = [&](unsigned n_words, auto&& write) {
+        unsigned all;
+        const unsigned at = block_scan(n_words, S.warp, &all);
+        if (n_words) write(buf + count + at);
+        count += (int)all;
+        if (count > K + kDue) {
+            __syncthreads();
+            reduce();
+        }
+    };
     for (int l0 = 0; l0 < listed; l0 += kThreads) {
         const bool in = l0 + t < listed;
-        Vec16<T> v[kAhead];
+        Vec16<T> v[kAhead], kept[kAhead];
         int at[kAhead];  // element of the slice at which the vector begins
         unsigned pass = 0;
-        if (in) {
-            const int g = list[l0 + t], i0 = x.first + g / kThreads * (kAhead * kThreads) + g % kThreads;
+        const unsigned inf = kShort ? 0xFF80FF80u : 0xFF800000u;
+        const int g = in ? list[l0 + t] : 0;
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const int i = i0 + j * kThreads;
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = x.first + g / kThreads * (kAhead * kThreads) + g % kThreads + j * kThreads;
+            at[j] = i * kPer - x.phase;
+            v[j].q = make_uint4(inf, inf, inf, inf);
+            if (in && i < x.last) {
+                v[j].q = x.vec()[i];
                 at[j] = i * kPer - x.phase;
-                if (i < x.last) v[j].q = x.vec()[i];
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) {
+                    const float2 f = halves(v[j].pair(e / 2));
+                    if (top_key(e & 1 ? f.y : f.x) >= bound) pass |= 1u << (j * kPer + e);
+                }
             }
+            kept[j] = v[j];
+            strike(v[j], pass >> (j * kPer) & ((1u << kPer) - 1u));
+        }
+        {  // what does not reach the bound
+            float m = v[0].top();
+            if (pass) most = max(most, top_key(kept[0].top_nan()));
+#pragma unroll
+            for (int j = 1; j < kAhead; ++j) {
+                m = fmaxf(m, v[j].top());
+                if (pass) most = max(most, top_key(kept[j].top_nan()));
+            }
+            MaxSum o = {clamp_max(-FLT_MAX, m), 0.f};
+            const F2 minus = f2(-o.m, -o.m);
+            F2 s = f2(0.f, 0.f);
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
-                if (i0 + j * kThreads < x.last)
 #pragma unroll
-                    for (int e = 0; e < kPer; ++e) {
-                        const float2 f = halves(v[j].pair(e / 2));
-                        const float y = e & 1 ? f.y : f.x;
-                        const unsigned k = top_key(y);
-                        if (k >= sel.bound) {
-                            pass |= 1u << (j * kPer + e);
-                            sel.most = max(sel.most, k);
-                        } else {
-                            add(sel.rest, y, c);
-                        }
-                    }
+                for (int e = 0; e < P; ++e) s = add2(s, ex2x2(mul2(add2(v[j].pair(e), minus), cc)));
+            const float2 h = halves(s);
+            o.s = h.x + h.y;
+            if (in) r = join(r, o, c);
         }
         // the words of elements [lo, hi) of the groups
-        auto write = [&](unsigned long long* to, int lo, int hi) {
+        const auto write = [&](unsigned long long* to, int lo, int hi) {
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
 #pragma unroll
                 for (int e = 0; e < kPer; ++e) {
                     const int b = j * kPer + e;
                     if (b >= lo && b < hi && (pass >> b & 1u)) {
-                        const float2 f = halves(v[j].pair(e / 2));
+                        const float2 f = halves(kept[j].pair(e / 2));
                         *to++ = word_of(top_key(e & 1 ? f.y : f.x), (unsigned)(v0 + at[j] + e));
                     }
                 }
         };
         // all at once where they are sure to fit, else four elements of each group at a time
         const int takers = __syncthreads_count(pass != 0);
-        if (sel.fits(takers * kG)) {
-            sel.take((unsigned)__popc(pass), [&](unsigned long long* to) { write(to, 0, kG); });
+        if (fits(takers * kG)) {
+            take((unsigned)__popc(pass), [&](unsigned long long* to) { write(to, 0, kG); });
         } else {
 #pragma unroll 1
             for (int b = 0; b < kG; b += kStep / kThreads) {
                 const unsigned some = pass >> b & ((1u << (kStep / kThreads)) - 1u);
-                sel.take((unsigned)__popc(some), [&](unsigned long long* to) { write(to, b, b + kStep / kThreads); });
+                take((unsigned)__popc(some), [&](unsigned long long* to) { write(to, b, b + kStep / kThreads); });
             }
         }
     }
     {  // the elements beside the whole vectors
         const int at = t < 2 * kPer ? x.beside(t) : x.n;
-        sel.one(at < x.n, at < x.n ? to_f32(x.src[at]) : 0.f, (unsigned)(v0 + at));
+        const float y = at < x.n ? to_f32(x.src[at]) : 0.f;
+        const unsigned k = at < x.n ? top_key(y) : 0u;
+        const bool pass = k != 0 && k >= bound;
+        if (pass) most = max(most, k);
+        else if (k) add(r, y, c);
+        take(pass, [&](unsigned long long* to) { *to = word_of(k, (unsigned)(v0 + at)); });
     }
     __syncthreads();
-    sel.select();
+    reduce();
 
     if (size > 1) {
-        if (t == 0) S.count = sel.count;
+        if (t == 0) S.count = count;
         cluster_barrier();
         if (rank == 0) {
             // the other slices' words, four per thread at once
-            constexpr int kWords = 4;
-            const int most = min(K, chunk), words = (size - 1) * most;
+            constexpr int kWords = kStep / kThreads;
+            const int each = min(K, chunk), words = (size - 1) * each;
             for (int i0 = 0; i0 < words; i0 += kWords * kThreads) {
                 unsigned long long w[kWords];
                 unsigned pass = 0;
 #pragma unroll
                 for (int j = 0; j < kWords; ++j) {
-                    const int i = i0 + j * kThreads + t, r = 1 + i / most;
+                    const int i = i0 + j * kThreads + t, from = 1 + i / each;
                     w[j] = 0;
-                    if (i < words && i % most < *cluster.map_shared_rank(&S.count, r))
-                        w[j] = cluster.map_shared_rank(buf, r)[i % most];
+                    if (i < words && i % each < *cluster.map_shared_rank(&S.count, from))
+                        w[j] = cluster.map_shared_rank(buf, from)[i % each];
                 }
 #pragma unroll
                 for (int j = 0; j < kWords; ++j) {
                     const unsigned k = (unsigned)(w[j] >> 32);  // 0: no word
                     if (k == 0) continue;
-                    if (k >= sel.bound) {
+                    if (k >= bound) {
                         pass |= 1u << j;
-                        sel.most = max(sel.most, k);
+                        most = max(most, k);
                     } else {
-                        add(sel.rest, key_logit(k), sel.c);
+                        add(r, key_logit(k), c);
                     }
                 }
-                sel.take((unsigned)__popc(pass), [&](unsigned long long* to) {
+                take((unsigned)__popc(pass), [&](unsigned long long* to) {
 #pragma unroll
                     for (int j = 0; j < kWords; ++j)
                         if (pass >> j & 1u) *to++ = w[j];
                 });
             }
             __syncthreads();
-            sel.select();
+            reduce();
         }
     }
     // the CTA's rest
     {
-        MaxSum r = sel.rest;
         const float m = warp_max(r.m);
-        r.s = warp_sum(r.s * ex2((r.m - m) * sel.c));
+        r.s = warp_sum(r.s * ex2((r.m - m) * c));
         if (lane == 0) S.part[warp] = {m, r.s};
         __syncthreads();
-        if (t == 0) {
-            r = S.part[0];
-            for (int w = 1; w < kWarps; ++w) r = join(r, S.part[w], sel.c);
-            S.rest = r;
+        if (warp == 0) {
+            r = lane < kWarps ? S.part[lane] : empty_set();
+            const float all = warp_max(r.m);
+            r.s = warp_sum(r.s * ex2((r.m - all) * c));
+            if (lane == 0) S.rest = {all, r.s};
         }
     }
     if (size > 1) {
         cluster_barrier();
         if (rank == 0 && t == 0) {
-            MaxSum r = S.rest;
-            for (int i = 1; i < size; ++i) r = join(r, *cluster.map_shared_rank(&S.rest, i), sel.c);
-            S.rest = r;
+            MaxSum whole_row = S.rest;
+            for (int i = 1; i < size; ++i) whole_row = join(whole_row, *cluster.map_shared_rank(&S.rest, i), c);
+            S.rest = whole_row;
         }
         cluster_barrier();  // the others' shared memory was read
         if (rank != 0) return;
     }
     if (t == 0) rest[n] = S.rest.s == 0.f ? -INFINITY : S.rest.m / temperature + logf(S.rest.s);
 
-    // ascending ids: a bit per id, counted in front of each thread's words of bits
+    if (K <= kFew) {  // ascending ids: a word's place is the number of lower ids
+        if (t - lane >= K) return;
+        const unsigned long long w = t < K ? buf[t] : 0;
+        const unsigned id = word_id(w);
+        int place = 0;
+#pragma unroll 8
+        for (int i = 0; i < K; ++i) place += word_id(buf[i]) < id;
+        if (t < K) {
+            ids[(size_t)n * K + place] = (int32_t)id;
+            top[(size_t)n * K + place] = key_logit((unsigned)(w >> 32));
+        }
+        return;
+    }
+    // many: a bit per id, counted in front of each thread's words of bits
     unsigned* bits = hist + kBins;  // over the list and the groups
     unsigned* before = hist;
     const int words = (V + 31) / 32, per = (words + kThreads - 1) / kThreads;
