@@ -36,13 +36,13 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kAhead = 2;
+constexpr int kAhead = 4;
 constexpr int kStages = 2;
 constexpr size_t kRingBytes = (size_t)kThreads * kAhead * kStages * 16;
 constexpr int kBins = 2048;
-constexpr int kFew = 256;    // a record whose ids are ordered by counting
+constexpr int kFew = 64;     // a record whose ids are ordered by counting
 constexpr int kDue = 512;    // words beyond K that make a select due
-constexpr int kStep = 2048;  // words that are sure to fit then: four per thread
+constexpr int kStep = 1024;  // words that are sure to fit then: two per thread
 constexpr size_t kMaxSmem = 224 * 1024;  // of a CTA, beside its static variables
 
 __device__ __forceinline__ unsigned top_key(float x) { return x != x ? 0xFFFFFFFFu : ord_f32(x); }
@@ -56,13 +56,15 @@ template <typename T>
 struct Group {
     static constexpr int kElems = kAhead * Vec16<T>::kElems;
 };
-// a key without the bits that a logit of this type cannot have
+// a group's maximum as it is stored: the logits' own type
 template <typename T>
-using Key = typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type;
-// The 16-bit keys drop a half of zeros, or of ones in negative numbers' and
-// NaN's keys: the order is the same, and a bound loses nothing by the zeros.
+using Raw = typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type;
 template <typename T>
-__device__ __forceinline__ unsigned whole(Key<T> k) { return sizeof(T) == 2 ? (unsigned)k << 16 : (unsigned)k; }
+__device__ __forceinline__ Raw<T> to_raw(float m) {
+    return (Raw<T>)(sizeof(T) == 2 ? __float_as_uint(m) >> 16 : __float_as_uint(m));
+}
+__device__ __forceinline__ float from_raw(uint16_t r) { return __uint_as_float((unsigned)r << 16); }
+__device__ __forceinline__ float from_raw(uint32_t r) { return __uint_as_float(r); }
 
 constexpr int kTile = 8;  // words per thread that a select moves at once
 
@@ -74,6 +76,15 @@ struct TopShared {
     MaxSum rest;   // the CTA's rest
     int count;     // the CTA's words
 };
+
+// element e of a vector
+__device__ __forceinline__ float element(const Vec16<float>& v, int e) {
+    return __uint_as_float(e < 2 ? (e == 0 ? v.q.x : v.q.y) : (e == 2 ? v.q.z : v.q.w));
+}
+__device__ __forceinline__ float element(const Vec16<__nv_bfloat16>& v, int e) {
+    const unsigned w = e < 4 ? (e < 2 ? v.q.x : v.q.y) : (e < 6 ? v.q.z : v.q.w);
+    return __uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16);
+}
 
 // Exclusive scan of one value per thread; *total gets the sum.
 __device__ __forceinline__ unsigned block_scan(unsigned x, unsigned* warp_tot, unsigned* total) {
@@ -108,19 +119,20 @@ __device__ __forceinline__ unsigned block_max(unsigned x, unsigned* warp_tot) {
     return x;
 }
 
-// Shared memory of a slice of `elems` elements: its groups, in whole steps of
-// the stream; the ring, later the histogram and the list of groups; the groups'
-// sums and keys.  Behind them: the buffer of K + kDue + kStep words.
+// Shared memory of a slice of `elems` elements: the ring of the stream, in whose
+// place come the histogram, the buffer of K + kDue + kStep words and the list of
+// groups; behind it the groups' sums and maxima, in whose place comes a bit per id.
 template <typename T>
 __host__ __device__ constexpr int groups_of(int elems) {
     return (elems / Group<T>::kElems + kThreads) / kThreads * kThreads;  // one vector more than elems if unaligned
 }
-__host__ __device__ constexpr size_t ring_bytes(int groups) {
-    const size_t later = (size_t)kBins * 4 + (size_t)groups * 2;
-    return kRingBytes > later ? kRingBytes : later;
+__host__ __device__ constexpr size_t words_bytes(int K) { return (size_t)(K + kDue + kStep) * 8; }
+__host__ __device__ constexpr size_t front_bytes(int groups, int K) {
+    const size_t later = (size_t)kBins * 4 + words_bytes(K) + (size_t)groups * 2;
+    return ((kRingBytes > later ? kRingBytes : later) + 15) / 16 * 16;
 }
 template <typename T>
-__host__ __device__ constexpr size_t group_bytes(int groups) { return (size_t)groups * (4 + sizeof(Key<T>)); }
+__host__ __device__ constexpr size_t group_bytes(int groups) { return (size_t)groups * (4 + sizeof(Raw<T>)); }
 
 // The digit of the `need`-th largest among the words word(0..n-1) that match
 // prefix under mask, its count and what remains to be found in it, to S.  All
@@ -129,7 +141,7 @@ template <typename F>
 __device__ __forceinline__ void digit_pass(TopShared& S, unsigned* hist, F&& word, int n, unsigned long long prefix,
                                            unsigned long long mask, int shift, int bins, unsigned need) {
     const int t = threadIdx.x;
-#pragma unroll 4
+#pragma unroll 2
     for (int i = t; i < n; i += kThreads) {
         const unsigned long long w = word(i);
         if ((w & mask) == prefix) atomicAdd(&hist[(unsigned)(w >> shift) & (unsigned)(bins - 1)], 1u);
@@ -162,11 +174,12 @@ __device__ __forceinline__ void search_range(unsigned low, unsigned largest, int
     *prefix = ((unsigned long long)largest << 32) & *mask;
 }
 
-// A bound for the K largest of n keys: the K-th largest, or a little less.
-template <typename KeyT>
-__device__ __noinline__ unsigned bound_by(TopShared& S, unsigned* hist, const KeyT* keys, int n, int K, unsigned lowest,
+// A bound for the K largest of n logits: the K-th largest's key, or a little
+// less.  All keys lie in [lowest, largest].
+template <bool kShort, typename R>
+__device__ __noinline__ unsigned bound_by(TopShared& S, unsigned* hist, const R* raw, int n, int K, unsigned lowest,
                                           unsigned largest) {
-    constexpr int kFloor = sizeof(KeyT) == 2 ? 16 : 0;
+    constexpr int kFloor = kShort ? 16 : 0;
     int bit;
     unsigned long long prefix, mask;
     search_range(lowest, largest, kFloor, &bit, &prefix, &mask);
@@ -174,8 +187,8 @@ __device__ __noinline__ unsigned bound_by(TopShared& S, unsigned* hist, const Ke
     while (bit > kFloor) {
         const int bits = min(11, bit - kFloor);
         bit -= bits;
-        digit_pass(S, hist, [&](int i) { return (unsigned long long)keys[i] << (sizeof(KeyT) == 2 ? 48 : 32); }, n,
-                   prefix, mask, 32 + bit, 1 << bits, need);
+        digit_pass(S, hist, [&](int i) { return (unsigned long long)top_key(from_raw(raw[i])) << 32; }, n, prefix, mask,
+                   32 + bit, 1 << bits, need);
         prefix |= (unsigned long long)S.digit << (32 + bit);
         mask |= (unsigned long long)((1u << bits) - 1) << (32 + bit);
         need = S.need;
@@ -260,35 +273,32 @@ __device__ __noinline__ Selected select(TopShared& S, unsigned long long* buf, u
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logits, long long ld, int V, int K,
                                                      float temperature, int32_t* __restrict__ ids,
-                                                     float* __restrict__ top, float* __restrict__ rest, int chunk, int front) {
+                                                     float* __restrict__ top, float* __restrict__ rest, int chunk) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ TopShared S;
     constexpr bool kShort = sizeof(T) == 2;
-    constexpr int kPer = Vec16<T>::kElems, P = kPer / 2, kG = Group<T>::kElems;
+    constexpr int kPer = Vec16<T>::kElems, P = kPer / 2;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
     const int n = blockIdx.x / size, t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    // shared memory: the ring of the stream (then the list of groups and the
-    // histogram), the groups' sums and keys, the buffer of words
-    uint4* ring = reinterpret_cast<uint4*>(smem);
     unsigned* hist = reinterpret_cast<unsigned*>(smem);
-    uint16_t* list = reinterpret_cast<uint16_t*>(hist + kBins);
+    unsigned long long* buf = reinterpret_cast<unsigned long long*>(hist + kBins);
+    uint16_t* list = reinterpret_cast<uint16_t*>(smem + kBins * 4 + words_bytes(K));
     const int most_groups = groups_of<T>(chunk);
-    float* sums = reinterpret_cast<float*>(smem + ring_bytes(most_groups));
-    Key<T>* keys = reinterpret_cast<Key<T>*>(sums + most_groups);
-    unsigned long long* buf = reinterpret_cast<unsigned long long*>(smem + front);
+    float* sums = reinterpret_cast<float*>(smem + front_bytes(most_groups, K));
+    Raw<T>* maxima = reinterpret_cast<Raw<T>*>(sums + most_groups);
     const int v0 = min(V, rank * chunk);
     const Vectors<T> x(logits + (size_t)n * ld + v0, min(V, v0 + chunk) - v0);
     const float c = kLog2e / temperature;
     const F2 cc = f2(c, c);
-    // the groups: a thread's two vectors of each step
-    unsigned largest = 0, lowest = 0xFFFFFFFFu;
-    stream<kThreads, kAhead, kStages>(x, ring, [&](int i0, Vec16<T>* v) {
+
+    // the groups: a thread's vectors of a step, kThreads groups a step (-inf where there is nothing)
+    float largest_here = -INFINITY;
+    int at_group = t;
+    stream<kThreads, kAhead, kStages>(x, reinterpret_cast<uint4*>(smem), [&](int, Vec16<T>* v) {
         float m = v[0].top_nan();
 #pragma unroll
         for (int j = 1; j < kAhead; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(v[j].top_nan()));
-        const int g = (i0 - t - x.first) / kAhead + t;  // kThreads groups a step
-        const unsigned k = i0 < x.last ? top_key(m) : 0u;
         // exponentials on the group's own scale
         const float at = clamp_max(-FLT_MAX, m);
         const F2 minus = f2(-at, -at);
@@ -298,12 +308,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
 #pragma unroll
             for (int e = 0; e < P; ++e) s = add2(s, ex2x2(mul2(add2(v[j].pair(e), minus), cc)));
         const float2 h = halves(s);
-        sums[g] = h.x + h.y;
-        keys[g] = (Key<T>)(kShort ? k >> 16 : k);
-        largest = max(largest, k);
-        if (k) lowest = min(lowest, k);
+        sums[at_group] = h.x + h.y;
+        maxima[at_group] = to_raw<T>(m);
+        at_group += kThreads;
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(largest_here) : "f"(m));
     });
-    const int groups = (x.last - x.first + kAhead * kThreads - 1) / (kAhead * kThreads) * kThreads;
+    const int groups = at_group - t;
+    __syncthreads();  // the ring is free, the groups are there
 
     // The bound.  For a K well below the number of threads the K-th largest of
     // the threads' maxima does: K elements reach it, and in a row without order
@@ -311,45 +322,47 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
     // groups'; with fewer groups than K every group is read again.
     unsigned bound = 0;
     {
-        __syncthreads();  // the ring is free
         for (int i = t; i < kBins; i += kThreads) hist[i] = 0;
-        unsigned* maxima = hist + kBins;
-        maxima[t] = largest;
         const bool by_threads = K <= kThreads * 3 / 4;
-        lowest = ~block_max(by_threads ? ~largest : ~lowest, S.warp);
-        largest = block_max(largest, S.warp);
+        unsigned lowest = top_key(largest_here);
+        const unsigned largest = block_max(lowest, S.warp);
+        uint32_t* all = reinterpret_cast<uint32_t*>(buf);
+        if (by_threads) {
+            all[t] = __float_as_uint(largest_here);
+        } else {
+            for (int g = t; g < groups; g += kThreads) lowest = min(lowest, top_key(from_raw(maxima[g])));
+        }
+        lowest = ~block_max(~lowest, S.warp);
         if (by_threads)
-            bound = bound_by(S, hist, maxima, kThreads, K, lowest, largest);
+            bound = bound_by<kShort>(S, hist, all, kThreads, K, lowest, largest);
         else if (x.last - x.first >= K * kAhead)
-            bound = bound_by(S, hist, keys, groups, K, kShort ? lowest & 0xFFFF0000u : lowest, largest);
+            bound = bound_by<kShort>(S, hist, maxima, groups, K, lowest, largest);
         if (kShort) bound &= 0xFFFF0000u;
+        bound = min(bound, 0xFF800000u);  // +inf: a NaN is never below the bound
     }
+    const float bound_logit = bound ? unord_f32(bound) : -INFINITY;  // what reaches the bound is not below this
 
-    // the groups below the bound are in the rest; the others' list, a warp's share after another's
+    // the groups below the bound are in the rest; the others' list, a thread's after another's
     MaxSum r = empty_set();
     int listed;
     {
-        const int share = (groups / kThreads) * 32, g0 = warp * share;  // a multiple of 32 groups per warp
-        // a group's maximum from its key (its low half: see Key)
-        const auto maximum = [&](unsigned k) {
-            return clamp_max(-FLT_MAX, key_logit(kShort && !(k >> 31) ? k | 0xFFFFu : k));
-        };
         int mine = 0;
-        unsigned most = 0;
-        for (int g = g0 + lane; g < g0 + share; g += 32) {
-            const unsigned k = whole<T>(keys[g]);
-            const bool in = k != 0 && k >= bound;
+        float m = -INFINITY;
+#pragma unroll 2
+        for (int g = t; g < groups; g += kThreads) {
+            const float y = from_raw(maxima[g]);
+            const bool in = !(y < bound_logit);
             mine += in;
-            if (!in) most = max(most, k);
+            if (!in) m = fmaxf(m, y);
         }
         unsigned all, at = block_scan((unsigned)mine, S.warp, &all);  // this thread's first place
         listed = (int)all;
-        r.m = most ? maximum(most) : -FLT_MAX;
-        for (int g = g0 + lane; g < g0 + share; g += 32) {
-            const unsigned k = whole<T>(keys[g]);
-            if (k == 0) continue;
-            if (k >= bound) list[at++] = (uint16_t)g;
-            else r.s += sums[g] * ex2((maximum(k) - r.m) * c);
+        r.m = clamp_max(-FLT_MAX, m);
+#pragma unroll 2
+        for (int g = t; g < groups; g += kThreads) {
+            const float y = from_raw(maxima[g]);
+            if (!(y < bound_logit)) list[at++] = (uint16_t)g;
+            else r.s += sums[g] * ex2((clamp_max(-FLT_MAX, y) - r.m) * c);
         }
     }
     __syncthreads();
@@ -376,71 +389,61 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
             reduce();
         }
     };
-    for (int l0 = 0; l0 < listed; l0 += kThreads) {
-        const bool in = l0 + t < listed;
-        Vec16<T> v[kAhead], kept[kAhead];
-        int at[kAhead];  // element of the slice at which the vector begins
-        unsigned pass = 0;
+    // the listed groups again, a vector per thread
+#pragma unroll 1
+    for (int l0 = 0; l0 < listed * kAhead; l0 += kThreads) {
+        const int l = l0 + t;
+        Vec16<T> v;
         const unsigned inf = kShort ? 0xFF80FF80u : 0xFF800000u;
-        const int g = in ? list[l0 + t] : 0;
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const int i = x.first + g / kThreads * (kAhead * kThreads) + g % kThreads + j * kThreads;
-            at[j] = i * kPer - x.phase;
-            v[j].q = make_uint4(inf, inf, inf, inf);
-            if (in && i < x.last) {
-                v[j].q = x.vec()[i];
-                at[j] = i * kPer - x.phase;
+        v.q = make_uint4(inf, inf, inf, inf);
+        unsigned pass = 0;
+        int first = 0;  // element of the slice at which the vector begins
+        if (l < listed * kAhead) {
+            const int g = list[l / kAhead];
+            const int i = x.first + g / kThreads * (kAhead * kThreads) + g % kThreads + l % kAhead * kThreads;
+            first = i * kPer - x.phase;
+            if (i < x.last) {
+                v.q = x.vec()[i];
 #pragma unroll
                 for (int e = 0; e < kPer; ++e) {
-                    const float2 f = halves(v[j].pair(e / 2));
-                    if (top_key(e & 1 ? f.y : f.x) >= bound) pass |= 1u << (j * kPer + e);
+                    const float2 f = halves(v.pair(e / 2));
+                    if (!((e & 1 ? f.y : f.x) < bound_logit)) pass |= 1u << e;
                 }
             }
-            kept[j] = v[j];
-            strike(v[j], pass >> (j * kPer) & ((1u << kPer) - 1u));
+        }
+        const Vec16<T> whole = v;
+        if (pass) {
+            most = max(most, top_key(v.top_nan()));
+            strike(v, pass);
         }
         {  // what does not reach the bound
-            float m = v[0].top();
-            if (pass) most = max(most, top_key(kept[0].top_nan()));
-#pragma unroll
-            for (int j = 1; j < kAhead; ++j) {
-                m = fmaxf(m, v[j].top());
-                if (pass) most = max(most, top_key(kept[j].top_nan()));
-            }
-            MaxSum o = {clamp_max(-FLT_MAX, m), 0.f};
+            MaxSum o = {clamp_max(-FLT_MAX, v.top()), 0.f};
             const F2 minus = f2(-o.m, -o.m);
             F2 s = f2(0.f, 0.f);
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-                for (int e = 0; e < P; ++e) s = add2(s, ex2x2(mul2(add2(v[j].pair(e), minus), cc)));
+            for (int e = 0; e < P; ++e) s = add2(s, ex2x2(mul2(add2(v.pair(e), minus), cc)));
             const float2 h = halves(s);
             o.s = h.x + h.y;
-            if (in) r = join(r, o, c);
+            r = join(r, o, c);
         }
-        // the words of elements [lo, hi) of the groups
-        const auto write = [&](unsigned long long* to, int lo, int hi) {
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) {
-                    const int b = j * kPer + e;
-                    if (b >= lo && b < hi && (pass >> b & 1u)) {
-                        const float2 f = halves(kept[j].pair(e / 2));
-                        *to++ = word_of(top_key(e & 1 ? f.y : f.x), (unsigned)(v0 + at[j] + e));
-                    }
-                }
+        // the words of the elements that `some` names
+        const auto write = [&](unsigned long long* to, unsigned some) {
+            while (some) {
+                const int e = __ffs((int)some) - 1;
+                some &= some - 1;
+                *to++ = word_of(top_key(element(whole, e)), (unsigned)(v0 + first + e));
+            }
         };
-        // all at once where they are sure to fit, else four elements of each group at a time
+        // all at once where they are sure to fit, else two elements of each vector at a time
         const int takers = __syncthreads_count(pass != 0);
-        if (fits(takers * kG)) {
-            take((unsigned)__popc(pass), [&](unsigned long long* to) { write(to, 0, kG); });
+        if (fits(takers * kPer)) {
+            take((unsigned)__popc(pass), [&](unsigned long long* to) { write(to, pass); });
         } else {
+            constexpr int kSome = kStep / kThreads;
 #pragma unroll 1
-            for (int b = 0; b < kG; b += kStep / kThreads) {
-                const unsigned some = pass >> b & ((1u << (kStep / kThreads)) - 1u);
-                take((unsigned)__popc(some), [&](unsigned long long* to) { write(to, b, b + kStep / kThreads); });
+            for (int b = 0; b < kPer; b += kSome) {
+                const unsigned some = pass & (((1u << kSome) - 1u) << b);
+                take((unsigned)__popc(some), [&](unsigned long long* to) { write(to, some); });
             }
         }
     }
@@ -533,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
         return;
     }
     // many: a bit per id, counted in front of each thread's words of bits
-    unsigned* bits = hist + kBins;  // over the list and the groups
+    unsigned* bits = reinterpret_cast<unsigned*>(sums);  // over the groups
     unsigned* before = hist;
     const int words = (V + 31) / 32, per = (words + kThreads - 1) / kThreads;
     for (int i = t; i < per * kThreads; i += kThreads) bits[i] = 0;
@@ -565,17 +568,13 @@ cudaError_t launch(domino_train_ctx* c, const void* x, long long ld, int n, int 
     auto slice = [&](int parts) { return ((V + parts - 1) / parts + 63) / 64 * 64; };
     // few rows: spread them while the slices stay longer than what they keep
     while (size < kMaxCluster && (long long)n * size < 2 * c->num_sms && slice(2 * size) >= 2 * K + 2048) size *= 2;
-    // in front of the words: what the stream and the selection use, later a bit per id
-    const size_t bits = (size_t)kBins * 4 + (size_t)((V + 31) / 32 + kThreads) * 4;
-    const size_t words = (size_t)(K + kDue + kStep) * 8;
-    size_t front;
+    const size_t bits = (size_t)((V + 31) / 32 + kThreads) * 4;
+    size_t smem;
     for (;; size *= 2) {
         const int groups = groups_of<T>(slice(size));
-        front = ring_bytes(groups) + group_bytes<T>(groups);
-        if (front < bits) front = (bits + 15) / 16 * 16;
-        if (size == kMaxCluster || front + words <= kMaxSmem) break;
+        smem = front_bytes(groups, K) + (group_bytes<T>(groups) > bits ? group_bytes<T>(groups) : bits);
+        if (size == kMaxCluster || smem <= kMaxSmem) break;
     }
-    const size_t smem = front + words;
     auto kern = k_top<T>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -583,8 +582,7 @@ cudaError_t launch(domino_train_ctx* c, const void* x, long long ld, int n, int 
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = cluster_config((unsigned)n * size, kThreads, size, smem, st, &attr);
     c->last_launches = 1;
-    return cudaLaunchKernelEx(&cfg, kern, static_cast<const T*>(x), ld, V, K, temperature, ids, top, rest, slice(size),
-                              (int)front);
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<const T*>(x), ld, V, K, temperature, ids, top, rest, slice(size));
 }
 
 }  // namespace
