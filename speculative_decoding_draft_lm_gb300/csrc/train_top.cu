@@ -43,6 +43,10 @@ constexpr int kBins = 2048;
 constexpr int kFew = 64;     // a record whose ids are ordered by counting
 constexpr int kDue = 512;    // words beyond K that make a select due
 constexpr int kStep = 1024;  // words that are sure to fit then: two per thread
+#ifndef TOP_SPREAD
+#define TOP_SPREAD 8
+#endif
+constexpr int kSpread = TOP_SPREAD;
 constexpr size_t kMaxSmem = 224 * 1024;  // of a CTA, beside its static variables
 
 __device__ __forceinline__ unsigned top_key(float x) { return x != x ? 0xFFFFFFFFu : ord_f32(x); }
@@ -66,15 +70,16 @@ __device__ __forceinline__ Raw<T> to_raw(float m) {
 __device__ __forceinline__ float from_raw(uint16_t r) { return __uint_as_float((unsigned)r << 16); }
 __device__ __forceinline__ float from_raw(uint32_t r) { return __uint_as_float(r); }
 
+constexpr int kTies = 64;  // equal logits that are ordered by counting
 constexpr int kTile = 8;  // words per thread that a select moves at once
 
 struct TopShared {
     unsigned warp[kWarps];
-    unsigned digit, need, in_bin;
+    unsigned digit, need, in_bin, ties;
+    unsigned long long last;
     unsigned bound;
     MaxSum part[kWarps];
     MaxSum rest;   // the CTA's rest
-    int count;     // the CTA's words
 };
 
 // element e of a vector
@@ -216,7 +221,7 @@ __device__ __noinline__ Selected select(TopShared& S, unsigned long long* buf, u
     unsigned long long prefix, mask;
     search_range(low, largest, kFloor, &bit, &prefix, &mask);
     const auto word = [&](int i) { return buf[i]; };
-    unsigned need = (unsigned)K;
+    unsigned need = (unsigned)K, equal = (unsigned)count;  // words that match the prefix, and how many of them stay
     bool found = false;
     while (bit > kFloor && !found) {
         const int bits = min(11, bit - kFloor);
@@ -225,9 +230,29 @@ __device__ __noinline__ Selected select(TopShared& S, unsigned long long* buf, u
         prefix |= (unsigned long long)S.digit << (32 + bit);
         mask |= (unsigned long long)((1u << bits) - 1) << (32 + bit);
         need = S.need;
-        found = S.in_bin == need;  // the whole bin belongs: everything from `prefix` up
+        equal = S.in_bin;
+        found = equal == need;  // the whole bin belongs: everything from `prefix` up
     }
-    if (!found) {
+    if (!found && equal <= kTies) {
+        // a few equal logits: each one's place among them
+        if (t == 0) S.ties = 0;
+        __syncthreads();
+        unsigned long long* tie = reinterpret_cast<unsigned long long*>(hist);
+        for (int i = t; i < count; i += kThreads)
+            if ((buf[i] & mask) == prefix) tie[atomicAdd(&S.ties, 1u)] = buf[i];
+        __syncthreads();
+        const int ties = (int)S.ties;
+        if (t < ties) {
+            const unsigned long long w = tie[t];
+            unsigned place = 0;
+            for (int i = 0; i < ties; ++i) place += tie[i] > w;
+            if (place == need - 1) S.last = w;  // the last one to stay
+        }
+        __syncthreads();
+        prefix = S.last;
+        if (t < 2 * ties) hist[t] = 0;
+        __syncthreads();
+    } else if (!found) {
         // equal logits: the lowest ids, two digits of the inverted id (the bits above are all ones).  A 16-bit
         // logit's key ends in zeros, or in ones if it is negative or NaN
         if (kShort && (!(prefix >> 63) || prefix >> 48 == 0xFFFFull)) prefix |= 0xFFFFull << 32;
@@ -340,7 +365,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
         if (kShort) bound &= 0xFFFF0000u;
         bound = min(bound, 0xFF800000u);  // +inf: a NaN is never below the bound
     }
-    const float bound_logit = bound ? unord_f32(bound) : -INFINITY;  // what reaches the bound is not below this
+    // as a logit; keys up to -inf's: -inf; a 16-bit logit's key ends in ones if it is negative
+    const float bound_logit =
+        bound <= 0x007FFFFFu ? -INFINITY : unord_f32(kShort && !(bound >> 31) ? bound | 0xFFFFu : bound);
 
     // the groups below the bound are in the rest; the others' list, a thread's after another's
     MaxSum r = empty_set();
@@ -367,120 +394,160 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
     }
     __syncthreads();
 
+    // Words are made of what lies above the bound.  What equals it (masked rows
+    // are full of -inf, 16-bit rows of any value) only leaves a bit in `equal`,
+    // in the order of the ids, over the groups' place.
+    unsigned* equal = reinterpret_cast<unsigned*>(sums);
+    const int equal_words = (x.phase + x.n + 31) / 32;
+    for (int i = t; i < equal_words; i += kThreads) equal[i] = 0;
+    __syncthreads();
     unsigned most = 0;  // largest key of this thread's words
     int count = 0;      // words in the buffer
+    unsigned last = bound;  // no larger than the key of the K-th best
     const auto reduce = [&] {  // the buffer's best K
         if (count <= K) return;
         const unsigned top_key_seen = block_max(most, S.warp);
         const Selected got = select<kShort>(S, buf, hist, count, K, bound, top_key_seen, r, c);
-        bound = got.bound;
+        last = got.bound;
         r = got.rest;
         count = K;
     };
-    // Takes `n` words of this thread: kStep in all, or as many as `fits` said.
-    const auto fits = [&](int words) { return count + words <= K + kDue + kStep; };
+    // Takes `n` words of this thread; says no, and takes none, where the buffer
+    // has no room for all threads' words (for kStep it always has).
     const auto take = [&](unsigned n_words, auto&& write) {
         unsigned all;
         const unsigned at = block_scan(n_words, S.warp, &all);
+        if (count + (int)all > K + kDue + kStep) return false;
         if (n_words) write(buf + count + at);
         count += (int)all;
         if (count > K + kDue) {
             __syncthreads();
             reduce();
         }
+        return true;
     };
-    // the listed groups again, a vector per thread
+    // the listed groups again, a group per thread
 #pragma unroll 1
-    for (int l0 = 0; l0 < listed * kAhead; l0 += kThreads) {
-        const int l = l0 + t;
-        Vec16<T> v;
+    for (int l0 = 0; l0 < listed; l0 += kThreads) {
+        Vec16<T> v[kAhead];
         const unsigned inf = kShort ? 0xFF80FF80u : 0xFF800000u;
-        v.q = make_uint4(inf, inf, inf, inf);
+        const int g = l0 + t < listed ? list[l0 + t] : groups;
+        const int i0 = x.first + g / kThreads * (kAhead * kThreads) + g % kThreads;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            v[j].q = make_uint4(inf, inf, inf, inf);
+            if (i0 + j * kThreads < x.last) v[j].q = x.vec()[i0 + j * kThreads];
+        }
+        // a bit per element above the bound; those below it into the rest
         unsigned pass = 0;
-        int first = 0;  // element of the slice at which the vector begins
-        if (l < listed * kAhead) {
-            const int g = list[l / kAhead];
-            const int i = x.first + g / kThreads * (kAhead * kThreads) + g % kThreads + l % kAhead * kThreads;
-            first = i * kPer - x.phase;
-            if (i < x.last) {
-                v.q = x.vec()[i];
+        MaxSum o = empty_set();
+        F2 s = f2(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            unsigned in = 0, eq = 0;
+            if (i0 + j * kThreads < x.last) {
 #pragma unroll
                 for (int e = 0; e < kPer; ++e) {
-                    const float2 f = halves(v.pair(e / 2));
-                    if (!((e & 1 ? f.y : f.x) < bound_logit)) pass |= 1u << e;
+                    const float2 f = halves(v[j].pair(e / 2));
+                    const float y = e & 1 ? f.y : f.x;
+                    if (!(y <= bound_logit)) in |= 1u << e;
+                    if (y == bound_logit) eq |= 1u << e;
                 }
             }
-        }
-        const Vec16<T> whole = v;
-        if (pass) {
-            most = max(most, top_key(v.top_nan()));
-            strike(v, pass);
-        }
-        {  // what does not reach the bound
-            MaxSum o = {clamp_max(-FLT_MAX, v.top()), 0.f};
+            pass |= in << (j * kPer);
+            Vec16<T> others = v[j];
+            if (in | eq) {
+                if (in) most = max(most, top_key(v[j].top_nan()));
+                const int at = (i0 + j * kThreads) * kPer;
+                if (eq) atomicOr(&equal[at >> 5], eq << (at & 31));
+                strike(others, in | eq);
+            }
+            const float m = others.top();
+            if (m > o.m) {
+                const float to = clamp_max(o.m, m), f = ex2((o.m - to) * c);
+                s = mul2(s, f2(f, f));
+                o.m = to;
+            }
             const F2 minus = f2(-o.m, -o.m);
-            F2 s = f2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < P; ++e) s = add2(s, ex2x2(mul2(add2(v.pair(e), minus), cc)));
-            const float2 h = halves(s);
-            o.s = h.x + h.y;
-            r = join(r, o, c);
+            for (int e = 0; e < P; ++e) s = add2(s, ex2x2(mul2(add2(others.pair(e), minus), cc)));
         }
+        const float2 h = halves(s);
+        o.s = h.x + h.y;
+        r = join(r, o, c);
         // the words of the elements that `some` names
         const auto write = [&](unsigned long long* to, unsigned some) {
-            while (some) {
-                const int e = __ffs((int)some) - 1;
-                some &= some - 1;
-                *to++ = word_of(top_key(element(whole, e)), (unsigned)(v0 + first + e));
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                unsigned in = some >> (j * kPer) & ((1u << kPer) - 1u);
+                while (in) {
+                    const int e = __ffs((int)in) - 1;
+                    in &= in - 1;
+                    *to++ = word_of(top_key(element(v[j], e)),
+                                    (unsigned)(v0 + (i0 + j * kThreads) * kPer - x.phase + e));
+                }
             }
         };
-        // all at once where they are sure to fit, else two elements of each vector at a time
-        const int takers = __syncthreads_count(pass != 0);
-        if (fits(takers * kPer)) {
-            take((unsigned)__popc(pass), [&](unsigned long long* to) { write(to, pass); });
-        } else {
-            constexpr int kSome = kStep / kThreads;
+        if (!take((unsigned)__popc(pass), [&](unsigned long long* to) { write(to, pass); })) {
+            constexpr int kSome = kStep / kThreads;  // elements of each group at a time
 #pragma unroll 1
-            for (int b = 0; b < kPer; b += kSome) {
+            for (int b = 0; b < kAhead * kPer; b += kSome) {
                 const unsigned some = pass & (((1u << kSome) - 1u) << b);
                 take((unsigned)__popc(some), [&](unsigned long long* to) { write(to, some); });
             }
         }
     }
-    {  // the elements beside the whole vectors
+    if (x.n > (x.last - x.first) * kPer) {  // the elements beside the whole vectors
         const int at = t < 2 * kPer ? x.beside(t) : x.n;
         const float y = at < x.n ? to_f32(x.src[at]) : 0.f;
-        const unsigned k = at < x.n ? top_key(y) : 0u;
-        const bool pass = k != 0 && k >= bound;
-        if (pass) most = max(most, k);
-        else if (k) add(r, y, c);
-        take(pass, [&](unsigned long long* to) { *to = word_of(k, (unsigned)(v0 + at)); });
+        const bool in = at < x.n && !(y <= bound_logit);
+        if (in) most = max(most, top_key(y));
+        else if (at < x.n && y == bound_logit) atomicOr(&equal[(at + x.phase) >> 5], 1u << ((at + x.phase) & 31));
+        else if (at < x.n) add(r, y, c);
+        take(in, [&](unsigned long long* to) { *to = word_of(top_key(y), (unsigned)(v0 + at)); });
     }
     __syncthreads();
     reduce();
+    {  // of what equals the bound: the lowest ids, as many as the buffer still lacks
+        const int lack = K - count, per = (equal_words + kThreads - 1) / kThreads;
+        const int from = min(equal_words, t * per), to = min(equal_words, from + per);
+        unsigned mine = 0, all;
+        for (int i = from; i < to; ++i) mine += (unsigned)__popc(equal[i]);
+        int at = (int)block_scan(mine, S.warp, &all);
+        const int taken = min(lack, (int)all);
+        for (int i = from; i < to && at < taken; ++i)
+            for (unsigned m = equal[i]; m && at < taken; m &= m - 1)
+                buf[count + at++] = word_of(top_key(bound_logit), (unsigned)(v0 + i * 32 + __ffs((int)m) - 1 - x.phase));
+        if (taken) most = max(most, top_key(bound_logit));
+        if (t == 0 && (int)all > taken && bound_logit != -INFINITY)
+            r = join(r, MaxSum{clamp_max(-FLT_MAX, bound_logit), bound_logit == INFINITY ? INFINITY : (float)((int)all - taken)}, c);
+        count += taken;
+        __syncthreads();
+    }
 
     if (size > 1) {
-        if (t == 0) S.count = count;
         cluster_barrier();
         if (rank == 0) {
-            // the other slices' words, four per thread at once
+            // the other slices' words: a warp per slice, kWords of a lane at once
+            static_assert(kWarps >= kMaxCluster, "a warp per slice");
+            const unsigned beaten = count == K ? last : 0u;  // a higher id with this key comes after all K of this slice
             constexpr int kWords = kStep / kThreads;
-            const int each = min(K, chunk), words = (size - 1) * each;
-            for (int i0 = 0; i0 < words; i0 += kWords * kThreads) {
+            const int from = 1 + warp, each = min(K, chunk);
+            const int here = from < size ? min(K, min(V, (from + 1) * chunk) - min(V, from * chunk)) : 0;
+            const unsigned long long* theirs = cluster.map_shared_rank(buf, min(from, size - 1));
+            for (int i0 = 0; i0 < each; i0 += 32 * kWords) {
                 unsigned long long w[kWords];
                 unsigned pass = 0;
 #pragma unroll
                 for (int j = 0; j < kWords; ++j) {
-                    const int i = i0 + j * kThreads + t, from = 1 + i / each;
-                    w[j] = 0;
-                    if (i < words && i % each < *cluster.map_shared_rank(&S.count, from))
-                        w[j] = cluster.map_shared_rank(buf, from)[i % each];
+                    const int i = i0 + 32 * j + lane;
+                    w[j] = i < here ? theirs[i] : 0;
                 }
 #pragma unroll
                 for (int j = 0; j < kWords; ++j) {
                     const unsigned k = (unsigned)(w[j] >> 32);  // 0: no word
                     if (k == 0) continue;
-                    if (k >= bound) {
+                    if (k > beaten) {
                         pass |= 1u << j;
                         most = max(most, k);
                     } else {
@@ -567,7 +634,7 @@ cudaError_t launch(domino_train_ctx* c, const void* x, long long ld, int n, int 
     int size = 1;
     auto slice = [&](int parts) { return ((V + parts - 1) / parts + 63) / 64 * 64; };
     // few rows: spread them while the slices stay longer than what they keep
-    while (size < kMaxCluster && (long long)n * size < 2 * c->num_sms && slice(2 * size) >= 2 * K + 2048) size *= 2;
+    while (size < kSpread && (long long)n * size < 2 * c->num_sms && slice(2 * size) >= 2 * K + 2048) size *= 2;
     const size_t bits = (size_t)((V + 31) / 32 + kThreads) * 4;
     size_t smem;
     for (;; size *= 2) {

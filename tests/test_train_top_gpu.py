@@ -157,3 +157,34 @@ def test_refusals():
     with pytest.raises(ValueError):
         _train(100, dtype="fp16")
     assert tr.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("K", [5, 64, 300, 700])
+def test_ties_at_every_level(dtype, K):
+    """Few distinct logits, of either sign, so that the cut falls inside large
+    groups of equal ones; and masks that leave whole slices of a row empty."""
+    g = np.random.default_rng(K)
+    V = 40000
+    x = np.stack([g.integers(-3, 4, V) * 1.0, -g.integers(1, 4, V) * 0.5, np.where(g.random(V) < 0.01, 2.0, -1.5),
+                  np.where(g.random(V) < 0.9, -np.inf, g.normal(0, 1, V)), np.where(np.arange(V) < 39000, -np.inf, 1.0),
+                  np.where(np.arange(V) > 200, -np.inf, g.normal(0, 1, V)), np.full(V, -np.inf),
+                  np.where(g.random(V) < 0.5, np.nan, 3.0)])
+    for rows_at_once in (x, x[4:5]):  # one CTA a row or a few, and a cluster a row
+        check(rows(rows_at_once, TORCH[dtype], 1), K, 1.0)
+        check(rows(rows_at_once, TORCH[dtype], 0), K, 1.0)
+    check(rows(np.repeat(x, 60, 0), TORCH[dtype], 3), K, 1.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_clustered_candidates(dtype):
+    """The best logits all in one place, or all a vector apart: more words than the buffer holds."""
+    g = np.random.default_rng(9)
+    V = 70001
+    a, b = g.normal(0, 1, V), g.normal(0, 1, V)
+    a[30000:36000] += 20.0
+    b[::8] += 20.0
+    x = np.stack([a, b, np.sort(a), -np.sort(a)])
+    for K in (1, 50, 400, 3000):
+        check(rows(x, TORCH[dtype]), K, 1.0)
+    check(rows(np.repeat(x, 100, 0), TORCH[dtype]), 50, 1.0)
