@@ -82,13 +82,44 @@ struct TopShared {
     MaxSum rest;   // the CTA's rest
 };
 
-// element e of a vector
-__device__ __forceinline__ float element(const Vec16<float>& v, int e) {
-    return __uint_as_float(e < 2 ? (e == 0 ? v.q.x : v.q.y) : (e == 2 ? v.q.z : v.q.w));
+// A bit per element of v that lies above b (NaN does) and per element that
+// equals it; v without either (-inf in their places).  b is a logit of the type.
+__device__ __forceinline__ Vec16<float> above(const Vec16<float>& v, float b, unsigned* in, unsigned* eq) {
+    Vec16<float> r;
+    const auto one = [&](unsigned w, int e) {
+        const float y = __uint_as_float(w);
+        const bool gt = !(y <= b), same = y == b;
+        *in |= gt ? 1u << e : 0u;
+        *eq |= same ? 1u << e : 0u;
+        return gt || same ? 0xFF800000u : w;
+    };
+    r.q = make_uint4(one(v.q.x, 0), one(v.q.y, 1), one(v.q.z, 2), one(v.q.w, 3));
+    return r;
 }
-__device__ __forceinline__ float element(const Vec16<__nv_bfloat16>& v, int e) {
-    const unsigned w = e < 4 ? (e < 2 ? v.q.x : v.q.y) : (e < 6 ? v.q.z : v.q.w);
-    return __uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16);
+__device__ __forceinline__ Vec16<__nv_bfloat16> above(const Vec16<__nv_bfloat16>& v, float b, unsigned* in,
+                                                      unsigned* eq) {
+    Vec16<__nv_bfloat16> r;
+    const __nv_bfloat162 bb = __float2bfloat162_rn(b);
+    unsigned gt_bits = 0, eq_bits = 0;  // elements 0, 2, 4, 6 in bits 0..3, elements 1, 3, 5, 7 in bits 16..19
+    const auto two = [&](unsigned w, int k) {
+        const __nv_bfloat162 y = *reinterpret_cast<const __nv_bfloat162*>(&w);
+        const unsigned le = __hle2_mask(y, bb), same = __heq2_mask(y, bb);
+        gt_bits |= ~le & (0x00010001u << k);
+        eq_bits |= same & (0x00010001u << k);
+        return (w & le & ~same) | (0xFF80FF80u & (~le | same));
+    };
+    r.q = make_uint4(two(v.q.x, 0), two(v.q.y, 1), two(v.q.z, 2), two(v.q.w, 3));
+    // bit k of either half to bits 2k and 2k + 1
+    const auto spread = [](unsigned m) {
+        const unsigned lo = m & 15u, hi = m >> 16 & 15u;
+        const auto wide = [](unsigned x) { return (x & 1u) | (x & 2u) << 1 | (x & 4u) << 2 | (x & 8u) << 3; };
+        return wide(lo) | wide(hi) << 1;
+    };
+    if (gt_bits | eq_bits) {
+        *in = spread(gt_bits);
+        *eq = spread(eq_bits);
+    }
+    return r;
 }
 
 // Exclusive scan of one value per thread; *total gets the sum.
@@ -214,7 +245,7 @@ struct Selected {
 // threads, after a barrier, count > K.
 template <bool kShort>
 __device__ __noinline__ Selected select(TopShared& S, unsigned long long* buf, unsigned* hist, int count, int K,
-                                        unsigned low, unsigned largest, MaxSum rest, float c) {
+                                        unsigned low, unsigned largest, MaxSum rest, float c, bool want_bound) {
     const int t = threadIdx.x;
     constexpr int kFloor = kShort ? 16 : 0;
     int bit;
@@ -292,7 +323,7 @@ __device__ __noinline__ Selected select(TopShared& S, unsigned long long* buf, u
         }
         kept += all;
     }
-    return {~block_max(~least, S.warp), rest};
+    return {want_bound ? ~block_max(~least, S.warp) : 0u, rest};
 }
 
 template <typename T>
@@ -404,10 +435,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
     unsigned most = 0;  // largest key of this thread's words
     int count = 0;      // words in the buffer
     unsigned last = bound;  // no larger than the key of the K-th best
+    int equals = 0;         // this thread's elements that equal the bound
     const auto reduce = [&] {  // the buffer's best K
         if (count <= K) return;
         const unsigned top_key_seen = block_max(most, S.warp);
-        const Selected got = select<kShort>(S, buf, hist, count, K, bound, top_key_seen, r, c);
+        const Selected got = select<kShort>(S, buf, hist, count, K, bound, top_key_seen, r, c, size > 1);
         last = got.bound;
         r = got.rest;
         count = K;
@@ -444,23 +476,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
         F2 s = f2(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
+            if (l0 + t - lane >= listed) break;  // a warp without groups
             unsigned in = 0, eq = 0;
-            if (i0 + j * kThreads < x.last) {
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) {
-                    const float2 f = halves(v[j].pair(e / 2));
-                    const float y = e & 1 ? f.y : f.x;
-                    if (!(y <= bound_logit)) in |= 1u << e;
-                    if (y == bound_logit) eq |= 1u << e;
-                }
-            }
-            pass |= in << (j * kPer);
             Vec16<T> others = v[j];
-            if (in | eq) {
-                if (in) most = max(most, top_key(v[j].top_nan()));
+            if (i0 + j * kThreads < x.last) others = above(v[j], bound_logit, &in, &eq);
+            pass |= in << (j * kPer);
+            if (in) most = max(most, top_key(v[j].top_nan()));
+            if (eq) {
                 const int at = (i0 + j * kThreads) * kPer;
-                if (eq) atomicOr(&equal[at >> 5], eq << (at & 31));
-                strike(others, in | eq);
+                atomicOr(&equal[at >> 5], eq << (at & 31));
+                equals += __popc(eq);
             }
             const float m = others.top();
             if (m > o.m) {
@@ -475,17 +500,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
         const float2 h = halves(s);
         o.s = h.x + h.y;
         r = join(r, o, c);
-        // the words of the elements that `some` names
+        // the words of the elements that `some` names, their logits once more from memory
         const auto write = [&](unsigned long long* to, unsigned some) {
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                unsigned in = some >> (j * kPer) & ((1u << kPer) - 1u);
-                while (in) {
-                    const int e = __ffs((int)in) - 1;
-                    in &= in - 1;
-                    *to++ = word_of(top_key(element(v[j], e)),
-                                    (unsigned)(v0 + (i0 + j * kThreads) * kPer - x.phase + e));
-                }
+#pragma unroll 1
+            while (some) {
+                const int b = __ffs((int)some) - 1, at = (i0 + b / kPer * kThreads) * kPer - x.phase + b % kPer;
+                some &= some - 1;
+                *to++ = word_of(top_key(to_f32(x.src[at])), (unsigned)(v0 + at));
             }
         };
         if (!take((unsigned)__popc(pass), [&](unsigned long long* to) { write(to, pass); })) {
@@ -502,13 +523,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
         const float y = at < x.n ? to_f32(x.src[at]) : 0.f;
         const bool in = at < x.n && !(y <= bound_logit);
         if (in) most = max(most, top_key(y));
-        else if (at < x.n && y == bound_logit) atomicOr(&equal[(at + x.phase) >> 5], 1u << ((at + x.phase) & 31));
+        else if (at < x.n && y == bound_logit) atomicOr(&equal[(at + x.phase) >> 5], 1u << ((at + x.phase) & 31)), ++equals;
         else if (at < x.n) add(r, y, c);
         take(in, [&](unsigned long long* to) { *to = word_of(top_key(y), (unsigned)(v0 + at)); });
     }
     __syncthreads();
     reduce();
-    {  // of what equals the bound: the lowest ids, as many as the buffer still lacks
+    __syncthreads();
+    if (count < K) {  // of what equals the bound: the lowest ids, as many as the buffer still lacks
         const int lack = K - count, per = (equal_words + kThreads - 1) / kThreads;
         const int from = min(equal_words, t * per), to = min(equal_words, from + per);
         unsigned mine = 0, all;
@@ -519,11 +541,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
             for (unsigned m = equal[i]; m && at < taken; m &= m - 1)
                 buf[count + at++] = word_of(top_key(bound_logit), (unsigned)(v0 + i * 32 + __ffs((int)m) - 1 - x.phase));
         if (taken) most = max(most, top_key(bound_logit));
-        if (t == 0 && (int)all > taken && bound_logit != -INFINITY)
-            r = join(r, MaxSum{clamp_max(-FLT_MAX, bound_logit), bound_logit == INFINITY ? INFINITY : (float)((int)all - taken)}, c);
+        equals = t == 0 ? (int)all - taken : 0;
         count += taken;
         __syncthreads();
     }
+    if (equals && bound_logit != -INFINITY)
+        r = join(r, MaxSum{clamp_max(-FLT_MAX, bound_logit), bound_logit == INFINITY ? INFINITY : (float)equals}, c);
 
     if (size > 1) {
         cluster_barrier();
