@@ -104,7 +104,7 @@ int domino_train_init(domino_train_ctx** out, const domino_train_config* cfg, in
     c->named = (unsigned*)(base + o_named);
     c->claim = (unsigned*)(base + o_claim);
     if (cudaMemset(c->err, 0, sizeof(int)) != cudaSuccess || train::prepare_embed_kernels() != cudaSuccess ||
-        train::prepare_distill_kernels() != cudaSuccess ||
+        train::prepare_distill_kernels() != cudaSuccess || train::prepare_top_kernels() != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
         cudaFree(c->ws_base);
         free(c);

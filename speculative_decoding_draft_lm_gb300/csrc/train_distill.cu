@@ -597,9 +597,6 @@ cudaError_t launch_stream(domino_train_ctx* ctx, const DistillArgs& a, cudaStrea
     const int chunk = slice(size);
     const size_t smem = kRingBytes + (kForward ? (size_t)chunk / 8 + 8 : 0);
     auto kern = k_stream<T, kForward, kBackward>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = cluster_config((unsigned)a.n * size, kThreads, size, smem, st, &attr);
     ctx->last_launches = 1;
@@ -630,8 +627,6 @@ cudaError_t launch_step(domino_train_ctx* ctx, const DistillArgs& a, cudaStream_
     while (size < kMaxCluster && (long long)a.n * size < 2 * ctx->num_sms && slice(2 * size) >= 4096) size *= 2;
     const int chunk = slice(size);
     const size_t smem = (size_t)chunk * sizeof(T) + 32 + (size_t)chunk / 8;
-    cudaError_t e = cudaFuncSetAttribute(k_step<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kStepThreads);
     cfg.dynamicSmemBytes = smem;
@@ -648,7 +643,7 @@ cudaError_t launch_step(domino_train_ctx* ctx, const DistillArgs& a, cudaStream_
     int& most = ctx->step_clusters[size];
     if (most == 0) {
         cfg.gridDim = dim3(size);
-        e = cudaOccupancyMaxActiveClusters(&most, k_step<T>, &cfg);
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&most, k_step<T>, &cfg);
         if (e != cudaSuccess) return e;
         if (most < 1) most = 1;
     }
@@ -659,9 +654,12 @@ cudaError_t launch_step(domino_train_ctx* ctx, const DistillArgs& a, cudaStream_
 }  // namespace
 
 cudaError_t prepare_distill_kernels() {
-    cudaError_t e = cudaFuncSetAttribute(k_step<float>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_step<__nv_bfloat16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaError_t e = allow_all(k_step<float>);
+    if (e == cudaSuccess) e = allow_all(k_step<__nv_bfloat16>);
+    if (e == cudaSuccess) e = allow_all(k_stream<float, true, false>);
+    if (e == cudaSuccess) e = allow_all(k_stream<float, false, true>);
+    if (e == cudaSuccess) e = allow_all(k_stream<__nv_bfloat16, true, false>);
+    if (e == cudaSuccess) e = allow_all(k_stream<__nv_bfloat16, false, true>);
     return e;
 }
 

@@ -673,13 +673,9 @@ int max_sum_units(int max_tokens, int num_sms) {
 }
 
 cudaError_t prepare_embed_kernels() {
-    cudaError_t e = cudaFuncSetAttribute(k_sort_cluster, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sizeof(SortClusterShared));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_sort_cluster, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_sort_count, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SortShared));
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_sort_place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SortShared));
+    cudaError_t e = allow_all(k_sort_cluster);
+    if (e == cudaSuccess) e = allow_all(k_sort_count);
+    if (e == cudaSuccess) e = allow_all(k_sort_place);
     return e;
 }
 

@@ -25,6 +25,19 @@ struct domino_train_ctx {
 namespace domino {
 namespace train {
 
+// Lets a kernel be launched with all the shared memory an SM gives one block
+// and in clusters of 16, once for all launches.
+template <typename K>
+cudaError_t allow_all(K kern) {
+    cudaFuncAttributes a;
+    cudaError_t e = cudaFuncGetAttributes(&a, kern);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)(227 * 1024 - a.sharedSizeBytes));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return e;
+}
+
 constexpr int kSortTile = 8192;      // tokens per tile of the sort
 constexpr int kSortMaxCluster = 16;  // tiles that one cluster sorts
 constexpr int kSortMaxBins = 1024;   // two digits cover tokens up to DOMINO_TRAIN_MAX_V
@@ -46,6 +59,7 @@ struct DistillArgs {
     int* err;
 };
 
+cudaError_t prepare_top_kernels();
 cudaError_t launch_top(domino_train_ctx* c, const void* x, int dtype, long long ld, int n, int K, float temperature,
                        int32_t* ids, float* top, float* rest, cudaStream_t st);
 cudaError_t prepare_distill_kernels();

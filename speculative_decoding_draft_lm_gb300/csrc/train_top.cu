@@ -666,9 +666,6 @@ cudaError_t launch(domino_train_ctx* c, const void* x, long long ld, int n, int 
         if (size == kMaxCluster || smem <= kMaxSmem) break;
     }
     auto kern = k_top<T>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = cluster_config((unsigned)n * size, kThreads, size, smem, st, &attr);
     c->last_launches = 1;
@@ -676,6 +673,11 @@ cudaError_t launch(domino_train_ctx* c, const void* x, long long ld, int n, int 
 }
 
 }  // namespace
+
+cudaError_t prepare_top_kernels() {
+    const cudaError_t e = allow_all(k_top<float>);
+    return e == cudaSuccess ? allow_all(k_top<__nv_bfloat16>) : e;
+}
 
 cudaError_t launch_top(domino_train_ctx* c, const void* x, int dtype, long long ld, int n, int K, float temperature,
                        int32_t* ids, float* top, float* rest, cudaStream_t st) {

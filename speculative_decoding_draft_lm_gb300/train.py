@@ -9,7 +9,7 @@ from __future__ import annotations
 import ctypes
 
 from . import rollout as _r
-from .rollout import DOMINO_DTYPE_BF16, DOMINO_DTYPE_FP32, DOMINO_OK, DominoError, _check
+from .rollout import DOMINO_DTYPE_BF16, DOMINO_DTYPE_FP32, DominoError, _check
 
 DOMINO_TRAIN_MAX_V = 524288
 DOMINO_TRAIN_MAX_K = 8192
@@ -75,145 +75,153 @@ class DominoTrain:
         self.V, self.E, self.max_tokens, self.dtype = V, E, max_tokens, dtype
         self.device = torch.device("cuda", device)
         self.torch_dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
+        self._index, self._bf16, self._f32, self._i32 = device, torch.bfloat16, torch.float32, torch.int32
+        # the raw handle where torch gives it: a Stream object costs more than a launch
+        self._current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                       lambda i: torch.cuda.current_stream(i).cuda_stream)
         cfg = domino_train_config(V, E, max_tokens, DOMINO_DTYPE_BF16 if dtype == "bf16" else DOMINO_DTYPE_FP32)
         self.ctx = ctypes.c_void_p()
         _check(self._lib.domino_train_init(ctypes.byref(self.ctx), ctypes.byref(cfg), device), "domino_train_init")
 
-    # -- checks ----------------------------------------------------------------
+    # -- checks (on every call's path: plain integers and identities) -------------
 
     def _rows(self, t, cols, name, dtype=None, n=None):
         """Row stride of a [n, cols] tensor whose rows are contiguous."""
-        dtype = self.torch_dtype if dtype is None else dtype
-        if (t.dim() != 2 or t.shape[1] != cols or t.dtype != dtype or t.device != self.device
-                or (n is not None and t.shape[0] != n) or (cols > 1 and t.stride(1) != 1)
-                or (t.shape[0] > 1 and t.stride(0) < cols)):
-            raise ValueError(f"{name}: want CUDA [{'n' if n is None else n}, {cols}] {dtype} with contiguous rows on "
-                             f"{self.device}, got {tuple(t.shape)} {t.dtype} strides {t.stride()} on {t.device}")
-        return max(t.stride(0), cols)
+        shape = t.shape
+        if (len(shape) == 2 and shape[1] == cols and t.dtype is (dtype or self.torch_dtype)
+                and t.get_device() == self._index and (n is None or shape[0] == n)):
+            ld, inner = t.stride()
+            if inner == 1 or cols <= 1:
+                if ld >= cols:
+                    return ld
+                if shape[0] <= 1:
+                    return cols
+        raise ValueError(f"{name}: want CUDA [{'n' if n is None else n}, {cols}] {dtype or self.torch_dtype} with "
+                         f"contiguous rows on {self.device}, got {tuple(shape)} {t.dtype} strides {t.stride()} on "
+                         f"{t.device}")
 
     def _flat(self, t, shape, dtype, name):
-        """A contiguous tensor of exactly this shape and type."""
-        if t.shape != shape or t.dtype != dtype or t.device != self.device or not t.is_contiguous():
-            raise ValueError(f"{name}: want contiguous CUDA {tuple(shape)} {dtype} on {self.device}, "
-                             f"got {tuple(t.shape)} {t.dtype} on {t.device}")
-        return t.data_ptr()
+        """The address of a contiguous tensor of exactly this shape and type."""
+        if t.shape == shape and t.dtype is dtype and t.get_device() == self._index and t.is_contiguous():
+            return t.data_ptr()
+        raise ValueError(f"{name}: want contiguous CUDA {tuple(shape)} {dtype} on {self.device}, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
 
     def _stream(self, stream):
         if stream is None:
-            import torch
-            return torch.cuda.current_stream(self.device).cuda_stream
+            return self._current_stream(self._index)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
-    def _record(self, ids, top, rest, n):
+    def _new(self, shape, dtype):
         import torch
+        return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _record(self, ids, top, rest, n):
         if ids.dim() != 2:
             raise ValueError(f"ids: want [n, K], got {tuple(ids.shape)}")
         shape = (n, ids.shape[1])
-        return (self._flat(ids, shape, torch.int32, "ids"), self._flat(top, shape, torch.float32, "top"),
-                None if rest is None else self._flat(rest, (n,), torch.float32, "rest"), shape[1])
+        return (self._flat(ids, shape, self._i32, "ids"), self._flat(top, shape, self._f32, "top"),
+                None if rest is None else self._flat(rest, (n,), self._f32, "rest"), shape[1])
 
     # -- operators ---------------------------------------------------------------
 
     def top_logits(self, logits, K, temperature=1.0, out=None, stream=None):
         """(ids [n, K] int32 ascending, top [n, K], rest [n]) of a teacher's
         logits [n, V] (bf16 or fp32)."""
-        import torch
-        n = logits.shape[0]
-        if logits.dtype not in (torch.bfloat16, torch.float32):
-            raise ValueError(f"logits: want bfloat16 or float32, got {logits.dtype}")
-        ld = self._rows(logits, self.V, "logits", logits.dtype)
+        n, dtype = logits.shape[0], logits.dtype
+        if dtype is not self._bf16 and dtype is not self._f32:
+            raise ValueError(f"logits: want bfloat16 or float32, got {dtype}")
+        ld = self._rows(logits, self.V, "logits", dtype)
         if out is None:
-            out = (torch.empty((n, max(K, 0)), dtype=torch.int32, device=self.device),
-                   torch.empty((n, max(K, 0)), dtype=torch.float32, device=self.device),
-                   torch.empty((n,), dtype=torch.float32, device=self.device))
+            out = self._new((n, max(K, 0)), self._i32), self._new((n, max(K, 0)), self._f32), self._new((n,), self._f32)
         ids, top, rest = out
-        _check(self._lib.domino_train_top_logits(
-            self.ctx, logits.data_ptr(), DOMINO_DTYPE_BF16 if logits.dtype == torch.bfloat16 else DOMINO_DTYPE_FP32,
-            ld, n, K, temperature, self._flat(ids, (n, K), torch.int32, "ids"),
-            self._flat(top, (n, K), torch.float32, "top"), self._flat(rest, (n,), torch.float32, "rest"),
-            self._stream(stream)), "domino_train_top_logits")
+        status = self._lib.domino_train_top_logits(
+            self.ctx, logits.data_ptr(), DOMINO_DTYPE_BF16 if dtype is self._bf16 else DOMINO_DTYPE_FP32, ld, n, K,
+            temperature, self._flat(ids, (n, K), self._i32, "ids"), self._flat(top, (n, K), self._f32, "top"),
+            self._flat(rest, (n,), self._f32, "rest"), self._stream(stream))
+        if status:
+            raise DominoError(status, "domino_train_top_logits")
         return ids, top, rest
 
     def distill_forward(self, logits, ids, top, rest=None, temperature=1.0, out=None, stream=None):
         """(loss [n], stats [n, 8]) of student logits [n, V]; ``stats`` is for distill_backward."""
-        import torch
         n = logits.shape[0]
         ld = self._rows(logits, self.V, "logits")
         pi, pt, pr, K = self._record(ids, top, rest, n)
         if out is None:
-            out = (torch.empty((n,), dtype=torch.float32, device=self.device),
-                   torch.empty((n, DOMINO_TRAIN_STATS), dtype=torch.float32, device=self.device))
+            out = self._new((n,), self._f32), self._new((n, DOMINO_TRAIN_STATS), self._f32)
         loss, stats = out
-        _check(self._lib.domino_train_distill_forward(
-            self.ctx, logits.data_ptr(), ld, n, pi, pt, pr, K, temperature,
-            self._flat(loss, (n,), torch.float32, "loss"),
-            self._flat(stats, (n, DOMINO_TRAIN_STATS), torch.float32, "stats"), self._stream(stream)),
-            "domino_train_distill_forward")
+        status = self._lib.domino_train_distill_forward(
+            self.ctx, logits.data_ptr(), ld, n, pi, pt, pr, K, temperature, self._flat(loss, (n,), self._f32, "loss"),
+            self._flat(stats, (n, DOMINO_TRAIN_STATS), self._f32, "stats"), self._stream(stream))
+        if status:
+            raise DominoError(status, "domino_train_distill_forward")
         return loss, stats
 
     def distill_backward(self, logits, ids, top, rest, stats, dloss, temperature=1.0, out=None, stream=None):
         """dlogits [n, V] from the gradient dloss [n] by each row's loss."""
-        import torch
         n = logits.shape[0]
         ld = self._rows(logits, self.V, "logits")
         pi, pt, pr, K = self._record(ids, top, rest, n)
         if out is None:
-            out = torch.empty((n, self.V), dtype=self.torch_dtype, device=self.device)
-        ld_d = self._rows(out, self.V, "dlogits", n=n)
-        _check(self._lib.domino_train_distill_backward(
+            out = self._new((n, self.V), self.torch_dtype)
+        status = self._lib.domino_train_distill_backward(
             self.ctx, logits.data_ptr(), ld, n, pi, pt, pr, K, temperature,
-            self._flat(stats, (n, DOMINO_TRAIN_STATS), torch.float32, "stats"),
-            self._flat(dloss, (n,), torch.float32, "dloss"), out.data_ptr(), ld_d, self._stream(stream)),
-            "domino_train_distill_backward")
+            self._flat(stats, (n, DOMINO_TRAIN_STATS), self._f32, "stats"),
+            self._flat(dloss, (n,), self._f32, "dloss"), out.data_ptr(), self._rows(out, self.V, "dlogits", n=n),
+            self._stream(stream))
+        if status:
+            raise DominoError(status, "domino_train_distill_backward")
         return out
 
     def distill_step(self, logits, ids, top, rest, weight, temperature=1.0, out=None, stream=None):
         """(loss [n], dlogits [n, V]) in one call; dlogits is the gradient of sum(weight * loss)."""
-        import torch
         n = logits.shape[0]
         ld = self._rows(logits, self.V, "logits")
         pi, pt, pr, K = self._record(ids, top, rest, n)
         if out is None:
-            out = (torch.empty((n,), dtype=torch.float32, device=self.device),
-                   torch.empty((n, self.V), dtype=self.torch_dtype, device=self.device))
+            out = self._new((n,), self._f32), self._new((n, self.V), self.torch_dtype)
         loss, grad = out
-        ld_d = self._rows(grad, self.V, "dlogits", n=n)
-        _check(self._lib.domino_train_distill_step(
+        status = self._lib.domino_train_distill_step(
             self.ctx, logits.data_ptr(), ld, n, pi, pt, pr, K, temperature,
-            self._flat(weight, (n,), torch.float32, "weight"), self._flat(loss, (n,), torch.float32, "loss"),
-            grad.data_ptr(), ld_d, self._stream(stream)), "domino_train_distill_step")
+            self._flat(weight, (n,), self._f32, "weight"), self._flat(loss, (n,), self._f32, "loss"),
+            grad.data_ptr(), self._rows(grad, self.V, "dlogits", n=n), self._stream(stream))
+        if status:
+            raise DominoError(status, "domino_train_distill_step")
         return loss, grad
 
     def embed(self, table, tokens, scale=1.0, out=None, stream=None):
         """scale * table[tokens] for tokens [n] int32 (-1: zeros)."""
-        import torch
         n = tokens.shape[0]
         if out is None:
-            out = torch.empty((n, self.E), dtype=self.torch_dtype, device=self.device)
-        ld = self._rows(out, self.E, "out", n=n)
-        _check(self._lib.domino_train_embed(
+            out = self._new((n, self.E), self.torch_dtype)
+        status = self._lib.domino_train_embed(
             self.ctx, self._flat(table, (self.V, self.E), self.torch_dtype, "table"),
-            self._flat(tokens, (n,), torch.int32, "tokens"), n, scale, out.data_ptr(), ld, self._stream(stream)),
-            "domino_train_embed")
+            self._flat(tokens, (n,), self._i32, "tokens"), n, scale, out.data_ptr(),
+            self._rows(out, self.E, "out", n=n), self._stream(stream))
+        if status:
+            raise DominoError(status, "domino_train_embed")
         return out
 
     def embed_grad(self, dout, tokens, scale=1.0, out=None, grad_dtype=None, accumulate=False, stream=None):
         """dtable [V, E] (fp32 unless ``grad_dtype`` or ``out`` says bfloat16) from dout [n, E];
         ``accumulate`` adds to ``out``."""
-        import torch
         n = tokens.shape[0]
         ld = self._rows(dout, self.E, "dout", n=n)
         if out is None:
             if accumulate:
                 raise ValueError("accumulate needs out")
-            out = torch.empty((self.V, self.E), dtype=grad_dtype or torch.float32, device=self.device)
-        if out.dtype not in (torch.bfloat16, torch.float32) or grad_dtype not in (None, out.dtype):
-            raise ValueError(f"dtable: want bfloat16 or float32 (grad_dtype {grad_dtype}), got {out.dtype}")
-        _check(self._lib.domino_train_embed_grad(
-            self.ctx, dout.data_ptr(), ld, self._flat(tokens, (n,), torch.int32, "tokens"), n, scale,
-            self._flat(out, (self.V, self.E), out.dtype, "dtable"),
-            DOMINO_DTYPE_BF16 if out.dtype == torch.bfloat16 else DOMINO_DTYPE_FP32, int(bool(accumulate)),
-            self._stream(stream)), "domino_train_embed_grad")
+            out = self._new((self.V, self.E), grad_dtype or self._f32)
+        dtype = out.dtype
+        if (dtype is not self._bf16 and dtype is not self._f32) or (grad_dtype is not None and grad_dtype is not dtype):
+            raise ValueError(f"dtable: want bfloat16 or float32 (grad_dtype {grad_dtype}), got {dtype}")
+        status = self._lib.domino_train_embed_grad(
+            self.ctx, dout.data_ptr(), ld, self._flat(tokens, (n,), self._i32, "tokens"), n, scale,
+            self._flat(out, (self.V, self.E), dtype, "dtable"),
+            DOMINO_DTYPE_BF16 if dtype is self._bf16 else DOMINO_DTYPE_FP32, 1 if accumulate else 0,
+            self._stream(stream))
+        if status:
+            raise DominoError(status, "domino_train_embed_grad")
         return out
 
     # -- context -------------------------------------------------------------------
