@@ -85,42 +85,54 @@ __device__ __forceinline__ Sums warp_join(Sums u, float c) {
     return u;
 }
 
-// The row's statistics and loss from its sums; rest = -inf where there is none.
-__device__ Stats finish(const Sums& u, float rest, float inv_t, float c, float* loss) {
-    Stats st = {};
-    *loss = 0.f;
-    if (u.t.s == 0.f && rest == -INFINITY) return st;  // no target
-    // the teacher's two parts on the larger one's scale
-    float part = 1.f, part_r = 0.f, top = 0.f;  // top: the scale, kept apart where it is mt / T
-    bool top_is_t = true;
+// The teacher's two parts on the larger one's scale, e^(level): `part` times
+// t.s and part_r; rest = -inf where there is none.
+struct Teacher {
+    float part, part_r, inv_w;  // and the reciprocal of their sum
+    float d;                    // mt / T - rest
+};
+__device__ __forceinline__ Teacher teacher(const Sums& u, float rest, float inv_t) {
+    Teacher r = {1.f, 0.f, 0.f, INFINITY};
     if (rest != -INFINITY) {
-        const float d = u.t.s == 0.f ? -INFINITY : fmaf(u.t.m, inv_t, -rest);
-        if (d >= 0.f) {
-            part_r = ex2(-d * kLog2e);
-        } else {
-            part = ex2(d * kLog2e);  // NaN stays NaN
-            part_r = 1.f;
-            top = rest;
-            top_is_t = false;
-        }
+        r.d = u.t.s == 0.f ? -INFINITY : fmaf(u.t.m, inv_t, -rest);
+        const float e = ex2(-fabsf(r.d) * kLog2e);  // NaN stays NaN
+        r.part = r.d >= 0.f ? 1.f : e;
+        r.part_r = r.d >= 0.f ? e : 1.f;
     }
-    const float w = u.t.s * part + part_r, inv_w = 1.f / w;
-    const float pr = part_r * inv_w;
+    r.inv_w = 1.f / (u.t.s * r.part + r.part_r);
+    return r;
+}
+__device__ __forceinline__ bool has_target(const Sums& u, float rest) { return !(u.t.s == 0.f && rest == -INFINITY); }
+
+// What the gradient goes by, from the row's sums.
+__device__ __forceinline__ Stats finish(const Sums& u, float rest, float inv_t, float c) {
+    Stats st = {};
+    if (!has_target(u, rest)) return st;
+    const Teacher w = teacher(u, rest, inv_t);
+    const float pr = w.part_r * w.inv_w;
     const MaxSum x = join(u.s, u.o, c);
     st.has = 1.f;
     st.mt = u.t.m;
-    st.pt = part * inv_w;
+    st.pt = w.part * w.inv_w;
     st.mx = x.m;
     st.qx = 1.f / x.s;
     st.mo = u.o.m;
-    float l = rescaled(u.a, st.pt) + (top_is_t ? (x.m - u.t.m) * inv_t : fmaf(x.m, inv_t, -top)) + logf(x.s * inv_w);
     st.co = ex2((u.o.m - x.m) * c) * st.qx;
-    if (pr != 0.f) {
-        l -= pr * (fmaf(u.o.m, inv_t, -rest) + logf(u.o.s));
-        st.co = u.o.s == 0.f ? 0.f : st.co - pr / u.o.s;
-    }
-    *loss = l;
+    if (pr != 0.f) st.co = u.o.s == 0.f ? 0.f : st.co - pr / u.o.s;
     return st;
+}
+
+// The row's loss, from the same sums.
+__device__ __forceinline__ float row_loss(const Sums& u, float rest, float inv_t, float c) {
+    if (!has_target(u, rest)) return 0.f;
+    const Teacher w = teacher(u, rest, inv_t);
+    const float pr = w.part_r * w.inv_w;
+    const MaxSum x = join(u.s, u.o, c);
+    // the normalisers' ratio, their scales apart: exact where the record holds the larger part
+    float l = w.d >= 0.f ? (x.m - u.t.m) * inv_t : fmaf(x.m, inv_t, -rest);
+    l += rescaled(u.a, w.part * w.inv_w) + logf(x.s * w.inv_w);
+    if (pr != 0.f) l -= pr * (fmaf(u.o.m, inv_t, -rest) + logf(u.o.s));
+    return l;
 }
 
 // Whether entry k of the record takes part: a valid id, and its first place.
@@ -137,22 +149,13 @@ __device__ __noinline__ bool takes_part(const int32_t* ids, int k, int id, int V
 // A cluster of CTAs holds one row in shared memory, a slice each: bulk copies
 // bring it in, the sums and the gradient are two passes over shared memory, and
 // bulk copies take the gradient, written in place, out.  So the logits are read
-// once and the gradient written once, which is all the traffic there is.  A
-// slice is at most kSliceBytes, so that five CTAs share an SM and one's copies
-// run under another's arithmetic; with few rows the slices are smaller and the
-// row is spread over up to 16 SMs.
+// once and the gradient written once, which is all the traffic there is.  A CTA
+// has two such buffers: the next row comes in, and the last one's gradient
+// leaves, while a row is computed.
 //
 // Entries of the record are taken out of the slice (set to -inf) once their
 // logits are read, so that the first pass is a plain sum over the outside.
 
-#ifndef STREAM_KB
-#define STREAM_KB 160
-#define STREAM_THREADS 256
-#define STREAM_AHEAD 2
-#define STREAM_STAGES 3
-#define STREAM_MINB 5
-#define STREAM_WAVES 4
-#endif
 #ifndef SLICE_KB
 #define SLICE_KB 40
 #define STEP_THREADS 128
@@ -160,12 +163,13 @@ __device__ __noinline__ bool takes_part(const int32_t* ids, int k, int id, int V
 #define UNR 4
 #endif
 constexpr int kSliceBytes = SLICE_KB * 1024;
+constexpr unsigned kNone = 0xFFFFFFFFu;
 constexpr int kStepThreads = STEP_THREADS;
 constexpr int kStepWarps = kStepThreads / 32;
 struct StepShared {
     Sums part[2][kMaxCluster * kStepWarps];  // every warp of the row, by the row's parity
     Stats row;
-    unsigned long long bar;
+    unsigned long long bar;  // the row's copy has come
     int twice, abort;
 };
 
@@ -192,9 +196,10 @@ struct Slice {
     }
     // fills what the copies leave of the first and last vectors: the row's own
     // elements, and -inf where there are none
-    __device__ void load_edges() const {
+    __device__ void load_edges(int from = 0) const {  // by the threads from `from` on
         const int first = (int)(data - reinterpret_cast<T*>(vec)), per = 16 / (int)sizeof(T);
-        const int t = threadIdx.x;
+        const int t = (int)threadIdx.x - from;
+        if (t < 0) return;
         if (t < first) reinterpret_cast<T*>(vec)[t] = from_f32<T>(-INFINITY);
         if (t < head) data[t] = src[t];
         const int tail = n - head - body;
@@ -254,45 +259,73 @@ __global__ void __launch_bounds__(kStepThreads, MINB) k_step(DistillArgs p, int 
     __shared__ StepShared S;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, stride = gridDim.x / size;
     const float inv_t = 1.f / p.temperature, c = kLog2e / p.temperature;
-    unsigned* bits = reinterpret_cast<unsigned*>(smem + (size_t)chunk * sizeof(T) + 32);
+    const uint32_t buffer = (uint32_t)chunk * sizeof(T) + 32;
+    unsigned* bits = reinterpret_cast<unsigned*>(smem + buffer);
     const uint32_t bar = tc::smem_u32(&S.bar);
+    const auto slice = [&](int n) {
+        return Slice<T>(static_cast<const T*>(p.x) + (size_t)n * p.ld, p.V, chunk, rank, smem);
+    };
+    const auto request = [&](const Slice<T>& x) {  // one thread
+        const uint32_t bytes = (uint32_t)x.body * sizeof(T);
+        tc::mbar_arrive_expect_tx(bar, bytes);
+        if (bytes) tc::bulk_load(tc::smem_u32(x.data + x.head), x.src + x.head, bytes, bar, tc::policy_evict_first());
+    };
+    // what is read ahead of a row: its weight, its rest and this thread's first entry
+    struct Ahead {
+        float weight, rest, top;
+        int id;
+    };
+    const auto ahead = [&](int n) {
+        Ahead a = {0.f, -INFINITY, 0.f, -1};
+        if (n < p.n) {
+            a.weight = p.weight[n];
+            if (p.rest) a.rest = p.rest[n];
+            if (t < p.K) {
+                a.id = p.ids[(size_t)n * p.K + t];
+                a.top = p.top[(size_t)n * p.K + t];
+            }
+        }
+        return a;
+    };
+    int n = blockIdx.x / size;
+    Ahead now = ahead(n);
     if (t == 0) {
         tc::mbar_init(bar, 1);
         S.twice = S.abort = 0;
         tc::fence_barrier_init();
+        if (now.weight != 0.f) request(slice(n));
     }
+    if (now.weight != 0.f) slice(n).load_edges();
     for (int i = t; i < chunk / 32; i += kStepThreads) bits[i] = 0;
     cluster_barrier();  // every CTA of the cluster is running
-    uint32_t loaded = 0;  // parity of the next bulk load, and of the cluster's next exchange
-    for (int n = blockIdx.x / size; n < p.n; n += gridDim.x / size) {
-        const float weight = p.weight[n], rest = p.rest ? p.rest[n] : -INFINITY;
-        const Slice<T> x(static_cast<const T*>(p.x) + (size_t)n * p.ld, p.V, chunk, rank, smem);
+    uint32_t phase = 0;  // parity of the next copy and of the next exchange
+    for (; n < p.n; n += stride) {
+        const Ahead next = ahead(n + stride);
+        const Slice<T> x = slice(n);
         T* dx = static_cast<T*>(p.dx) + (size_t)n * p.ld_d + x.v0;
         float w = 0.f;
-        if (weight != 0.f) {
-            if (t == 0 && !S.abort) {
-                const uint32_t bytes = (uint32_t)x.body * sizeof(T);
-                tc::mbar_arrive_expect_tx(bar, bytes);
-                if (bytes)
-                    tc::bulk_load(tc::smem_u32(x.data + x.head), x.src + x.head, bytes, bar, tc::policy_evict_first());
-            }
+        if (now.weight != 0.f) {
             const int32_t* ids = p.ids + (size_t)n * p.K;
             const float* top = p.top + (size_t)n * p.K;
-            x.load_edges();
+            // entry k of the record (this thread's first is held): its place in the slice, or none
+            const auto place = [&](int id) {
+                const unsigned a = (unsigned)id - (unsigned)x.v0;
+                return a < (unsigned)x.n ? a : kNone;
+            };
 #pragma unroll 1
             for (int k = t; k < p.K; k += kStepThreads) {
-                const int id = ids[k];
-                const unsigned a = (unsigned)id - (unsigned)x.v0;
-                if (a < (unsigned)x.n) {
+                const int id = k == t ? now.id : ids[k];
+                const unsigned a = place(id);
+                if (a != kNone) {
                     const unsigned bit = 1u << (a & 31);
                     if (atomicOr(&bits[a >> 5], bit) & bit) S.twice = 1;
                 } else if (rank == 0 && id != -1 && (unsigned)id >= (unsigned)p.V) {
                     atomicOr(p.err, kErrBadToken);
                 }
             }
-            if (t == 0) tc::mbar_wait(bar, loaded, &S.abort, p.err);
+            if (t == 0) tc::mbar_wait(bar, phase, &S.abort, p.err);
             __syncthreads();
             const bool twice = S.twice != 0;
 
@@ -300,10 +333,10 @@ __global__ void __launch_bounds__(kStepThreads, MINB) k_step(DistillArgs p, int 
             float held = 0.f;  // the logit of this thread's first entry; later entries' are read again
 #pragma unroll 1
             for (int k = t; k < p.K; k += kStepThreads) {
-                const int id = ids[k];
-                const unsigned a = (unsigned)id - (unsigned)x.v0;
-                if (a >= (unsigned)x.n || (twice && !takes_part(ids, k, id, p.V, true))) continue;
-                const float tv = top[k], v = to_f32(x.data[a]);
+                const int id = k == t ? now.id : ids[k];
+                const unsigned a = place(id);
+                if (a == kNone || (twice && !takes_part(ids, k, id, p.V, true))) continue;
+                const float tv = k == t ? now.top : top[k], v = to_f32(x.data[a]);
                 x.data[a] = from_f32<T>(-INFINITY);  // no part of the outside
                 bits[a >> 5] = 0;
                 if (k == t) held = v;
@@ -323,23 +356,25 @@ __global__ void __launch_bounds__(kStepThreads, MINB) k_step(DistillArgs p, int 
             u.o = sum_vectors<T>(x.vec, x.nvec, c);
             u = warp_join(u, c);
             // every warp's sums to every CTA of the row
-            if (lane < size) *cluster.map_shared_rank(&S.part[loaded][rank * kStepWarps + warp], lane) = u;
+            if (lane < size) *cluster.map_shared_rank(&S.part[phase][rank * kStepWarps + warp], lane) = u;
             cluster_barrier();
             if (warp == 0) {
-                const Sums* part = S.part[loaded];
+                const Sums* part = S.part[phase];
                 u = part[min(lane, size * kStepWarps - 1)];
                 if (lane >= size * kStepWarps) u = {empty_set(), empty_set(), empty_set(), 0.f};
                 for (int i = lane + 32; i < size * kStepWarps; i += 32) u = join(u, part[i], c);
                 u = warp_join(u, c);
-                float loss;
-                const Stats st = finish(u, rest, inv_t, c, &loss);
+                const Stats st = finish(u, now.rest, inv_t, c);
                 if (lane == 0) S.row = st;
-                if (rank == 0 && lane == 0) p.loss[n] = loss;
             }
             __syncthreads();
-            loaded ^= 1;
+            phase ^= 1;
+            if (rank == 0 && warp == 0) {
+                const float loss = row_loss(u, now.rest, inv_t, c);
+                if (lane == 0) p.loss[n] = loss;
+            }
             const Stats st = S.row;
-            w = st.has == 0.f ? 0.f : weight * inv_t;
+            w = st.has == 0.f ? 0.f : now.weight * inv_t;
             if (w != 0.f) {
                 constexpr int P = Vec16<T>::kElems / 2;
                 const float wc = w * st.co;
@@ -355,16 +390,16 @@ __global__ void __launch_bounds__(kStepThreads, MINB) k_step(DistillArgs p, int 
                 __syncthreads();
 #pragma unroll 1
                 for (int k = t; k < p.K; k += kStepThreads) {
-                    const int id = ids[k];
-                    const unsigned a = (unsigned)id - (unsigned)x.v0;
-                    if (a >= (unsigned)x.n || (twice && !takes_part(ids, k, id, p.V, true))) continue;
-                    const float v = k == t ? held : to_f32(x.src[a]);
-                    const float q = st.qx * ex2((v - st.mx) * c), pk = st.pt * ex2((top[k] - st.mt) * c);
+                    const int id = k == t ? now.id : ids[k];
+                    const unsigned a = place(id);
+                    if (a == kNone || (twice && !takes_part(ids, k, id, p.V, true))) continue;
+                    const float tv = k == t ? now.top : top[k], v = k == t ? held : to_f32(x.src[a]);
+                    const float q = st.qx * ex2((v - st.mx) * c), pk = st.pt * ex2((tv - st.mt) * c);
                     x.data[a] = from_f32<T>(w * (q - pk));
                 }
             }
-        } else if (rank == 0 && t == 0) {
-            p.loss[n] = 0.f;
+        } else {
+            if (rank == 0 && t == 0) p.loss[n] = 0.f;
         }
         if (w == 0.f)
             for (int i = t; i < x.nvec; i += kStepThreads) x.vec[i] = make_uint4(0, 0, 0, 0);
@@ -376,21 +411,25 @@ __global__ void __launch_bounds__(kStepThreads, MINB) k_step(DistillArgs p, int 
             if (t < x.head) dx[t] = x.data[t];
             const int tail = x.n - x.head - x.body;
             if (t < tail) dx[x.head + x.body + t] = x.data[x.head + x.body + t];
-            if (t == 0 && x.body) {
-                bulk_store(dx + x.head, tc::smem_u32(x.data + x.head), (uint32_t)x.body * sizeof(T));
-                bulk_store_wait_read();
-            }
+            if (t == 0 && x.body) bulk_store(dx + x.head, tc::smem_u32(x.data + x.head), (uint32_t)x.body * sizeof(T));
         } else {
             for (int i = t; i < x.n; i += kStepThreads) dx[i] = x.data[i];
         }
-        __syncthreads();
+        now = next;
+        if (t == 0) bulk_store_wait_read();
+        __syncthreads();  // the buffer is free
+        if (now.weight != 0.f) {
+            const Slice<T> y = slice(n + stride);
+            if (t == 0 && !S.abort) request(y);
+            y.load_edges();
+        }
     }
-    // A CTA whose copy never came goes on through its cluster's exchanges, with
-    // meaningless data and without further copies, and gives the lost one a last
-    // chance to land before it leaves.
-    if (S.abort && t == 0) {
+    // A CTA whose copy never came has gone on through its cluster's exchanges,
+    // with meaningless data and without further copies; it gives the lost one a
+    // last chance to land before it leaves.
+    if (t == 0 && S.abort) {
         const unsigned long long t0 = tc::globaltimer();
-        while (!tc::mbar_try_wait(bar, loaded ^ 1) && tc::globaltimer() - t0 < 2000000ull) {
+        while (!tc::mbar_try_wait(bar, phase ^ 1) && tc::globaltimer() - t0 < 2000000ull) {
         }
     }
 }
@@ -403,10 +442,10 @@ __global__ void __launch_bounds__(kStepThreads, MINB) k_step(DistillArgs p, int 
 // element as if it were outside the record and then, after a barrier, the
 // entries again.  A row is one CTA's, or a cluster's where there are few rows.
 
-constexpr int kThreads = STREAM_THREADS;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kAhead = STREAM_AHEAD;
-constexpr int kStages = STREAM_STAGES;
+constexpr int kAhead = 2;
+constexpr int kStages = 3;
 constexpr size_t kRingBytes = (size_t)kThreads * kAhead * kStages * 16;
 
 struct StreamShared {
@@ -416,8 +455,8 @@ struct StreamShared {
 };
 
 template <typename T, bool kForward, bool kBackward>
-__global__ void __launch_bounds__(kThreads, STREAM_MINB) k_stream(DistillArgs p, int chunk) {
-    extern __shared__ __align__(16) uint8_t smem[];
+__global__ void __launch_bounds__(kThreads, 5) k_stream(DistillArgs p, int chunk) {
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ StreamShared S;
     uint4* ring = reinterpret_cast<uint4*>(smem);
     unsigned* bits = reinterpret_cast<unsigned*>(smem + kRingBytes);
@@ -523,9 +562,9 @@ __global__ void __launch_bounds__(kThreads, STREAM_MINB) k_stream(DistillArgs p,
             if (lane >= parts) u = {empty_set(), empty_set(), empty_set(), 0.f};
             for (int i = lane + 32; i < parts; i += 32) u = join(u, S.part[i], c);
             u = warp_join(u, c);
-            float loss;
-            st = finish(u, rest, inv_t, c, &loss);
+            st = finish(u, rest, inv_t, c);
             if (lane == 0) S.row = st;
+            const float loss = row_loss(u, rest, inv_t, c);
             if (rank == 0 && lane == 0) p.loss[n] = loss;
         }
         if (kBackward) {
@@ -592,8 +631,8 @@ template <typename T, bool kForward, bool kBackward>
 cudaError_t launch_stream(domino_train_ctx* ctx, const DistillArgs& a, cudaStream_t st) {
     int size = 1;
     auto slice = [&](int parts) { return ((a.V + parts - 1) / parts + 63) / 64 * 64; };
-    while (size < kMaxCluster && (long long)a.n * size < STREAM_WAVES * ctx->num_sms && slice(2 * size) >= 2048) size *= 2;
-    while (size < kMaxCluster && slice(size) * (int)sizeof(T) > STREAM_KB * 1024) size *= 2;
+    while (size < kMaxCluster && (long long)a.n * size < 4 * ctx->num_sms && slice(2 * size) >= 2048) size *= 2;
+    while (size < kMaxCluster && slice(size) * (int)sizeof(T) > 160 * 1024) size *= 2;
     const int chunk = slice(size);
     const size_t smem = kRingBytes + (kForward ? (size_t)chunk / 8 + 8 : 0);
     auto kern = k_stream<T, kForward, kBackward>;
