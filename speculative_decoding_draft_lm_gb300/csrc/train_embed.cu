@@ -23,7 +23,7 @@
 #include <cooperative_groups.h>
 
 #include "train_internal.h"
-#include "train_math.cuh"
+#include "train_stream.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -352,43 +352,40 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_place(const int32_t* __re
 // ---- zeros ---------------------------------------------------------------------
 
 constexpr int kMarkThreads = 1024;
-constexpr int kMarkBlocks = 16;   // slices of the vocabulary
+constexpr int kMarkBlocks = 8;
 constexpr int kFillThreads = 512;
 constexpr int kFillBlocksPerSm = 2;  // half of an SM's threads: the sort needs the others
 constexpr int kFillRows = 32;     // rows per claim: one word of the bits
 
-// A bit per row of the table that some token names (a block per slice of the
-// vocabulary, each scanning all tokens), and the claim counter of k_fill.
-__global__ void __launch_bounds__(kMarkThreads) k_mark(const int32_t* __restrict__ tokens, int n, int V, int words,
+// A bit per row of the table that some token names, and the claim counter of
+// k_fill.  One cluster: every CTA marks its share of the tokens in a copy of the
+// bits of its own, then puts together its slice of all copies.
+__global__ void __launch_bounds__(kMarkThreads) k_mark(const int32_t* __restrict__ tokens, int n, int V,
                                                        unsigned* __restrict__ named, unsigned* __restrict__ claim) {
     extern __shared__ unsigned bits[];
     pdl_trigger();
-    const int w0 = blockIdx.x * words, count = max(0, min(words, (V + 31) / 32 - w0));
-    const int v0 = w0 * 32;
-    for (int i = threadIdx.x; i < count; i += kMarkThreads) bits[i] = 0;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *claim = 0;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), words = (V + 31) / 32, t = threadIdx.x;
+    for (int i = t; i < words; i += kMarkThreads) bits[i] = 0;
+    if (rank == 0 && t == 0) *claim = 0;
     __syncthreads();
-    auto mark = [&](int tok) {
-        const unsigned r = (unsigned)tok - (unsigned)v0;  // a token below the slice wraps past it
-        if ((unsigned)tok >= (unsigned)V || r >= (unsigned)count * 32u) return;
-        const unsigned bit = 1u << (r & 31);
+#pragma unroll 4
+    for (int i = rank * kMarkThreads + t; i < n; i += kMarkBlocks * kMarkThreads) {
+        const int tok = tokens[i];
+        if ((unsigned)tok >= (unsigned)V) continue;
+        const unsigned bit = 1u << (tok & 31);
         // look first: a frequent token's thousands of places would queue at its word
-        if (!(reinterpret_cast<volatile unsigned*>(bits)[r >> 5] & bit)) atomicOr(&bits[r >> 5], bit);
-    };
-    const int head = min(n, (int)((16 - ((uintptr_t)tokens & 15)) & 15) / 4), quads = (n - head) / 4;
-    const int4* t4 = reinterpret_cast<const int4*>(tokens + head);
-#pragma unroll 8
-    for (int i = threadIdx.x; i < quads; i += kMarkThreads) {
-        const int4 t = t4[i];
-        mark(t.x);
-        mark(t.y);
-        mark(t.z);
-        mark(t.w);
+        if (!(reinterpret_cast<volatile unsigned*>(bits)[tok >> 5] & bit)) atomicOr(&bits[tok >> 5], bit);
     }
-    if ((int)threadIdx.x < head) mark(tokens[threadIdx.x]);
-    if ((int)threadIdx.x < n - head - 4 * quads) mark(tokens[head + 4 * quads + threadIdx.x]);
-    __syncthreads();
-    for (int i = threadIdx.x; i < count; i += kMarkThreads) named[w0 + i] = bits[i];
+    cluster.sync();
+    const int slice = (words + kMarkBlocks - 1) / kMarkBlocks, to = min(words, (rank + 1) * slice);
+    for (int i = rank * slice + t; i < to; i += kMarkThreads) {
+        unsigned w = 0;
+#pragma unroll
+        for (int r = 0; r < kMarkBlocks; ++r) w |= cluster.map_shared_rank(bits, r)[i];
+        named[i] = w;
+    }
+    cluster.sync();  // nobody leaves while its copy is read
 }
 
 // Zeros to the rows that no token names.  One wave of blocks that claims 32
@@ -625,9 +622,11 @@ cudaError_t launch_sort(domino_train_ctx* c, const int32_t* tokens, int n, bool 
 template <typename G>
 cudaError_t launch_fill(domino_train_ctx* c, const int32_t* tokens, int n, G* dtable, cudaStream_t st) {
     const int V = c->cfg.V, E = c->cfg.E;
-    const int all = (V + 31) / 32, words = (all + kMarkBlocks - 1) / kMarkBlocks;
-    k_mark<<<kMarkBlocks, kMarkThreads, (size_t)words * 4, st>>>(tokens, n, V, words, c->named, c->claim);
-    cudaError_t e = cudaGetLastError();
+    const int all = (V + 31) / 32;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg =
+        cluster_config(kMarkBlocks, kMarkThreads, kMarkBlocks, (size_t)all * 4, st, &attr);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_mark, tokens, n, V, c->named, c->claim);
     if (e != cudaSuccess) return e;
     const int most = c->num_sms * kFillBlocksPerSm, blocks = all < most ? all : most;
     const bool vec = ((uintptr_t)dtable & 15) == 0 && (size_t)E * sizeof(G) % 16 == 0;
@@ -676,6 +675,7 @@ cudaError_t prepare_embed_kernels() {
     cudaError_t e = allow_all(k_sort_cluster);
     if (e == cudaSuccess) e = allow_all(k_sort_count);
     if (e == cudaSuccess) e = allow_all(k_sort_place);
+    if (e == cudaSuccess) e = allow_all(k_mark);
     return e;
 }
 
