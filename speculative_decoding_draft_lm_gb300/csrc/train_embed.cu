@@ -142,13 +142,14 @@ __global__ void __launch_bounds__(kEmbedThreads) k_embed(const T* __restrict__ t
 // Two passes of a stable counting sort, low digit first.  A tile's tokens are
 // split into 32-token steps in their order, a warp's steps adjacent; a token's
 // place is (smaller digits) + (its digit in the tiles before) + (in the warps
-// before) + (in its warp before it), the last from a warp-wide match.  Tokens
+// before) + (in its warp before it), the last from ballots.  Tokens
 // outside [0, V) sort last, as V.
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortSteps = kSortTile / kSortThreads;  // tokens per thread
 static_assert(kSortTile % kSortThreads == 0 && kSortMaxBins <= kSortThreads, "one bin per thread");
+static_assert(kSortTile == 1 << 13, "the largest tile of a cluster's sort");
 
 struct SortShared {
     uint16_t warp[kSortWarps][kSortMaxBins];  // a warp's counts, then the tile's counts in the warps before it
@@ -185,8 +186,14 @@ __device__ void tile_count(SortShared& s, const uint32_t* key, unsigned* rank, i
     for (int j = 0; j < kSortSteps; ++j) {
         if (j >= steps) break;
         const bool in = tile_place(j, steps) < count;
-        const unsigned d = in ? key[j] >> shift & (unsigned)(bins - 1) : (unsigned)bins;
-        const unsigned peers = __match_any_sync(0xffffffffu, d);
+        const unsigned d = key[j] >> shift & (unsigned)(bins - 1);
+        // the lanes with the same digit, a ballot per bit (__match_any_sync took
+        // 3.3 K cycles a step of 32 warps)
+        unsigned peers = __ballot_sync(0xffffffffu, in);
+        for (int b = 1; b < bins; b <<= 1) {
+            const unsigned ones = __ballot_sync(0xffffffffu, (d & (unsigned)b) != 0);
+            peers &= d & (unsigned)b ? ones : ~ones;
+        }
         const unsigned below = __popc(peers & ((1u << lane) - 1u));
         if (in) rank[j] = s.warp[warp][d] + below;
         __syncwarp();
@@ -225,31 +232,34 @@ __device__ void tile_base(SortShared& s, unsigned before, unsigned all, int bins
     __syncthreads();
 }
 
-// All tokens in one cluster: a tile per CTA, exchanged through distributed
-// shared memory.  151,936 ids, 65,536 tokens: ??? us alone, hidden behind k_fill.
+// All tokens in one cluster: a tile of 2^log_tile tokens per CTA, exchanged
+// through distributed shared memory.  Alone, most of a pass are the scattered
+// stores, 32 sectors each, so the tokens are spread over up to 16 CTAs (65,536
+// tokens: 26 us against 38 us on 8; 8,192 tokens: 12 us; the tiled passes below
+// take 42 us for either).  Beside k_fill, whose stores crowd theirs out, full
+// tiles on fewer CTAs end earlier (the whole gradient of 65,536 tokens: 196 us
+// against 205 us).
 __global__ void __launch_bounds__(kSortThreads) k_sort_cluster(const int32_t* __restrict__ tokens, int n, int V,
-                                                               int digit, uint32_t* __restrict__ keys_out,
+                                                               int digit, int log_tile, uint32_t* __restrict__ keys_out,
                                                                int32_t* __restrict__ pos_out, int* err) {
     extern __shared__ __align__(16) uint8_t smem[];
     SortClusterShared& S = *reinterpret_cast<SortClusterShared*>(smem);
     cg::cluster_group cluster = cg::this_cluster();
     const int tiles = (int)cluster.num_blocks(), tile = (int)cluster.block_rank();
     const int warp = threadIdx.x >> 5, bins = 1 << digit;
-    const int count = max(0, min(kSortTile, n - tile * kSortTile)), steps = tile_steps(count);
+    const int count = max(0, min(1 << log_tile, n - (tile << log_tile))), steps = tile_steps(count);
     uint32_t key[kSortSteps];
-    int32_t pos[kSortSteps];
     unsigned rank[kSortSteps];
 #pragma unroll
     for (int j = 0; j < kSortSteps; ++j) {
         const int i = tile_place(j, steps);
-        key[j] = j < steps && i < count ? token_key(tokens[tile * kSortTile + i], V, err) : 0u;
-        pos[j] = tile * kSortTile + i;
+        key[j] = j < steps && i < count ? token_key(tokens[(tile << log_tile) + i], V, err) : 0u;
     }
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         const int shift = pass * digit;
         tile_count(S.s, key, rank, count, shift, bins);
-        cluster.sync();
+        cluster_barrier();
         unsigned before = 0, all = 0;
         if ((int)threadIdx.x < bins)
 #pragma unroll
@@ -264,22 +274,20 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_cluster(const int32_t* __
             if (j < steps && tile_place(j, steps) < count) {
                 const unsigned d = key[j] >> shift & (unsigned)(bins - 1);
                 const unsigned at = S.s.base[d] + S.s.warp[warp][d] + rank[j];
+                const int i = tile_place(j, steps);
                 if (pass == 0) {
-                    cluster.map_shared_rank(S.key, at / kSortTile)[at % kSortTile] = key[j];
-                    cluster.map_shared_rank(S.pos, at / kSortTile)[at % kSortTile] = pos[j];
+                    cluster.map_shared_rank(S.key, at >> log_tile)[at & ((1u << log_tile) - 1u)] = key[j];
+                    cluster.map_shared_rank(S.pos, at >> log_tile)[at & ((1u << log_tile) - 1u)] = (tile << log_tile) + i;
                 } else {
                     keys_out[at] = key[j];
-                    pos_out[at] = pos[j];
+                    pos_out[at] = S.pos[i];
                 }
             }
-        cluster.sync();  // the tile's new tokens are here; nobody reads these counts any more
+        cluster_barrier();  // the tile's new tokens are here; nobody reads these counts any more
         if (pass == 0) {
 #pragma unroll
             for (int j = 0; j < kSortSteps; ++j)
-                if (j < steps && tile_place(j, steps) < count) {
-                    key[j] = S.key[tile_place(j, steps)];
-                    pos[j] = S.pos[tile_place(j, steps)];
-                }
+                if (j < steps && tile_place(j, steps) < count) key[j] = S.key[tile_place(j, steps)];
         }
     }
     // launched beside k_fill (whose kernels before it are done and write nothing
@@ -377,7 +385,7 @@ __global__ void __launch_bounds__(kMarkThreads) k_mark(const int32_t* __restrict
         // look first: a frequent token's thousands of places would queue at its word
         if (!(reinterpret_cast<volatile unsigned*>(bits)[tok >> 5] & bit)) atomicOr(&bits[tok >> 5], bit);
     }
-    cluster.sync();
+    cluster_barrier();
     const int slice = (words + kMarkBlocks - 1) / kMarkBlocks, to = min(words, (rank + 1) * slice);
     for (int i = rank * slice + t; i < to; i += kMarkThreads) {
         unsigned w = 0;
@@ -385,7 +393,7 @@ __global__ void __launch_bounds__(kMarkThreads) k_mark(const int32_t* __restrict
         for (int r = 0; r < kMarkBlocks; ++r) w |= cluster.map_shared_rank(bits, r)[i];
         named[i] = w;
     }
-    cluster.sync();  // nobody leaves while its copy is read
+    cluster_barrier();  // nobody leaves while its copy is read
 }
 
 // Zeros to the rows that no token names.  One wave of blocks that claims 32
@@ -589,8 +597,9 @@ cudaError_t launch_sort(domino_train_ctx* c, const int32_t* tokens, int n, bool 
     while ((V >> bits) != 0) ++bits;  // keys 0..V
     const int digit = (bits + 1) / 2, bins = 1 << digit, tiles = (n + kSortTile - 1) / kSortTile;
     if (tiles <= kSortMaxCluster) {
-        int size = 1;
-        while (size < tiles) size *= 2;
+        int log_tile = beside ? 13 : 10, size = 1;
+        while ((n - 1) >> log_tile >= kSortMaxCluster) ++log_tile;
+        while (size << log_tile < n) size *= 2;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(size);
         cfg.blockDim = dim3(kSortThreads);
@@ -605,7 +614,7 @@ cudaError_t launch_sort(domino_train_ctx* c, const int32_t* tokens, int n, bool 
         cfg.attrs = attr;
         cfg.numAttrs = beside ? 2 : 1;
         c->last_launches += 1;
-        return cudaLaunchKernelEx(&cfg, k_sort_cluster, tokens, n, V, digit, c->keys[0], c->pos[0], c->err);
+        return cudaLaunchKernelEx(&cfg, k_sort_cluster, tokens, n, V, digit, log_tile, c->keys[0], c->pos[0], c->err);
     }
     for (int pass = 0; pass < 2; ++pass) {
         const int32_t* tok = pass == 0 ? tokens : nullptr;

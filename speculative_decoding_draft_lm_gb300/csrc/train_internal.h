@@ -38,7 +38,7 @@ cudaError_t allow_all(K kern) {
     return e;
 }
 
-constexpr int kSortTile = 8192;      // tokens per tile of the sort
+constexpr int kSortTile = 8192;      // most tokens per tile of the sort
 constexpr int kSortMaxCluster = 16;  // tiles that one cluster sorts
 constexpr int kSortMaxBins = 1024;   // two digits cover tokens up to DOMINO_TRAIN_MAX_V
 
