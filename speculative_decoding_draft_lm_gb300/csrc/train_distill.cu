@@ -156,15 +156,9 @@ __device__ __noinline__ bool takes_part(const int32_t* ids, int k, int id, int V
 // Entries of the record are taken out of the slice (set to -inf) once their
 // logits are read, so that the first pass is a plain sum over the outside.
 
-#ifndef SLICE_KB
-#define SLICE_KB 40
-#define STEP_THREADS 128
-#define MINB 5
-#define UNR 4
-#endif
-constexpr int kSliceBytes = SLICE_KB * 1024;
+constexpr int kSliceBytes = 40 * 1024;
 constexpr unsigned kNone = 0xFFFFFFFFu;
-constexpr int kStepThreads = STEP_THREADS;
+constexpr int kStepThreads = 128;
 constexpr int kStepWarps = kStepThreads / 32;
 struct StepShared {
     Sums part[2][kMaxCluster * kStepWarps];  // every warp of the row, by the row's parity
@@ -217,44 +211,49 @@ __device__ __forceinline__ void bulk_store_wait_read() {
     asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
-// Adds the values of shared vectors to a set, four vectors of a thread at once:
-// one look at their maximum, then the exponentials.
+// Adds U vectors to a set: one look at their maximum, then the exponentials.
+template <int U, typename T>
+__device__ __forceinline__ void add_vectors(float& m, F2& s, const Vec16<T>* v, float c, F2 cc) {
+    const float top = top_of<U>(v);
+    if (top > m) {
+        const float to = clamp_max(m, top), f = ex2((m - to) * c);
+        s = mul2(s, f2(f, f));
+        m = to;
+    }
+    const F2 minus = f2(-m, -m);
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int k = 0; k < Vec16<T>::kElems / 2; ++k) s = add2(s, ex2x2(mul2(add2(v[j].pair(k), minus), cc)));
+}
+
+// The set of the values of shared vectors (this thread's of them).
 template <typename T>
 __device__ __forceinline__ MaxSum sum_vectors(const uint4* vec, int nvec, float c) {
-    constexpr int U = UNR, P = Vec16<T>::kElems / 2;
+    constexpr int U = 4;
     const F2 cc = f2(c, c);
-    MaxSum r = empty_set();
+    float m = -FLT_MAX;
     F2 s = f2(0.f, 0.f);
-    for (int i0 = threadIdx.x; i0 < nvec; i0 += U * kStepThreads) {
+    int i = threadIdx.x;
+#pragma unroll 1
+    for (; i + (U - 1) * kStepThreads < nvec; i += U * kStepThreads) {
         Vec16<T> v[U];
-        float top = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int i = i0 + j * kStepThreads;
-            if (i < nvec) {
-                v[j].q = vec[i];
-                top = fmaxf(top, v[j].top());
-            }
-        }
-        if (top > r.m) {
-            const float m = clamp_max(r.m, top), f = ex2((r.m - m) * c);
-            s = mul2(s, f2(f, f));
-            r.m = m;
-        }
-        const F2 minus = f2(-r.m, -r.m);
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-            if (i0 + j * kStepThreads < nvec)
-#pragma unroll
-                for (int k = 0; k < P; ++k) s = add2(s, ex2x2(mul2(add2(v[j].pair(k), minus), cc)));
+        for (int j = 0; j < U; ++j) v[j].q = vec[i + j * kStepThreads];
+        add_vectors<U>(m, s, v, c, cc);
+    }
+#pragma unroll 1
+    for (; i < nvec; i += kStepThreads) {
+        Vec16<T> v;
+        v.q = vec[i];
+        add_vectors<1>(m, s, &v, c, cc);
     }
     const float2 h = halves(s);
-    r.s = h.x + h.y;
-    return r;
+    return {m, h.x + h.y};
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kStepThreads, MINB) k_step(DistillArgs p, int chunk) {
+__global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chunk) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ StepShared S;
     cg::cluster_group cluster = cg::this_cluster();
@@ -529,19 +528,7 @@ __global__ void __launch_bounds__(kThreads, 5) k_stream(DistillArgs p, int chunk
 #pragma unroll
                 for (int j = 0; j < kAhead; ++j) strike(v[j], m[j]);
             }
-            float most = v[0].top();
-#pragma unroll
-            for (int j = 1; j < kAhead; ++j) most = fmaxf(most, v[j].top());
-            if (most > u.o.m) {
-                const float m = clamp_max(u.o.m, most), f = ex2((u.o.m - m) * c);
-                s = mul2(s, f2(f, f));
-                u.o.m = m;
-            }
-            const F2 minus = f2(-u.o.m, -u.o.m);
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-                for (int k = 0; k < P; ++k) s = add2(s, ex2x2(mul2(add2(v[j].pair(k), minus), cc)));
+            add_vectors<kAhead>(u.o.m, s, v, c, cc);
         });
         const float2 h = halves(s);
         u.o.s = h.x + h.y;

@@ -137,6 +137,25 @@ struct Vec16<__nv_bfloat16> {
     }
 };
 
+// The largest value of U vectors (NaN only if all are), pairs of 16-bit values
+// compared at once.
+template <int U>
+__device__ __forceinline__ float top_of(const Vec16<float>* v) {
+    float m = v[0].top();
+#pragma unroll
+    for (int j = 1; j < U; ++j) m = fmaxf(m, v[j].top());
+    return m;
+}
+template <int U>
+__device__ __forceinline__ float top_of(const Vec16<__nv_bfloat16>* v) {
+    auto h = [](unsigned w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+    __nv_bfloat162 m = __hmax2(__hmax2(h(v[0].q.x), h(v[0].q.y)), __hmax2(h(v[0].q.z), h(v[0].q.w)));
+#pragma unroll
+    for (int j = 1; j < U; ++j)
+        m = __hmax2(m, __hmax2(__hmax2(h(v[j].q.x), h(v[j].q.y)), __hmax2(h(v[j].q.z), h(v[j].q.w))));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+
 template <typename T>
 __device__ __forceinline__ T from_f32(float x);
 template <>
