@@ -20,6 +20,9 @@
 
 namespace cg = cooperative_groups;
 
+#ifndef POL
+#define POL tc::policy_evict_normal
+#endif
 namespace domino {
 namespace train {
 
@@ -203,14 +206,6 @@ struct Slice {
     }
 };
 
-__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void bulk_store_wait_read() {
-    asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-
 // Adds U vectors to a set: one look at their maximum, then the exponentials.
 template <int U, typename T>
 __device__ __forceinline__ void add_vectors(float& m, F2& s, const Vec16<T>* v, float c, F2 cc) {
@@ -269,7 +264,7 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
     const auto request = [&](const Slice<T>& x) {  // one thread
         const uint32_t bytes = (uint32_t)x.body * sizeof(T);
         tc::mbar_arrive_expect_tx(bar, bytes);
-        if (bytes) tc::bulk_load(tc::smem_u32(x.data + x.head), x.src + x.head, bytes, bar, tc::policy_evict_first());
+        if (bytes) tc::bulk_load(tc::smem_u32(x.data + x.head), x.src + x.head, bytes, bar, POL());
     };
     // what is read ahead of a row: its weight, its rest and this thread's first entry
     struct Ahead {
@@ -304,7 +299,9 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
         const Ahead next = ahead(n + stride);
         const Slice<T> x = slice(n);
         T* dx = static_cast<T*>(p.dx) + (size_t)n * p.ld_d + x.v0;
-        float w = 0.f;
+        const bool together = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x.src)) & 15) == 0;
+        float w = 0.f, held = 0.f;  // held: the logit of this thread's first entry; later entries' are read again
+        bool twice = false;
         if (now.weight != 0.f) {
             const int32_t* ids = p.ids + (size_t)n * p.K;
             const float* top = p.top + (size_t)n * p.K;
@@ -326,10 +323,9 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
             }
             if (t == 0) tc::mbar_wait(bar, phase, &S.abort, p.err);
             __syncthreads();
-            const bool twice = S.twice != 0;
+            twice = S.twice != 0;
 
             Sums u = {empty_set(), empty_set(), empty_set(), 0.f};
-            float held = 0.f;  // the logit of this thread's first entry; later entries' are read again
 #pragma unroll 1
             for (int k = t; k < p.K; k += kStepThreads) {
                 const int id = k == t ? now.id : ids[k];
@@ -375,53 +371,62 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
             const Stats st = S.row;
             w = st.has == 0.f ? 0.f : now.weight * inv_t;
             if (w != 0.f) {
-                constexpr int P = Vec16<T>::kElems / 2;
+                // the gradient straight to memory: the buffer is free as soon as it is read
                 const float wc = w * st.co;
                 const F2 cc = f2(c, c), minus = f2(-st.mo, -st.mo), scale = f2(wc, wc);
+                if (together) {
+                    constexpr int P = Vec16<T>::kElems / 2;
+                    uint4* out = reinterpret_cast<uint4*>(dx + x.head);
+                    const uint4* in = reinterpret_cast<const uint4*>(x.data + x.head);
 #pragma unroll 2
-                for (int i = t; i < x.nvec; i += kStepThreads) {
-                    Vec16<T> v, g;
-                    v.q = x.vec[i];
+                    for (int i = t; i < x.body / Vec16<T>::kElems; i += kStepThreads) {
+                        Vec16<T> v, g;
+                        v.q = in[i];
 #pragma unroll
-                    for (int k = 0; k < P; ++k) g.set(k, mul2(scale, ex2x2(mul2(add2(v.pair(k), minus), cc))));
-                    x.vec[i] = g.q;
+                        for (int k = 0; k < P; ++k) g.set(k, mul2(scale, ex2x2(mul2(add2(v.pair(k), minus), cc))));
+                        out[i] = g.q;
+                    }
                 }
-                __syncthreads();
-#pragma unroll 1
-                for (int k = t; k < p.K; k += kStepThreads) {
-                    const int id = k == t ? now.id : ids[k];
-                    const unsigned a = place(id);
-                    if (a == kNone || (twice && !takes_part(ids, k, id, p.V, true))) continue;
-                    const float tv = k == t ? now.top : top[k], v = k == t ? held : to_f32(x.src[a]);
-                    const float q = st.qx * ex2((v - st.mx) * c), pk = st.pt * ex2((tv - st.mt) * c);
-                    x.data[a] = from_f32<T>(w * (q - pk));
+                // the elements beside whole vectors, or all where the two rows start differently modulo 16 bytes
+                const int beside = x.n - (together ? x.body : 0);
+                for (int i = t; i < beside; i += kStepThreads) {
+                    const int e = together && i >= x.head ? i + x.body : i;
+                    dx[e] = from_f32<T>(wc * ex2((to_f32(x.data[e]) - st.mo) * c));
                 }
             }
-        } else {
-            if (rank == 0 && t == 0) p.loss[n] = 0.f;
+        } else if (rank == 0 && t == 0) {
+            p.loss[n] = 0.f;
         }
-        if (w == 0.f)
-            for (int i = t; i < x.nvec; i += kStepThreads) x.vec[i] = make_uint4(0, 0, 0, 0);
-        // out: whole vectors by bulk copy where the gradient's row starts at the same place modulo 16 bytes
-        const bool together = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x.src)) & 15) == 0;
-        tc::fence_proxy_async();
-        __syncthreads();
-        if (together) {
-            if (t < x.head) dx[t] = x.data[t];
-            const int tail = x.n - x.head - x.body;
-            if (t < tail) dx[x.head + x.body + t] = x.data[x.head + x.body + t];
-            if (t == 0 && x.body) bulk_store(dx + x.head, tc::smem_u32(x.data + x.head), (uint32_t)x.body * sizeof(T));
-        } else {
-            for (int i = t; i < x.n; i += kStepThreads) dx[i] = x.data[i];
+        if (w == 0.f) {
+            if (together) {
+                uint4* out = reinterpret_cast<uint4*>(dx + x.head);
+                for (int i = t; i < x.body / Vec16<T>::kElems; i += kStepThreads) out[i] = make_uint4(0, 0, 0, 0);
+            }
+            const int beside = x.n - (together ? x.body : 0);
+            for (int i = t; i < beside; i += kStepThreads)
+                dx[together && i >= x.head ? i + x.body : i] = from_f32<T>(0.f);
         }
-        now = next;
-        if (t == 0) bulk_store_wait_read();
-        __syncthreads();  // the buffer is free
-        if (now.weight != 0.f) {
+        __syncthreads();  // the buffer is read, and the outside's gradient written
+        if (next.weight != 0.f) {
             const Slice<T> y = slice(n + stride);
             if (t == 0 && !S.abort) request(y);
             y.load_edges();
         }
+        if (w != 0.f) {  // the record's entries over it
+            const int32_t* ids = p.ids + (size_t)n * p.K;
+            const float* top = p.top + (size_t)n * p.K;
+            const Stats st = S.row;
+#pragma unroll 1
+            for (int k = t; k < p.K; k += kStepThreads) {
+                const int id = k == t ? now.id : ids[k];
+                const unsigned a = (unsigned)id - (unsigned)x.v0;
+                if (a >= (unsigned)x.n || (twice && !takes_part(ids, k, id, p.V, true))) continue;
+                const float tv = k == t ? now.top : top[k], v = k == t ? held : to_f32(x.src[a]);
+                const float q = st.qx * ex2((v - st.mx) * c), pk = st.pt * ex2((tv - st.mt) * c);
+                dx[a] = from_f32<T>(w * (q - pk));
+            }
+        }
+        now = next;
     }
     // A CTA whose copy never came has gone on through its cluster's exchanges,
     // with meaningless data and without further copies; it gives the lost one a
