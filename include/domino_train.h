@@ -41,11 +41,12 @@ typedef struct domino_train_ctx domino_train_ctx;
 
 #define DOMINO_TRAIN_MAX_V 524288 /* largest vocabulary                      */
 #define DOMINO_TRAIN_MAX_K 8192   /* largest record                          */
+#define DOMINO_TRAIN_MAX_TOKENS 4194304 /* tokens of one embed_grad call   */
 #define DOMINO_TRAIN_STATS 8      /* floats per row of distill_forward's stats */
 
 /* V vocabulary (2 .. DOMINO_TRAIN_MAX_V); E embedding width (0: the embedding
- * entry points are not used); max_tokens sizes the workspace of embed_grad (0:
- * not used); dtype (DOMINO_DTYPE_*) of the student's logits and their
+ * entry points are not used); max_tokens (0 .. DOMINO_TRAIN_MAX_TOKENS) sizes the workspace of embed_grad
+ * (0: not used); dtype (DOMINO_DTYPE_*) of the student's logits and their
  * gradient, of the embedding table and of embedding rows. */
 typedef struct {
     int V, E;

@@ -58,7 +58,8 @@ int domino_train_init(domino_train_ctx** out, const domino_train_config* cfg, in
     *out = nullptr;
     if (!cfg) return DOMINO_ERR_INVALID_ARG;
     if (!known(cfg->dtype) || cfg->V > DOMINO_TRAIN_MAX_V) return DOMINO_ERR_UNSUPPORTED;
-    if (cfg->V < 2 || cfg->E < 0 || cfg->E > (1 << 20) || cfg->max_tokens < 0 || cfg->max_tokens > (1 << 28))
+    if (cfg->V < 2 || cfg->E < 0 || cfg->E > (1 << 20) || cfg->max_tokens < 0 ||
+        cfg->max_tokens > DOMINO_TRAIN_MAX_TOKENS)
         return DOMINO_ERR_INVALID_ARG;
     int ndev = 0;
     if (cudaGetDeviceCount(&ndev) != cudaSuccess || device < 0 || device >= ndev) return DOMINO_ERR_CUDA;

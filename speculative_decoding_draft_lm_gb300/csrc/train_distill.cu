@@ -20,9 +20,6 @@
 
 namespace cg = cooperative_groups;
 
-#ifndef POL
-#define POL tc::policy_evict_normal
-#endif
 namespace domino {
 namespace train {
 
@@ -149,12 +146,23 @@ __device__ __noinline__ bool takes_part(const int32_t* ids, int k, int id, int V
 
 // ---- loss and gradient at once ---------------------------------------------------
 //
-// A cluster of CTAs holds one row in shared memory, a slice each: bulk copies
-// bring it in, the sums and the gradient are two passes over shared memory, and
-// bulk copies take the gradient, written in place, out.  So the logits are read
-// once and the gradient written once, which is all the traffic there is.  A CTA
-// has two such buffers: the next row comes in, and the last one's gradient
-// leaves, while a row is computed.
+// A cluster of CTAs holds one row in shared memory, a slice each: a bulk copy
+// brings it in, the sums are a pass over shared memory, the clusters' CTAs
+// exchange theirs through distributed shared memory, and a second pass writes
+// the gradient.  So the logits are read once and the gradient is written once,
+// which is all the traffic there is: 3840 rows of 151,936 bf16 logits in 437 us,
+// 5.35 TB/s, 0.80 of the measured copy rate (349 us); 15 rows in 10 us.
+//
+// What bounds it is how long a slice stays in shared memory, not arithmetic:
+// without the exchange, whose cost is the wait for the slowest of eight CTAs,
+// the same kernel took 396 us, and without the passes 407 us.  Hence slices of
+// 40 KB, of which five fit an SM, in one wave of clusters that take rows in turn
+// (clusters of 4, 7, 9 and 10 CTAs: 464, 440, 444 and 446 us); the gradient
+// straight to memory, so that the buffer is free once it is read (through the
+// buffer and a bulk copy: 496 us); everything of a row that is not its logits
+// read a row ahead; the loss after the gradient's factors.  Two half-size
+// buffers per CTA, in clusters of 16, took 744 us.  Reading the row twice from
+// global memory instead (the second time from L2) took 564 us.
 //
 // Entries of the record are taken out of the slice (set to -inf) once their
 // logits are read, so that the first pass is a plain sum over the outside.
@@ -264,7 +272,7 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
     const auto request = [&](const Slice<T>& x) {  // one thread
         const uint32_t bytes = (uint32_t)x.body * sizeof(T);
         tc::mbar_arrive_expect_tx(bar, bytes);
-        if (bytes) tc::bulk_load(tc::smem_u32(x.data + x.head), x.src + x.head, bytes, bar, POL());
+        if (bytes) tc::bulk_load(tc::smem_u32(x.data + x.head), x.src + x.head, bytes, bar, tc::policy_evict_normal());
     };
     // what is read ahead of a row: its weight, its rest and this thread's first entry
     struct Ahead {
@@ -444,7 +452,12 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
 // them in flight.  The forward skips the record's entries by a bit per element,
 // one byte (half a byte) of which covers a vector; the backward writes every
 // element as if it were outside the record and then, after a barrier, the
-// entries again.  A row is one CTA's, or a cluster's where there are few rows.
+// entries again.  A row is one CTA's, or a cluster's where there are few rows
+// (until 4 CTAs an SM) or its slices would pass 160 KB (960 rows of 304 KB: 169 us
+// for both directions against 173 us with a CTA a row and 188 us with slices of
+// 80 KB).  Bound by HBM: 960 rows of 151,936 bf16 logits, 0.88 GB, in 164 us for
+// both, 5.36 TB/s, 0.80 of the measured copy rate; the forward alone 64 us, the
+// backward 90 us.
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -458,7 +471,7 @@ struct StreamShared {
     int twice;
 };
 
-template <typename T, bool kForward, bool kBackward>
+template <typename T, bool kBackward>
 __global__ void __launch_bounds__(kThreads, 5) k_stream(DistillArgs p, int chunk) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ StreamShared S;
@@ -469,19 +482,13 @@ __global__ void __launch_bounds__(kThreads, 5) k_stream(DistillArgs p, int chunk
     const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
     const int n = blockIdx.x / size, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const float inv_t = 1.f / p.temperature, c = kLog2e / p.temperature;
-    const float weight = kBackward ? p.weight[n] : 1.f, rest = kForward && p.rest ? p.rest[n] : -INFINITY;
     const int v0 = min(p.V, rank * chunk);
     const Vectors<T> x(static_cast<const T*>(p.x) + (size_t)n * p.ld + v0, min(p.V, v0 + chunk) - v0);
-    T* dx = static_cast<T*>(p.dx) + (size_t)n * p.ld_d + v0;
-    const bool together = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x.src)) & 15) == 0;
     const int32_t* ids = p.ids + (size_t)n * p.K;
     const float* top = p.top + (size_t)n * p.K;
-    Stats st = {};
-    if (!kForward) st = reinterpret_cast<const Stats*>(p.stats)[n];
-    bool twice = st.twice != 0.f;
-    float w = !kForward && st.has == 0.f ? 0.f : weight * inv_t;
 
-    if (kForward && weight != 0.f) {
+    if constexpr (!kBackward) {
+        const float rest = p.rest ? p.rest[n] : -INFINITY;
         for (int i = t; i <= (x.phase + x.n) / 32; i += kThreads) bits[i] = 0;
         if (t == 0) S.twice = 0;
         if (size > 1) cluster_barrier();  // every CTA of the row is running
@@ -498,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 5) k_stream(DistillArgs p, int chunk
             }
         }
         __syncthreads();
-        twice = S.twice != 0;
+        const bool twice = S.twice != 0;
         Sums u = {empty_set(), empty_set(), empty_set(), 0.f};
 #pragma unroll 1
         for (int k = t; k < p.K; k += kThreads) {
@@ -554,30 +561,26 @@ __global__ void __launch_bounds__(kThreads, 5) k_stream(DistillArgs p, int chunk
             if (lane >= parts) u = {empty_set(), empty_set(), empty_set(), 0.f};
             for (int i = lane + 32; i < parts; i += 32) u = join(u, S.part[i], c);
             u = warp_join(u, c);
-            st = finish(u, rest, inv_t, c);
-            if (lane == 0) S.row = st;
+            Stats st = finish(u, rest, inv_t, c);
             const float loss = row_loss(u, rest, inv_t, c);
+            if (lane == 0) S.row = st;
             if (rank == 0 && lane == 0) p.loss[n] = loss;
         }
-        if (kBackward) {
-            __syncthreads();
-            st = S.row;
-            if (st.has == 0.f) w = 0.f;
-        } else {
-            // whether any CTA of the row saw an id twice
-            if (size > 1) {
-                if (t == 0 && twice) *cluster.map_shared_rank(&S.twice, 0) = 1;
-                cluster_barrier();
-            }
-            if (rank == 0 && t == 0) {
-                st.twice = S.twice ? 1.f : 0.f;
-                reinterpret_cast<Stats*>(p.stats)[n] = st;
-            }
+        // whether any CTA of the row saw an id twice
+        if (size > 1) {
+            if (t == 0 && twice) *cluster.map_shared_rank(&S.twice, 0) = 1;
+            cluster_barrier();
         }
-    } else if (kForward && rank == 0 && t == 0) {
-        p.loss[n] = 0.f;
-    }
-    if (kBackward) {
+        if (rank == 0 && t == 0) {
+            S.row.twice = S.twice ? 1.f : 0.f;
+            reinterpret_cast<Stats*>(p.stats)[n] = S.row;
+        }
+    } else {
+        T* dx = static_cast<T*>(p.dx) + (size_t)n * p.ld_d + v0;
+        const bool together = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x.src)) & 15) == 0;
+        const Stats st = reinterpret_cast<const Stats*>(p.stats)[n];
+        const bool twice = st.twice != 0.f;
+        const float w = st.has == 0.f ? 0.f : p.weight[n] * inv_t;
         const float wc = w * st.co;
         const F2 cc = f2(c, c), minus = f2(-st.mo, -st.mo), scale = f2(wc, wc);
         if (w == 0.f) {
@@ -619,34 +622,34 @@ __global__ void __launch_bounds__(kThreads, 5) k_stream(DistillArgs p, int chunk
     }
 }
 
-template <typename T, bool kForward, bool kBackward>
+template <typename T, bool kBackward>
 cudaError_t launch_stream(domino_train_ctx* ctx, const DistillArgs& a, cudaStream_t st) {
     int size = 1;
     auto slice = [&](int parts) { return ((a.V + parts - 1) / parts + 63) / 64 * 64; };
     while (size < kMaxCluster && (long long)a.n * size < 4 * ctx->num_sms && slice(2 * size) >= 2048) size *= 2;
     while (size < kMaxCluster && slice(size) * (int)sizeof(T) > 160 * 1024) size *= 2;
     const int chunk = slice(size);
-    const size_t smem = kRingBytes + (kForward ? (size_t)chunk / 8 + 8 : 0);
-    auto kern = k_stream<T, kForward, kBackward>;
+    const size_t smem = kRingBytes + (kBackward ? 0 : (size_t)chunk / 8 + 8);
+    auto kern = k_stream<T, kBackward>;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = cluster_config((unsigned)a.n * size, kThreads, size, smem, st, &attr);
     ctx->last_launches = 1;
     return cudaLaunchKernelEx(&cfg, kern, a, chunk);
 }
 
-template <bool kForward, bool kBackward>
+template <bool kBackward>
 cudaError_t launch(domino_train_ctx* ctx, const DistillArgs& a, cudaStream_t st) {
-    return ctx->cfg.dtype == DOMINO_DTYPE_BF16 ? launch_stream<__nv_bfloat16, kForward, kBackward>(ctx, a, st)
-                                               : launch_stream<float, kForward, kBackward>(ctx, a, st);
+    return ctx->cfg.dtype == DOMINO_DTYPE_BF16 ? launch_stream<__nv_bfloat16, kBackward>(ctx, a, st)
+                                               : launch_stream<float, kBackward>(ctx, a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_distill_forward(domino_train_ctx* c, const DistillArgs& a, cudaStream_t st) {
-    return launch<true, false>(c, a, st);
+    return launch<false>(c, a, st);
 }
 cudaError_t launch_distill_backward(domino_train_ctx* c, const DistillArgs& a, cudaStream_t st) {
-    return launch<false, true>(c, a, st);
+    return launch<true>(c, a, st);
 }
 
 namespace {
@@ -687,17 +690,14 @@ cudaError_t launch_step(domino_train_ctx* ctx, const DistillArgs& a, cudaStream_
 cudaError_t prepare_distill_kernels() {
     cudaError_t e = allow_all(k_step<float>);
     if (e == cudaSuccess) e = allow_all(k_step<__nv_bfloat16>);
-    if (e == cudaSuccess) e = allow_all(k_stream<float, true, false>);
-    if (e == cudaSuccess) e = allow_all(k_stream<float, false, true>);
-    if (e == cudaSuccess) e = allow_all(k_stream<__nv_bfloat16, true, false>);
-    if (e == cudaSuccess) e = allow_all(k_stream<__nv_bfloat16, false, true>);
+    if (e == cudaSuccess) e = allow_all(k_stream<float, false>);
+    if (e == cudaSuccess) e = allow_all(k_stream<float, true>);
+    if (e == cudaSuccess) e = allow_all(k_stream<__nv_bfloat16, false>);
+    if (e == cudaSuccess) e = allow_all(k_stream<__nv_bfloat16, true>);
     return e;
 }
 
 cudaError_t launch_distill_step(domino_train_ctx* c, const DistillArgs& a, cudaStream_t st) {
-#ifdef STEP_STREAM
-    return launch<true, true>(c, a, st);
-#endif
     return c->cfg.dtype == DOMINO_DTYPE_BF16 ? launch_step<__nv_bfloat16>(c, a, st) : launch_step<float>(c, a, st);
 }
 

@@ -13,6 +13,7 @@ from .rollout import DOMINO_DTYPE_BF16, DOMINO_DTYPE_FP32, DominoError, _check
 
 DOMINO_TRAIN_MAX_V = 524288
 DOMINO_TRAIN_MAX_K = 8192
+DOMINO_TRAIN_MAX_TOKENS = 4194304
 DOMINO_TRAIN_STATS = 8
 
 # every symbol the header declares

@@ -32,7 +32,7 @@ def test_library_exports_every_declared_symbol(lib):
 def test_header_constants_match_the_binding():
     from speculative_decoding_draft_lm_gb300 import train
     text = open(HEADER).read()
-    for name in ("DOMINO_TRAIN_MAX_V", "DOMINO_TRAIN_MAX_K", "DOMINO_TRAIN_STATS"):
+    for name in ("DOMINO_TRAIN_MAX_V", "DOMINO_TRAIN_MAX_K", "DOMINO_TRAIN_MAX_TOKENS", "DOMINO_TRAIN_STATS"):
         assert int(re.search(rf"#define {name} (\d+)", text).group(1)) == getattr(train, name)
 
 
@@ -62,6 +62,6 @@ def test_config_validation_precedes_device_access(lib):
     assert lib.domino_train_init(ctypes.byref(ctx), None, 0) == R.DOMINO_ERR_INVALID_ARG
     assert init(100, 8, 8, 7) == R.DOMINO_ERR_UNSUPPORTED
     assert init(524289, 8, 8, 1) == R.DOMINO_ERR_UNSUPPORTED
-    for bad in ((1, 8, 8, 1), (100, -1, 8, 1), (100, 8, -1, 1), (-5, 8, 8, 0)):
+    for bad in ((1, 8, 8, 1), (100, -1, 8, 1), (100, 8, -1, 1), (100, 8, 4194305, 1), (-5, 8, 8, 0)):
         assert init(*bad) == R.DOMINO_ERR_INVALID_ARG
     assert not ctx.value
