@@ -528,12 +528,12 @@ __global__ void __launch_bounds__(kThreads, 5) k_stream(DistillArgs p, int chunk
         const unsigned char* masks = reinterpret_cast<const unsigned char*>(bits);
         const F2 cc = f2(c, c);
         F2 s = f2(0.f, 0.f);
-        stream<kThreads, kAhead, kStages>(x, ring, [&](int i0, Vec16<T>* v) {
+        stream<kThreads, kAhead, kStages>(x, ring, [&](int i0, Vec16<T>* v, auto all) {
             unsigned m[kAhead], any = 0;
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
                 const int i = i0 + j * kThreads;
-                m[j] = i < x.last ? (kPer == 8 ? masks[i] : masks[i >> 1] >> (i & 1) * 4 & 15u) : 0u;
+                m[j] = all() || i < x.last ? (kPer == 8 ? masks[i] : masks[i >> 1] >> (i & 1) * 4 & 15u) : 0u;
                 any |= m[j];
             }
             if (any) {
@@ -596,13 +596,13 @@ __global__ void __launch_bounds__(kThreads, 5) k_stream(DistillArgs p, int chunk
         }
         if (together) {
             uint4* out = reinterpret_cast<uint4*>(dx - x.phase);
-            stream<kThreads, kAhead, kStages>(x, ring, [&](int i0, Vec16<T>* v) {
+            stream<kThreads, kAhead, kStages>(x, ring, [&](int i0, Vec16<T>* v, auto all) {
 #pragma unroll
                 for (int j = 0; j < kAhead; ++j) {
                     Vec16<T> g;
 #pragma unroll
                     for (int k = 0; k < P; ++k) g.set(k, mul2(scale, ex2x2(mul2(add2(v[j].pair(k), minus), cc))));
-                    if (i0 + j * kThreads < x.last) out[i0 + j * kThreads] = g.q;
+                    if (all() || i0 + j * kThreads < x.last) out[i0 + j * kThreads] = g.q;
                 }
             });
             const int side = t < 2 * kPer ? x.beside(t) : x.n;

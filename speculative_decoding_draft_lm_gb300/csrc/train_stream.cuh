@@ -1,6 +1,8 @@
 // Streaming of rows of any alignment through a CTA, and cluster helpers.
 #pragma once
 
+#include <type_traits>
+
 #include "tc_common.cuh"
 #include "train_math.cuh"
 
@@ -33,42 +35,61 @@ struct Vectors {
     }
 };
 
-// Calls f(i, v) on the vectors [x.first, x.last) of this thread, kAhead
-// adjacent places of the thread at once (v.q is -inf in every element where i
-// is past the end).  The vectors pass through a ring in shared memory that no
+// Calls f(i, v, all) on the vectors [x.first, x.last) of this thread: kAhead of
+// them, i, i + kThreads, ...; `all` is a std::true_type where every thread has
+// all of them, and v.q is -inf in every element of one past the end where it is
+// not (the last call).  The vectors pass through a ring in shared memory that no
 // other thread touches, filled by asynchronous copies kStages calls ahead: the
 // bytes in flight cost no registers, and nothing waits on a barrier.
 template <int kThreads, int kAhead, int kStages, typename T, typename F>
 __device__ __forceinline__ void stream(const Vectors<T>& x, uint4* ring, F&& f) {
-    const int t = threadIdx.x, calls = (x.last - x.first + kAhead * kThreads - 1) / (kAhead * kThreads);
+    constexpr int kCall = kAhead * kThreads;
+    const int t = threadIdx.x, vectors = x.last - x.first, whole = vectors / kCall, calls = (vectors + kCall - 1) / kCall;
     const unsigned inf = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
-    const uint4* src = x.vec();
-    auto fill = [&](int call) {
-        uint4* slot = ring + (call % kStages) * (kAhead * kThreads) + t;
-        int i = x.first + call * (kAhead * kThreads) + t;
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j, i += kThreads, slot += kThreads) {
-            if (i < x.last)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(slot)), "l"(src + i) : "memory");
-            else
-                *slot = make_uint4(inf, inf, inf, inf);
-        }
+    const uint4* src = x.vec() + x.first + t;  // of the next call to be filled
+    int filled = 0, fill_stage = 0, stage = 0;
+    const auto copy = [](uint4* to, const uint4* from) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(to)), "l"(from) : "memory");
     };
+    const auto fill = [&] {
+        uint4* slot = ring + fill_stage * kCall + t;
+        if (filled < whole) {
 #pragma unroll
-    for (int g = 0; g < kStages; ++g) {
-        if (g < calls) fill(g);
+            for (int j = 0; j < kAhead; ++j) copy(slot + j * kThreads, src + j * kThreads);
+        } else if (filled < calls) {
+            const int left = vectors - filled * kCall - t;  // of this thread on
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (j * kThreads < left) copy(slot + j * kThreads, src + j * kThreads);
+                else slot[j * kThreads] = make_uint4(inf, inf, inf, inf);
+            }
+        }
         asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-#pragma unroll 1
-    for (int g = 0; g < calls; ++g) {
+        ++filled;
+        src += kCall;
+        fill_stage = fill_stage + 1 == kStages ? 0 : fill_stage + 1;
+    };
+    const auto take = [&](Vec16<T>* v) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-        const uint4* slot = ring + (g % kStages) * (kAhead * kThreads) + t;
-        Vec16<T> v[kAhead];
+        const uint4* slot = ring + stage * kCall + t;
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) v[j].q = slot[j * kThreads];
-        f(x.first + g * (kAhead * kThreads) + t, v);
-        if (g + kStages < calls) fill(g + kStages);
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+    };
+#pragma unroll
+    for (int g = 0; g < kStages; ++g) fill();
+    int i = x.first + t;
+#pragma unroll 1
+    for (int g = 0; g < whole; ++g, i += kCall) {
+        Vec16<T> v[kAhead];
+        take(v);
+        f(i, v, std::true_type());
+        fill();
+    }
+    if (calls > whole) {
+        Vec16<T> v[kAhead];
+        take(v);
+        f(i, v, std::false_type());
     }
 }
 

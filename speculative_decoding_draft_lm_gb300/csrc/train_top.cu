@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
     // the groups: a thread's vectors of a step, kThreads groups a step (-inf where there is nothing)
     float largest_here = -INFINITY;
     int at_group = t;
-    stream<kThreads, kAhead, kStages>(x, reinterpret_cast<uint4*>(smem), [&](int, Vec16<T>* v) {
+    stream<kThreads, kAhead, kStages>(x, reinterpret_cast<uint4*>(smem), [&](int, Vec16<T>* v, auto) {
         float m = v[0].top_nan();
 #pragma unroll
         for (int j = 1; j < kAhead; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(v[j].top_nan()));
