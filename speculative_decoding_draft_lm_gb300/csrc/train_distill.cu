@@ -25,7 +25,6 @@ namespace train {
 
 namespace {
 
-
 // What a row's loss and gradient go by; row layout of `stats`.
 struct Stats {
     float mo, co;   // outside: T dloss/dx = co 2^((x - mo) c)
@@ -50,18 +49,6 @@ __device__ __forceinline__ Sums join(const Sums& x, const Sums& y, float c) {
     r.s = join(x.s, y.s, c);
     r.o = join(x.o, y.o, c);
     r.a = rescaled(x.a, ex2((x.t.m - r.t.m) * c)) + rescaled(y.a, ex2((y.t.m - r.t.m) * c));
-    return r;
-}
-
-__device__ __forceinline__ Sums shuffled(const Sums& x, int mask) {
-    Sums r;
-    r.t.m = __shfl_xor_sync(0xffffffffu, x.t.m, mask);
-    r.t.s = __shfl_xor_sync(0xffffffffu, x.t.s, mask);
-    r.s.m = __shfl_xor_sync(0xffffffffu, x.s.m, mask);
-    r.s.s = __shfl_xor_sync(0xffffffffu, x.s.s, mask);
-    r.o.m = __shfl_xor_sync(0xffffffffu, x.o.m, mask);
-    r.o.s = __shfl_xor_sync(0xffffffffu, x.o.s, mask);
-    r.a = __shfl_xor_sync(0xffffffffu, x.a, mask);
     return r;
 }
 
@@ -150,8 +137,8 @@ __device__ __noinline__ bool takes_part(const int32_t* ids, int k, int id, int V
 // brings it in, the sums are a pass over shared memory, the clusters' CTAs
 // exchange theirs through distributed shared memory, and a second pass writes
 // the gradient.  So the logits are read once and the gradient is written once,
-// which is all the traffic there is: 3840 rows of 151,936 bf16 logits in 437 us,
-// 5.35 TB/s, 0.80 of the measured copy rate (349 us); 15 rows in 10 us.
+// which is all the traffic there is: 3840 rows of 151,936 bf16 logits in 433 us,
+// 5.4 TB/s, 0.81 of the measured copy rate (349 us); 15 rows in 9.3 us.
 //
 // What bounds it is how long a slice stays in shared memory, not arithmetic:
 // without the exchange, whose cost is the wait for the slowest of eight CTAs,
@@ -160,9 +147,12 @@ __device__ __noinline__ bool takes_part(const int32_t* ids, int k, int id, int V
 // (clusters of 4, 7, 9 and 10 CTAs: 464, 440, 444 and 446 us); the gradient
 // straight to memory, so that the buffer is free once it is read (through the
 // buffer and a bulk copy: 496 us); everything of a row that is not its logits
-// read a row ahead; the loss after the gradient's factors.  Two half-size
+// read a row ahead (two entries of the record a thread: with one, 436 us); the loss after the gradient's factors.  Two half-size
 // buffers per CTA, in clusters of 16, took 744 us.  Reading the row twice from
 // global memory instead (the second time from L2) took 564 us.
+//
+// The forward alone streams its rows instead (below): this kernel without its
+// second pass took 87 us for 960 rows against 66 us.
 //
 // Entries of the record are taken out of the slice (set to -inf) once their
 // logits are read, so that the first pass is a plain sum over the outside.
@@ -170,6 +160,7 @@ __device__ __noinline__ bool takes_part(const int32_t* ids, int k, int id, int V
 constexpr int kSliceBytes = 40 * 1024;
 constexpr unsigned kNone = 0xFFFFFFFFu;
 constexpr int kStepThreads = 128;
+constexpr int kHeld = 2;  // entries of a record that a thread holds; later ones are read again
 constexpr int kStepWarps = kStepThreads / 32;
 struct StepShared {
     Sums part[2][kMaxCluster * kStepWarps];  // every warp of the row, by the row's parity
@@ -269,24 +260,29 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
     const auto slice = [&](int n) {
         return Slice<T>(static_cast<const T*>(p.x) + (size_t)n * p.ld, p.V, chunk, rank, smem);
     };
-    const auto request = [&](const Slice<T>& x) {  // one thread
+    const auto request = [&](const Slice<T>& x) {  // one thread, after a barrier behind the buffer's last use
+        tc::fence_proxy_async();
         const uint32_t bytes = (uint32_t)x.body * sizeof(T);
         tc::mbar_arrive_expect_tx(bar, bytes);
         if (bytes) tc::bulk_load(tc::smem_u32(x.data + x.head), x.src + x.head, bytes, bar, tc::policy_evict_normal());
     };
-    // what is read ahead of a row: its weight, its rest and this thread's first entry
+    // what is read ahead of a row: its weight, its rest and this thread's first entries
     struct Ahead {
-        float weight, rest, top;
-        int id;
+        float weight, rest, top[kHeld];
+        int id[kHeld];
     };
     const auto ahead = [&](int n) {
-        Ahead a = {0.f, -INFINITY, 0.f, -1};
+        Ahead a;
+        a.weight = 0.f;
+        a.rest = -INFINITY;
         if (n < p.n) {
             a.weight = p.weight[n];
             if (p.rest) a.rest = p.rest[n];
-            if (t < p.K) {
-                a.id = p.ids[(size_t)n * p.K + t];
-                a.top = p.top[(size_t)n * p.K + t];
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j) {
+                const int k = t + j * kStepThreads;
+                a.id[j] = k < p.K ? p.ids[(size_t)n * p.K + k] : -1;
+                a.top[j] = k < p.K ? p.top[(size_t)n * p.K + k] : 0.f;
             }
         }
         return a;
@@ -308,7 +304,7 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
         const Slice<T> x = slice(n);
         T* dx = static_cast<T*>(p.dx) + (size_t)n * p.ld_d + x.v0;
         const bool together = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x.src)) & 15) == 0;
-        float w = 0.f, held = 0.f;  // held: the logit of this thread's first entry; later entries' are read again
+        float w = 0.f, held[kHeld] = {};  // held: the logits of this thread's first entries; later entries' are read again
         bool twice = false;
         if (now.weight != 0.f) {
             const int32_t* ids = p.ids + (size_t)n * p.K;
@@ -318,9 +314,7 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
                 const unsigned a = (unsigned)id - (unsigned)x.v0;
                 return a < (unsigned)x.n ? a : kNone;
             };
-#pragma unroll 1
-            for (int k = t; k < p.K; k += kStepThreads) {
-                const int id = k == t ? now.id : ids[k];
+            const auto mark = [&](int id) {
                 const unsigned a = place(id);
                 if (a != kNone) {
                     const unsigned bit = 1u << (a & 31);
@@ -328,21 +322,22 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
                 } else if (rank == 0 && id != -1 && (unsigned)id >= (unsigned)p.V) {
                     atomicOr(p.err, kErrBadToken);
                 }
-            }
+            };
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j) mark(now.id[j]);
+#pragma unroll 1
+            for (int k = t + kHeld * kStepThreads; k < p.K; k += kStepThreads) mark(ids[k]);
             if (t == 0) tc::mbar_wait(bar, phase, &S.abort, p.err);
             __syncthreads();
             twice = S.twice != 0;
 
             Sums u = {empty_set(), empty_set(), empty_set(), 0.f};
-#pragma unroll 1
-            for (int k = t; k < p.K; k += kStepThreads) {
-                const int id = k == t ? now.id : ids[k];
+            const auto gather = [&](int k, int id, float tv) {
                 const unsigned a = place(id);
-                if (a == kNone || (twice && !takes_part(ids, k, id, p.V, true))) continue;
-                const float tv = k == t ? now.top : top[k], v = to_f32(x.data[a]);
+                if (a == kNone || (twice && !takes_part(ids, k, id, p.V, true))) return 0.f;
+                const float v = to_f32(x.data[a]);
                 x.data[a] = from_f32<T>(-INFINITY);  // no part of the outside
                 bits[a >> 5] = 0;
-                if (k == t) held = v;
                 if (tv > u.t.m) {
                     const float m = clamp_max(u.t.m, tv), f = ex2((u.t.m - m) * c);
                     u.t.s *= f;
@@ -353,7 +348,12 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
                 u.t.s += e;
                 if (e != 0.f) u.a += e * (tv - v) * inv_t;
                 add(u.s, v, c);
-            }
+                return v;
+            };
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j) held[j] = gather(t + j * kStepThreads, now.id[j], now.top[j]);
+#pragma unroll 1
+            for (int k = t + kHeld * kStepThreads; k < p.K; k += kStepThreads) gather(k, ids[k], top[k]);
             __syncthreads();
             if (t == 0) S.twice = 0;
             u.o = sum_vectors<T>(x.vec, x.nvec, c);
@@ -371,11 +371,11 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
                 if (lane == 0) S.row = st;
             }
             __syncthreads();
-            phase ^= 1;
             if (rank == 0 && warp == 0) {
                 const float loss = row_loss(u, now.rest, inv_t, c);
                 if (lane == 0) p.loss[n] = loss;
             }
+            phase ^= 1;
             const Stats st = S.row;
             w = st.has == 0.f ? 0.f : now.weight * inv_t;
             if (w != 0.f) {
@@ -424,15 +424,19 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
             const int32_t* ids = p.ids + (size_t)n * p.K;
             const float* top = p.top + (size_t)n * p.K;
             const Stats st = S.row;
-#pragma unroll 1
-            for (int k = t; k < p.K; k += kStepThreads) {
-                const int id = k == t ? now.id : ids[k];
-                const unsigned a = (unsigned)id - (unsigned)x.v0;
-                if (a >= (unsigned)x.n || (twice && !takes_part(ids, k, id, p.V, true))) continue;
-                const float tv = k == t ? now.top : top[k], v = k == t ? held : to_f32(x.src[a]);
+            const auto entry = [&](int id, float tv, float v) {
                 const float q = st.qx * ex2((v - st.mx) * c), pk = st.pt * ex2((tv - st.mt) * c);
-                dx[a] = from_f32<T>(w * (q - pk));
-            }
+                dx[id - x.v0] = from_f32<T>(w * (q - pk));
+            };
+            const auto here = [&](int k, int id) {
+                return (unsigned)id - (unsigned)x.v0 < (unsigned)x.n && !(twice && !takes_part(ids, k, id, p.V, true));
+            };
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j)
+                if (here(t + j * kStepThreads, now.id[j])) entry(now.id[j], now.top[j], held[j]);
+#pragma unroll 1
+            for (int k = t + kHeld * kStepThreads; k < p.K; k += kStepThreads)
+                if (here(k, ids[k])) entry(ids[k], top[k], to_f32(x.src[ids[k] - x.v0]));
         }
         now = next;
     }
@@ -446,23 +450,23 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
     }
 }
 
-// ---- forward and backward by themselves -------------------------------------------
+// ---- forward by itself ---------------------------------------------------------------
 //
-// Every thread streams 16-byte vectors of its CTA's slice of the row, kAhead of
-// them in flight.  The forward skips the record's entries by a bit per element,
-// one byte (half a byte) of which covers a vector; the backward writes every
-// element as if it were outside the record and then, after a barrier, the
-// entries again.  A row is one CTA's, or a cluster's where there are few rows
-// (until 4 CTAs an SM) or its slices would pass 160 KB (960 rows of 304 KB: 169 us
-// for both directions against 173 us with a CTA a row and 188 us with slices of
-// 80 KB).  Bound by HBM: 960 rows of 151,936 bf16 logits, 0.88 GB, in 164 us for
-// both, 5.36 TB/s, 0.80 of the measured copy rate; the forward alone 64 us, the
-// backward 90 us.
+// Every thread streams 16-byte vectors of its CTA's slice of the row, and skips
+// the record's entries by a bit per element, one byte (half a byte) of which
+// covers a vector.  A row is one CTA's, or a cluster's where there are few rows
+// (until 4 CTAs an SM) or its slices would pass 160 KB.  960 rows of 151,936 bf16
+// logits, 0.29 GB: 66 us, 4.4 TB/s.  Without the masks and the additions it took
+// 65 us when it took 70 with them: what bounds it is how the CTAs start, which is
+// why the first vectors are asked for before the record is read (71 us where
+// they were not).  512 and 128 threads: 71 and 72 us; 2 vectors at once and 3
+// stages: 65 us, and 53.5 against 51.5 us for forward and backward of 240 fp32 rows
+// of 79,999.
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kAhead = 2;
-constexpr int kStages = 3;
+constexpr int kAhead = 4;
+constexpr int kStages = 2;
 constexpr size_t kRingBytes = (size_t)kThreads * kAhead * kStages * 16;
 
 struct StreamShared {
@@ -471,212 +475,214 @@ struct StreamShared {
     int twice;
 };
 
-template <typename T, bool kBackward>
-__global__ void __launch_bounds__(kThreads, 5) k_stream(DistillArgs p, int chunk) {
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) k_forward(DistillArgs p, int chunk) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ StreamShared S;
     uint4* ring = reinterpret_cast<uint4*>(smem);
     unsigned* bits = reinterpret_cast<unsigned*>(smem + kRingBytes);
-    constexpr int P = Vec16<T>::kElems / 2, kPer = Vec16<T>::kElems;
+    constexpr int kPer = Vec16<T>::kElems;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
     const int n = blockIdx.x / size, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const float inv_t = 1.f / p.temperature, c = kLog2e / p.temperature;
     const int v0 = min(p.V, rank * chunk);
     const Vectors<T> x(static_cast<const T*>(p.x) + (size_t)n * p.ld + v0, min(p.V, v0 + chunk) - v0);
+    // the first vectors are on their way while the record is read
+    Streamer<kThreads, kAhead, kStages, T> vectors(x, ring);
     const int32_t* ids = p.ids + (size_t)n * p.K;
     const float* top = p.top + (size_t)n * p.K;
 
-    if constexpr (!kBackward) {
-        const float rest = p.rest ? p.rest[n] : -INFINITY;
-        for (int i = t; i <= (x.phase + x.n) / 32; i += kThreads) bits[i] = 0;
-        if (t == 0) S.twice = 0;
-        if (size > 1) cluster_barrier();  // every CTA of the row is running
-        else __syncthreads();
+    const float rest = p.rest ? p.rest[n] : -INFINITY;
+    for (int i = t; i <= (x.phase + x.n) / 32; i += kThreads) bits[i] = 0;
+    if (t == 0) S.twice = 0;
+    if (size > 1) cluster_barrier();  // every CTA of the row is running
+    else __syncthreads();
 #pragma unroll 1
-        for (int k = t; k < p.K; k += kThreads) {
-            const int id = ids[k];
-            const unsigned a = (unsigned)id - (unsigned)v0;
-            if (a < (unsigned)x.n) {
-                const unsigned b = a + x.phase, bit = 1u << (b & 31);
-                if (atomicOr(&bits[b >> 5], bit) & bit) S.twice = 1;
-            } else if (rank == 0 && id != -1 && (unsigned)id >= (unsigned)p.V) {
-                atomicOr(p.err, kErrBadToken);
-            }
+    for (int k = t; k < p.K; k += kThreads) {
+        const int id = ids[k];
+        const unsigned a = (unsigned)id - (unsigned)v0;
+        if (a < (unsigned)x.n) {
+            const unsigned b = a + x.phase, bit = 1u << (b & 31);
+            if (atomicOr(&bits[b >> 5], bit) & bit) S.twice = 1;
+        } else if (rank == 0 && id != -1 && (unsigned)id >= (unsigned)p.V) {
+            atomicOr(p.err, kErrBadToken);
         }
-        __syncthreads();
-        const bool twice = S.twice != 0;
-        Sums u = {empty_set(), empty_set(), empty_set(), 0.f};
+    }
+    __syncthreads();
+    const bool twice = S.twice != 0;
+    Sums u = {empty_set(), empty_set(), empty_set(), 0.f};
 #pragma unroll 1
-        for (int k = t; k < p.K; k += kThreads) {
-            const int id = ids[k];
-            const unsigned a = (unsigned)id - (unsigned)v0;
-            if (a >= (unsigned)x.n || (twice && !takes_part(ids, k, id, p.V, true))) continue;
-            const float tv = top[k], v = to_f32(x.src[a]);
-            if (tv > u.t.m) {
-                const float m = clamp_max(u.t.m, tv), f = ex2((u.t.m - m) * c);
-                u.t.s *= f;
-                u.a = rescaled(u.a, f);
-                u.t.m = m;
-            }
-            const float e = ex2((tv - u.t.m) * c);
-            u.t.s += e;
-            if (e != 0.f) u.a += e * (tv - v) * inv_t;
-            add(u.s, v, c);
+    for (int k = t; k < p.K; k += kThreads) {
+        const int id = ids[k];
+        const unsigned a = (unsigned)id - (unsigned)v0;
+        if (a >= (unsigned)x.n || (twice && !takes_part(ids, k, id, p.V, true))) continue;
+        const float tv = top[k], v = to_f32(x.src[a]);
+        if (tv > u.t.m) {
+            const float m = clamp_max(u.t.m, tv), f = ex2((u.t.m - m) * c);
+            u.t.s *= f;
+            u.a = rescaled(u.a, f);
+            u.t.m = m;
         }
-        // the outside
-        const unsigned char* masks = reinterpret_cast<const unsigned char*>(bits);
-        const F2 cc = f2(c, c);
-        F2 s = f2(0.f, 0.f);
-        stream<kThreads, kAhead, kStages>(x, ring, [&](int i0, Vec16<T>* v, auto all) {
-            unsigned m[kAhead], any = 0;
+        const float e = ex2((tv - u.t.m) * c);
+        u.t.s += e;
+        if (e != 0.f) u.a += e * (tv - v) * inv_t;
+        add(u.s, v, c);
+    }
+    // the outside
+    const unsigned char* masks = reinterpret_cast<const unsigned char*>(bits);
+    const F2 cc = f2(c, c);
+    F2 s = f2(0.f, 0.f);
+    vectors.run([&](int i0, Vec16<T>* v, auto all) {
+        unsigned m[kAhead], any = 0;
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const int i = i0 + j * kThreads;
-                m[j] = all() || i < x.last ? (kPer == 8 ? masks[i] : masks[i >> 1] >> (i & 1) * 4 & 15u) : 0u;
-                any |= m[j];
-            }
-            if (any) {
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j * kThreads;
+            m[j] = all() || i < x.last ? (kPer == 8 ? masks[i] : masks[i >> 1] >> (i & 1) * 4 & 15u) : 0u;
+            any |= m[j];
+        }
+        if (any) {
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j) strike(v[j], m[j]);
-            }
-            add_vectors<kAhead>(u.o.m, s, v, c, cc);
-        });
-        const float2 h = halves(s);
-        u.o.s = h.x + h.y;
-        const int side = t < 2 * kPer ? x.beside(t) : x.n;
-        if (side < x.n && !(bits[(side + x.phase) >> 5] >> ((side + x.phase) & 31) & 1u)) add(u.o, to_f32(x.src[side]), c);
-        u = warp_join(u, c);
-        // every warp's sums to every CTA of the row
-        if (size > 1) {
-            if (lane < size) *cluster.map_shared_rank(&S.part[rank * kWarps + warp], lane) = u;
-            cluster_barrier();
-        } else {
-            if (lane == 0) S.part[warp] = u;
-            __syncthreads();
+            for (int j = 0; j < kAhead; ++j) strike(v[j], m[j]);
         }
-        if (warp == 0) {
-            const int parts = size * kWarps;
-            u = S.part[min(lane, parts - 1)];
-            if (lane >= parts) u = {empty_set(), empty_set(), empty_set(), 0.f};
-            for (int i = lane + 32; i < parts; i += 32) u = join(u, S.part[i], c);
-            u = warp_join(u, c);
-            Stats st = finish(u, rest, inv_t, c);
-            const float loss = row_loss(u, rest, inv_t, c);
-            if (lane == 0) S.row = st;
-            if (rank == 0 && lane == 0) p.loss[n] = loss;
-        }
-        // whether any CTA of the row saw an id twice
-        if (size > 1) {
-            if (t == 0 && twice) *cluster.map_shared_rank(&S.twice, 0) = 1;
-            cluster_barrier();
-        }
-        if (rank == 0 && t == 0) {
-            S.row.twice = S.twice ? 1.f : 0.f;
-            reinterpret_cast<Stats*>(p.stats)[n] = S.row;
-        }
+        add_vectors<kAhead>(u.o.m, s, v, c, cc);
+    });
+    const float2 h = halves(s);
+    u.o.s = h.x + h.y;
+    const int side = t < 2 * kPer ? x.beside(t) : x.n;
+    if (side < x.n && !(bits[(side + x.phase) >> 5] >> ((side + x.phase) & 31) & 1u)) add(u.o, to_f32(x.src[side]), c);
+    u = warp_join(u, c);
+    // every warp's sums to every CTA of the row
+    if (size > 1) {
+        if (lane < size) *cluster.map_shared_rank(&S.part[rank * kWarps + warp], lane) = u;
+        cluster_barrier();
     } else {
-        T* dx = static_cast<T*>(p.dx) + (size_t)n * p.ld_d + v0;
-        const bool together = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x.src)) & 15) == 0;
-        const Stats st = reinterpret_cast<const Stats*>(p.stats)[n];
-        const bool twice = st.twice != 0.f;
-        const float w = st.has == 0.f ? 0.f : p.weight[n] * inv_t;
-        const float wc = w * st.co;
-        const F2 cc = f2(c, c), minus = f2(-st.mo, -st.mo), scale = f2(wc, wc);
-        if (w == 0.f) {
-            if (together) {
-                uint4* out = reinterpret_cast<uint4*>(dx - x.phase);
-                for (int i = x.first + t; i < x.last; i += kThreads) out[i] = make_uint4(0, 0, 0, 0);
-                const int side = t < 2 * kPer ? x.beside(t) : x.n;
-                if (side < x.n) dx[side] = from_f32<T>(0.f);
-            } else {
-                for (int i = t; i < x.n; i += kThreads) dx[i] = from_f32<T>(0.f);
-            }
-            return;
-        }
-        if (together) {
-            uint4* out = reinterpret_cast<uint4*>(dx - x.phase);
-            stream<kThreads, kAhead, kStages>(x, ring, [&](int i0, Vec16<T>* v, auto all) {
-#pragma unroll
-                for (int j = 0; j < kAhead; ++j) {
-                    Vec16<T> g;
-#pragma unroll
-                    for (int k = 0; k < P; ++k) g.set(k, mul2(scale, ex2x2(mul2(add2(v[j].pair(k), minus), cc))));
-                    if (all() || i0 + j * kThreads < x.last) out[i0 + j * kThreads] = g.q;
-                }
-            });
-            const int side = t < 2 * kPer ? x.beside(t) : x.n;
-            if (side < x.n) dx[side] = from_f32<T>(wc * ex2((to_f32(x.src[side]) - st.mo) * c));
-        } else {
-            for (int i = t; i < x.n; i += kThreads) dx[i] = from_f32<T>(wc * ex2((to_f32(x.src[i]) - st.mo) * c));
-        }
+        if (lane == 0) S.part[warp] = u;
         __syncthreads();
-#pragma unroll 1
-        for (int k = t; k < p.K; k += kThreads) {
-            const int id = ids[k];
-            const unsigned a = (unsigned)id - (unsigned)v0;
-            if (a >= (unsigned)x.n || (twice && !takes_part(ids, k, id, p.V, true))) continue;
-            const float q = st.qx * ex2((to_f32(x.src[a]) - st.mx) * c), pk = st.pt * ex2((top[k] - st.mt) * c);
-            dx[a] = from_f32<T>(w * (q - pk));
-        }
+    }
+    if (warp == 0) {
+        const int parts = size * kWarps;
+        u = S.part[min(lane, parts - 1)];
+        if (lane >= parts) u = {empty_set(), empty_set(), empty_set(), 0.f};
+        for (int i = lane + 32; i < parts; i += 32) u = join(u, S.part[i], c);
+        u = warp_join(u, c);
+        Stats st = finish(u, rest, inv_t, c);
+        const float loss = row_loss(u, rest, inv_t, c);
+        if (lane == 0) S.row = st;
+        if (rank == 0 && lane == 0) p.loss[n] = loss;
+    }
+    // whether any CTA of the row saw an id twice
+    if (size > 1) {
+        if (t == 0 && twice) *cluster.map_shared_rank(&S.twice, 0) = 1;
+        cluster_barrier();
+    }
+    if (rank == 0 && t == 0) {
+        S.row.twice = S.twice ? 1.f : 0.f;
+        reinterpret_cast<Stats*>(p.stats)[n] = S.row;
     }
 }
 
-template <typename T, bool kBackward>
-cudaError_t launch_stream(domino_train_ctx* ctx, const DistillArgs& a, cudaStream_t st) {
+// ---- backward by itself -------------------------------------------------------------
+//
+// Every thread streams 16-byte vectors of its block's slice of the row, writes
+// every element as if it were outside the record and then, after a barrier, the
+// record's entries again.  A row is one block's, or several where there are few
+// rows (until 4 blocks an SM) or its slices would pass 160 KB.  Bound by HBM: 960
+// rows of 151,936 bf16 logits, 0.58 GB, in 90 us, 6.5 TB/s, 0.97 of the measured
+// copy rate.
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) k_backward(DistillArgs p, int chunk, int size) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int P = Vec16<T>::kElems / 2, kPer = Vec16<T>::kElems;
+    const int n = blockIdx.x / size, v0 = min(p.V, (int)(blockIdx.x % size) * chunk), t = threadIdx.x;
+    const float inv_t = 1.f / p.temperature, c = kLog2e / p.temperature;
+    const Vectors<T> x(static_cast<const T*>(p.x) + (size_t)n * p.ld + v0, min(p.V, v0 + chunk) - v0);
+    T* dx = static_cast<T*>(p.dx) + (size_t)n * p.ld_d + v0;
+    const bool together = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x.src)) & 15) == 0;
+    uint4* out = reinterpret_cast<uint4*>(dx - x.phase);
+    const int side = t < 2 * kPer ? x.beside(t) : x.n;
+    const Stats st = reinterpret_cast<const Stats*>(p.stats)[n];
+    const float w = st.has == 0.f ? 0.f : p.weight[n] * inv_t;
+    if (w == 0.f) {
+        if (together) {
+            for (int i = x.first + t; i < x.last; i += kThreads) out[i] = make_uint4(0, 0, 0, 0);
+            if (side < x.n) dx[side] = from_f32<T>(0.f);
+        } else {
+            for (int i = t; i < x.n; i += kThreads) dx[i] = from_f32<T>(0.f);
+        }
+        return;
+    }
+    const float wc = w * st.co;
+    const F2 cc = f2(c, c), minus = f2(-st.mo, -st.mo), scale = f2(wc, wc);
+    if (together) {
+        stream<kThreads, kAhead, kStages>(x, reinterpret_cast<uint4*>(smem), [&](int i0, Vec16<T>* v, auto all) {
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                Vec16<T> g;
+#pragma unroll
+                for (int k = 0; k < P; ++k) g.set(k, mul2(scale, ex2x2(mul2(add2(v[j].pair(k), minus), cc))));
+                if (all() || i0 + j * kThreads < x.last) out[i0 + j * kThreads] = g.q;
+            }
+        });
+        if (side < x.n) dx[side] = from_f32<T>(wc * ex2((to_f32(x.src[side]) - st.mo) * c));
+    } else {
+        for (int i = t; i < x.n; i += kThreads) dx[i] = from_f32<T>(wc * ex2((to_f32(x.src[i]) - st.mo) * c));
+    }
+    __syncthreads();
+    const int32_t* ids = p.ids + (size_t)n * p.K;
+    const float* top = p.top + (size_t)n * p.K;
+    const bool twice = st.twice != 0.f;
+#pragma unroll 1
+    for (int k = t; k < p.K; k += kThreads) {
+        const int id = ids[k];
+        const unsigned a = (unsigned)id - (unsigned)v0;
+        if (a >= (unsigned)x.n || (twice && !takes_part(ids, k, id, p.V, true))) continue;
+        const float q = st.qx * ex2((to_f32(x.src[a]) - st.mx) * c), pk = st.pt * ex2((top[k] - st.mt) * c);
+        dx[a] = from_f32<T>(w * (q - pk));
+    }
+}
+
+// elements of a row's slice when it is cut into `parts`
+inline int slice_of(int V, int parts) { return ((V + parts - 1) / parts + 63) / 64 * 64; }
+
+template <typename T>
+cudaError_t launch_forward(domino_train_ctx* ctx, const DistillArgs& a, cudaStream_t st) {
     int size = 1;
-    auto slice = [&](int parts) { return ((a.V + parts - 1) / parts + 63) / 64 * 64; };
-    while (size < kMaxCluster && (long long)a.n * size < 4 * ctx->num_sms && slice(2 * size) >= 2048) size *= 2;
-    while (size < kMaxCluster && slice(size) * (int)sizeof(T) > 160 * 1024) size *= 2;
-    const int chunk = slice(size);
-    const size_t smem = kRingBytes + (kBackward ? 0 : (size_t)chunk / 8 + 8);
-    auto kern = k_stream<T, kBackward>;
+    while (size < kMaxCluster && (long long)a.n * size < 4 * ctx->num_sms && slice_of(a.V, 2 * size) >= 2048) size *= 2;
+    while (size < kMaxCluster && slice_of(a.V, size) * (int)sizeof(T) > 160 * 1024) size *= 2;
+    const int chunk = slice_of(a.V, size);
+    const size_t smem = kRingBytes + (size_t)chunk / 8 + 8;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = cluster_config((unsigned)a.n * size, kThreads, size, smem, st, &attr);
     ctx->last_launches = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a, chunk);
+    return cudaLaunchKernelEx(&cfg, k_forward<T>, a, chunk);
 }
 
-template <bool kBackward>
-cudaError_t launch(domino_train_ctx* ctx, const DistillArgs& a, cudaStream_t st) {
-    return ctx->cfg.dtype == DOMINO_DTYPE_BF16 ? launch_stream<__nv_bfloat16, kBackward>(ctx, a, st)
-                                               : launch_stream<float, kBackward>(ctx, a, st);
+template <typename T>
+cudaError_t launch_backward(domino_train_ctx* ctx, const DistillArgs& a, cudaStream_t st) {
+    int size = 1;
+    while (size < 64 && (long long)a.n * size < 4 * ctx->num_sms && slice_of(a.V, 2 * size) >= 2048) size *= 2;
+    while (slice_of(a.V, size) * (int)sizeof(T) > 160 * 1024) size *= 2;
+    k_backward<T><<<(unsigned)a.n * size, kThreads, kRingBytes, st>>>(a, slice_of(a.V, size), size);
+    ctx->last_launches = 1;
+    return cudaGetLastError();
 }
 
-}  // namespace
-
-cudaError_t launch_distill_forward(domino_train_ctx* c, const DistillArgs& a, cudaStream_t st) {
-    return launch<false>(c, a, st);
-}
-cudaError_t launch_distill_backward(domino_train_ctx* c, const DistillArgs& a, cudaStream_t st) {
-    return launch<true>(c, a, st);
-}
-
-namespace {
 template <typename T>
 cudaError_t launch_step(domino_train_ctx* ctx, const DistillArgs& a, cudaStream_t st) {
     int size = 1;
-    auto slice = [&](int parts) { return ((a.V + parts - 1) / parts + 63) / 64 * 64; };
-    while (size < kMaxCluster && slice(size) * (int)sizeof(T) > kSliceBytes) size *= 2;
-    while (size < kMaxCluster && (long long)a.n * size < 2 * ctx->num_sms && slice(2 * size) >= 4096) size *= 2;
-    const int chunk = slice(size);
+    while (size < kMaxCluster && slice_of(a.V, size) * (int)sizeof(T) > kSliceBytes) size *= 2;
+    while (size < kMaxCluster && (long long)a.n * size < 2 * ctx->num_sms && slice_of(a.V, 2 * size) >= 4096) size *= 2;
+    const int chunk = slice_of(a.V, size);
     const size_t smem = (size_t)chunk * sizeof(T) + 32 + (size_t)chunk / 8;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kStepThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = size;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = cluster_config(size, kStepThreads, size, smem, st, &attr);
     // one wave of clusters, each taking rows in turn; how many the GPU holds at
     // once depends on how its SMs are grouped, so it is asked (once per context
     // and cluster size)
     int& most = ctx->step_clusters[size];
     if (most == 0) {
-        cfg.gridDim = dim3(size);
         const cudaError_t e = cudaOccupancyMaxActiveClusters(&most, k_step<T>, &cfg);
         if (e != cudaSuccess) return e;
         if (most < 1) most = 1;
@@ -685,18 +691,23 @@ cudaError_t launch_step(domino_train_ctx* ctx, const DistillArgs& a, cudaStream_
     ctx->last_launches = 1;
     return cudaLaunchKernelEx(&cfg, k_step<T>, a, chunk);
 }
+
 }  // namespace
 
 cudaError_t prepare_distill_kernels() {
     cudaError_t e = allow_all(k_step<float>);
     if (e == cudaSuccess) e = allow_all(k_step<__nv_bfloat16>);
-    if (e == cudaSuccess) e = allow_all(k_stream<float, false>);
-    if (e == cudaSuccess) e = allow_all(k_stream<float, true>);
-    if (e == cudaSuccess) e = allow_all(k_stream<__nv_bfloat16, false>);
-    if (e == cudaSuccess) e = allow_all(k_stream<__nv_bfloat16, true>);
+    if (e == cudaSuccess) e = allow_all(k_forward<float>);
+    if (e == cudaSuccess) e = allow_all(k_forward<__nv_bfloat16>);
     return e;
 }
 
+cudaError_t launch_distill_forward(domino_train_ctx* c, const DistillArgs& a, cudaStream_t st) {
+    return c->cfg.dtype == DOMINO_DTYPE_BF16 ? launch_forward<__nv_bfloat16>(c, a, st) : launch_forward<float>(c, a, st);
+}
+cudaError_t launch_distill_backward(domino_train_ctx* c, const DistillArgs& a, cudaStream_t st) {
+    return c->cfg.dtype == DOMINO_DTYPE_BF16 ? launch_backward<__nv_bfloat16>(c, a, st) : launch_backward<float>(c, a, st);
+}
 cudaError_t launch_distill_step(domino_train_ctx* c, const DistillArgs& a, cudaStream_t st) {
     return c->cfg.dtype == DOMINO_DTYPE_BF16 ? launch_step<__nv_bfloat16>(c, a, st) : launch_step<float>(c, a, st);
 }

@@ -35,29 +35,38 @@ struct Vectors {
     }
 };
 
-// Calls f(i, v, all) on the vectors [x.first, x.last) of this thread: kAhead of
-// them, i, i + kThreads, ...; `all` is a std::true_type where every thread has
-// all of them, and v.q is -inf in every element of one past the end where it is
-// not (the last call).  The vectors pass through a ring in shared memory that no
-// other thread touches, filled by asynchronous copies kStages calls ahead: the
-// bytes in flight cost no registers, and nothing waits on a barrier.
-template <int kThreads, int kAhead, int kStages, typename T, typename F>
-__device__ __forceinline__ void stream(const Vectors<T>& x, uint4* ring, F&& f) {
-    constexpr int kCall = kAhead * kThreads;
-    const int t = threadIdx.x, vectors = x.last - x.first, whole = vectors / kCall, calls = (vectors + kCall - 1) / kCall;
-    const unsigned inf = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
-    const uint4* src = x.vec() + x.first + t;  // of the next call to be filled
-    int filled = 0, fill_stage = 0, stage = 0;
-    const auto copy = [](uint4* to, const uint4* from) {
+// The vectors [x.first, x.last) of this thread through a ring in shared memory
+// that no other thread touches, filled by asynchronous copies kStages calls
+// ahead (the first ones by the constructor): the bytes in flight cost no
+// registers, and nothing waits on a barrier.  run(f) calls f(i, v, all) with
+// kAhead vectors, i, i + kThreads, ...; `all` is a std::true_type where every
+// thread has all of them, and v.q is -inf in every element of one past the end
+// where it is not (the last call).
+template <int kThreads, int kAhead, int kStages, typename T>
+struct Streamer {
+    static constexpr int kCall = kAhead * kThreads;
+    uint4* ring;
+    const uint4* src;  // of the next call to be filled
+    int i, vectors, whole, calls, filled, fill_stage;
+
+    __device__ __forceinline__ Streamer(const Vectors<T>& x, uint4* ring_)
+        : ring(ring_ + threadIdx.x), src(x.vec() + x.first + threadIdx.x), i(x.first + (int)threadIdx.x),
+          vectors(x.last - x.first), whole(vectors / kCall), calls((vectors + kCall - 1) / kCall), filled(0),
+          fill_stage(0) {
+#pragma unroll
+        for (int g = 0; g < kStages; ++g) fill();
+    }
+    static __device__ __forceinline__ void copy(uint4* to, const uint4* from) {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(to)), "l"(from) : "memory");
-    };
-    const auto fill = [&] {
-        uint4* slot = ring + fill_stage * kCall + t;
+    }
+    __device__ __forceinline__ void fill() {
+        uint4* slot = ring + fill_stage * kCall;
         if (filled < whole) {
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) copy(slot + j * kThreads, src + j * kThreads);
         } else if (filled < calls) {
-            const int left = vectors - filled * kCall - t;  // of this thread on
+            const unsigned inf = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
+            const int left = vectors - filled * kCall - (int)threadIdx.x;  // of this thread on
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
                 if (j * kThreads < left) copy(slot + j * kThreads, src + j * kThreads);
@@ -68,29 +77,34 @@ __device__ __forceinline__ void stream(const Vectors<T>& x, uint4* ring, F&& f) 
         ++filled;
         src += kCall;
         fill_stage = fill_stage + 1 == kStages ? 0 : fill_stage + 1;
-    };
-    const auto take = [&](Vec16<T>* v) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-        const uint4* slot = ring + stage * kCall + t;
+    }
+    template <typename F>
+    __device__ __forceinline__ void run(F&& f) {
+        int stage = 0;
+        const auto take = [&](Vec16<T>* v) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            const uint4* slot = ring + stage * kCall;
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) v[j].q = slot[j * kThreads];
-        stage = stage + 1 == kStages ? 0 : stage + 1;
-    };
-#pragma unroll
-    for (int g = 0; g < kStages; ++g) fill();
-    int i = x.first + t;
+            for (int j = 0; j < kAhead; ++j) v[j].q = slot[j * kThreads];
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+        };
 #pragma unroll 1
-    for (int g = 0; g < whole; ++g, i += kCall) {
-        Vec16<T> v[kAhead];
-        take(v);
-        f(i, v, std::true_type());
-        fill();
+        for (int g = 0; g < whole; ++g, i += kCall) {
+            Vec16<T> v[kAhead];
+            take(v);
+            f(i, v, std::true_type());
+            fill();
+        }
+        if (calls > whole) {
+            Vec16<T> v[kAhead];
+            take(v);
+            f(i, v, std::false_type());
+        }
     }
-    if (calls > whole) {
-        Vec16<T> v[kAhead];
-        take(v);
-        f(i, v, std::false_type());
-    }
+};
+template <int kThreads, int kAhead, int kStages, typename T, typename F>
+__device__ __forceinline__ void stream(const Vectors<T>& x, uint4* ring, F&& f) {
+    Streamer<kThreads, kAhead, kStages, T>(x, ring).run(f);
 }
 
 // the elements of a vector that `m` names set to -inf
