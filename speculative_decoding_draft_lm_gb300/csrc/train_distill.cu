@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_forward(DistillArgs p, int chun
     const int v0 = min(p.V, rank * chunk);
     const Vectors<T> x(static_cast<const T*>(p.x) + (size_t)n * p.ld + v0, min(p.V, v0 + chunk) - v0);
     // the first vectors are on their way while the record is read
-    Streamer<kThreads, kAhead, kStages, T> vectors(x, ring);
+    Streamer<kThreads, kAhead, kStages, false, T> vectors(x, ring);
     const int32_t* ids = p.ids + (size_t)n * p.K;
     const float* top = p.top + (size_t)n * p.K;
 

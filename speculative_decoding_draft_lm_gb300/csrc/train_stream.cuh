@@ -42,17 +42,29 @@ struct Vectors {
 // kAhead vectors, i, i + kThreads, ...; `all` is a std::true_type where every
 // thread has all of them, and v.q is -inf in every element of one past the end
 // where it is not (the last call).
-template <int kThreads, int kAhead, int kStages, typename T>
+//
+// kTogether: the vectors of a call are kAhead consecutive ones of each thread,
+// from i on, in an order of the lane's own; a warp's copies are one piece of the
+// ring and every lane reads what other lanes asked for.
+template <int kThreads, int kAhead, int kStages, bool kTogether, typename T>
 struct Streamer {
     static constexpr int kCall = kAhead * kThreads;
+    static constexpr int kStep = kTogether ? 32 : kThreads;  // between a thread's copies of a call
+    static_assert(!kTogether || kAhead == 4, "the order in which a lane reads is without bank conflicts for 4");
     uint4* ring;
     const uint4* src;  // of the next call to be filled
-    int i, vectors, whole, calls, filled, fill_stage;
+    int i, ahead, vectors, whole, calls, filled, fill_stage;
 
-    __device__ __forceinline__ Streamer(const Vectors<T>& x, uint4* ring_)
-        : ring(ring_ + threadIdx.x), src(x.vec() + x.first + threadIdx.x), i(x.first + (int)threadIdx.x),
-          vectors(x.last - x.first), whole(vectors / kCall), calls((vectors + kCall - 1) / kCall), filled(0),
-          fill_stage(0) {
+    __device__ __forceinline__ Streamer(const Vectors<T>& x, uint4* ring_) {
+        const int t = (int)threadIdx.x, first = kTogether ? t / 32 * (32 * kAhead) + t % 32 : t;  // copy of a call
+        ring = ring_ + first;
+        src = x.vec() + x.first + first;
+        i = x.first + (kTogether ? t * kAhead : t);
+        vectors = x.last - x.first;
+        whole = vectors / kCall;
+        calls = (vectors + kCall - 1) / kCall;
+        filled = fill_stage = 0;
+        ahead = first;
 #pragma unroll
         for (int g = 0; g < kStages; ++g) fill();
     }
@@ -63,14 +75,14 @@ struct Streamer {
         uint4* slot = ring + fill_stage * kCall;
         if (filled < whole) {
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) copy(slot + j * kThreads, src + j * kThreads);
+            for (int j = 0; j < kAhead; ++j) copy(slot + j * kStep, src + j * kStep);
         } else if (filled < calls) {
             const unsigned inf = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
-            const int left = vectors - filled * kCall - (int)threadIdx.x;  // of this thread on
+            const int left = vectors - filled * kCall - ahead;  // of this thread's first on
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                if (j * kThreads < left) copy(slot + j * kThreads, src + j * kThreads);
-                else slot[j * kThreads] = make_uint4(inf, inf, inf, inf);
+                if (j * kStep < left) copy(slot + j * kStep, src + j * kStep);
+                else slot[j * kStep] = make_uint4(inf, inf, inf, inf);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -84,8 +96,18 @@ struct Streamer {
         const auto take = [&](Vec16<T>* v) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
             const uint4* slot = ring + stage * kCall;
+            if (kTogether) {
+                // eight lanes' reads lie in different banks
+                const int lane = (int)threadIdx.x % 32, turn = lane / 2 % 4;
+                slot += lane * 3;  // of the warp's piece: lane * kAhead
+                __syncwarp();
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) v[j].q = slot[j * kThreads];
+                for (int j = 0; j < kAhead; ++j) v[j].q = slot[j ^ turn];
+                __syncwarp();  // before the next copies over them
+            } else {
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) v[j].q = slot[j * kThreads];
+            }
             stage = stage + 1 == kStages ? 0 : stage + 1;
         };
 #pragma unroll 1
@@ -104,7 +126,7 @@ struct Streamer {
 };
 template <int kThreads, int kAhead, int kStages, typename T, typename F>
 __device__ __forceinline__ void stream(const Vectors<T>& x, uint4* ring, F&& f) {
-    Streamer<kThreads, kAhead, kStages, T>(x, ring).run(f);
+    Streamer<kThreads, kAhead, kStages, false, T>(x, ring).run(f);
 }
 
 // the elements of a vector that `m` names set to -inf

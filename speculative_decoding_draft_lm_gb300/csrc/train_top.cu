@@ -5,11 +5,11 @@
 // two zeros equal; a 64-bit word, orderable logit over inverted id, has that
 // order.
 //
-// The row is read once.  A thread's four vectors of a step of the stream are a
-// group; the CTA keeps every group's largest logit and the sum of its
-// exponentials in shared memory, so the stream itself has no barrier and no
-// branch on the data.  A bound that K elements reach and few others comes from
-// the threads' maxima (small K) or the groups'.  The groups below it are in the
+// The row is read once.  Four vectors in a row, 64 bytes, are a group; the CTA
+// keeps every group's largest logit and the sum of its exponentials in shared
+// memory, so the stream itself has no block-wide barrier and no branch on the
+// data.  A bound that K elements reach and few others comes from two maxima per
+// thread (small K) or the groups'.  The groups below it are in the
 // rest with their sums, the others (about K of them) are read again, mostly from
 // L2: what lies above the bound becomes a word in a buffer, of which an exact
 // radix select leaves K; what equals it only leaves a bit in the order of the
@@ -23,13 +23,16 @@
 // each: every CTA finds its slice's best K and rank 0 takes the others' through
 // distributed shared memory.
 //
-// 960 rows of 151,936 bf16 logits, K = 256: 105 us, 2.8 TB/s, 0.42 of the
-// measured copy rate.  Of a row's 55 K cycles (two CTAs an SM) the stream takes
-// 25 K, the second read 12 K, the select 6 K, the list of groups, the bound and
-// the order of the ids 3 K each: instructions (58 % of the issue slots) and the
-// barriers between the small steps bound it, not HBM.  333 rows of 79,999 fp32
-// logits, K = 2048: 99 us (41 % of the row is read again); 15 rows, K = 64: 21 us.
-// A running bound raised by selects during the stream took 369, 281 and 76 us.
+// 960 rows of 151,936 bf16 logits, K = 256: 86 us, 3.4 TB/s, 0.51 of the measured
+// copy rate.  Of a row's 66 K cycles (three CTAs an SM) the stream takes 35 K, the
+// second read 12 K, the select 6 K, the bound, the list of groups and the order of
+// the ids 3 K each: the chains of small steps behind the stream and the
+// instructions (half of the issue slots) bound it, not HBM.  333 rows of 79,999
+// fp32 logits, K = 2048: 92 us (41 % of the row is read again); 15 rows, K = 64:
+// 17.5 us.  Groups of four vectors 4 or 8 KB apart: 93 us for the 960 rows (half of
+// every sector read again was not wanted); several groups per thread between two
+// counts of the words: 87 to 89 us.  A running bound raised by selects during the
+// stream took 369, 281 and 76 us.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -44,17 +47,18 @@ namespace train {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kAhead = 4;
 constexpr int kStages = 2;
-constexpr size_t kRingBytes = (size_t)kThreads * kAhead * kStages * 16;
 constexpr int kBins = 2048;
 constexpr int kFew = 64;     // a record whose ids are ordered by counting
 constexpr int kDue = 512;    // words beyond K that make a select due
-constexpr int kStep = 1024;  // words that are sure to fit then: two per thread
+constexpr int kStep = 1024;  // words that are sure to fit then, a multiple of the threads
 constexpr int kSpread = 8;  // CTAs that a row is spread over for speed alone (15 rows: 4 25 us, 8 21 us; of 16 only 14 clusters fit at once: 39 us)
 constexpr size_t kMaxSmem = 224 * 1024;  // of a CTA, beside its static variables
+// A CTA has 256 threads where three such fit an SM, else 512: every step that the
+// whole CTA takes costs instructions by the warp.  960 rows, K = 256: 86 us with
+// 256, 95 with 512; 333 rows, K = 2048, two CTAs an SM either way: 105 and 92 us.
+constexpr size_t kThirdSmem = 74 * 1024;  // of one of three CTAs on an SM
 
 __device__ __forceinline__ unsigned top_key(float x) { return x != x ? 0xFFFFFFFFu : ord_f32(x); }
 __device__ __forceinline__ float key_logit(unsigned k) { return k == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : unord_f32(k); }
@@ -81,12 +85,12 @@ constexpr int kTies = 64;  // equal logits that are ordered by counting
 constexpr int kTile = 8;  // words per thread that a select moves at once
 
 struct TopShared {
-    unsigned warp[kWarps];
+    unsigned warp[16];  // 512 threads at most
     unsigned digit, need, in_bin, ties;
     unsigned long long last;
     unsigned bound;
-    MaxSum part[kWarps];
-    MaxSum rest;   // the CTA's rest
+    MaxSum part[16];
+    MaxSum rest[kMaxCluster];  // of every CTA of the row, at rank 0
 };
 
 // A bit per element of v that lies above b (NaN does) and per element that
@@ -130,6 +134,7 @@ __device__ __forceinline__ Vec16<__nv_bfloat16> above(const Vec16<__nv_bfloat16>
 }
 
 // Exclusive scan of one value per thread; *total gets the sum.
+template <int kThreads>
 __device__ __forceinline__ unsigned block_scan(unsigned x, unsigned* warp_tot, unsigned* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     unsigned incl = x;
@@ -142,7 +147,7 @@ __device__ __forceinline__ unsigned block_scan(unsigned x, unsigned* warp_tot, u
     __syncthreads();
     unsigned before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         const unsigned v = warp_tot[w];
         if (w < warp) before += v;
         all += v;
@@ -152,12 +157,13 @@ __device__ __forceinline__ unsigned block_scan(unsigned x, unsigned* warp_tot, u
     return before + incl - x;
 }
 
+template <int kThreads>
 __device__ __forceinline__ unsigned block_max(unsigned x, unsigned* warp_tot) {
     x = __reduce_max_sync(0xffffffffu, x);
     if ((threadIdx.x & 31) == 0) warp_tot[threadIdx.x >> 5] = x;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) x = max(x, warp_tot[w]);
+    for (int w = 0; w < kThreads / 32; ++w) x = max(x, warp_tot[w]);
     __syncthreads();
     return x;
 }
@@ -165,12 +171,14 @@ __device__ __forceinline__ unsigned block_max(unsigned x, unsigned* warp_tot) {
 // Shared memory of a slice of `elems` elements: the ring of the stream, in whose
 // place come the histogram, the buffer of K + kDue + kStep words and the list of
 // groups; behind it the groups' sums and maxima, in whose place comes a bit per id.
-template <typename T>
+template <typename T, int kThreads>
 __host__ __device__ constexpr int groups_of(int elems) {
     return (elems / Group<T>::kElems + kThreads) / kThreads * kThreads;  // one vector more than elems if unaligned
 }
 __host__ __device__ constexpr size_t words_bytes(int K) { return (size_t)(K + kDue + kStep) * 8; }
+template <int kThreads>
 __host__ __device__ constexpr size_t front_bytes(int groups, int K) {
+    constexpr size_t kRingBytes = (size_t)kThreads * kAhead * kStages * 16;
     const size_t later = (size_t)kBins * 4 + words_bytes(K) + (size_t)groups * 2;
     return ((kRingBytes > later ? kRingBytes : later) + 15) / 16 * 16;
 }
@@ -180,7 +188,7 @@ __host__ __device__ constexpr size_t group_bytes(int groups) { return (size_t)gr
 // The digit of the `need`-th largest among the words word(0..n-1) that match
 // prefix under mask, its count and what remains to be found in it, to S.  All
 // threads; hist is all zeros before and after.
-template <typename F>
+template <int kThreads, typename F>
 __device__ __forceinline__ void digit_pass(TopShared& S, unsigned* hist, F&& word, int n, unsigned long long prefix,
                                            unsigned long long mask, int shift, int bins, unsigned need) {
     const int t = threadIdx.x;
@@ -195,7 +203,7 @@ __device__ __forceinline__ void digit_pass(TopShared& S, unsigned* hist, F&& wor
     unsigned mine = 0, all;
     if (first >= 0)
         for (int j = 0; j < per; ++j) mine += hist[first - j];
-    unsigned above = block_scan(mine, S.warp, &all);
+    unsigned above = block_scan<kThreads>(mine, S.warp, &all);
     if (above < need && above + mine >= need) {
         int b = first;
         while (above + hist[b] < need) above += hist[b--];
@@ -219,7 +227,7 @@ __device__ __forceinline__ void search_range(unsigned low, unsigned largest, int
 
 // A bound for the K largest of n logits: the K-th largest's key, or a little
 // less.  All keys lie in [lowest, largest].
-template <bool kShort, typename R>
+template <int kThreads, bool kShort, typename R>
 __device__ __noinline__ unsigned bound_by(TopShared& S, unsigned* hist, const R* raw, int n, int K, unsigned lowest,
                                           unsigned largest) {
     constexpr int kFloor = kShort ? 16 : 0;
@@ -230,7 +238,7 @@ __device__ __noinline__ unsigned bound_by(TopShared& S, unsigned* hist, const R*
     while (bit > kFloor) {
         const int bits = min(11, bit - kFloor);
         bit -= bits;
-        digit_pass(S, hist, [&](int i) { return (unsigned long long)top_key(from_raw(raw[i])) << 32; }, n, prefix, mask,
+        digit_pass<kThreads>(S, hist, [&](int i) { return (unsigned long long)top_key(from_raw(raw[i])) << 32; }, n, prefix, mask,
                    32 + bit, 1 << bits, need);
         prefix |= (unsigned long long)S.digit << (32 + bit);
         mask |= (unsigned long long)((1u << bits) - 1) << (32 + bit);
@@ -250,7 +258,7 @@ struct Selected {
 // Leaves the best K of `count` words at the front of the buffer; every word's
 // key lies in [low, largest].  kShort: logits with 16 significant bits.  All
 // threads, after a barrier, count > K.
-template <bool kShort>
+template <int kThreads, bool kShort>
 __device__ __noinline__ Selected select(TopShared& S, unsigned long long* buf, unsigned* hist, int count, int K,
                                         unsigned low, unsigned largest, MaxSum rest, float c, bool want_bound) {
     const int t = threadIdx.x;
@@ -264,7 +272,7 @@ __device__ __noinline__ Selected select(TopShared& S, unsigned long long* buf, u
     while (bit > kFloor && !found) {
         const int bits = min(11, bit - kFloor);
         bit -= bits;
-        digit_pass(S, hist, word, count, prefix, mask, 32 + bit, 1 << bits, need);
+        digit_pass<kThreads>(S, hist, word, count, prefix, mask, 32 + bit, 1 << bits, need);
         prefix |= (unsigned long long)S.digit << (32 + bit);
         mask |= (unsigned long long)((1u << bits) - 1) << (32 + bit);
         need = S.need;
@@ -297,7 +305,7 @@ __device__ __noinline__ Selected select(TopShared& S, unsigned long long* buf, u
         prefix |= 0xFFF00000ull;
         mask = ~0ull << 20;
         for (int shift = 10; shift >= 0 && !found; shift -= 10) {
-            digit_pass(S, hist, word, count, prefix, mask, shift, 1024, need);
+            digit_pass<kThreads>(S, hist, word, count, prefix, mask, shift, 1024, need);
             prefix |= (unsigned long long)S.digit << shift;
             mask |= 1023ull << shift;
             need = S.need;
@@ -322,7 +330,7 @@ __device__ __noinline__ Selected select(TopShared& S, unsigned long long* buf, u
                 add(rest, key_logit((unsigned)(w[j] >> 32)), c);
             }
         }
-        unsigned at = kept + block_scan((unsigned)__popc(keep), S.warp, &all);
+        unsigned at = kept + block_scan<kThreads>((unsigned)__popc(keep), S.warp, &all);
 #pragma unroll
         for (int j = 0; j < kTile; ++j) {
             if (i0 + j * kThreads >= count) break;
@@ -330,16 +338,18 @@ __device__ __noinline__ Selected select(TopShared& S, unsigned long long* buf, u
         }
         kept += all;
     }
-    return {want_bound ? ~block_max(~least, S.warp) : 0u, rest};
+    return {want_bound ? ~block_max<kThreads>(~least, S.warp) : 0u, rest};
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logits, long long ld, int V, int K,
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 2) k_top(const T* __restrict__ logits, long long ld, int V, int K,
                                                      float temperature, int32_t* __restrict__ ids,
                                                      float* __restrict__ top, float* __restrict__ rest, int chunk) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ TopShared S;
     constexpr bool kShort = sizeof(T) == 2;
+    constexpr int kWarps = kThreads / 32;
+    constexpr int kSlots = 2 * kThreads;  // maxima that a bound may be taken from: of every thread's even and odd steps
     constexpr int kPer = Vec16<T>::kElems, P = kPer / 2;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
@@ -347,8 +357,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
     unsigned* hist = reinterpret_cast<unsigned*>(smem);
     unsigned long long* buf = reinterpret_cast<unsigned long long*>(hist + kBins);
     uint16_t* list = reinterpret_cast<uint16_t*>(smem + kBins * 4 + words_bytes(K));
-    const int most_groups = groups_of<T>(chunk);
-    float* sums = reinterpret_cast<float*>(smem + front_bytes(most_groups, K));
+    const int most_groups = groups_of<T, kThreads>(chunk);
+    float* sums = reinterpret_cast<float*>(smem + front_bytes<kThreads>(most_groups, K));
     Raw<T>* maxima = reinterpret_cast<Raw<T>*>(sums + most_groups);
     const int v0 = min(V, rank * chunk);
     const Vectors<T> x(logits + (size_t)n * ld + v0, min(V, v0 + chunk) - v0);
@@ -356,9 +366,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
     const F2 cc = f2(c, c);
 
     // the groups: a thread's vectors of a step, kThreads groups a step (-inf where there is nothing)
-    float largest_here = -INFINITY;
+    float slot[2] = {-INFINITY, -INFINITY};
     int at_group = t;
-    stream<kThreads, kAhead, kStages>(x, reinterpret_cast<uint4*>(smem), [&](int, Vec16<T>* v, auto) {
+    Streamer<kThreads, kAhead, kStages, true, T> vectors(x, reinterpret_cast<uint4*>(smem));
+    vectors.run([&](int, Vec16<T>* v, auto) {
         float m = v[0].top_nan();
 #pragma unroll
         for (int j = 1; j < kAhead; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(v[j].top_nan()));
@@ -374,7 +385,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
         sums[at_group] = h.x + h.y;
         maxima[at_group] = to_raw<T>(m);
         at_group += kThreads;
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(largest_here) : "f"(m));
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(slot[0]));
+        slot[0] = slot[1];
+        slot[1] = m;
     });
     const int groups = at_group - t;
     __syncthreads();  // the ring is free, the groups are there
@@ -386,20 +399,22 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
     unsigned bound = 0;
     {
         for (int i = t; i < kBins; i += kThreads) hist[i] = 0;
-        const bool by_threads = K <= kThreads * 3 / 4;
-        unsigned lowest = top_key(largest_here);
-        const unsigned largest = block_max(lowest, S.warp);
+        const bool by_slots = K <= kSlots * 3 / 4;
+        const unsigned keys[2] = {top_key(slot[0]), top_key(slot[1])};
+        unsigned lowest = min(keys[0], keys[1]);
+        const unsigned largest = block_max<kThreads>(max(keys[0], keys[1]), S.warp);
         uint32_t* all = reinterpret_cast<uint32_t*>(buf);
-        if (by_threads) {
-            all[t] = __float_as_uint(largest_here);
+        if (by_slots) {
+            all[t] = __float_as_uint(slot[0]);
+            all[kThreads + t] = __float_as_uint(slot[1]);
         } else {
             for (int g = t; g < groups; g += kThreads) lowest = min(lowest, top_key(from_raw(maxima[g])));
         }
-        lowest = ~block_max(~lowest, S.warp);
-        if (by_threads)
-            bound = bound_by<kShort>(S, hist, all, kThreads, K, lowest, largest);
+        lowest = ~block_max<kThreads>(~lowest, S.warp);
+        if (by_slots)
+            bound = bound_by<kThreads, kShort>(S, hist, all, kSlots, K, lowest, largest);
         else if (x.last - x.first >= K * kAhead)
-            bound = bound_by<kShort>(S, hist, maxima, groups, K, lowest, largest);
+            bound = bound_by<kThreads, kShort>(S, hist, maxima, groups, K, lowest, largest);
         if (kShort) bound &= 0xFFFF0000u;
         bound = min(bound, 0xFF800000u);  // +inf: a NaN is never below the bound
     }
@@ -411,23 +426,37 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
     MaxSum r = empty_set();
     int listed;
     {
+        struct alignas(4 * sizeof(Raw<T>)) Four {
+            Raw<T> m[4];
+        };
+        const Four* four = reinterpret_cast<const Four*>(maxima);
         int mine = 0;
         float m = -INFINITY;
 #pragma unroll 2
-        for (int g = t; g < groups; g += kThreads) {
-            const float y = from_raw(maxima[g]);
-            const bool in = !(y < bound_logit);
-            mine += in;
-            if (!in) m = fmaxf(m, y);
+        for (int i = t; i < groups / 4; i += kThreads) {
+            const Four y4 = four[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float y = from_raw(y4.m[j]);
+                const bool in = !(y < bound_logit);
+                mine += in;
+                if (!in) m = fmaxf(m, y);
+            }
         }
-        unsigned all, at = block_scan((unsigned)mine, S.warp, &all);  // this thread's first place
+        unsigned all, at = block_scan<kThreads>((unsigned)mine, S.warp, &all);  // this thread's first place
         listed = (int)all;
         r.m = clamp_max(-FLT_MAX, m);
-#pragma unroll 2
-        for (int g = t; g < groups; g += kThreads) {
-            const float y = from_raw(maxima[g]);
-            if (!(y < bound_logit)) list[at++] = (uint16_t)g;
-            else r.s += sums[g] * ex2((clamp_max(-FLT_MAX, y) - r.m) * c);
+#pragma unroll 1
+        for (int i = t; i < groups / 4; i += kThreads) {
+            const Four y4 = four[i];
+            const float4 s4 = reinterpret_cast<const float4*>(sums)[i];
+            const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float y = from_raw(y4.m[j]);
+                if (!(y < bound_logit)) list[at++] = (uint16_t)(4 * i + j);
+                else r.s += s[j] * ex2((clamp_max(-FLT_MAX, y) - r.m) * c);
+            }
         }
     }
     __syncthreads();
@@ -445,8 +474,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
     int equals = 0;         // this thread's elements that equal the bound
     const auto reduce = [&] {  // the buffer's best K
         if (count <= K) return;
-        const unsigned top_key_seen = block_max(most, S.warp);
-        const Selected got = select<kShort>(S, buf, hist, count, K, bound, top_key_seen, r, c, size > 1);
+        const unsigned top_key_seen = block_max<kThreads>(most, S.warp);
+        const Selected got = select<kThreads, kShort>(S, buf, hist, count, K, bound, top_key_seen, r, c, size > 1);
         last = got.bound;
         r = got.rest;
         count = K;
@@ -455,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
     // has no room for all threads' words (for kStep it always has).
     const auto take = [&](unsigned n_words, auto&& write) {
         unsigned all;
-        const unsigned at = block_scan(n_words, S.warp, &all);
+        const unsigned at = block_scan<kThreads>(n_words, S.warp, &all);
         if (count + (int)all > K + kDue + kStep) return false;
         if (n_words) write(buf + count + at);
         count += (int)all;
@@ -468,51 +497,47 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
     // the listed groups again, a group per thread
 #pragma unroll 1
     for (int l0 = 0; l0 < listed; l0 += kThreads) {
-        Vec16<T> v[kAhead];
-        const unsigned inf = kShort ? 0xFF80FF80u : 0xFF800000u;
-        const int g = l0 + t < listed ? list[l0 + t] : groups;
-        const int i0 = x.first + g / kThreads * (kAhead * kThreads) + g % kThreads;
+        unsigned pass = 0;  // a bit per element above the bound; those below it into the rest
+        const int i0 = x.first + (l0 + t < listed ? list[l0 + t] : groups) * kAhead;
+        if (l0 + t - lane < listed) {
+            Vec16<T> v[kAhead];
+            const unsigned inf = kShort ? 0xFF80FF80u : 0xFF800000u;
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            v[j].q = make_uint4(inf, inf, inf, inf);
-            if (i0 + j * kThreads < x.last) v[j].q = x.vec()[i0 + j * kThreads];
-        }
-        // a bit per element above the bound; those below it into the rest
-        unsigned pass = 0;
-        MaxSum o = empty_set();
-        F2 s = f2(0.f, 0.f);
+            for (int j = 0; j < kAhead; ++j) {
+                v[j].q = make_uint4(inf, inf, inf, inf);
+                if (i0 + j < x.last) v[j].q = x.vec()[i0 + j];
+            }
+            MaxSum o = empty_set();
+            F2 s = f2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            if (l0 + t - lane >= listed) break;  // a warp without groups
-            unsigned in = 0, eq = 0;
-            Vec16<T> others = v[j];
-            if (i0 + j * kThreads < x.last) others = above(v[j], bound_logit, &in, &eq);
-            pass |= in << (j * kPer);
-            if (in) most = max(most, top_key(v[j].top_nan()));
-            if (eq) {
-                const int at = (i0 + j * kThreads) * kPer;
-                atomicOr(&equal[at >> 5], eq << (at & 31));
-                equals += __popc(eq);
+            for (int j = 0; j < kAhead; ++j) {
+                unsigned in = 0, eq = 0;
+                Vec16<T> others = v[j];
+                if (i0 + j < x.last) others = above(v[j], bound_logit, &in, &eq);
+                pass |= in << (j * kPer);
+                if (in) most = max(most, top_key(v[j].top_nan()));
+                if (eq) {
+                    const int at = (i0 + j) * kPer;
+                    atomicOr(&equal[at >> 5], eq << (at & 31));
+                    equals += __popc(eq);
+                }
+                v[j] = others;
             }
-            const float m = others.top();
-            if (m > o.m) {
-                const float to = clamp_max(o.m, m), f = ex2((o.m - to) * c);
-                s = mul2(s, f2(f, f));
-                o.m = to;
-            }
+            o.m = clamp_max(-FLT_MAX, top_of<kAhead>(v));
             const F2 minus = f2(-o.m, -o.m);
 #pragma unroll
-            for (int e = 0; e < P; ++e) s = add2(s, ex2x2(mul2(add2(others.pair(e), minus), cc)));
+            for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+                for (int e = 0; e < P; ++e) s = add2(s, ex2x2(mul2(add2(v[j].pair(e), minus), cc)));
+            const float2 h = halves(s);
+            o.s = h.x + h.y;
+            r = join(r, o, c);
         }
-        const float2 h = halves(s);
-        o.s = h.x + h.y;
-        r = join(r, o, c);
         // the words of the elements that `some` names, their logits once more from memory
         const auto write = [&](unsigned long long* to, unsigned some) {
 #pragma unroll 1
-            while (some) {
-                const int b = __ffs((int)some) - 1, at = (i0 + b / kPer * kThreads) * kPer - x.phase + b % kPer;
-                some &= some - 1;
+            for (; some; some &= some - 1) {
+                const int at = i0 * kPer - x.phase + __ffs((int)some) - 1;
                 *to++ = word_of(top_key(to_f32(x.src[at])), (unsigned)(v0 + at));
             }
         };
@@ -542,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
         const int from = min(equal_words, t * per), to = min(equal_words, from + per);
         unsigned mine = 0, all;
         for (int i = from; i < to; ++i) mine += (unsigned)__popc(equal[i]);
-        int at = (int)block_scan(mine, S.warp, &all);
+        int at = (int)block_scan<kThreads>(mine, S.warp, &all);
         const int taken = min(lack, (int)all);
         for (int i = from; i < to && at < taken; ++i)
             for (unsigned m = equal[i]; m && at < taken; m &= m - 1)
@@ -559,36 +584,38 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
         cluster_barrier();
         if (rank == 0) {
             // the other slices' words: a warp per slice, kWords of a lane at once
-            static_assert(kWarps >= kMaxCluster, "a warp per slice");
             const unsigned beaten = count == K ? last : 0u;  // a higher id with this key comes after all K of this slice
             constexpr int kWords = kStep / kThreads;
-            const int from = 1 + warp, each = min(K, chunk);
-            const int here = from < size ? min(K, min(V, (from + 1) * chunk) - min(V, from * chunk)) : 0;
-            const unsigned long long* theirs = cluster.map_shared_rank(buf, min(from, size - 1));
-            for (int i0 = 0; i0 < each; i0 += 32 * kWords) {
-                unsigned long long w[kWords];
-                unsigned pass = 0;
+            const int each = min(K, chunk);
+#pragma unroll 1
+            for (int from = 1 + warp; from - warp < size; from += kWarps) {
+                const int here = from < size ? min(K, min(V, (from + 1) * chunk) - min(V, from * chunk)) : 0;
+                const unsigned long long* theirs = cluster.map_shared_rank(buf, min(from, size - 1));
+                for (int i0 = 0; i0 < each; i0 += 32 * kWords) {
+                    unsigned long long w[kWords];
+                    unsigned pass = 0;
 #pragma unroll
-                for (int j = 0; j < kWords; ++j) {
-                    const int i = i0 + 32 * j + lane;
-                    w[j] = i < here ? theirs[i] : 0;
-                }
-#pragma unroll
-                for (int j = 0; j < kWords; ++j) {
-                    const unsigned k = (unsigned)(w[j] >> 32);  // 0: no word
-                    if (k == 0) continue;
-                    if (k > beaten) {
-                        pass |= 1u << j;
-                        most = max(most, k);
-                    } else {
-                        add(r, key_logit(k), c);
+                    for (int j = 0; j < kWords; ++j) {
+                        const int i = i0 + 32 * j + lane;
+                        w[j] = i < here ? theirs[i] : 0;
                     }
-                }
-                take((unsigned)__popc(pass), [&](unsigned long long* to) {
 #pragma unroll
-                    for (int j = 0; j < kWords; ++j)
-                        if (pass >> j & 1u) *to++ = w[j];
-                });
+                    for (int j = 0; j < kWords; ++j) {
+                        const unsigned k = (unsigned)(w[j] >> 32);  // 0: no word
+                        if (k == 0) continue;
+                        if (k > beaten) {
+                            pass |= 1u << j;
+                            most = max(most, k);
+                        } else {
+                            add(r, key_logit(k), c);
+                        }
+                    }
+                    take((unsigned)__popc(pass), [&](unsigned long long* to) {
+#pragma unroll
+                        for (int j = 0; j < kWords; ++j)
+                            if (pass >> j & 1u) *to++ = w[j];
+                    });
+                }
             }
             __syncthreads();
             reduce();
@@ -604,20 +631,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
             r = lane < kWarps ? S.part[lane] : empty_set();
             const float all = warp_max(r.m);
             r.s = warp_sum(r.s * ex2((r.m - all) * c));
-            if (lane == 0) S.rest = {all, r.s};
+            r.m = all;
+            if (lane == 0) *cluster.map_shared_rank(&S.rest[rank], 0) = r;
         }
     }
     if (size > 1) {
         cluster_barrier();
-        if (rank == 0 && t == 0) {
-            MaxSum whole_row = S.rest;
-            for (int i = 1; i < size; ++i) whole_row = join(whole_row, *cluster.map_shared_rank(&S.rest, i), c);
-            S.rest = whole_row;
-        }
-        cluster_barrier();  // the others' shared memory was read
         if (rank != 0) return;
+        if (warp == 0) {
+            r = lane < size ? S.rest[lane] : empty_set();
+            const float all = warp_max(r.m);
+            r.s = warp_sum(r.s * ex2((r.m - all) * c));
+            r.m = all;
+        }
     }
-    if (t == 0) rest[n] = S.rest.s == 0.f ? -INFINITY : S.rest.m / temperature + logf(S.rest.s);
+    if (t == 0) rest[n] = r.s == 0.f ? -INFINITY : r.m / temperature + logf(r.s);
 
     if (K <= kFew) {  // ascending ids: a word's place is the number of lower ids
         if (t - lane >= K) return;
@@ -645,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
     __syncthreads();
     unsigned mine = 0, all;
     for (int j = 0; j < per; ++j) mine += (unsigned)__popc(bits[t * per + j]);
-    before[t] = block_scan(mine, S.warp, &all);
+    before[t] = block_scan<kThreads>(mine, S.warp, &all);
     __syncthreads();
     for (int i = t; i < K; i += kThreads) {
         const unsigned long long w = buf[i];
@@ -657,33 +685,52 @@ __global__ void __launch_bounds__(kThreads, 2) k_top(const T* __restrict__ logit
     }
 }
 
+inline int slice_of(int V, int parts) { return ((V + parts - 1) / parts + 63) / 64 * 64; }
+
+// the CTAs of a row, from `size` on, and the shared memory that each needs
+template <typename T, int kThreads>
+size_t spread(int V, int K, int* size) {
+    const size_t bits = (size_t)((V + 31) / 32 + kThreads) * 4;
+    for (;; *size *= 2) {
+        const int groups = groups_of<T, kThreads>(slice_of(V, *size));
+        const size_t back = group_bytes<T>(groups);
+        const size_t smem = front_bytes<kThreads>(groups, K) + (back > bits ? back : bits);
+        if (*size == kMaxCluster || smem <= kMaxSmem) return smem;
+    }
+}
+
+template <typename T, int kThreads>
+cudaError_t launch_with(int size, size_t smem, int V, const void* x, long long ld, int n, int K, float temperature,
+                        int32_t* ids, float* top, float* rest, cudaStream_t st) {
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = cluster_config((unsigned)n * size, kThreads, size, smem, st, &attr);
+    return cudaLaunchKernelEx(&cfg, k_top<T, kThreads>, static_cast<const T*>(x), ld, V, K, temperature, ids, top, rest,
+                              slice_of(V, size));
+}
+
 template <typename T>
 cudaError_t launch(domino_train_ctx* c, const void* x, long long ld, int n, int K, float temperature, int32_t* ids,
                    float* top, float* rest, cudaStream_t st) {
     const int V = c->cfg.V;
     int size = 1;
-    auto slice = [&](int parts) { return ((V + parts - 1) / parts + 63) / 64 * 64; };
     // few rows: spread them while the slices stay longer than what they keep
-    while (size < kSpread && (long long)n * size < 2 * c->num_sms && slice(2 * size) >= 2 * K + 2048) size *= 2;
-    const size_t bits = (size_t)((V + 31) / 32 + kThreads) * 4;
-    size_t smem;
-    for (;; size *= 2) {
-        const int groups = groups_of<T>(slice(size));
-        smem = front_bytes(groups, K) + (group_bytes<T>(groups) > bits ? group_bytes<T>(groups) : bits);
-        if (size == kMaxCluster || smem <= kMaxSmem) break;
-    }
-    auto kern = k_top<T>;
-    cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = cluster_config((unsigned)n * size, kThreads, size, smem, st, &attr);
+    while (size < kSpread && (long long)n * size < 2 * c->num_sms && slice_of(V, 2 * size) >= 2 * K + 2048) size *= 2;
     c->last_launches = 1;
-    return cudaLaunchKernelEx(&cfg, kern, static_cast<const T*>(x), ld, V, K, temperature, ids, top, rest, slice(size));
+    int small = size;
+    const size_t smem = spread<T, 256>(V, K, &small);
+    if (smem <= kThirdSmem) return launch_with<T, 256>(small, smem, V, x, ld, n, K, temperature, ids, top, rest, st);
+    const size_t more = spread<T, 512>(V, K, &size);
+    return launch_with<T, 512>(size, more, V, x, ld, n, K, temperature, ids, top, rest, st);
 }
 
 }  // namespace
 
 cudaError_t prepare_top_kernels() {
-    const cudaError_t e = allow_all(k_top<float>);
-    return e == cudaSuccess ? allow_all(k_top<__nv_bfloat16>) : e;
+    cudaError_t e = allow_all(k_top<float, 256>);
+    if (e == cudaSuccess) e = allow_all(k_top<float, 512>);
+    if (e == cudaSuccess) e = allow_all(k_top<__nv_bfloat16, 256>);
+    if (e == cudaSuccess) e = allow_all(k_top<__nv_bfloat16, 512>);
+    return e;
 }
 
 cudaError_t launch_top(domino_train_ctx* c, const void* x, int dtype, long long ld, int n, int K, float temperature,
