@@ -35,10 +35,28 @@ struct Stats {
 };
 static_assert(sizeof(Stats) == DOMINO_TRAIN_STATS * sizeof(float), "stats row");
 
-struct Sums {
+struct alignas(16) Sums {
     MaxSum t, s, o;  // teacher's record, student's record, student's outside
     float a;         // sum 2^((t - mt) c) (t - x) / T
+    float twice;     // forward: an id was seen twice
 };
+__device__ __forceinline__ Sums no_sums() { return {empty_set(), empty_set(), empty_set(), 0.f, 0.f}; }
+
+// One thread's sums into a CTA's shared memory, counted on that CTA's barrier:
+// the reader waits for the bytes alone.  A barrier of the cluster would make
+// every thread wait until its stores to global memory are done.
+__device__ __forceinline__ void send(const Sums& u, Sums* to, unsigned long long* bar, int rank) {
+    static_assert(sizeof(Sums) == 32, "two 16-byte stores");
+    uint32_t dst, mbar;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(tc::smem_u32(to)), "r"(rank));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(mbar) : "r"(tc::smem_u32(bar)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+                 "f"(u.t.m), "f"(u.t.s), "f"(u.s.m), "f"(u.s.s), "r"(mbar)
+                 : "memory");
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst + 16),
+                 "f"(u.o.m), "f"(u.o.s), "f"(u.a), "f"(u.twice), "r"(mbar)
+                 : "memory");
+}
 
 // a sum scaled to a new maximum; an infinite term whose weight vanished is 0
 __device__ __forceinline__ float rescaled(float a, float f) { return f == 0.f ? 0.f : a * f; }
@@ -49,6 +67,7 @@ __device__ __forceinline__ Sums join(const Sums& x, const Sums& y, float c) {
     r.s = join(x.s, y.s, c);
     r.o = join(x.o, y.o, c);
     r.a = rescaled(x.a, ex2((x.t.m - r.t.m) * c)) + rescaled(y.a, ex2((y.t.m - r.t.m) * c));
+    r.twice = fmaxf(x.twice, y.twice);
     return r;
 }
 
@@ -134,22 +153,22 @@ __device__ __noinline__ bool takes_part(const int32_t* ids, int k, int id, int V
 // ---- loss and gradient at once ---------------------------------------------------
 //
 // A cluster of CTAs holds one row in shared memory, a slice each: a bulk copy
-// brings it in, the sums are a pass over shared memory, the clusters' CTAs
-// exchange theirs through distributed shared memory, and a second pass writes
-// the gradient.  So the logits are read once and the gradient is written once,
-// which is all the traffic there is: 3840 rows of 151,936 bf16 logits in 433 us,
-// 5.4 TB/s, 0.81 of the measured copy rate (349 us); 15 rows in 9.3 us.
+// brings it in, the sums are a pass over shared memory, the cluster's CTAs send
+// theirs into each other's shared memory, and a second pass writes the gradient.
+// So the logits are read once and the gradient is written once, which is all the
+// traffic there is: 3840 rows of 151,936 bf16 logits in 367 us, 6.4 TB/s, 0.95 of
+// the measured copy rate (349 us); 15 rows in 8.3 us.
 //
-// What bounds it is how long a slice stays in shared memory, not arithmetic:
-// without the exchange, whose cost is the wait for the slowest of eight CTAs,
-// the same kernel took 396 us, and without the passes 407 us.  Hence slices of
-// 40 KB, of which five fit an SM, in one wave of clusters that take rows in turn
-// (clusters of 4, 7, 9 and 10 CTAs: 464, 440, 444 and 446 us); the gradient
-// straight to memory, so that the buffer is free once it is read (through the
-// buffer and a bulk copy: 496 us); everything of a row that is not its logits
-// read a row ahead (two entries of the record a thread: with one, 436 us); the loss after the gradient's factors.  Two half-size
-// buffers per CTA, in clusters of 16, took 744 us.  Reading the row twice from
-// global memory instead (the second time from L2) took 564 us.
+// What bounds it is HBM, and how long a slice stays in shared memory.  Hence
+// slices of 40 KB, of which five fit an SM, in one wave of clusters that take rows
+// in turn (clusters of 4, 7, 9 and 10 CTAs were slower); the sums by stores that
+// count on the reader's barrier (with a barrier of the cluster, which also waits
+// for the last row's gradient to arrive in memory: 433 us); the gradient straight
+// to memory, so that the buffer is free once it is read (through the buffer and a
+// bulk copy: 60 us more); everything of a row that is not its logits read a row
+// ahead, two entries of the record a thread; the loss after the gradient's
+// factors.  Two half-size buffers per CTA, in clusters of 16, took 744 us, reading
+// the row twice from global memory (the second time from L2) 564 us.
 //
 // The forward alone streams its rows instead (below): this kernel without its
 // second pass took 87 us for 960 rows against 66 us.
@@ -165,7 +184,8 @@ constexpr int kStepWarps = kStepThreads / 32;
 struct StepShared {
     Sums part[2][kMaxCluster * kStepWarps];  // every warp of the row, by the row's parity
     Stats row;
-    unsigned long long bar;  // the row's copy has come
+    unsigned long long bar;          // the row's copy has come
+    unsigned long long exchange[2];  // the row's sums have come, by the row's parity
     int twice, abort;
 };
 
@@ -291,6 +311,7 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
     Ahead now = ahead(n);
     if (t == 0) {
         tc::mbar_init(bar, 1);
+        for (int i = 0; i < 2; ++i) tc::mbar_init(tc::smem_u32(&S.exchange[i]), 1);
         S.twice = S.abort = 0;
         tc::fence_barrier_init();
         if (now.weight != 0.f) request(slice(n));
@@ -298,7 +319,7 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
     if (now.weight != 0.f) slice(n).load_edges();
     for (int i = t; i < chunk / 32; i += kStepThreads) bits[i] = 0;
     cluster_barrier();  // every CTA of the cluster is running
-    uint32_t phase = 0;  // parity of the next copy and of the next exchange
+    uint32_t turn = 0;  // rows so far that had weight
     for (; n < p.n; n += stride) {
         const Ahead next = ahead(n + stride);
         const Slice<T> x = slice(n);
@@ -327,11 +348,12 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
             for (int j = 0; j < kHeld; ++j) mark(now.id[j]);
 #pragma unroll 1
             for (int k = t + kHeld * kStepThreads; k < p.K; k += kStepThreads) mark(ids[k]);
+            const uint32_t phase = turn & 1;  // of the copy, and which exchange it is
             if (t == 0) tc::mbar_wait(bar, phase, &S.abort, p.err);
             __syncthreads();
             twice = S.twice != 0;
 
-            Sums u = {empty_set(), empty_set(), empty_set(), 0.f};
+            Sums u = no_sums();
             const auto gather = [&](int k, int id, float tv) {
                 const unsigned a = place(id);
                 if (a == kNone || (twice && !takes_part(ids, k, id, p.V, true))) return 0.f;
@@ -359,12 +381,15 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
             u.o = sum_vectors<T>(x.vec, x.nvec, c);
             u = warp_join(u, c);
             // every warp's sums to every CTA of the row
-            if (lane < size) *cluster.map_shared_rank(&S.part[phase][rank * kStepWarps + warp], lane) = u;
-            cluster_barrier();
+            // (to the other place than the last row's: who sends for this row has seen
+            // every CTA's sums of the last one, so all have read those of the one before)
+            if (t == 0) tc::mbar_arrive_expect_tx(tc::smem_u32(&S.exchange[phase]), size * kStepWarps * sizeof(Sums));
+            if (lane < size) send(u, &S.part[phase][rank * kStepWarps + warp], &S.exchange[phase], lane);
             if (warp == 0) {
+                tc::mbar_wait(tc::smem_u32(&S.exchange[phase]), turn >> 1 & 1, &S.abort, p.err);
                 const Sums* part = S.part[phase];
                 u = part[min(lane, size * kStepWarps - 1)];
-                if (lane >= size * kStepWarps) u = {empty_set(), empty_set(), empty_set(), 0.f};
+                if (lane >= size * kStepWarps) u = no_sums();
                 for (int i = lane + 32; i < size * kStepWarps; i += 32) u = join(u, part[i], c);
                 u = warp_join(u, c);
                 const Stats st = finish(u, now.rest, inv_t, c);
@@ -375,7 +400,7 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
                 const float loss = row_loss(u, now.rest, inv_t, c);
                 if (lane == 0) p.loss[n] = loss;
             }
-            phase ^= 1;
+            ++turn;
             const Stats st = S.row;
             w = st.has == 0.f ? 0.f : now.weight * inv_t;
             if (w != 0.f) {
@@ -440,14 +465,15 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
         }
         now = next;
     }
-    // A CTA whose copy never came has gone on through its cluster's exchanges,
-    // with meaningless data and without further copies; it gives the lost one a
-    // last chance to land before it leaves.
+    // A CTA whose copy or whose peers' sums never came has gone on, with
+    // meaningless data and without further copies; it gives the lost ones a last
+    // chance to land before it leaves.
     if (t == 0 && S.abort) {
         const unsigned long long t0 = tc::globaltimer();
-        while (!tc::mbar_try_wait(bar, phase ^ 1) && tc::globaltimer() - t0 < 2000000ull) {
+        while (!tc::mbar_try_wait(bar, (turn & 1) ^ 1) && tc::globaltimer() - t0 < 2000000ull) {
         }
     }
+    cluster_barrier();  // nobody leaves before all have their sums
 }
 
 // ---- forward by itself ---------------------------------------------------------------
@@ -455,13 +481,15 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
 // Every thread streams 16-byte vectors of its CTA's slice of the row, and skips
 // the record's entries by a bit per element, one byte (half a byte) of which
 // covers a vector.  A row is one CTA's, or a cluster's where there are few rows
-// (until 4 CTAs an SM) or its slices would pass 160 KB.  960 rows of 151,936 bf16
-// logits, 0.29 GB: 66 us, 4.4 TB/s.  Without the masks and the additions it took
-// 65 us when it took 70 with them: what bounds it is how the CTAs start, which is
-// why the first vectors are asked for before the record is read (71 us where
-// they were not).  512 and 128 threads: 71 and 72 us; 2 vectors at once and 3
-// stages: 65 us, and 53.5 against 51.5 us for forward and backward of 240 fp32 rows
-// of 79,999.
+// (until 4 CTAs an SM) or its slices would pass 160 KB; only rank 0 waits for the
+// others' sums.  960 rows of 151,936 bf16 logits, 0.29 GB: 63 us, 4.6 TB/s.  What
+// bounds it is how the CTAs start and end, and instructions (two thirds of the
+// issue slots): without the masks and the additions it was 5 us faster.  Hence the
+// first vectors are asked for before the record is read (else 5 us more), and the
+// sums go by stores that count on rank 0's barrier (with barriers of the cluster:
+// 66 us, and 51 us instead of 47 for forward and backward of 240 fp32 rows of 79,999).
+// 512 and 128 threads: 5 and 6 us more; 2 vectors at once and 3 stages: 2 us more
+// for the fp32 rows.
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -470,9 +498,9 @@ constexpr int kStages = 2;
 constexpr size_t kRingBytes = (size_t)kThreads * kAhead * kStages * 16;
 
 struct StreamShared {
-    Sums part[kMaxCluster * kWarps];
-    Stats row;
-    int twice;
+    Sums part[kMaxCluster * kWarps];  // every warp of the row, at rank 0
+    unsigned long long bar;           // they have come
+    int twice, abort;
 };
 
 template <typename T>
@@ -495,9 +523,13 @@ __global__ void __launch_bounds__(kThreads, 4) k_forward(DistillArgs p, int chun
 
     const float rest = p.rest ? p.rest[n] : -INFINITY;
     for (int i = t; i <= (x.phase + x.n) / 32; i += kThreads) bits[i] = 0;
-    if (t == 0) S.twice = 0;
-    if (size > 1) cluster_barrier();  // every CTA of the row is running
-    else __syncthreads();
+    if (t == 0) {
+        S.twice = S.abort = 0;
+        tc::mbar_init(tc::smem_u32(&S.bar), 1);
+        tc::fence_barrier_init();
+    }
+    __syncthreads();
+    if (size > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 #pragma unroll 1
     for (int k = t; k < p.K; k += kThreads) {
         const int id = ids[k];
@@ -511,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_forward(DistillArgs p, int chun
     }
     __syncthreads();
     const bool twice = S.twice != 0;
-    Sums u = {empty_set(), empty_set(), empty_set(), 0.f};
+    Sums u = no_sums();
 #pragma unroll 1
     for (int k = t; k < p.K; k += kThreads) {
         const int id = ids[k];
@@ -552,33 +584,32 @@ __global__ void __launch_bounds__(kThreads, 4) k_forward(DistillArgs p, int chun
     const int side = t < 2 * kPer ? x.beside(t) : x.n;
     if (side < x.n && !(bits[(side + x.phase) >> 5] >> ((side + x.phase) & 31) & 1u)) add(u.o, to_f32(x.src[side]), c);
     u = warp_join(u, c);
-    // every warp's sums to every CTA of the row
+    // every warp's sums to rank 0, which is running by now; the others are done
+    u.twice = twice ? 1.f : 0.f;
+    const int parts = size * kWarps;
     if (size > 1) {
-        if (lane < size) *cluster.map_shared_rank(&S.part[rank * kWarps + warp], lane) = u;
-        cluster_barrier();
+        __syncwarp();
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (rank == 0 && t == 0) tc::mbar_arrive_expect_tx(tc::smem_u32(&S.bar), parts * sizeof(Sums));
+        if (lane == 0) send(u, &S.part[rank * kWarps + warp], &S.bar, 0);
+        if (rank != 0 || warp != 0) return;
+        tc::mbar_wait(tc::smem_u32(&S.bar), 0, &S.abort, p.err);
     } else {
         if (lane == 0) S.part[warp] = u;
         __syncthreads();
+        if (warp != 0) return;
     }
-    if (warp == 0) {
-        const int parts = size * kWarps;
-        u = S.part[min(lane, parts - 1)];
-        if (lane >= parts) u = {empty_set(), empty_set(), empty_set(), 0.f};
-        for (int i = lane + 32; i < parts; i += 32) u = join(u, S.part[i], c);
-        u = warp_join(u, c);
-        Stats st = finish(u, rest, inv_t, c);
-        const float loss = row_loss(u, rest, inv_t, c);
-        if (lane == 0) S.row = st;
-        if (rank == 0 && lane == 0) p.loss[n] = loss;
-    }
-    // whether any CTA of the row saw an id twice
-    if (size > 1) {
-        if (t == 0 && twice) *cluster.map_shared_rank(&S.twice, 0) = 1;
-        cluster_barrier();
-    }
-    if (rank == 0 && t == 0) {
-        S.row.twice = S.twice ? 1.f : 0.f;
-        reinterpret_cast<Stats*>(p.stats)[n] = S.row;
+    u = S.part[min(lane, parts - 1)];
+    if (lane >= parts) u = no_sums();
+    for (int i = lane + 32; i < parts; i += 32) u = join(u, S.part[i], c);
+    u = warp_join(u, c);
+    const bool any_twice = __any_sync(0xffffffffu, u.twice != 0.f);
+    Stats st = finish(u, rest, inv_t, c);
+    st.twice = any_twice ? 1.f : 0.f;
+    const float loss = row_loss(u, rest, inv_t, c);
+    if (lane == 0) {
+        p.loss[n] = loss;
+        reinterpret_cast<Stats*>(p.stats)[n] = st;
     }
 }
 

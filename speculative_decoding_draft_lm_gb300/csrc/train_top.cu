@@ -53,7 +53,7 @@ constexpr int kBins = 2048;
 constexpr int kFew = 64;     // a record whose ids are ordered by counting
 constexpr int kDue = 512;    // words beyond K that make a select due
 constexpr int kStep = 1024;  // words that are sure to fit then, a multiple of the threads
-constexpr int kSpread = 8;  // CTAs that a row is spread over for speed alone (15 rows: 4 25 us, 8 21 us; of 16 only 14 clusters fit at once: 39 us)
+constexpr int kSpread = 8;  // CTAs that a row is spread over for speed alone (15 rows: half as many cost a fifth more; of 16 only 14 clusters fit at once: twice the time)
 constexpr size_t kMaxSmem = 224 * 1024;  // of a CTA, beside its static variables
 // A CTA has 256 threads where three such fit an SM, else 512: every step that the
 // whole CTA takes costs instructions by the warp.  960 rows, K = 256: 86 us with
@@ -392,10 +392,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 2) k_top(const
     const int groups = at_group - t;
     __syncthreads();  // the ring is free, the groups are there
 
-    // The bound.  For a K well below the number of threads the K-th largest of
-    // the threads' maxima does: K elements reach it, and in a row without order
-    // about -ln(1 - K / kThreads) kThreads do.  Else the K-th largest of the
-    // groups'; with fewer groups than K every group is read again.
+    // The bound.  For a K well below the number of slots (every thread's even and
+    // odd steps) the K-th largest of their maxima does: K elements reach it, and in
+    // a row without order about -ln(1 - K / kSlots) kSlots do.  Else the K-th
+    // largest of the groups'; with fewer groups than K every group is read again.
     unsigned bound = 0;
     {
         for (int i = t; i < kBins; i += kThreads) hist[i] = 0;
