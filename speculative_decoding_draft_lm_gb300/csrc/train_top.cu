@@ -19,9 +19,11 @@
 // the rounding of the whole.  Places in lists come from scans, not from atomics,
 // so that equal calls sum in equal order.
 //
-// Few rows, and rows whose groups do not fit one CTA, are spread over a cluster
-// each: every CTA finds its slice's best K and rank 0 takes the others' through
-// distributed shared memory.
+// Rows whose groups do not fit one CTA are spread over a cluster: every CTA finds
+// its slice's best K and rank 0 takes the others' through distributed shared
+// memory.  Few rows are not: the merge costs more than the stream gains (15 rows,
+// a CTA each or eight: K = 64 14.5 and 17.5 us, K = 512 27 and 54 us, K = 2048 48
+// and 150 us).
 //
 // 960 rows of 151,936 bf16 logits, K = 256: 86 us, 3.4 TB/s, 0.51 of the measured
 // copy rate.  Of a row's 66 K cycles (three CTAs an SM) the stream takes 35 K, the
@@ -29,7 +31,7 @@
 // the ids 3 K each: the chains of small steps behind the stream and the
 // instructions (half of the issue slots) bound it, not HBM.  333 rows of 79,999
 // fp32 logits, K = 2048: 92 us (41 % of the row is read again); 15 rows, K = 64:
-// 17.5 us.  Groups of four vectors 4 or 8 KB apart: 93 us for the 960 rows (half of
+// 14.5 us.  Groups of four vectors 4 or 8 KB apart: 93 us for the 960 rows (half of
 // every sector read again was not wanted); several groups per thread between two
 // counts of the words: 87 to 89 us.  A running bound raised by selects during the
 // stream took 369, 281 and 76 us.
@@ -53,11 +55,12 @@ constexpr int kBins = 2048;
 constexpr int kFew = 64;     // a record whose ids are ordered by counting
 constexpr int kDue = 512;    // words beyond K that make a select due
 constexpr int kStep = 1024;  // words that are sure to fit then, a multiple of the threads
-constexpr int kSpread = 8;  // CTAs that a row is spread over for speed alone (15 rows: half as many cost a fifth more; of 16 only 14 clusters fit at once: twice the time)
 constexpr size_t kMaxSmem = 224 * 1024;  // of a CTA, beside its static variables
-// A CTA has 256 threads where three such fit an SM, else 512: every step that the
-// whole CTA takes costs instructions by the warp.  960 rows, K = 256: 86 us with
-// 256, 95 with 512; 333 rows, K = 2048, two CTAs an SM either way: 105 and 92 us.
+// A CTA has 256 threads where three such fit an SM: every step that the whole CTA
+// takes costs instructions by the warp (960 rows, K = 256: 86 us with 256, 95 with
+// 512).  It has 512 where fewer fit (333 rows, K = 2048: 105 and 92 us) and where
+// rows are alone on their SMs, if the record is not small (15 rows, K = 2048: 56 and
+// 48 us, K = 256: 23 and 21; K = 64: 14.8 and 16.5).
 constexpr size_t kThirdSmem = 74 * 1024;  // of one of three CTAs on an SM
 
 __device__ __forceinline__ unsigned top_key(float x) { return x != x ? 0xFFFFFFFFu : ord_f32(x); }
@@ -80,6 +83,8 @@ __device__ __forceinline__ Raw<T> to_raw(float m) {
 }
 __device__ __forceinline__ float from_raw(uint16_t r) { return __uint_as_float((unsigned)r << 16); }
 __device__ __forceinline__ float from_raw(uint32_t r) { return __uint_as_float(r); }
+__device__ __forceinline__ float from_raw(float r) { return r; }
+__device__ __forceinline__ float from_raw(__nv_bfloat16 r) { return to_f32(r); }
 
 constexpr int kTies = 64;  // equal logits that are ordered by counting
 constexpr int kTile = 8;  // words per thread that a select moves at once
@@ -392,14 +397,17 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 2) k_top(const
     const int groups = at_group - t;
     __syncthreads();  // the ring is free, the groups are there
 
-    // The bound.  For a K well below the number of slots (every thread's even and
-    // odd steps) the K-th largest of their maxima does: K elements reach it, and in
-    // a row without order about -ln(1 - K / kSlots) kSlots do.  Else the K-th
-    // largest of the groups'; with fewer groups than K every group is read again.
+    // The bound.  For a K well below the number of slots in use (every thread's even
+    // and odd steps) the K-th largest of their maxima does: K elements reach it, and
+    // in a row without order about -ln(1 - K / slots) slots do.  Else the K-th
+    // largest of the groups', or, where the groups are few, of the elements
+    // themselves (19 rows of 12,064 bf16 logits, K = 1888: 23 us; with every group
+    // read again without a bound 69 us).
     unsigned bound = 0;
     {
         for (int i = t; i < kBins; i += kThreads) hist[i] = 0;
-        const bool by_slots = K <= kSlots * 3 / 4;
+        const int nvec = x.last - x.first, used = min(nvec / kAhead, kSlots);
+        const bool by_slots = 4 * K <= 3 * used, by_groups = 4 * (long long)K * kAhead <= 3 * (long long)nvec;
         const unsigned keys[2] = {top_key(slot[0]), top_key(slot[1])};
         unsigned lowest = min(keys[0], keys[1]);
         const unsigned largest = block_max<kThreads>(max(keys[0], keys[1]), S.warp);
@@ -407,14 +415,16 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 2) k_top(const
         if (by_slots) {
             all[t] = __float_as_uint(slot[0]);
             all[kThreads + t] = __float_as_uint(slot[1]);
-        } else {
+        } else if (by_groups) {
             for (int g = t; g < groups; g += kThreads) lowest = min(lowest, top_key(from_raw(maxima[g])));
         }
         lowest = ~block_max<kThreads>(~lowest, S.warp);
         if (by_slots)
             bound = bound_by<kThreads, kShort>(S, hist, all, kSlots, K, lowest, largest);
-        else if (x.last - x.first >= K * kAhead)
+        else if (by_groups)
             bound = bound_by<kThreads, kShort>(S, hist, maxima, groups, K, lowest, largest);
+        else if (nvec * kPer > K + kDue)
+            bound = bound_by<kThreads, kShort>(S, hist, reinterpret_cast<const T*>(x.vec() + x.first), nvec * kPer, K, 0u, largest);
         if (kShort) bound &= 0xFFFF0000u;
         bound = min(bound, 0xFF800000u);  // +inf: a NaN is never below the bound
     }
@@ -712,13 +722,12 @@ template <typename T>
 cudaError_t launch(domino_train_ctx* c, const void* x, long long ld, int n, int K, float temperature, int32_t* ids,
                    float* top, float* rest, cudaStream_t st) {
     const int V = c->cfg.V;
-    int size = 1;
-    // few rows: spread them while the slices stay longer than what they keep
-    while (size < kSpread && (long long)n * size < 2 * c->num_sms && slice_of(V, 2 * size) >= 2 * K + 2048) size *= 2;
     c->last_launches = 1;
-    int small = size;
-    const size_t smem = spread<T, 256>(V, K, &small);
-    if (smem <= kThirdSmem) return launch_with<T, 256>(small, smem, V, x, ld, n, K, temperature, ids, top, rest, st);
+    int size = 1;
+    const size_t smem = spread<T, 256>(V, K, &size);
+    if (smem <= kThirdSmem && (n > c->num_sms || K <= kFew))
+        return launch_with<T, 256>(size, smem, V, x, ld, n, K, temperature, ids, top, rest, st);
+    size = 1;
     const size_t more = spread<T, 512>(V, K, &size);
     return launch_with<T, 512>(size, more, V, x, ld, n, K, temperature, ids, top, rest, st);
 }

@@ -188,3 +188,26 @@ def test_clustered_candidates(dtype):
     for K in (1, 50, 400, 3000):
         check(rows(x, TORCH[dtype]), K, 1.0)
     check(rows(np.repeat(x, 100, 0), TORCH[dtype]), 50, 1.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("N,V,K", [(19, 12064, 1888), (400, 9001, 380), (400, 12063, 4000), (3, 30000, 8192), (700, 2500, 700)])
+def test_records_of_much_of_a_row(dtype, N, V, K):
+    """K near the number of vectors, or above it; plain rows, few distinct logits, masked ones and sorted ones."""
+    g = np.random.default_rng(V + K)
+    x = g.normal(0, 2, (N, V))
+    x[1 % N] = g.integers(-2, 3, V)
+    x[2 % N, K // 2:] = -np.inf
+    x[0] = np.sort(x[0])
+    check(rows(x, TORCH[dtype], 3, 1), K, 1.0)
+
+
+@pytest.mark.parametrize("K", [1, 64, 700, 8192])
+def test_rows_longer_than_a_block_holds(K):
+    """fp32 rows whose groups are spread over several blocks: ties, masks that leave slices empty, all in one slice."""
+    V = 500003
+    g = np.random.default_rng(K)
+    x = np.stack([g.normal(0, 2, V), g.integers(-3, 4, V) * 1.0, np.where(np.arange(V) < V - 100, -np.inf, 1.0),
+                  np.where(np.arange(V) > 9000, -np.inf, g.normal(0, 1, V)), np.full(V, -np.inf), np.sort(g.normal(0, 1, V)),
+                  np.where(g.random(V) < 0.01, np.nan, 3.0)])
+    check(rows(x, torch.float32, 1), K, 1.0)
