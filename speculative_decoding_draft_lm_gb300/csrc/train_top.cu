@@ -402,12 +402,15 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 2) k_top(const
     // in a row without order about -ln(1 - K / slots) slots do.  Else the K-th
     // largest of the groups', or, where the groups are few, of the elements
     // themselves (19 rows of 12,064 bf16 logits, K = 1888: 23 us; with every group
-    // read again without a bound 69 us).
+    // read again without a bound 69 us), or not twice K and the row short (400 rows of
+    // 9,001 fp32 logits, K = 380: 33 us, by the slots 76; but 400 rows of 60,000 bf16
+    // logits, K = 1200: 107 us by the elements, 66 by the groups).
     unsigned bound = 0;
     {
         for (int i = t; i < kBins; i += kThreads) hist[i] = 0;
         const int nvec = x.last - x.first, used = min(nvec / kAhead, kSlots);
-        const bool by_slots = 4 * K <= 3 * used, by_groups = 4 * (long long)K * kAhead <= 3 * (long long)nvec;
+        const bool loose = nvec < 2 * K * kAhead && nvec * kPer <= 16384;  // many elements may pass, few are to be read
+        const bool by_slots = !loose && 4 * K <= 3 * used, by_groups = !loose && 4 * K * kAhead <= 3 * nvec;
         const unsigned keys[2] = {top_key(slot[0]), top_key(slot[1])};
         unsigned lowest = min(keys[0], keys[1]);
         const unsigned largest = block_max<kThreads>(max(keys[0], keys[1]), S.warp);
