@@ -128,7 +128,8 @@ DOMINO_API int domino_train_embed_grad(domino_train_ctx* ctx, const void* dout, 
                                        int n_tokens, float scale, void* dtable, int grad_dtype, int accumulate,
                                        void* cuda_stream);
 
-/* Synchronise `cuda_stream`, then return and clear the device error word
+/* Take the device error word in the order of `cuda_stream`, leave 0 in its
+ * place, synchronise that stream (no other) and return the word's status
  * (DOMINO_OK, DOMINO_ERR_BAD_TOKEN, or DOMINO_ERR_TIMEOUT after a device-side
  * wait ran out of time and left its row's results meaningless), or
  * DOMINO_ERR_CUDA. */

@@ -49,6 +49,10 @@ train::DistillArgs distill_args(const domino_train_ctx* c, const void* x, long l
     return a;
 }
 
+// The error word to `taken`, and 0 in its place: in one step, so that what
+// another stream raises meanwhile is in this answer or in the next.
+__global__ void k_take_error(int* err, int* taken) { *taken = atomicExch(err, 0); }
+
 }  // namespace
 
 extern "C" {
@@ -79,7 +83,7 @@ int domino_train_init(domino_train_ctx** out, const domino_train_config* cfg, in
         return o;
     };
     const size_t n = (size_t)cfg->max_tokens, tiles = (n + train::kSortTile - 1) / train::kSortTile;
-    const size_t o_err = take(sizeof(int));
+    const size_t o_err = take(2 * sizeof(int));
     size_t o_keys[2], o_pos[2];
     for (int i = 0; i < 2; ++i) {
         o_keys[i] = take(n * 4);
@@ -221,10 +225,16 @@ int domino_train_embed_grad(domino_train_ctx* c, const void* dout, long long ld,
 int domino_train_status(domino_train_ctx* c, void* stream) {
     if (!c) return DOMINO_ERR_INVALID_ARG;
     DeviceGuard guard(c->device);
-    if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return DOMINO_ERR_CUDA;
+    // all in the stream's order: another stream, the default one too, is not ordered with it
+    const cudaStream_t st = (cudaStream_t)stream;
+    cudaLaunchConfig_t one = {};
+    one.gridDim = one.blockDim = dim3(1);
+    one.stream = st;
     int word = 0;
-    if (cudaMemcpy(&word, c->err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return DOMINO_ERR_CUDA;
-    if (word && cudaMemset(c->err, 0, sizeof(int)) != cudaSuccess) return DOMINO_ERR_CUDA;
+    if (cudaLaunchKernelEx(&one, k_take_error, c->err, c->err + 1) != cudaSuccess ||
+        cudaMemcpyAsync(&word, c->err + 1, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return DOMINO_ERR_CUDA;
     if (word & kErrTimeout) return DOMINO_ERR_TIMEOUT;
     return word & kErrBadToken ? DOMINO_ERR_BAD_TOKEN : DOMINO_OK;
 }

@@ -10,7 +10,7 @@ struct domino_train_ctx {
     int device;
     int num_sms;
     int last_launches;
-    int* err;             // device error word
+    int* err;             // device error word, and behind it the word that domino_train_status took
     int step_clusters[17];  // clusters of each size that the GPU holds at once in distill_step (0: not asked yet)
     // embed_grad workspace (max_tokens > 0)
     uint32_t* keys[2];    // [max_tokens] tokens between the passes of the sort

@@ -1,0 +1,46 @@
+"""The device error word: read and cleared in the order of the caller's stream."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def _tok(a):
+    return torch.as_tensor(np.asarray(a, dtype=np.int32)).cuda()
+
+
+def test_status_waits_for_its_own_stream_only():
+    """Work on the default stream (a spin of about half a second) neither delays status() nor is waited for."""
+    from speculative_decoding_draft_lm_gb300 import rollout as R
+    from speculative_decoding_draft_lm_gb300.train import DominoTrain
+    tr = DominoTrain(20, E=8, dtype="fp32")
+    W, bad, side = torch.ones(20, 8, device="cuda"), _tok([3, 20]), torch.cuda.Stream()
+    with torch.cuda.stream(side):  # a kernel's first launch loads it, which may wait for the device
+        tr.embed(W, bad)
+        assert tr.status() == R.DOMINO_ERR_BAD_TOKEN
+    torch.cuda.synchronize()
+    torch.cuda._sleep(1_000_000_000)
+    busy = torch.cuda.Event()
+    busy.record()
+    with torch.cuda.stream(side):
+        tr.embed(W, bad)
+        assert tr.status() == R.DOMINO_ERR_BAD_TOKEN
+        assert tr.status() == 0
+    assert not busy.query()
+    torch.cuda.synchronize()
+
+
+def test_an_error_right_after_a_cleared_one_is_kept():
+    from speculative_decoding_draft_lm_gb300 import rollout as R
+    from speculative_decoding_draft_lm_gb300.train import DominoTrain
+    tr = DominoTrain(20, E=8, dtype="fp32")
+    W, bad, good, side = torch.ones(20, 8, device="cuda"), _tok([3, 20]), _tok([3, -1]), torch.cuda.Stream()
+    out = torch.empty(2, 8, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(200):
+            tr.embed(W, bad, out=out)
+            assert tr.status() == R.DOMINO_ERR_BAD_TOKEN
+        tr.embed(W, good, out=out)
+        assert tr.status() == 0
