@@ -19,10 +19,14 @@
  * asynchronous on `cuda_stream` (a cudaStream_t, NULL = legacy default
  * stream), make no host synchronisation and allocate nothing, so they can be
  * captured into a CUDA graph after one ordinary call.  A context may be used
- * from one host thread at a time; embed_grad uses the context's workspace, so
- * two of its calls on one context must be ordered on the device (one stream,
- * or events).  Results do not depend on the launch: repeated calls on equal
- * inputs give equal bits.  Sums and softmax statistics are held in fp32.
+ * from one host thread at a time, on any streams.  embed_grad uses the
+ * context's workspace: its calls on one context run one after another on the
+ * device, whatever their streams (each waits for an event of the last one;
+ * inside a graph capture, of the last one of that capture).  A replayed graph
+ * does not take part in this: the caller orders the replay of a graph that
+ * holds embed_grad with the context's other embed_grad calls and replays.
+ * Results do not depend on the launch: repeated calls on equal inputs give
+ * equal bits.  Sums and softmax statistics are held in fp32.
  *
  * Ids and tokens are int32.  -1 is padding: it takes no part.  Any other value
  * outside [0, V) is treated as padding too and raises DOMINO_ERR_BAD_TOKEN at

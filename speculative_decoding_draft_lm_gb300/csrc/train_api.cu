@@ -49,6 +49,44 @@ train::DistillArgs distill_args(const domino_train_ctx* c, const void* x, long l
     return a;
 }
 
+void release(domino_train_ctx* c) {  // on the context's device
+    if (c->used) cudaEventDestroy(c->used);
+    if (c->captured) cudaEventDestroy(c->captured);
+    cudaFree(c->ws_base);
+    free(c);
+}
+
+// Orders the calls that use the workspace among each other, whatever their
+// streams: a call waits for the event that the last one recorded.  Always, even
+// on what looks like the same stream: a handle's value may be another stream's by
+// now.  An event recorded outside of a capture cannot be waited for inside it, nor
+// the other way round, so a capture has an event of its own for its calls.
+struct WorkspaceOrder {
+    domino_train_ctx* c;
+    cudaStream_t st;
+    bool capturing = false;
+    cudaError_t error;
+
+    WorkspaceOrder(domino_train_ctx* c_, cudaStream_t st_) : c(c_), st(st_) {
+        cudaStreamCaptureStatus status;
+        unsigned long long id = 0;
+        error = cudaStreamGetCaptureInfo(st, &status, &id);
+        if (error != cudaSuccess) return;
+        capturing = status == cudaStreamCaptureStatusActive;
+        if (capturing) {
+            if (c->captured_id == id) error = cudaStreamWaitEvent(st, c->captured, 0);
+            c->captured_id = id;
+        } else if (c->was_used) {
+            error = cudaStreamWaitEvent(st, c->used, 0);
+        }
+    }
+    // after the launches, also where one of them failed
+    cudaError_t done() {
+        if (!capturing) c->was_used = true;
+        return cudaEventRecord(capturing ? c->captured : c->used, st);
+    }
+};
+
 // The error word to `taken`, and 0 in its place: in one step, so that what
 // another stream raises meanwhile is in this answer or in the next.
 __global__ void k_take_error(int* err, int* taken) { *taken = atomicExch(err, 0); }
@@ -108,11 +146,12 @@ int domino_train_init(domino_train_ctx** out, const domino_train_config* cfg, in
     c->part = (float*)(base + o_part);
     c->named = (unsigned*)(base + o_named);
     c->claim = (unsigned*)(base + o_claim);
-    if (cudaMemset(c->err, 0, sizeof(int)) != cudaSuccess || train::prepare_embed_kernels() != cudaSuccess ||
+    if (cudaEventCreateWithFlags(&c->used, cudaEventDisableTiming) != cudaSuccess ||
+        cudaEventCreateWithFlags(&c->captured, cudaEventDisableTiming) != cudaSuccess ||
+        cudaMemset(c->err, 0, sizeof(int)) != cudaSuccess || train::prepare_embed_kernels() != cudaSuccess ||
         train::prepare_distill_kernels() != cudaSuccess || train::prepare_top_kernels() != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
-        cudaFree(c->ws_base);
-        free(c);
+        release(c);
         return DOMINO_ERR_CUDA;
     }
     *out = c;
@@ -216,10 +255,13 @@ int domino_train_embed_grad(domino_train_ctx* c, const void* dout, long long ld,
                          !aligned(tokens, 4) || dout == dtable))
         return DOMINO_ERR_INVALID_ARG;
     DeviceGuard guard(c->device);
-    return train::launch_embed_grad(c, dout, ld, tokens, n_tokens, scale, dtable, grad_dtype, accumulate != 0,
-                                    (cudaStream_t)stream) == cudaSuccess
-               ? DOMINO_OK
-               : DOMINO_ERR_CUDA;
+    const cudaStream_t st = (cudaStream_t)stream;
+    WorkspaceOrder order(c, st);
+    if (order.error != cudaSuccess) return DOMINO_ERR_CUDA;
+    const cudaError_t launched =
+        train::launch_embed_grad(c, dout, ld, tokens, n_tokens, scale, dtable, grad_dtype, accumulate != 0, st);
+    const cudaError_t recorded = order.done();
+    return launched == cudaSuccess && recorded == cudaSuccess ? DOMINO_OK : DOMINO_ERR_CUDA;
 }
 
 int domino_train_status(domino_train_ctx* c, void* stream) {
@@ -243,12 +285,9 @@ int domino_train_last_launch_count(const domino_train_ctx* c) { return c ? c->la
 
 void domino_train_destroy(domino_train_ctx* c) {
     if (!c) return;
-    {
-        DeviceGuard guard(c->device);
-        cudaDeviceSynchronize();
-        cudaFree(c->ws_base);
-    }
-    free(c);
+    DeviceGuard guard(c->device);
+    cudaDeviceSynchronize();
+    release(c);
 }
 
 }  // extern "C"

@@ -20,6 +20,10 @@ struct domino_train_ctx {
     unsigned* claim;      // rows of zeros claimed so far
     float* part;          // [units][2][E] partial sums of the runs that cross a unit's edge
     void* ws_base;
+    // the workspace's last user: outside of graph capture, and in the capture `captured_id` (0: none)
+    cudaEvent_t used, captured;
+    bool was_used;
+    unsigned long long captured_id;
 };
 
 namespace domino {

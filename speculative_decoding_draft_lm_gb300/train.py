@@ -65,7 +65,9 @@ class DominoTrain:
     contiguous).  Every method takes ``out``, the tensors to write, and
     ``stream`` (a torch stream or raw handle; default: the current one).  With a
     stream other than the current one the caller orders the two, as for any
-    kernel, and gives ``out``.
+    kernel, and gives ``out``.  ``embed_grad`` calls of one context, whose
+    workspace they share, run one after another on the device whatever their
+    streams; only replays of captured graphs that hold one are the caller's to order.
     """
 
     def __init__(self, V, E=0, max_tokens=0, dtype="bf16", device=0):
