@@ -251,13 +251,13 @@ class DominoTrain:
 # ---- autograd ------------------------------------------------------------------
 
 def distill_loss(train: DominoTrain, logits, ids, top, rest=None, temperature=1.0):
-    """Loss [n] of student logits [n, V], differentiable by the logits."""
+    """Loss [n] of student logits [n, V], differentiable (once) by the logits."""
     return _functions()[0].apply(logits, train, ids, top, rest, temperature)
 
 
 def embedding(train: DominoTrain, table, tokens, scale=1.0):
-    """scale * table[tokens] [n, E], differentiable by the table (whose gradient
-    comes in the table's type)."""
+    """scale * table[tokens] [n, E], differentiable (once) by the table (whose
+    gradient comes in the table's type)."""
     return _functions()[1].apply(table, train, tokens, scale)
 
 
@@ -268,6 +268,7 @@ def _functions():
     global _autograd
     if _autograd is None:
         import torch
+        from torch.autograd.function import once_differentiable
 
         class Distill(torch.autograd.Function):
             @staticmethod
@@ -278,6 +279,7 @@ def _functions():
                 return loss
 
             @staticmethod
+            @once_differentiable
             def backward(ctx, dloss):
                 logits, ids, top, rest, stats = ctx.saved_tensors
                 grad = ctx.train.distill_backward(logits, ids, top, rest, stats, dloss.contiguous(), ctx.temperature)
@@ -291,6 +293,7 @@ def _functions():
                 return train.embed(table, tokens, scale)
 
             @staticmethod
+            @once_differentiable
             def backward(ctx, dout):
                 (tokens,) = ctx.saved_tensors
                 if dout.stride(1) != 1 or dout.stride(0) < dout.shape[1]:
