@@ -94,7 +94,7 @@ class DominoTrain:
         if (len(shape) == 2 and shape[1] == cols and t.dtype is (dtype or self.torch_dtype)
                 and t.get_device() == self._index and (n is None or shape[0] == n)):
             ld, inner = t.stride()
-            if inner == 1 or cols <= 1:
+            if inner == 1 or cols <= 1 or shape[0] == 0:  # no rows: strides mean nothing
                 if ld >= cols:
                     return ld
                 if shape[0] <= 1:
