@@ -257,7 +257,8 @@ def distill_loss(train: DominoTrain, logits, ids, top, rest=None, temperature=1.
 
 def embedding(train: DominoTrain, table, tokens, scale=1.0):
     """scale * table[tokens] [n, E], differentiable (once) by the table (whose
-    gradient comes in the table's type)."""
+    gradient comes in the table's type).  Any number of tokens: more than
+    ``max_tokens`` take several ``embed_grad`` calls."""
     return _functions()[1].apply(table, train, tokens, scale)
 
 
@@ -298,7 +299,17 @@ def _functions():
                 (tokens,) = ctx.saved_tensors
                 if dout.stride(1) != 1 or dout.stride(0) < dout.shape[1]:
                     dout = dout.contiguous()
-                return ctx.train.embed_grad(dout, tokens, ctx.scale, grad_dtype=ctx.train.torch_dtype), None, None, None
+                train, n = ctx.train, tokens.shape[0]
+                if n <= train.max_tokens:
+                    return train.embed_grad(dout, tokens, ctx.scale, grad_dtype=train.torch_dtype), None, None, None
+                if train.max_tokens < 1:
+                    raise ValueError("embedding: the table's gradient needs a context with max_tokens > 0")
+                # more tokens than one call takes: their parts add up in fp32 and are rounded once
+                grad = None
+                for i in range(0, n, train.max_tokens):
+                    j = min(n, i + train.max_tokens)
+                    grad = train.embed_grad(dout[i:j], tokens[i:j], ctx.scale, out=grad, accumulate=grad is not None)
+                return grad.to(train.torch_dtype), None, None, None
 
         _autograd = (Distill, Embedding)
     return _autograd
