@@ -141,13 +141,29 @@ __device__ __forceinline__ float row_loss(const Sums& u, float rest, float inv_t
     return l;
 }
 
-// Whether entry k of the record takes part: a valid id, and its first place.
-__device__ __noinline__ bool takes_part(const int32_t* ids, int k, int id, int V, bool twice) {
-    if ((unsigned)id >= (unsigned)V) return false;
-    if (twice)
-        for (int j = 0; j < k; ++j)
-            if (ids[j] == id) return false;
-    return true;
+// Records that name an id of the slice [v0, v0 + n) more than once: one warp goes
+// through the record, 32 entries a step, forwards or from the end, and calls
+// f(k, id, a) for the entries of the slice, a their place in it, of which the
+// lowest k where several of a step name one id.  What f does in one step is seen
+// by all lanes in the next, so f can tell by a bit whether an id came before, or,
+// backwards, write over what a later entry wrote.  8192 entries are 256 steps; a
+// scan of all earlier entries for each took 12 ms.
+template <bool kForwards, typename F>
+__device__ __forceinline__ void walk(const int32_t* ids, int K, int v0, int n, F&& f) {
+    const int lane = (int)threadIdx.x & 31, steps = (K + 31) / 32;
+    const auto entry = [&](int i) { return (kForwards ? i : steps - 1 - i) * 32 + lane; };
+    const auto load = [&](int i) { return i < steps && entry(i) < K ? ids[entry(i)] : -1; };
+    int id = load(0);
+#pragma unroll 1
+    for (int i = 0; i < steps; ++i) {
+        const int next = load(i + 1);
+        const unsigned a = (unsigned)id - (unsigned)v0;
+        const bool in = a < (unsigned)n;
+        const unsigned peers = __match_any_sync(0xffffffffu, in ? a : 0x80000000u + lane);
+        if (in && (peers & ((1u << lane) - 1u)) == 0) f(entry(i), id, a);
+        __syncwarp();
+        id = next;
+    }
 }
 
 // ---- loss and gradient at once ---------------------------------------------------
@@ -354,12 +370,9 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
             twice = S.twice != 0;
 
             Sums u = no_sums();
-            const auto gather = [&](int k, int id, float tv) {
-                const unsigned a = place(id);
-                if (a == kNone || (twice && !takes_part(ids, k, id, p.V, true))) return 0.f;
+            const auto gather = [&](unsigned a, float tv) {
                 const float v = to_f32(x.data[a]);
                 x.data[a] = from_f32<T>(-INFINITY);  // no part of the outside
-                bits[a >> 5] = 0;
                 if (tv > u.t.m) {
                     const float m = clamp_max(u.t.m, tv), f = ex2((u.t.m - m) * c);
                     u.t.s *= f;
@@ -372,10 +385,25 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
                 add(u.s, v, c);
                 return v;
             };
+            const auto gather_once = [&](int id, float tv) {
+                const unsigned a = place(id);
+                if (a == kNone) return 0.f;
+                bits[a >> 5] = 0;
+                return gather(a, tv);
+            };
+            if (!twice) {
 #pragma unroll
-            for (int j = 0; j < kHeld; ++j) held[j] = gather(t + j * kStepThreads, now.id[j], now.top[j]);
+                for (int j = 0; j < kHeld; ++j) held[j] = gather_once(now.id[j], now.top[j]);
 #pragma unroll 1
-            for (int k = t + kHeld * kStepThreads; k < p.K; k += kStepThreads) gather(k, ids[k], top[k]);
+                for (int k = t + kHeld * kStepThreads; k < p.K; k += kStepThreads) gather_once(ids[k], top[k]);
+            } else if (warp == 0) {
+                walk<true>(ids, p.K, x.v0, x.n, [&](int k, int, unsigned a) {
+                    const unsigned bit = 1u << (a & 31);
+                    if (!(bits[a >> 5] & bit)) return;
+                    gather(a, top[k]);
+                    atomicAnd(&bits[a >> 5], ~bit);
+                });
+            }
             __syncthreads();
             if (t == 0) S.twice = 0;
             u.o = sum_vectors<T>(x.vec, x.nvec, c);
@@ -453,15 +481,17 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
                 const float q = st.qx * ex2((v - st.mx) * c), pk = st.pt * ex2((tv - st.mt) * c);
                 dx[id - x.v0] = from_f32<T>(w * (q - pk));
             };
-            const auto here = [&](int k, int id) {
-                return (unsigned)id - (unsigned)x.v0 < (unsigned)x.n && !(twice && !takes_part(ids, k, id, p.V, true));
-            };
+            const auto here = [&](int id) { return (unsigned)id - (unsigned)x.v0 < (unsigned)x.n; };
+            if (!twice) {
 #pragma unroll
-            for (int j = 0; j < kHeld; ++j)
-                if (here(t + j * kStepThreads, now.id[j])) entry(now.id[j], now.top[j], held[j]);
+                for (int j = 0; j < kHeld; ++j)
+                    if (here(now.id[j])) entry(now.id[j], now.top[j], held[j]);
 #pragma unroll 1
-            for (int k = t + kHeld * kStepThreads; k < p.K; k += kStepThreads)
-                if (here(k, ids[k])) entry(ids[k], top[k], to_f32(x.src[ids[k] - x.v0]));
+                for (int k = t + kHeld * kStepThreads; k < p.K; k += kStepThreads)
+                    if (here(ids[k])) entry(ids[k], top[k], to_f32(x.src[ids[k] - x.v0]));
+            } else if (warp == 0) {
+                walk<false>(ids, p.K, x.v0, x.n, [&](int k, int id, unsigned a) { entry(id, top[k], to_f32(x.src[a])); });
+            }
         }
         now = next;
     }
@@ -544,12 +574,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_forward(DistillArgs p, int chun
     __syncthreads();
     const bool twice = S.twice != 0;
     Sums u = no_sums();
-#pragma unroll 1
-    for (int k = t; k < p.K; k += kThreads) {
-        const int id = ids[k];
-        const unsigned a = (unsigned)id - (unsigned)v0;
-        if (a >= (unsigned)x.n || (twice && !takes_part(ids, k, id, p.V, true))) continue;
-        const float tv = top[k], v = to_f32(x.src[a]);
+    const auto gather = [&](unsigned a, float tv) {
+        const float v = to_f32(x.src[a]);
         if (tv > u.t.m) {
             const float m = clamp_max(u.t.m, tv), f = ex2((u.t.m - m) * c);
             u.t.s *= f;
@@ -560,6 +586,27 @@ __global__ void __launch_bounds__(kThreads, 4) k_forward(DistillArgs p, int chun
         u.t.s += e;
         if (e != 0.f) u.a += e * (tv - v) * inv_t;
         add(u.s, v, c);
+    };
+    if (!twice) {
+#pragma unroll 1
+        for (int k = t; k < p.K; k += kThreads) {
+            const unsigned a = (unsigned)ids[k] - (unsigned)v0;
+            if (a < (unsigned)x.n) gather(a, top[k]);
+        }
+    } else {
+        // the bits once more, in the order of the record
+        for (int k = t; k < p.K; k += kThreads) {
+            const unsigned a = (unsigned)ids[k] - (unsigned)v0, b = a + x.phase;
+            if (a < (unsigned)x.n) bits[b >> 5] = 0;
+        }
+        __syncthreads();
+        if (warp == 0)
+            walk<true>(ids, p.K, v0, x.n, [&](int k, int, unsigned a) {
+                const unsigned b = a + x.phase, bit = 1u << (b & 31);
+                if (atomicOr(&bits[b >> 5], bit) & bit) return;
+                gather(a, top[k]);
+            });
+        __syncthreads();
     }
     // the outside
     const unsigned char* masks = reinterpret_cast<const unsigned char*>(bits);
@@ -663,14 +710,18 @@ __global__ void __launch_bounds__(kThreads, 4) k_backward(DistillArgs p, int chu
     __syncthreads();
     const int32_t* ids = p.ids + (size_t)n * p.K;
     const float* top = p.top + (size_t)n * p.K;
-    const bool twice = st.twice != 0.f;
-#pragma unroll 1
-    for (int k = t; k < p.K; k += kThreads) {
-        const int id = ids[k];
-        const unsigned a = (unsigned)id - (unsigned)v0;
-        if (a >= (unsigned)x.n || (twice && !takes_part(ids, k, id, p.V, true))) continue;
-        const float q = st.qx * ex2((to_f32(x.src[a]) - st.mx) * c), pk = st.pt * ex2((top[k] - st.mt) * c);
+    const auto entry = [&](unsigned a, float tv) {
+        const float q = st.qx * ex2((to_f32(x.src[a]) - st.mx) * c), pk = st.pt * ex2((tv - st.mt) * c);
         dx[a] = from_f32<T>(w * (q - pk));
+    };
+    if (st.twice == 0.f) {
+#pragma unroll 1
+        for (int k = t; k < p.K; k += kThreads) {
+            const unsigned a = (unsigned)ids[k] - (unsigned)v0;
+            if (a < (unsigned)x.n) entry(a, top[k]);
+        }
+    } else if (t < 32) {
+        walk<false>(ids, p.K, v0, x.n, [&](int k, int, unsigned a) { entry(a, top[k]); });
     }
 }
 
