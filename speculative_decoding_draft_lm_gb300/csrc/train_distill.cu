@@ -5,10 +5,15 @@
 // teacher's, write
 //   Z_S = sum_S e^u,  Z_o = sum_{v not in S} e^u,  W = sum_S e^(t/T) + e^rest,
 //   p_k = e^(t_k/T) / W,  p_r = e^rest / W,  q_v = e^(u_v) / (Z_S + Z_o).
-// Since sum p + p_r = 1,
-//   loss = sum_S p_k (t_k - x_k) / T + p_r (rest - log Z_o) + log((Z_S + Z_o) / W),
-// in which the two normalisers meet as one ratio (their logarithms, near log V,
-// never appear alone), and, dividing the outside by its own sum,
+// Every sum is held as s e^(m / T) with m a maximum: m_S and m_o the student's, m_x
+// the larger of them, m_t the teacher's over the record.  With d = m_t / T - rest and
+// since P + p_r = 1 for P = sum_S p_k,
+//   loss = sum_S p_k ((t_k - m_t) - (x_k - m_S)) / T + P ((m_x - m_S) / T + min(d, 0))
+//          + p_r ((m_x - m_o) / T - max(d, 0) - log s_o) + log(s_x / s_W),
+// s_W on the scale of the larger of m_t / T and rest.  What all logits of a row share
+// cancels in differences of two of them, which are exact where they are close: a row
+// masked by the type's lowest value throughout is as good as a row of zeros.  The two
+// normalisers meet as one ratio.  Dividing the outside by its own sum,
 //   T dloss/dx_v = q_v - p_v                                  v in S
 //                = e^(u_v) (1 / (Z_S + Z_o) - p_r / Z_o)      otherwise.
 // Z_o is summed over the ids outside the record and not taken as a difference:
@@ -37,7 +42,7 @@ static_assert(sizeof(Stats) == DOMINO_TRAIN_STATS * sizeof(float), "stats row");
 
 struct alignas(16) Sums {
     MaxSum t, s, o;  // teacher's record, student's record, student's outside
-    float a;         // sum 2^((t - mt) c) (t - x) / T
+    float a;         // sum 2^((t - mt) c) ((t - mt) - (x - ms)) / T
     float twice;     // forward: an id was seen twice
 };
 __device__ __forceinline__ Sums no_sums() { return {empty_set(), empty_set(), empty_set(), 0.f, 0.f}; }
@@ -58,15 +63,36 @@ __device__ __forceinline__ void send(const Sums& u, Sums* to, unsigned long long
                  : "memory");
 }
 
-// a sum scaled to a new maximum; an infinite term whose weight vanished is 0
-__device__ __forceinline__ float rescaled(float a, float f) { return f == 0.f ? 0.f : a * f; }
+// a term scaled by a weight; an infinite one whose weight vanished is 0
+__device__ __forceinline__ float weighted(float a, float f) { return f == 0.f ? 0.f : a * f; }
 
-__device__ __forceinline__ Sums join(const Sums& x, const Sums& y, float c) {
+// u.a when mt and ms become those given, f = 2^((u.t.m - mt) c)
+__device__ __forceinline__ float moved(const Sums& u, float mt, float ms, float f, float inv_t) {
+    if (u.t.s == 0.f) return 0.f;
+    return weighted(fmaf(u.t.s, ((u.t.m - mt) - (u.s.m - ms)) * inv_t, u.a), f);
+}
+
+// Adds an entry of the record: the teacher's logit and the student's.
+__device__ __forceinline__ void add_entry(Sums& u, float tv, float v, float c, float inv_t) {
+    if (tv > u.t.m || v > u.s.m) {
+        const float mt = tv > u.t.m ? clamp_max(u.t.m, tv) : u.t.m, ms = v > u.s.m ? clamp_max(u.s.m, v) : u.s.m;
+        const float f = ex2((u.t.m - mt) * c);
+        u.a = moved(u, mt, ms, f, inv_t);
+        u.t = {mt, u.t.s * f};
+        u.s = {ms, u.s.s * ex2((u.s.m - ms) * c)};
+    }
+    const float e = ex2((tv - u.t.m) * c);
+    u.t.s += e;
+    u.s.s += ex2((v - u.s.m) * c);
+    if (e != 0.f) u.a += e * ((tv - u.t.m) - (v - u.s.m)) * inv_t;
+}
+
+__device__ __forceinline__ Sums join(const Sums& x, const Sums& y, float c, float inv_t) {
     Sums r;
     r.t = join(x.t, y.t, c);
     r.s = join(x.s, y.s, c);
     r.o = join(x.o, y.o, c);
-    r.a = rescaled(x.a, ex2((x.t.m - r.t.m) * c)) + rescaled(y.a, ex2((y.t.m - r.t.m) * c));
+    r.a = moved(x, r.t.m, r.s.m, ex2((x.t.m - r.t.m) * c), inv_t) + moved(y, r.t.m, r.s.m, ex2((y.t.m - r.t.m) * c), inv_t);
     r.twice = fmaxf(x.twice, y.twice);
     return r;
 }
@@ -74,11 +100,11 @@ __device__ __forceinline__ Sums join(const Sums& x, const Sums& y, float c) {
 // The warp's join of its lanes' sums: the maxima first, then one rescaling and
 // plain sums (a third of the exponentials and half of the latency of five
 // pairwise joins).  Every lane gets it.
-__device__ __forceinline__ Sums warp_join(Sums u, float c) {
+__device__ __forceinline__ Sums warp_join(Sums u, float c, float inv_t) {
     const float mt = warp_max(u.t.m), ms = warp_max(u.s.m), mo = warp_max(u.o.m);
     const float ft = ex2((u.t.m - mt) * c);
+    u.a = moved(u, mt, ms, ft, inv_t);
     u.t = {mt, u.t.s * ft};
-    u.a = rescaled(u.a, ft);
     u.s = {ms, u.s.s * ex2((u.s.m - ms) * c)};
     u.o = {mo, u.o.s * ex2((u.o.m - mo) * c)};
 #pragma unroll
@@ -134,10 +160,10 @@ __device__ __forceinline__ float row_loss(const Sums& u, float rest, float inv_t
     const Teacher w = teacher(u, rest, inv_t);
     const float pr = w.part_r * w.inv_w;
     const MaxSum x = join(u.s, u.o, c);
-    // the normalisers' ratio, their scales apart: exact where the record holds the larger part
-    float l = w.d >= 0.f ? (x.m - u.t.m) * inv_t : fmaf(x.m, inv_t, -rest);
-    l += rescaled(u.a, w.part * w.inv_w) + logf(x.s * w.inv_w);
-    if (pr != 0.f) l -= pr * (fmaf(u.o.m, inv_t, -rest) + logf(u.o.s));
+    const float ps = u.t.s * w.part * w.inv_w;
+    float l = logf(x.s * w.inv_w);
+    if (ps != 0.f) l += weighted(u.a, w.part) * w.inv_w + ps * ((x.m - u.s.m) * inv_t + fminf(w.d, 0.f));
+    if (pr != 0.f) l += pr * ((x.m - u.o.m) * inv_t - fmaxf(w.d, 0.f) - logf(u.o.s));
     return l;
 }
 
@@ -373,16 +399,7 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
             const auto gather = [&](unsigned a, float tv) {
                 const float v = to_f32(x.data[a]);
                 x.data[a] = from_f32<T>(-INFINITY);  // no part of the outside
-                if (tv > u.t.m) {
-                    const float m = clamp_max(u.t.m, tv), f = ex2((u.t.m - m) * c);
-                    u.t.s *= f;
-                    u.a = rescaled(u.a, f);
-                    u.t.m = m;
-                }
-                const float e = ex2((tv - u.t.m) * c);
-                u.t.s += e;
-                if (e != 0.f) u.a += e * (tv - v) * inv_t;
-                add(u.s, v, c);
+                add_entry(u, tv, v, c, inv_t);
                 return v;
             };
             const auto gather_once = [&](int id, float tv) {
@@ -407,7 +424,7 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
             __syncthreads();
             if (t == 0) S.twice = 0;
             u.o = sum_vectors<T>(x.vec, x.nvec, c);
-            u = warp_join(u, c);
+            u = warp_join(u, c, inv_t);
             // every warp's sums to every CTA of the row
             // (to the other place than the last row's: who sends for this row has seen
             // every CTA's sums of the last one, so all have read those of the one before)
@@ -418,8 +435,8 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
                 const Sums* part = S.part[phase];
                 u = part[min(lane, size * kStepWarps - 1)];
                 if (lane >= size * kStepWarps) u = no_sums();
-                for (int i = lane + 32; i < size * kStepWarps; i += 32) u = join(u, part[i], c);
-                u = warp_join(u, c);
+                for (int i = lane + 32; i < size * kStepWarps; i += 32) u = join(u, part[i], c, inv_t);
+                u = warp_join(u, c, inv_t);
                 const Stats st = finish(u, now.rest, inv_t, c);
                 if (lane == 0) S.row = st;
             }
@@ -574,19 +591,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_forward(DistillArgs p, int chun
     __syncthreads();
     const bool twice = S.twice != 0;
     Sums u = no_sums();
-    const auto gather = [&](unsigned a, float tv) {
-        const float v = to_f32(x.src[a]);
-        if (tv > u.t.m) {
-            const float m = clamp_max(u.t.m, tv), f = ex2((u.t.m - m) * c);
-            u.t.s *= f;
-            u.a = rescaled(u.a, f);
-            u.t.m = m;
-        }
-        const float e = ex2((tv - u.t.m) * c);
-        u.t.s += e;
-        if (e != 0.f) u.a += e * (tv - v) * inv_t;
-        add(u.s, v, c);
-    };
+    const auto gather = [&](unsigned a, float tv) { add_entry(u, tv, to_f32(x.src[a]), c, inv_t); };
     if (!twice) {
 #pragma unroll 1
         for (int k = t; k < p.K; k += kThreads) {
@@ -630,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_forward(DistillArgs p, int chun
     u.o.s = h.x + h.y;
     const int side = t < 2 * kPer ? x.beside(t) : x.n;
     if (side < x.n && !(bits[(side + x.phase) >> 5] >> ((side + x.phase) & 31) & 1u)) add(u.o, to_f32(x.src[side]), c);
-    u = warp_join(u, c);
+    u = warp_join(u, c, inv_t);
     // every warp's sums to rank 0, which is running by now; the others are done
     u.twice = twice ? 1.f : 0.f;
     const int parts = size * kWarps;
@@ -648,8 +653,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_forward(DistillArgs p, int chun
     }
     u = S.part[min(lane, parts - 1)];
     if (lane >= parts) u = no_sums();
-    for (int i = lane + 32; i < parts; i += 32) u = join(u, S.part[i], c);
-    u = warp_join(u, c);
+    for (int i = lane + 32; i < parts; i += 32) u = join(u, S.part[i], c, inv_t);
+    u = warp_join(u, c, inv_t);
     const bool any_twice = __any_sync(0xffffffffu, u.twice != 0.f);
     Stats st = finish(u, rest, inv_t, c);
     st.twice = any_twice ? 1.f : 0.f;
