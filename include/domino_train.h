@@ -135,7 +135,8 @@ DOMINO_API int domino_train_embed_grad(domino_train_ctx* ctx, const void* dout, 
 /* Take the device error word in the order of `cuda_stream`, leave 0 in its
  * place, synchronise that stream (no other) and return the word's status
  * (DOMINO_OK, DOMINO_ERR_BAD_TOKEN, or DOMINO_ERR_TIMEOUT after a device-side
- * wait ran out of time and left its row's results meaningless), or
+ * wait of a distillation call ran out of time: all outputs of that call are
+ * undefined, rows unwritten among them, and it has to be made again), or
  * DOMINO_ERR_CUDA. */
 DOMINO_API int domino_train_status(domino_train_ctx* ctx, void* cuda_stream);
 

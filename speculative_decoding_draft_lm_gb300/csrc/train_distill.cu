@@ -63,6 +63,14 @@ __device__ __forceinline__ void send(const Sums& u, Sums* to, unsigned long long
                  : "memory");
 }
 
+// Before a CTA leaves although a wait gave up: what is still on its way into its
+// shared memory may land, for 2 ms at most.
+__device__ __noinline__ void last_chance(uint32_t bar, uint32_t parity) {
+    const unsigned long long t0 = tc::globaltimer();
+    while (!tc::mbar_try_wait(bar, parity) && tc::globaltimer() - t0 < 2000000ull) {
+    }
+}
+
 // a term scaled by a weight; an infinite one whose weight vanished is 0
 __device__ __forceinline__ float weighted(float a, float f) { return f == 0.f ? 0.f : a * f; }
 
@@ -485,9 +493,10 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
                 dx[together && i >= x.head ? i + x.body : i] = from_f32<T>(0.f);
         }
         __syncthreads();  // the buffer is read, and the outside's gradient written
+        if (S.abort) break;  // a copy or a peer's sums never came: no further rows, so that no further copy is asked for
         if (next.weight != 0.f) {
             const Slice<T> y = slice(n + stride);
-            if (t == 0 && !S.abort) request(y);
+            if (t == 0) request(y);
             y.load_edges();
         }
         if (w != 0.f) {  // the record's entries over it
@@ -512,14 +521,8 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
         }
         now = next;
     }
-    // A CTA whose copy or whose peers' sums never came has gone on, with
-    // meaningless data and without further copies; it gives the lost ones a last
-    // chance to land before it leaves.
-    if (t == 0 && S.abort) {
-        const unsigned long long t0 = tc::globaltimer();
-        while (!tc::mbar_try_wait(bar, (turn & 1) ^ 1) && tc::globaltimer() - t0 < 2000000ull) {
-        }
-    }
+    // after a break: the row's own copy, the last one asked for
+    if (t == 0 && S.abort) last_chance(bar, (turn & 1) ^ 1);
     cluster_barrier();  // nobody leaves before all have their sums
 }
 
@@ -645,7 +648,12 @@ __global__ void __launch_bounds__(kThreads, 4) k_forward(DistillArgs p, int chun
         if (rank == 0 && t == 0) tc::mbar_arrive_expect_tx(tc::smem_u32(&S.bar), parts * sizeof(Sums));
         if (lane == 0) send(u, &S.part[rank * kWarps + warp], &S.bar, 0);
         if (rank != 0 || warp != 0) return;
-        tc::mbar_wait(tc::smem_u32(&S.bar), 0, &S.abort, p.err);
+        const bool came = tc::mbar_wait(tc::smem_u32(&S.bar), 0, &S.abort, p.err);
+        if (!__all_sync(0xffffffffu, came)) {
+            // who was late sends all the same: this CTA's shared memory stays until the others have left
+            cluster_barrier();
+            last_chance(tc::smem_u32(&S.bar), 0);
+        }
     } else {
         if (lane == 0) S.part[warp] = u;
         __syncthreads();

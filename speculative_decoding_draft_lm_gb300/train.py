@@ -230,7 +230,8 @@ class DominoTrain:
     # -- context -------------------------------------------------------------------
 
     def status(self, stream=None) -> int:
-        """Synchronise the stream; return and clear the device's error word as a status code."""
+        """Synchronise the stream; return and clear the device's error word as a status code.
+        After DOMINO_ERR_TIMEOUT all outputs of the distillation call that timed out are undefined."""
         return self._lib.domino_train_status(self.ctx, self._stream(stream))
 
     def last_launch_count(self) -> int:
