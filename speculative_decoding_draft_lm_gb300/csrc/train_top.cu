@@ -19,7 +19,7 @@
 // the rounding of the whole.  Places in lists come from scans, not from atomics,
 // so that equal calls sum in equal order.
 //
-// Rows whose groups do not fit one CTA are spread over a cluster: every CTA finds
+// fp32 rows whose groups do not fit one CTA are spread over a cluster: every CTA finds
 // its slice's best K and rank 0 takes the others' through distributed shared
 // memory.  Few rows are not: the merge costs more than the stream gains (15 rows,
 // a CTA each or eight: K = 64 14.5 and 17.5 us, K = 512 27 and 54 us, K = 2048 48
@@ -263,9 +263,9 @@ struct Selected {
 // Leaves the best K of `count` words at the front of the buffer; every word's
 // key lies in [low, largest].  kShort: logits with 16 significant bits.  All
 // threads, after a barrier, count > K.
-template <int kThreads, bool kShort>
+template <int kThreads, bool kShort, bool kWantBound>
 __device__ __noinline__ Selected select(TopShared& S, unsigned long long* buf, unsigned* hist, int count, int K,
-                                        unsigned low, unsigned largest, MaxSum rest, float c, bool want_bound) {
+                                        unsigned low, unsigned largest, MaxSum rest, float c) {
     const int t = threadIdx.x;
     constexpr int kFloor = kShort ? 16 : 0;
     int bit;
@@ -343,10 +343,11 @@ __device__ __noinline__ Selected select(TopShared& S, unsigned long long* buf, u
         }
         kept += all;
     }
-    return {want_bound ? ~block_max<kThreads>(~least, S.warp) : 0u, rest};
+    return {kWantBound ? ~block_max<kThreads>(~least, S.warp) : 0u, rest};
 }
 
-template <typename T, int kThreads>
+// kSplit: a row is a cluster's, else one CTA's.
+template <typename T, int kThreads, bool kSplit>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 2) k_top(const T* __restrict__ logits, long long ld, int V, int K,
                                                      float temperature, int32_t* __restrict__ ids,
                                                      float* __restrict__ top, float* __restrict__ rest, int chunk) {
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 2) k_top(const
     constexpr int kSlots = 2 * kThreads;  // maxima that a bound may be taken from: of every thread's even and odd steps
     constexpr int kPer = Vec16<T>::kElems, P = kPer / 2;
     cg::cluster_group cluster = cg::this_cluster();
-    const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
+    const int rank = kSplit ? (int)cluster.block_rank() : 0, size = kSplit ? (int)cluster.num_blocks() : 1;
     const int n = blockIdx.x / size, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     unsigned* hist = reinterpret_cast<unsigned*>(smem);
     unsigned long long* buf = reinterpret_cast<unsigned long long*>(hist + kBins);
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 2) k_top(const
     const auto reduce = [&] {  // the buffer's best K
         if (count <= K) return;
         const unsigned top_key_seen = block_max<kThreads>(most, S.warp);
-        const Selected got = select<kThreads, kShort>(S, buf, hist, count, K, bound, top_key_seen, r, c, size > 1);
+        const Selected got = select<kThreads, kShort, kSplit>(S, buf, hist, count, K, bound, top_key_seen, r, c);
         last = got.bound;
         r = got.rest;
         count = K;
@@ -593,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 2) k_top(const
     if (equals && bound_logit != -INFINITY)
         r = join(r, MaxSum{clamp_max(-FLT_MAX, bound_logit), bound_logit == INFINITY ? INFINITY : (float)equals}, c);
 
-    if (size > 1) {
+    if constexpr (kSplit) {
         cluster_barrier();
         if (rank == 0) {
             // the other slices' words: a warp per slice, kWords of a lane at once
@@ -645,10 +646,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 2) k_top(const
             const float all = warp_max(r.m);
             r.s = warp_sum(r.s * ex2((r.m - all) * c));
             r.m = all;
-            if (lane == 0) *cluster.map_shared_rank(&S.rest[rank], 0) = r;
+            if (kSplit && lane == 0) *cluster.map_shared_rank(&S.rest[rank], 0) = r;
         }
     }
-    if (size > 1) {
+    if constexpr (kSplit) {
         cluster_barrier();
         if (rank != 0) return;
         if (warp == 0) {
@@ -698,27 +699,29 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 2) k_top(const
     }
 }
 
-inline int slice_of(int V, int parts) { return ((V + parts - 1) / parts + 63) / 64 * 64; }
+constexpr int slice_of(int V, int parts) { return ((V + parts - 1) / parts + 63) / 64 * 64; }
 
-// the CTAs of a row, from `size` on, and the shared memory that each needs
+// shared memory of each of a row's `size` CTAs
 template <typename T, int kThreads>
-size_t spread(int V, int K, int* size) {
+constexpr size_t smem_of(int V, int K, int size) {
     const size_t bits = (size_t)((V + 31) / 32 + kThreads) * 4;
-    for (;; *size *= 2) {
-        const int groups = groups_of<T, kThreads>(slice_of(V, *size));
-        const size_t back = group_bytes<T>(groups);
-        const size_t smem = front_bytes<kThreads>(groups, K) + (back > bits ? back : bits);
-        if (*size == kMaxCluster || smem <= kMaxSmem) return smem;
-    }
+    const int groups = groups_of<T, kThreads>(slice_of(V, size));
+    const size_t back = group_bytes<T>(groups);
+    return front_bytes<kThreads>(groups, K) + (back > bits ? back : bits);
 }
+static_assert(smem_of<__nv_bfloat16, 512>(DOMINO_TRAIN_MAX_V, DOMINO_TRAIN_MAX_K, 1) <= kMaxSmem,
+              "every bf16 row is one CTA's");
+static_assert(smem_of<float, 512>(DOMINO_TRAIN_MAX_V, DOMINO_TRAIN_MAX_K, 4) <= kMaxSmem, "of fp32 rows four CTAs'");
 
-template <typename T, int kThreads>
-cudaError_t launch_with(int size, size_t smem, int V, const void* x, long long ld, int n, int K, float temperature,
-                        int32_t* ids, float* top, float* rest, cudaStream_t st) {
+template <typename T, int kThreads, bool kSplit>
+cudaError_t launch_with(int size, int V, const void* x, long long ld, int n, int K, float temperature, int32_t* ids,
+                        float* top, float* rest, cudaStream_t st) {
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = cluster_config((unsigned)n * size, kThreads, size, smem, st, &attr);
-    return cudaLaunchKernelEx(&cfg, k_top<T, kThreads>, static_cast<const T*>(x), ld, V, K, temperature, ids, top, rest,
-                              slice_of(V, size));
+    cudaLaunchConfig_t cfg =
+        cluster_config((unsigned)n * size, kThreads, size, smem_of<T, kThreads>(V, K, size), st, &attr);
+    if (!kSplit) cfg.numAttrs = 0;
+    return cudaLaunchKernelEx(&cfg, k_top<T, kThreads, kSplit>, static_cast<const T*>(x), ld, V, K, temperature, ids, top,
+                              rest, slice_of(V, size));
 }
 
 template <typename T>
@@ -726,22 +729,25 @@ cudaError_t launch(domino_train_ctx* c, const void* x, long long ld, int n, int 
                    float* top, float* rest, cudaStream_t st) {
     const int V = c->cfg.V;
     c->last_launches = 1;
-    int size = 1;
-    const size_t smem = spread<T, 256>(V, K, &size);
-    if (smem <= kThirdSmem && (n > c->num_sms || K <= kFew))
-        return launch_with<T, 256>(size, smem, V, x, ld, n, K, temperature, ids, top, rest, st);
-    size = 1;
-    const size_t more = spread<T, 512>(V, K, &size);
-    return launch_with<T, 512>(size, more, V, x, ld, n, K, temperature, ids, top, rest, st);
+    if (smem_of<T, 256>(V, K, 1) <= kThirdSmem && (n > c->num_sms || K <= kFew))
+        return launch_with<T, 256, false>(1, V, x, ld, n, K, temperature, ids, top, rest, st);
+    if constexpr (sizeof(T) == 4) {
+        // fp32 rows from 229,313 (K = 8192) or 327,617 (K <= 64) entries on
+        int size = 1;
+        while (smem_of<T, 512>(V, K, size) > kMaxSmem) size *= 2;
+        if (size > 1) return launch_with<T, 512, true>(size, V, x, ld, n, K, temperature, ids, top, rest, st);
+    }
+    return launch_with<T, 512, false>(1, V, x, ld, n, K, temperature, ids, top, rest, st);
 }
 
 }  // namespace
 
 cudaError_t prepare_top_kernels() {
-    cudaError_t e = allow_all(k_top<float, 256>);
-    if (e == cudaSuccess) e = allow_all(k_top<float, 512>);
-    if (e == cudaSuccess) e = allow_all(k_top<__nv_bfloat16, 256>);
-    if (e == cudaSuccess) e = allow_all(k_top<__nv_bfloat16, 512>);
+    cudaError_t e = allow_all(k_top<float, 256, false>);
+    if (e == cudaSuccess) e = allow_all(k_top<float, 512, false>);
+    if (e == cudaSuccess) e = allow_all(k_top<float, 512, true>);
+    if (e == cudaSuccess) e = allow_all(k_top<__nv_bfloat16, 256, false>);
+    if (e == cudaSuccess) e = allow_all(k_top<__nv_bfloat16, 512, false>);
     return e;
 }
 
