@@ -9,18 +9,6 @@ using namespace domino;
 
 namespace {
 
-struct DeviceGuard {
-    int prev = -1;
-    bool switched = false;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) == cudaSuccess && prev != dev) switched = cudaSetDevice(dev) == cudaSuccess;
-    }
-    ~DeviceGuard() {
-        if (switched) cudaSetDevice(prev);
-    }
-};
-
-inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline int esize(int dtype) { return dtype == DOMINO_DTYPE_BF16 ? 2 : 4; }
 inline bool known(int dtype) { return dtype == DOMINO_DTYPE_FP32 || dtype == DOMINO_DTYPE_BF16; }
 inline bool aligned(const void* p, int a) { return ((uintptr_t)p & (uintptr_t)(a - 1)) == 0; }

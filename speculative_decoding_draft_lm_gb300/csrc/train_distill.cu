@@ -262,10 +262,9 @@ struct Slice {
     }
     // fills what the copies leave of the first and last vectors: the row's own
     // elements, and -inf where there are none
-    __device__ void load_edges(int from = 0) const {  // by the threads from `from` on
+    __device__ void load_edges() const {
         const int first = (int)(data - reinterpret_cast<T*>(vec)), per = 16 / (int)sizeof(T);
-        const int t = (int)threadIdx.x - from;
-        if (t < 0) return;
+        const int t = (int)threadIdx.x;
         if (t < first) reinterpret_cast<T*>(vec)[t] = from_f32<T>(-INFINITY);
         if (t < head) data[t] = src[t];
         const int tail = n - head - body;
@@ -737,9 +736,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_backward(DistillArgs p, int chu
         walk<false>(ids, p.K, v0, x.n, [&](int k, int, unsigned a) { entry(a, top[k]); });
     }
 }
-
-// elements of a row's slice when it is cut into `parts`
-inline int slice_of(int V, int parts) { return ((V + parts - 1) / parts + 63) / 64 * 64; }
 
 template <typename T>
 cudaError_t launch_forward(domino_train_ctx* ctx, const DistillArgs& a, cudaStream_t st) {

@@ -35,6 +35,9 @@ struct Vectors {
     }
 };
 
+// elements of a row's slice when it is cut into `parts`
+constexpr int slice_of(int V, int parts) { return ((V + parts - 1) / parts + 63) / 64 * 64; }
+
 // The vectors [x.first, x.last) of this thread through a ring in shared memory
 // that no other thread touches, filled by asynchronous copies kStages calls
 // ahead (the first ones by the constructor): the bytes in flight cost no

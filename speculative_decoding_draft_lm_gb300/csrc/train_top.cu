@@ -699,8 +699,6 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 2) k_top(const
     }
 }
 
-constexpr int slice_of(int V, int parts) { return ((V + parts - 1) / parts + 63) / 64 * 64; }
-
 // shared memory of each of a row's `size` CTAs
 template <typename T, int kThreads>
 constexpr size_t smem_of(int V, int K, int size) {
