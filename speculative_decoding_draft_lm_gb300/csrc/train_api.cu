@@ -257,14 +257,19 @@ int domino_train_status(domino_train_ctx* c, void* stream) {
     DeviceGuard guard(c->device);
     // all in the stream's order: another stream, the default one too, is not ordered with it
     const cudaStream_t st = (cudaStream_t)stream;
-    cudaLaunchConfig_t one = {};
-    one.gridDim = one.blockDim = dim3(1);
-    one.stream = st;
     int word = 0;
-    if (cudaLaunchKernelEx(&one, k_take_error, c->err, c->err + 1) != cudaSuccess ||
-        cudaMemcpyAsync(&word, c->err + 1, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
-        cudaStreamSynchronize(st) != cudaSuccess)
-        return DOMINO_ERR_CUDA;
+    const auto read = [&](const int* from) {
+        return cudaMemcpyAsync(&word, from, sizeof(int), cudaMemcpyDeviceToHost, st) == cudaSuccess &&
+               cudaStreamSynchronize(st) == cudaSuccess;
+    };
+    if (!read(c->err)) return DOMINO_ERR_CUDA;
+    if (word) {
+        cudaLaunchConfig_t one = {};
+        one.gridDim = one.blockDim = dim3(1);
+        one.stream = st;
+        if (cudaLaunchKernelEx(&one, k_take_error, c->err, c->err + 1) != cudaSuccess || !read(c->err + 1))
+            return DOMINO_ERR_CUDA;
+    }
     if (word & kErrTimeout) return DOMINO_ERR_TIMEOUT;
     return word & kErrBadToken ? DOMINO_ERR_BAD_TOKEN : DOMINO_OK;
 }
