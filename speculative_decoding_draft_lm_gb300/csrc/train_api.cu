@@ -14,6 +14,11 @@ inline bool known(int dtype) { return dtype == DOMINO_DTYPE_FP32 || dtype == DOM
 inline bool aligned(const void* p, int a) { return ((uintptr_t)p & (uintptr_t)(a - 1)) == 0; }
 inline bool good_temperature(float t) { return t >= 1e-3f && t <= 1e3f; }  // false for NaN
 
+int nothing_to_do(domino_train_ctx* c) {
+    c->last_launches = 0;
+    return DOMINO_OK;
+}
+
 // what the three distillation calls share; n = 0 is checked by the caller
 bool good_record(const domino_train_ctx* c, const void* x, long long ld, const int32_t* ids, const float* top,
                  const float* rest, int K, float temperature) {
@@ -151,8 +156,7 @@ int domino_train_top_logits(domino_train_ctx* c, const void* logits, int dtype, 
     if (!c || n_rows < 0) return DOMINO_ERR_INVALID_ARG;
     if (!known(dtype)) return DOMINO_ERR_UNSUPPORTED;
     if (K < 1 || K > c->cfg.V || K > DOMINO_TRAIN_MAX_K || !good_temperature(temperature)) return DOMINO_ERR_INVALID_ARG;
-    c->last_launches = 0;
-    if (n_rows == 0) return DOMINO_OK;
+    if (n_rows == 0) return nothing_to_do(c);
     if (!logits || !ids || !top || !rest || ld < c->cfg.V || !aligned(logits, esize(dtype)) || !aligned(ids, 4) ||
         !aligned(top, 4) || !aligned(rest, 4))
         return DOMINO_ERR_INVALID_ARG;
@@ -166,8 +170,7 @@ int domino_train_distill_forward(domino_train_ctx* c, const void* logits, long l
                                  const float* top, const float* rest, int K, float temperature, float* loss,
                                  float* stats, void* stream) {
     if (!c || n_rows < 0) return DOMINO_ERR_INVALID_ARG;
-    c->last_launches = 0;
-    if (n_rows == 0) return DOMINO_OK;
+    if (n_rows == 0) return nothing_to_do(c);
     if (!good_record(c, logits, ld, ids, top, rest, K, temperature) || !loss || !stats || !aligned(loss, 4) ||
         !aligned(stats, 4))
         return DOMINO_ERR_INVALID_ARG;
@@ -183,8 +186,7 @@ int domino_train_distill_backward(domino_train_ctx* c, const void* logits, long 
                                   const float* stats, const float* dloss, void* dlogits, long long ld_d,
                                   void* stream) {
     if (!c || n_rows < 0) return DOMINO_ERR_INVALID_ARG;
-    c->last_launches = 0;
-    if (n_rows == 0) return DOMINO_OK;
+    if (n_rows == 0) return nothing_to_do(c);
     if (!good_record(c, logits, ld, ids, top, rest, K, temperature) || !stats || !dloss || !dlogits ||
         dlogits == logits || ld_d < c->cfg.V || !aligned(dlogits, esize(c->cfg.dtype)) || !aligned(stats, 4) ||
         !aligned(dloss, 4))
@@ -202,8 +204,7 @@ int domino_train_distill_step(domino_train_ctx* c, const void* logits, long long
                               const float* top, const float* rest, int K, float temperature, const float* weight,
                               float* loss, void* dlogits, long long ld_d, void* stream) {
     if (!c || n_rows < 0) return DOMINO_ERR_INVALID_ARG;
-    c->last_launches = 0;
-    if (n_rows == 0) return DOMINO_OK;
+    if (n_rows == 0) return nothing_to_do(c);
     if (!good_record(c, logits, ld, ids, top, rest, K, temperature) || !weight || !loss || !dlogits ||
         dlogits == logits || ld_d < c->cfg.V || !aligned(dlogits, esize(c->cfg.dtype)) || !aligned(weight, 4) ||
         !aligned(loss, 4))
@@ -220,8 +221,7 @@ int domino_train_distill_step(domino_train_ctx* c, const void* logits, long long
 int domino_train_embed(domino_train_ctx* c, const void* table, const int32_t* tokens, int n_tokens, float scale,
                        void* out, long long ld_out, void* stream) {
     if (!c || n_tokens < 0 || c->cfg.E < 1) return DOMINO_ERR_INVALID_ARG;
-    c->last_launches = 0;
-    if (n_tokens == 0) return DOMINO_OK;
+    if (n_tokens == 0) return nothing_to_do(c);
     const int es = esize(c->cfg.dtype);
     if (!table || !tokens || !out || ld_out < c->cfg.E || !aligned(table, es) || !aligned(out, es) ||
         !aligned(tokens, 4) || table == out)
@@ -236,9 +236,8 @@ int domino_train_embed_grad(domino_train_ctx* c, const void* dout, long long ld,
                             float scale, void* dtable, int grad_dtype, int accumulate, void* stream) {
     if (!c || n_tokens < 0 || c->cfg.E < 1 || n_tokens > c->cfg.max_tokens) return DOMINO_ERR_INVALID_ARG;
     if (!known(grad_dtype)) return DOMINO_ERR_UNSUPPORTED;
-    c->last_launches = 0;
     if (!dtable || !aligned(dtable, esize(grad_dtype))) return DOMINO_ERR_INVALID_ARG;
-    if (n_tokens == 0 && accumulate) return DOMINO_OK;
+    if (n_tokens == 0 && accumulate) return nothing_to_do(c);
     if (n_tokens > 0 && (!dout || !tokens || ld < c->cfg.E || !aligned(dout, esize(c->cfg.dtype)) ||
                          !aligned(tokens, 4) || dout == dtable))
         return DOMINO_ERR_INVALID_ARG;
@@ -246,6 +245,7 @@ int domino_train_embed_grad(domino_train_ctx* c, const void* dout, long long ld,
     const cudaStream_t st = (cudaStream_t)stream;
     WorkspaceOrder order(c, st);
     if (order.error != cudaSuccess) return DOMINO_ERR_CUDA;
+    c->last_launches = 0;
     const cudaError_t launched =
         train::launch_embed_grad(c, dout, ld, tokens, n_tokens, scale, dtable, grad_dtype, accumulate != 0, st);
     const cudaError_t recorded = order.done();
