@@ -84,7 +84,11 @@ DOMINO_API int domino_train_top_logits(domino_train_ctx* ctx, const void* logits
  *   p_r = exp(rest - L),  z = log sum_v exp(x_v / T),  q_v = exp(x_v / T - z),
  *   q_r = sum_{v not in S} q_v,
  *   loss = sum_S p_k (log p_k - log q_k) + p_r (log p_r - log q_r)
- * (0 log 0 = 0).  A row whose record holds no mass (L = -inf) has loss 0.
+ * (0 log 0 = 0).  A row whose record holds no mass (L = -inf) has loss 0.  A row
+ * with a target whose own logits are all -inf has no q: its loss is NaN.  What
+ * all logits of a row share cancels, up to the type's lowest value.  With K = 1
+ * and no rest the loss is the cross entropy with the label ids[n] (any finite
+ * top), and -1 is an ignored position.
  * stats [n_rows, DOMINO_TRAIN_STATS] fp32 is what distill_backward needs.
  * 1 <= K <= DOMINO_TRAIN_MAX_K; 1e-3 <= temperature <= 1e3.
  * Errors: INVALID_ARG, CUDA. */

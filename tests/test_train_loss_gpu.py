@@ -58,3 +58,31 @@ def test_shifted_rows(student, teacher):
     got = _losses(rows(x + student, torch.float32), ids, top + np.float32(teacher), rest + np.float32(teacher), T)
     for route, loss in got.items():
         assert (np.abs(loss - want) <= tol).all(), (route, np.abs(loss - want), tol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("with_rest", [False, True])
+def test_a_student_without_any_logit(dtype, with_rest):
+    """All logits -inf: no q.  NaN with a target, 0 without one; the rows beside it are untouched by it."""
+    from speculative_decoding_draft_lm_gb300.train import DominoTrain
+    g = np.random.default_rng(6)
+    V, K = 700, 9
+    xv = g.normal(0, 2, (4, V))
+    xv[[0, 2]] = -np.inf
+    x = rows(xv, TORCH[dtype])
+    ids = np.stack([g.permutation(V)[:K] for _ in range(4)]).astype(np.int32)
+    ids[2] = -1
+    top = g.normal(0, 2, (4, K)).astype(np.float32)
+    rest = np.asarray([0.5, 0.5, -np.inf, 0.5], np.float32) if with_rest else None
+    tr = DominoTrain(V, dtype=dtype)
+    i, t, r = torch.as_tensor(ids).cuda(), torch.as_tensor(top).cuda(), None if rest is None else torch.as_tensor(rest).cuda()
+    want, _, parts = O.distill(wide(x), ids, top.astype(np.float64), None if rest is None else rest.astype(np.float64), 1.0)
+    tol = (4 * sum_error(V) + 8 * EPS32) * (1.0 + parts["loss"])
+    loss, stats = tr.distill_forward(x, i, t, r)
+    w = torch.ones(4, device="cuda")
+    grad = tr.distill_backward(x, i, t, r, stats, w)
+    both = tr.distill_step(x, i, t, r, w)
+    torch.cuda.synchronize()
+    for l, d in ((loss, grad), both):
+        assert np.isnan(wide(l)[0]) and wide(l)[2] == 0 and not d[2].any()
+        assert (np.abs(wide(l) - want)[[1, 3]] <= tol[[1, 3]]).all() and torch.isfinite(d[[1, 3]]).all()
