@@ -206,22 +206,26 @@ __device__ __forceinline__ void walk(const int32_t* ids, int K, int v0, int n, F
 // brings it in, the sums are a pass over shared memory, the cluster's CTAs send
 // theirs into each other's shared memory, and a second pass writes the gradient.
 // So the logits are read once and the gradient is written once, which is all the
-// traffic there is: 3840 rows of 151,936 bf16 logits in 367 us, 6.4 TB/s, 0.95 of
-// the measured copy rate (349 us); 15 rows in 8.3 us.
+// traffic there is: 3840 rows of 151,936 bf16 logits in 370 us, 6.3 TB/s, 0.94 of
+// the measured copy rate (349 us); 15 rows in 8.2 us.
 //
 // What bounds it is HBM, and how long a slice stays in shared memory.  Hence
 // slices of 40 KB, of which five fit an SM, in one wave of clusters that take rows
-// in turn (20 and 80 KB: 430 and 432 us; 192 and 256 threads: 396 and 404); the sums by stores that
-// count on the reader's barrier (with a barrier of the cluster, which also waits
-// for the last row's gradient to arrive in memory: 433 us); the gradient straight
-// to memory, so that the buffer is free once it is read (through the buffer and a
-// bulk copy: 60 us more); everything of a row that is not its logits read a row
-// ahead, two entries of the record a thread; the loss after the gradient's
-// factors.  Two half-size buffers per CTA, in clusters of 16, took 744 us, reading
-// the row twice from global memory (the second time from L2) 564 us.
+// in turn (20 and 80 KB: 438 and 437 us; 192 and 256 threads: 400 and 410); the
+// sums by stores that count on the reader's barrier (with a barrier of the cluster,
+// which also waits for the last row's gradient to arrive in memory: 433 us instead
+// of 367); the gradient straight to memory, so that the buffer is free once it is
+// read; everything of a row that is not its logits read a row ahead, two entries of
+// the record a thread; the loss after the gradient's factors.  Forms tried while
+// the step took about 500 to 600 us and not since: the gradient through the buffer
+// and a bulk copy, 60 us more; two half-size buffers per CTA in clusters of 16,
+// 744 us; the row read twice from global memory (the second time from L2), 564 us.
 //
-// The forward alone streams its rows instead (below): this kernel without its
-// second pass took 87 us for 960 rows against 66 us.
+// Records above 256 entries go through loops without reads ahead: 15 rows with
+// K = 2048 take 16.6 us, with K = 8192 47 us, 960 rows with K = 2048 262 us.
+//
+// The forward alone streams its rows instead (below): when it took 66 us for 960
+// rows, this kernel without its second pass took 87 us.
 //
 // Entries of the record are taken out of the slice (set to -inf) once their
 // logits are read, so that the first pass is a plain sum over the outside.
@@ -531,14 +535,14 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_step(DistillArgs p, int chu
 // the record's entries by a bit per element, one byte (half a byte) of which
 // covers a vector.  A row is one CTA's, or a cluster's where there are few rows
 // (until 4 CTAs an SM) or its slices would pass 160 KB; only rank 0 waits for the
-// others' sums.  960 rows of 151,936 bf16 logits, 0.29 GB: 63 us, 4.6 TB/s.  What
-// bounds it is how the CTAs start and end, and instructions (two thirds of the
-// issue slots): without the masks and the additions it was 5 us faster.  Hence the
-// first vectors are asked for before the record is read (else 5 us more), and the
-// sums go by stores that count on rank 0's barrier (with barriers of the cluster:
-// 66 us, and 51 us instead of 47 for forward and backward of 240 fp32 rows of 79,999).
-// 512 and 128 threads: 5 and 6 us more; 2 vectors at once and 3 stages: 2 us more
-// for the fp32 rows.
+// others' sums.  960 rows of 151,936 bf16 logits, 0.29 GB: 57 us, 5.1 TB/s, 0.76 of
+// the measured copy rate; 240 fp32 rows of 79,999: 21 us.  What bounds it is how the
+// CTAs start and end, and instructions (0.73 of the issue slots): without the masks
+// and the additions it was 5 us faster.  Hence the first vectors are asked for
+// before the record is read (else 5 us more), and the sums go by stores that count
+// on rank 0's barrier (with barriers of the cluster 51 us instead of 47 for forward
+// and backward of the fp32 rows).  For both directions, 156 and 47.2 us: 128 threads
+// 166 and 47.7 us; 2 vectors at once and 3 stages 157 and 48.1 us.
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -678,8 +682,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_forward(DistillArgs p, int chun
 // every element as if it were outside the record and then, after a barrier, the
 // record's entries again.  A row is one block's, or several where there are few
 // rows (until 4 blocks an SM) or its slices would pass 160 KB.  Bound by HBM: 960
-// rows of 151,936 bf16 logits, 0.58 GB, in 90 us, 6.5 TB/s, 0.97 of the measured
-// copy rate.
+// rows of 151,936 bf16 logits, 0.58 GB, in 90 us alone, 6.5 TB/s, 0.97 of the
+// measured copy rate (96 us in calls after one another, whose writes still leave L2
+// when the next begins).
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) k_backward(DistillArgs p, int chunk, int size) {

@@ -110,7 +110,8 @@ constexpr int kEmbedThreads = 256;
 
 // Threads over a row's 16-byte vectors; each thread moves ROWS tokens' vectors
 // at once.  Bound by HBM and, for frequent tokens' rows, L2: 61,440 tokens of
-// E = 1536 bf16 in 45 us (0.38 GB: 8.0 TB/s, above the copy rate by what L2 holds).
+// E = 1536 bf16 in 47 us (0.38 GB: 8.0 TB/s, above the copy rate by what L2 holds).
+// Widths or strides off 16 bytes go by single elements: E = 1535 takes 152 us.
 template <typename T, int VEC, int ROWS>
 __global__ void __launch_bounds__(kEmbedThreads) k_embed(const T* __restrict__ table,
                                                          const int32_t* __restrict__ tokens, int n, int V, int E,
@@ -236,8 +237,8 @@ __device__ void tile_base(SortShared& s, unsigned before, unsigned all, int bins
 // All tokens in one cluster: a tile of 2^log_tile tokens per CTA, exchanged
 // through distributed shared memory.  Alone, most of a pass are the scattered
 // stores, 32 sectors each, so the tokens are spread over up to 16 CTAs (65,536
-// tokens: 26 us against 38 us on 8; 8,192 tokens: 12 us; the tiled passes below
-// take 42 us for either).  Beside k_fill, whose stores crowd theirs out, full
+// tokens: 26 us against 37 us on 8; 8,192 tokens: 13 us against 26 us on 1; the
+// tiled passes below took 42 us for either).  Beside k_fill, whose stores crowd theirs out, full
 // tiles on fewer CTAs end earlier (the whole gradient of 65,536 tokens: 196 us
 // against 205 us).
 __global__ void __launch_bounds__(kSortThreads) k_sort_cluster(const int32_t* __restrict__ tokens, int n, int V,
@@ -463,8 +464,8 @@ __device__ __forceinline__ void write_row(const SumArgs& p, uint32_t key, int co
     store<VEC>(to, f);
 }
 
-// 65,536 tokens of E = 1536 bf16 (0.2 GB) into 18,000 fp32 rows (0.11 GB): 68 us,
-// 0.7 of the copy rate.  Four columns a thread, four rows in flight and four
+// 65,536 tokens of E = 1536 bf16 (0.2 GB) into 18,000 fp32 rows (0.11 GB): 65 us,
+// 0.7 of the copy rate (115 us where they are added to the rows).  Four columns a thread, four rows in flight and four
 // being added, units of 64: eight columns 213 us for the whole gradient against
 // 196 us, eight rows 249 us (eight columns), units of 32 208 us.
 template <typename T, typename G, int VEC>

@@ -22,16 +22,16 @@
 // fp32 rows whose groups do not fit one CTA are spread over a cluster: every CTA finds
 // its slice's best K and rank 0 takes the others' through distributed shared
 // memory.  Few rows are not: the merge costs more than the stream gains (15 rows,
-// a CTA each or eight: K = 64 14.5 and 17.5 us, K = 512 27 and 54 us, K = 2048 48
+// a CTA each or eight: K = 64 14.4 and 17.5 us, K = 512 25 and 54 us, K = 2048 45
 // and 150 us).
 //
-// 960 rows of 151,936 bf16 logits, K = 256: 86 us, 3.4 TB/s, 0.51 of the measured
+// 960 rows of 151,936 bf16 logits, K = 256: 84 us, 3.5 TB/s, 0.52 of the measured
 // copy rate.  Of a row's 66 K cycles (three CTAs an SM) the stream takes 35 K, the
 // second read 12 K, the select 6 K, the bound, the list of groups and the order of
 // the ids 3 K each: the chains of small steps behind the stream and the
 // instructions (half of the issue slots) bound it, not HBM.  333 rows of 79,999
-// fp32 logits, K = 2048: 92 us (41 % of the row is read again); 15 rows, K = 64:
-// 14.5 us.  Groups of four vectors 4 or 8 KB apart: 93 us for the 960 rows (half of
+// fp32 logits, K = 2048: 90 us (41 % of the row is read again); 15 rows, K = 64:
+// 14.4 us.  Groups of four vectors 4 or 8 KB apart: 93 us for the 960 rows (half of
 // every sector read again was not wanted); several groups per thread between two
 // counts of the words: 87 to 89 us.  A running bound raised by selects during the
 // stream took 369, 281 and 76 us.
