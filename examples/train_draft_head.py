@@ -5,8 +5,10 @@
 The pieces in the order of a training step: the target's logits become records
 (``top_logits``), the teacher-forced tokens become GRU inputs (``embedding``),
 the head runs as the rollout runs it (bias-free GRU, SiLU projector, base
-logits added), and ``distill_loss`` gives each position's loss and gradient.
-The trained weights then go to ``DominoRollout``.  Everything is synthetic: the
+logits added), ``distill_loss`` gives each position's loss and gradient, and
+``DominoAdamW`` clips the gradients together and updates the weights.  What the
+target thinks of the head's first choices (``logprobs_forward``) is said beside
+the loss.  The trained weights then go to ``DominoRollout``.  Everything is synthetic: the
 "target" is a fixed random function of the previous token.
 """
 from __future__ import annotations
@@ -20,6 +22,7 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import torch  # noqa: E402
 
 from speculative_decoding_draft_lm_gb300 import inputs  # noqa: E402
+from speculative_decoding_draft_lm_gb300.optim import DominoAdamW  # noqa: E402
 from speculative_decoding_draft_lm_gb300.rollout import DominoRollout  # noqa: E402
 from speculative_decoding_draft_lm_gb300.train import DominoTrain, distill_loss, embedding  # noqa: E402
 
@@ -59,7 +62,7 @@ def main(steps: int = 60, B: int = 32, K: int = 64, temperature: float = 1.5, se
     # the target: what it says next depends on the token before, through a table of 8 classes
     likes = torch.randn(8, sh.V, device=dev) * 3.0
     train = DominoTrain(sh.V, E=sh.E, max_tokens=B * 15, dtype="fp32")
-    opt = torch.optim.Adam([t for t in p.values() if t.requires_grad], lr=3e-3)
+    opt = DominoAdamW([t for t in p.values() if t.requires_grad], lr=3e-3, weight_decay=0.0)
     losses = []
     for step in range(steps):
         hidden = torch.randn(B, 16, sh.H, device=dev)
@@ -70,12 +73,16 @@ def main(steps: int = 60, B: int = 32, K: int = 64, temperature: float = 1.5, se
         ids, top, rest = train.top_logits(target.reshape(B * STEPS, sh.V), K, temperature)
         logits = head_logits(train, p, tokens, s, base)
         loss = distill_loss(train, logits, ids, top, rest, temperature).mean()
-        opt.zero_grad(set_to_none=True)
+        opt.zero_grad()
         loss.backward()
-        opt.step()
+        _, clip = opt.grad_norm(max_norm=1.0)
+        opt.step(scale=clip)
         losses.append(loss.item())
         if step % 10 == 0 or step == steps - 1:
-            say(f"step {step:3d}  loss {losses[-1]:.4f}")
+            choice = logits.detach().argmax(1).to(torch.int32)
+            logprob, _ = train.logprobs_forward(target.reshape(B * STEPS, sh.V), choice, temperature)
+            say(f"step {step:3d}  loss {losses[-1]:.4f}  target's log probability of the head's choice "
+                f"{logprob.mean().item():.3f}")
     if train.status() != 0:
         raise RuntimeError("a token or id was out of range")
     # draft one block per request with the trained head
@@ -86,6 +93,7 @@ def main(steps: int = 60, B: int = 32, K: int = 64, temperature: float = 1.5, se
     torch.cuda.synchronize()
     say("proposals of request 0:", out[0].tolist())
     eng.close()
+    opt.close()
     train.close()
     return losses, out
 

@@ -3,14 +3,18 @@
  * (sm_103a), beside the rollout of domino_rollout.h (same library, same
  * status codes and dtypes).
  *
- * A draft head is trained on the target model's logits.  Three operators:
+ * A draft head is trained on the target model's logits.  Four operators:
  *
  *   top_logits   boils each row of the teacher's logits down to a record: the
  *                K largest logits, their ids, and the log-sum-exp of the rest;
  *   distill_*    the divergence of the student's distribution from that
  *                record, and its gradient by the student's logits;
+ *   logprobs_*   the log probability of each row's token, the row's entropy and
+ *                its most likely alternatives, and the gradient of the first two;
  *   embed*       the scaled embedding lookup (the GRU's input) and the
  *                gradient of its table.
+ *
+ * The weights' update and the gradients' norm are in domino_optim.h.
  *
  * Conventions.  All tensors are DEVICE pointers, row-major, owned by the
  * caller; `ld` arguments are row strides in elements.  Any pointer aligned to
@@ -47,6 +51,8 @@ typedef struct domino_train_ctx domino_train_ctx;
 #define DOMINO_TRAIN_MAX_K 8192   /* largest record                          */
 #define DOMINO_TRAIN_MAX_TOKENS 4194304 /* tokens of one embed_grad call   */
 #define DOMINO_TRAIN_STATS 8      /* floats per row of distill_forward's stats */
+#define DOMINO_TRAIN_MAX_ALTERNATIVES 32 /* of logprobs_forward              */
+#define DOMINO_TRAIN_LOGPROB_STATS 4     /* floats per row of its stats      */
 
 /* V vocabulary (2 .. DOMINO_TRAIN_MAX_V); E embedding width (0: the embedding
  * entry points are not used); max_tokens (0 .. DOMINO_TRAIN_MAX_TOKENS) sizes the workspace of embed_grad
@@ -118,6 +124,51 @@ DOMINO_API int domino_train_distill_step(domino_train_ctx* ctx, const void* logi
                                          float temperature, const float* weight, float* loss, void* dlogits,
                                          long long ld_d, void* cuda_stream);
 
+/* Scores of the rows of logits x [n_rows, V] of dtype `dtype` (whatever the
+ * context's), one token each.  With T = temperature, q_v = exp(x_v / T - z) and
+ * z = log sum_v exp(x_v / T):
+ *   logprob [n_rows]  log q_t of t = tokens[n]
+ *   entropy [n_rows]  -sum_v q_v log q_v (NULL: not written)
+ *   alt_ids, alt_logprobs [n_rows, n_alternatives]  the ids with the largest
+ *       logits, largest first, ties to the lower id, -0.0 equal to +0.0, NaN
+ *       largest, and their log q.  Ids whose logit is -inf are no alternatives:
+ *       places that remain hold -1 and -inf
+ *   stats [n_rows, DOMINO_TRAIN_LOGPROB_STATS]  what logprobs_backward needs
+ *       (NULL: not written)
+ * 0 <= n_alternatives <= min(V, DOMINO_TRAIN_MAX_ALTERNATIVES); at 0 the two
+ * arrays may be NULL.  1e-3 <= temperature <= 1e3.
+ * A row whose token is -1 takes no part, and its logits are not read: 0, 0 and
+ * no alternatives.  A row without a logit above -inf has no distribution: -inf,
+ * 0 and no alternatives.  A row with a NaN or +inf logit gets NaN for all its
+ * floats.  What all logits of a row share cancels, up to the type's lowest value.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype), CUDA. */
+DOMINO_API int domino_train_logprobs_forward(domino_train_ctx* ctx, const void* logits, int dtype, long long ld,
+                                             int n_rows, const int32_t* tokens, float temperature, float* logprob,
+                                             float* entropy, int n_alternatives, int32_t* alt_ids, float* alt_logprobs,
+                                             float* stats, void* cuda_stream);
+
+/* Gradient: dlogits [n_rows, V] (context dtype, row stride ld_d), written whole,
+ *   dlogits_v = 1 / T * (dlogprob ([v = t] - q_v) - dentropy q_v (log q_v + entropy))
+ * with dlogprob and dentropy [n_rows] fp32 the gradients by each row's two values
+ * (NULL: zeros; one of them at least is given) and stats from logprobs_forward on
+ * the same inputs in the context's dtype.  A row with both 0, without
+ * distribution, or whose token is -1 gets zeros whatever its logits.
+ * Errors: INVALID_ARG, CUDA. */
+DOMINO_API int domino_train_logprobs_backward(domino_train_ctx* ctx, const void* logits, long long ld, int n_rows,
+                                              const int32_t* tokens, float temperature, const float* stats,
+                                              const float* dlogprob, const float* dentropy, void* dlogits,
+                                              long long ld_d, void* cuda_stream);
+
+/* Scores and gradient in one call, for a training step that knows its rows'
+ * weights: logprob and entropy as logprobs_forward writes them (not multiplied;
+ * 0 for a row whose weights are both 0, which is skipped), dlogits as
+ * logprobs_backward with dlogprob = weight and dentropy = entropy_weight (either
+ * may be NULL: zeros, but not both).  Errors: INVALID_ARG, CUDA. */
+DOMINO_API int domino_train_logprobs_step(domino_train_ctx* ctx, const void* logits, long long ld, int n_rows,
+                                          const int32_t* tokens, float temperature, const float* weight,
+                                          const float* entropy_weight, float* logprob, float* entropy, void* dlogits,
+                                          long long ld_d, void* cuda_stream);
+
 /* out[i, :] = scale * table[tokens[i], :] in the context dtype (the product is
  * formed in fp32 and rounded once); zeros for padding.  table [V, E]
  * contiguous, out [n_tokens, E] with row stride ld_out.  Any n_tokens.
@@ -139,7 +190,7 @@ DOMINO_API int domino_train_embed_grad(domino_train_ctx* ctx, const void* dout, 
 /* Take the device error word in the order of `cuda_stream`, leave 0 in its
  * place, synchronise that stream (no other) and return the word's status
  * (DOMINO_OK, DOMINO_ERR_BAD_TOKEN, or DOMINO_ERR_TIMEOUT after a device-side
- * wait of a distillation call ran out of time: all outputs of that call are
+ * wait of a distillation or scoring call ran out of time: all outputs of that call are
  * undefined, rows unwritten among them, and it has to be made again), or
  * DOMINO_ERR_CUDA. */
 DOMINO_API int domino_train_status(domino_train_ctx* ctx, void* cuda_stream);

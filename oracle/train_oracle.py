@@ -87,6 +87,61 @@ def distill(x: np.ndarray, ids: np.ndarray, top: np.ndarray, rest, T: float):
     return loss, grad, {"loss": loss_parts, "grad": grad_parts}
 
 
+def logprobs(x: np.ndarray, tokens: np.ndarray, T: float, k: int = 0):
+    """(logprob [N], entropy [N], ids [N,k], alternatives [N,k], terms): the k largest
+    logits above -inf, largest first, NaN before all, ties to the lower id.  terms
+    holds per row log s, sum q |d| and sum q d^2 for d = (x - max) / T, which the
+    tolerances scale with."""
+    N, V = x.shape
+    logprob, entropy = np.zeros(N), np.zeros(N)
+    ids, alt = np.full((N, k), -1, dtype=np.int32), np.full((N, k), -np.inf)
+    terms = {"log_s": np.zeros(N), "a1": np.zeros(N), "a2": np.zeros(N)}
+    with np.errstate(all="ignore"):
+        for n in range(N):
+            t = int(tokens[n])
+            if not 0 <= t < V:
+                continue
+            if np.isnan(x[n]).any() or (x[n] == np.inf).any():
+                lq, entropy[n] = np.full(V, np.nan), np.nan
+            elif x[n].max() == -np.inf:
+                logprob[n] = -np.inf
+                continue
+            else:
+                d = (x[n] - x[n].max()) / T
+                log_s = np.log(np.exp(d).sum())
+                lq = d - log_s
+                q = np.exp(lq)
+                at = q > 0
+                entropy[n] = -(q[at] * lq[at]).sum()
+                terms["log_s"][n], terms["a1"][n] = log_s, (q[at] * -d[at]).sum()
+                terms["a2"][n] = (q[at] * d[at] ** 2).sum()
+            logprob[n] = lq[t]
+            order = np.lexsort((np.arange(V), -(x[n] + 0.0), ~np.isnan(x[n])))
+            order = [i for i in order[:k] if not x[n, i] == -np.inf]
+            ids[n, :len(order)], alt[n, :len(order)] = order, lq[order]
+    return logprob, entropy, ids, alt, terms
+
+
+def logprobs_grad(x: np.ndarray, tokens: np.ndarray, T: float, g: np.ndarray, h: np.ndarray):
+    """(gradient [N,V] of sum(g logprob + h entropy), q [N,V], log q + H [N,V]), zeros where a row takes no part."""
+    N, V = x.shape
+    grad, q, l = np.zeros((N, V)), np.zeros((N, V)), np.zeros((N, V))
+    with np.errstate(all="ignore"):
+        for n in range(N):
+            t = int(tokens[n])
+            if not 0 <= t < V or (g[n] == 0 and h[n] == 0) or x[n].max() == -np.inf:
+                continue
+            u = (x[n] - x[n].max()) / T  # far from zero the logarithm of the sum would be lost beside it
+            lq = u - _lse(u)
+            q[n] = np.exp(lq)
+            H = -np.where(q[n] > 0, q[n] * lq, 0.0).sum()
+            l[n] = np.where(q[n] > 0, lq + H, 0.0)
+            hot = np.zeros(V)
+            hot[t] = 1
+            grad[n] = (g[n] * (hot - q[n]) - h[n] * q[n] * l[n]) / T
+    return grad, q, l
+
+
 def embed(table: np.ndarray, tokens: np.ndarray, scale: float) -> np.ndarray:
     V, E = table.shape
     out = np.zeros((tokens.size, E))

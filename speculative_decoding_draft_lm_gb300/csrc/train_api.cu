@@ -42,43 +42,34 @@ train::DistillArgs distill_args(const domino_train_ctx* c, const void* x, long l
     return a;
 }
 
+// what the three scoring calls share; n = 0 is checked by the caller
+bool good_scores(const domino_train_ctx* c, const void* x, int dtype, long long ld, const int32_t* tokens) {
+    return x && tokens && ld >= c->cfg.V && aligned(x, esize(dtype)) && aligned(tokens, 4);
+}
+bool good_gradient(const domino_train_ctx* c, const void* x, const float* g, const float* h, const void* dx,
+                   long long ld_d) {
+    return (g || h) && aligned(g, 4) && aligned(h, 4) && dx && dx != x && ld_d >= c->cfg.V &&
+           aligned(dx, esize(c->cfg.dtype));
+}
+
+train::LogprobArgs logprob_args(const domino_train_ctx* c, const void* x, long long ld, int n, const int32_t* tokens,
+                                float temperature) {
+    train::LogprobArgs a = {};
+    a.x = x;
+    a.ld = ld;
+    a.n = n;
+    a.V = c->cfg.V;
+    a.tokens = tokens;
+    a.temperature = temperature;
+    a.err = c->err;
+    return a;
+}
+
 void release(domino_train_ctx* c) {  // on the context's device
-    if (c->used) cudaEventDestroy(c->used);
-    if (c->captured) cudaEventDestroy(c->captured);
+    c->use.release();
     cudaFree(c->ws_base);
     free(c);
 }
-
-// Orders the calls that use the workspace among each other, whatever their
-// streams: a call waits for the event that the last one recorded.  Always, even
-// on what looks like the same stream: a handle's value may be another stream's by
-// now.  An event recorded outside of a capture cannot be waited for inside it, nor
-// the other way round, so a capture has an event of its own for its calls.
-struct WorkspaceOrder {
-    domino_train_ctx* c;
-    cudaStream_t st;
-    bool capturing = false;
-    cudaError_t error;
-
-    WorkspaceOrder(domino_train_ctx* c_, cudaStream_t st_) : c(c_), st(st_) {
-        cudaStreamCaptureStatus status;
-        unsigned long long id = 0;
-        error = cudaStreamGetCaptureInfo(st, &status, &id);
-        if (error != cudaSuccess) return;
-        capturing = status == cudaStreamCaptureStatusActive;
-        if (capturing) {
-            if (c->captured_id == id) error = cudaStreamWaitEvent(st, c->captured, 0);
-            c->captured_id = id;
-        } else if (c->was_used) {
-            error = cudaStreamWaitEvent(st, c->used, 0);
-        }
-    }
-    // after the launches, also where one of them failed
-    cudaError_t done() {
-        if (!capturing) c->was_used = true;
-        return cudaEventRecord(capturing ? c->captured : c->used, st);
-    }
-};
 
 // The error word to `taken`, and 0 in its place: in one step, so that what
 // another stream raises meanwhile is in this answer or in the next.
@@ -139,9 +130,8 @@ int domino_train_init(domino_train_ctx** out, const domino_train_config* cfg, in
     c->part = (float*)(base + o_part);
     c->named = (unsigned*)(base + o_named);
     c->claim = (unsigned*)(base + o_claim);
-    if (cudaEventCreateWithFlags(&c->used, cudaEventDisableTiming) != cudaSuccess ||
-        cudaEventCreateWithFlags(&c->captured, cudaEventDisableTiming) != cudaSuccess ||
-        cudaMemset(c->err, 0, sizeof(int)) != cudaSuccess || train::prepare_embed_kernels() != cudaSuccess ||
+    if (c->use.create() != cudaSuccess || cudaMemset(c->err, 0, sizeof(int)) != cudaSuccess ||
+        train::prepare_embed_kernels() != cudaSuccess ||
         train::prepare_distill_kernels() != cudaSuccess || train::prepare_top_kernels() != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
         release(c);
@@ -218,6 +208,72 @@ int domino_train_distill_step(domino_train_ctx* c, const void* logits, long long
     return train::launch_distill_step(c, a, (cudaStream_t)stream) == cudaSuccess ? DOMINO_OK : DOMINO_ERR_CUDA;
 }
 
+int domino_train_logprobs_forward(domino_train_ctx* c, const void* logits, int dtype, long long ld, int n_rows,
+                                  const int32_t* tokens, float temperature, float* logprob, float* entropy,
+                                  int n_alternatives, int32_t* alt_ids, float* alt_logprobs, float* stats,
+                                  void* stream) {
+    if (!c || n_rows < 0) return DOMINO_ERR_INVALID_ARG;
+    if (!known(dtype)) return DOMINO_ERR_UNSUPPORTED;
+    if (n_alternatives < 0 || n_alternatives > c->cfg.V || n_alternatives > DOMINO_TRAIN_MAX_ALTERNATIVES ||
+        !good_temperature(temperature))
+        return DOMINO_ERR_INVALID_ARG;
+    if (n_rows == 0) return nothing_to_do(c);
+    if (!good_scores(c, logits, dtype, ld, tokens) || !logprob || !aligned(logprob, 4) || !aligned(entropy, 4) ||
+        !aligned(stats, 4))
+        return DOMINO_ERR_INVALID_ARG;
+    if (n_alternatives > 0 && (!alt_ids || !alt_logprobs || !aligned(alt_ids, 4) || !aligned(alt_logprobs, 4)))
+        return DOMINO_ERR_INVALID_ARG;
+    train::LogprobArgs a = logprob_args(c, logits, ld, n_rows, tokens, temperature);
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.k = n_alternatives;
+    a.alt_ids = alt_ids;
+    a.alt_logprobs = alt_logprobs;
+    a.stats = stats;
+    DeviceGuard guard(c->device);
+    return train::launch_logprobs_forward(c, dtype, a, (cudaStream_t)stream) == cudaSuccess ? DOMINO_OK
+                                                                                             : DOMINO_ERR_CUDA;
+}
+
+int domino_train_logprobs_backward(domino_train_ctx* c, const void* logits, long long ld, int n_rows,
+                                   const int32_t* tokens, float temperature, const float* stats,
+                                   const float* dlogprob, const float* dentropy, void* dlogits, long long ld_d,
+                                   void* stream) {
+    if (!c || n_rows < 0 || !good_temperature(temperature)) return DOMINO_ERR_INVALID_ARG;
+    if (n_rows == 0) return nothing_to_do(c);
+    if (!good_scores(c, logits, c->cfg.dtype, ld, tokens) || !stats || !aligned(stats, 4) ||
+        !good_gradient(c, logits, dlogprob, dentropy, dlogits, ld_d))
+        return DOMINO_ERR_INVALID_ARG;
+    train::LogprobArgs a = logprob_args(c, logits, ld, n_rows, tokens, temperature);
+    a.stats = const_cast<float*>(stats);
+    a.dlogprob = dlogprob;
+    a.dentropy = dentropy;
+    a.dx = dlogits;
+    a.ld_d = ld_d;
+    DeviceGuard guard(c->device);
+    return train::launch_logprobs_backward(c, a, (cudaStream_t)stream) == cudaSuccess ? DOMINO_OK : DOMINO_ERR_CUDA;
+}
+
+int domino_train_logprobs_step(domino_train_ctx* c, const void* logits, long long ld, int n_rows,
+                               const int32_t* tokens, float temperature, const float* weight,
+                               const float* entropy_weight, float* logprob, float* entropy, void* dlogits,
+                               long long ld_d, void* stream) {
+    if (!c || n_rows < 0 || !good_temperature(temperature)) return DOMINO_ERR_INVALID_ARG;
+    if (n_rows == 0) return nothing_to_do(c);
+    if (!good_scores(c, logits, c->cfg.dtype, ld, tokens) || !logprob || !entropy || !aligned(logprob, 4) ||
+        !aligned(entropy, 4) || !good_gradient(c, logits, weight, entropy_weight, dlogits, ld_d))
+        return DOMINO_ERR_INVALID_ARG;
+    train::LogprobArgs a = logprob_args(c, logits, ld, n_rows, tokens, temperature);
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.dlogprob = weight;
+    a.dentropy = entropy_weight;
+    a.dx = dlogits;
+    a.ld_d = ld_d;
+    DeviceGuard guard(c->device);
+    return train::launch_logprobs_step(c, a, (cudaStream_t)stream) == cudaSuccess ? DOMINO_OK : DOMINO_ERR_CUDA;
+}
+
 int domino_train_embed(domino_train_ctx* c, const void* table, const int32_t* tokens, int n_tokens, float scale,
                        void* out, long long ld_out, void* stream) {
     if (!c || n_tokens < 0 || c->cfg.E < 1) return DOMINO_ERR_INVALID_ARG;
@@ -243,7 +299,7 @@ int domino_train_embed_grad(domino_train_ctx* c, const void* dout, long long ld,
         return DOMINO_ERR_INVALID_ARG;
     DeviceGuard guard(c->device);
     const cudaStream_t st = (cudaStream_t)stream;
-    WorkspaceOrder order(c, st);
+    WorkspaceOrder order(&c->use, st);
     if (order.error != cudaSuccess) return DOMINO_ERR_CUDA;
     c->last_launches = 0;
     const cudaError_t launched =

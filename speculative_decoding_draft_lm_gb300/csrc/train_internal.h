@@ -2,6 +2,7 @@
 #pragma once
 
 #include "internal.h"
+#include "workspace_order.h"
 
 #include "domino_train.h"
 
@@ -20,10 +21,7 @@ struct domino_train_ctx {
     unsigned* claim;      // rows of zeros claimed so far
     float* part;          // [units][2][E] partial sums of the runs that cross a unit's edge
     void* ws_base;
-    // the workspace's last user: outside of graph capture, and in the capture `captured_id` (0: none)
-    cudaEvent_t used, captured;
-    bool was_used;
-    unsigned long long captured_id;
+    domino::WorkspaceUse use;  // of embed_grad's workspace
 };
 
 namespace domino {
@@ -63,6 +61,28 @@ struct DistillArgs {
     int* err;
 };
 
+struct LogprobArgs {
+    const void* x;           // [n, V] logits
+    long long ld;
+    int n, V;
+    const int32_t* tokens;   // [n]
+    float temperature;
+    float* logprob;          // [n]
+    float* entropy;          // [n] or null
+    int k;                   // alternatives
+    int32_t* alt_ids;        // [n, k]
+    float* alt_logprobs;
+    float* stats;            // [n, DOMINO_TRAIN_LOGPROB_STATS] or null, written by the forward, read by the backward
+    const float* dlogprob;   // [n] or null
+    const float* dentropy;   // [n] or null
+    void* dx;                // [n, V]
+    long long ld_d;
+    int* err;
+};
+
+cudaError_t launch_logprobs_forward(domino_train_ctx* c, int dtype, const LogprobArgs& a, cudaStream_t st);
+cudaError_t launch_logprobs_backward(domino_train_ctx* c, const LogprobArgs& a, cudaStream_t st);
+cudaError_t launch_logprobs_step(domino_train_ctx* c, const LogprobArgs& a, cudaStream_t st);
 cudaError_t prepare_top_kernels();
 cudaError_t launch_top(domino_train_ctx* c, const void* x, int dtype, long long ld, int n, int K, float temperature,
                        int32_t* ids, float* top, float* rest, cudaStream_t st);

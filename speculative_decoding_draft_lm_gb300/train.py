@@ -1,8 +1,8 @@
 """Python binding of the draft-head training operators in
 ``include/domino_train.h`` (ctypes): argument marshalling only, like
 ``rollout.py``.  ``DominoTrain`` takes torch CUDA tensors and the current torch
-stream; ``distill_loss`` and ``embedding`` are the operators as torch autograd
-functions.  There is no CPU fallback.
+stream; ``distill_loss``, ``token_logprobs`` and ``embedding`` are the operators
+as torch autograd functions.  There is no CPU fallback.
 """
 from __future__ import annotations
 
@@ -15,11 +15,14 @@ DOMINO_TRAIN_MAX_V = 524288
 DOMINO_TRAIN_MAX_K = 8192
 DOMINO_TRAIN_MAX_TOKENS = 4194304
 DOMINO_TRAIN_STATS = 8
+DOMINO_TRAIN_MAX_ALTERNATIVES = 32
+DOMINO_TRAIN_LOGPROB_STATS = 4
 
 # every symbol the header declares
 EXPORTED = (
     "domino_train_init", "domino_train_top_logits", "domino_train_distill_forward", "domino_train_distill_backward",
-    "domino_train_distill_step", "domino_train_embed", "domino_train_embed_grad", "domino_train_status",
+    "domino_train_distill_step", "domino_train_logprobs_forward", "domino_train_logprobs_backward",
+    "domino_train_logprobs_step", "domino_train_embed", "domino_train_embed_grad", "domino_train_status",
     "domino_train_last_launch_count", "domino_train_destroy",
 )
 
@@ -43,6 +46,9 @@ def load_library() -> ctypes.CDLL:
     lib.domino_train_distill_forward.argtypes = [vp, vp, ll, i, vp, vp, vp, i, f, vp, vp, vp]
     lib.domino_train_distill_backward.argtypes = [vp, vp, ll, i, vp, vp, vp, i, f, vp, vp, vp, ll, vp]
     lib.domino_train_distill_step.argtypes = [vp, vp, ll, i, vp, vp, vp, i, f, vp, vp, vp, ll, vp]
+    lib.domino_train_logprobs_forward.argtypes = [vp, vp, i, ll, i, vp, f, vp, vp, i, vp, vp, vp, vp]
+    lib.domino_train_logprobs_backward.argtypes = [vp, vp, ll, i, vp, f, vp, vp, vp, vp, ll, vp]
+    lib.domino_train_logprobs_step.argtypes = [vp, vp, ll, i, vp, f, vp, vp, vp, vp, vp, ll, vp]
     lib.domino_train_embed.argtypes = [vp, vp, vp, i, f, vp, ll, vp]
     lib.domino_train_embed_grad.argtypes = [vp, vp, ll, vp, i, f, vp, i, i, vp]
     lib.domino_train_status.argtypes = [vp, vp]
@@ -193,6 +199,70 @@ class DominoTrain:
             raise DominoError(status, "domino_train_distill_step")
         return loss, grad
 
+    def logprobs_forward(self, logits, tokens, temperature=1.0, alternatives=0, stats=None, out=None, stream=None):
+        """(logprob [n], entropy [n]) of logits [n, V] (bf16 or fp32) and their tokens [n] int32
+        (-1: the row takes no part); with ``alternatives`` = k > 0 also (ids [n, k] int32, logprobs
+        [n, k]) of the k most likely ids, most likely first.  ``stats``: True or a [n, 4] tensor adds
+        what logprobs_backward needs as the last value.  ``out``: the tensors before it."""
+        n, dtype, k, f32 = logits.shape[0], logits.dtype, alternatives, self._f32
+        if dtype is not self._bf16 and dtype is not f32:
+            raise ValueError(f"logits: want bfloat16 or float32, got {dtype}")
+        ld = self._rows(logits, self.V, "logits", dtype)
+        if out is None:
+            out = (self._new((n,), f32), self._new((n,), f32))
+            if k > 0:
+                out += (self._new((n, k), self._i32), self._new((n, k), f32))
+        elif len(out) != (4 if k > 0 else 2):
+            raise ValueError(f"out: want {4 if k > 0 else 2} tensors, got {len(out)}")
+        ids = scores = pstats = None
+        if k > 0:
+            ids, scores = self._flat(out[2], (n, k), self._i32, "ids"), self._flat(out[3], (n, k), f32, "alternatives")
+        if stats is not None and stats is not False:
+            if stats is True:
+                stats = self._new((n, DOMINO_TRAIN_LOGPROB_STATS), f32)
+            pstats = self._flat(stats, (n, DOMINO_TRAIN_LOGPROB_STATS), f32, "stats")
+        status = self._lib.domino_train_logprobs_forward(
+            self.ctx, logits.data_ptr(), DOMINO_DTYPE_BF16 if dtype is self._bf16 else DOMINO_DTYPE_FP32, ld, n,
+            self._flat(tokens, (n,), self._i32, "tokens"), temperature, self._flat(out[0], (n,), f32, "logprob"),
+            self._flat(out[1], (n,), f32, "entropy"), k, ids, scores, pstats, self._stream(stream))
+        if status:
+            raise DominoError(status, "domino_train_logprobs_forward")
+        return tuple(out) if pstats is None else (*out, stats)
+
+    def logprobs_backward(self, logits, tokens, stats, dlogprob, dentropy=None, temperature=1.0, out=None, stream=None):
+        """dlogits [n, V] from the gradients dlogprob and dentropy [n] (None: zeros, not both) by each row's two values."""
+        n = logits.shape[0]
+        ld = self._rows(logits, self.V, "logits")
+        if out is None:
+            out = self._new((n, self.V), self.torch_dtype)
+        status = self._lib.domino_train_logprobs_backward(
+            self.ctx, logits.data_ptr(), ld, n, self._flat(tokens, (n,), self._i32, "tokens"), temperature,
+            self._flat(stats, (n, DOMINO_TRAIN_LOGPROB_STATS), self._f32, "stats"),
+            None if dlogprob is None else self._flat(dlogprob, (n,), self._f32, "dlogprob"),
+            None if dentropy is None else self._flat(dentropy, (n,), self._f32, "dentropy"),
+            out.data_ptr(), self._rows(out, self.V, "dlogits", n=n), self._stream(stream))
+        if status:
+            raise DominoError(status, "domino_train_logprobs_backward")
+        return out
+
+    def logprobs_step(self, logits, tokens, weight, entropy_weight=None, temperature=1.0, out=None, stream=None):
+        """(logprob [n], entropy [n], dlogits [n, V]) in one call; dlogits is the gradient of
+        sum(weight * logprob + entropy_weight * entropy) (either may be None: zeros, not both)."""
+        n = logits.shape[0]
+        ld = self._rows(logits, self.V, "logits")
+        if out is None:
+            out = (self._new((n,), self._f32), self._new((n,), self._f32), self._new((n, self.V), self.torch_dtype))
+        logprob, entropy, grad = out
+        status = self._lib.domino_train_logprobs_step(
+            self.ctx, logits.data_ptr(), ld, n, self._flat(tokens, (n,), self._i32, "tokens"), temperature,
+            None if weight is None else self._flat(weight, (n,), self._f32, "weight"),
+            None if entropy_weight is None else self._flat(entropy_weight, (n,), self._f32, "entropy_weight"),
+            self._flat(logprob, (n,), self._f32, "logprob"), self._flat(entropy, (n,), self._f32, "entropy"),
+            grad.data_ptr(), self._rows(grad, self.V, "dlogits", n=n), self._stream(stream))
+        if status:
+            raise DominoError(status, "domino_train_logprobs_step")
+        return logprob, entropy, grad
+
     def embed(self, table, tokens, scale=1.0, out=None, stream=None):
         """scale * table[tokens] for tokens [n] int32 (-1: zeros)."""
         n = tokens.shape[0]
@@ -231,7 +301,7 @@ class DominoTrain:
 
     def status(self, stream=None) -> int:
         """Synchronise the stream; return and clear the device's error word as a status code.
-        After DOMINO_ERR_TIMEOUT all outputs of the distillation call that timed out are undefined."""
+        After DOMINO_ERR_TIMEOUT all outputs of the distillation or scoring call that timed out are undefined."""
         return self._lib.domino_train_status(self.ctx, self._stream(stream))
 
     def last_launch_count(self) -> int:
@@ -254,6 +324,15 @@ class DominoTrain:
 def distill_loss(train: DominoTrain, logits, ids, top, rest=None, temperature=1.0):
     """Loss [n] of student logits [n, V], differentiable (once) by the logits."""
     return _functions()[0].apply(logits, train, ids, top, rest, temperature)
+
+
+def token_logprobs(train: DominoTrain, logits, tokens, temperature=1.0, alternatives=0):
+    """(logprob [n], entropy [n]) of logits [n, V] (the context's type) and their
+    tokens, both differentiable (once) by the logits; with ``alternatives`` = k > 0
+    also the k most likely ids [n, k] and their logprobs, which are not."""
+    if logits.dtype is not train.torch_dtype:
+        raise ValueError(f"logits: want {train.torch_dtype}, got {logits.dtype}")
+    return _functions()[2].apply(logits, train, tokens, temperature, alternatives)
 
 
 def embedding(train: DominoTrain, table, tokens, scale=1.0):
@@ -312,5 +391,35 @@ def _functions():
                     grad = train.embed_grad(dout[i:j], tokens[i:j], ctx.scale, out=grad, accumulate=grad is not None)
                 return grad.to(train.torch_dtype), None, None, None
 
-        _autograd = (Distill, Embedding)
+        class Once(torch.autograd.Function):
+            """A gradient that depends on `x` and has no derivative of its own."""
+            @staticmethod
+            def forward(ctx, grad, x):
+                return grad.view_as(grad)
+
+            @staticmethod
+            def backward(ctx, _):
+                raise RuntimeError("token_logprobs is differentiable once")
+
+        class Logprobs(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, logits, train, tokens, temperature, alternatives):
+                *out, stats = train.logprobs_forward(logits, tokens, temperature, alternatives, stats=True)
+                ctx.save_for_backward(logits, tokens, stats)
+                ctx.train, ctx.temperature = train, temperature
+                ctx.mark_non_differentiable(*out[2:])
+                ctx.set_materialize_grads(False)
+                return tuple(out)
+
+            @staticmethod
+            def backward(ctx, dlogprob, dentropy, *_):
+                logits, tokens, stats = ctx.saved_tensors
+                if dlogprob is None and dentropy is None:
+                    return None, None, None, None, None
+                d = [None if t is None else t.detach().contiguous() for t in (dlogprob, dentropy)]
+                grad = ctx.train.logprobs_backward(logits.detach(), tokens, stats, *d, ctx.temperature)
+                # under create_graph a second derivative raises, also where the incoming gradient has none
+                return Once.apply(grad, logits) if torch.is_grad_enabled() else grad, None, None, None, None
+
+        _autograd = (Distill, Embedding, Logprobs)
     return _autograd
