@@ -50,7 +50,8 @@ typedef struct {
 
 /* state_bits 32: m and v are flat fp32 buffers.  state_bits 8: flat buffers of
  * e4m3 codes, with one fp32 scale per block of DOMINO_ADAMW_BLOCK positions in
- * m_scale and v_scale: a moment is its code's value times its block's scale.  All
+ * m_scale and v_scale: a moment is its code's value times its block's scale.  m, v
+ * and master are aligned to 32 bytes.  All
  * zero at the start.  count: the steps taken so far, device, 8-byte aligned.
  * 0 <= beta1, beta2 < 1; 1e-16 <= eps <= 1; 0 <= weight_decay <= 1. */
 typedef struct {
@@ -91,7 +92,7 @@ DOMINO_API int domino_adamw_init(domino_adamw_ctx** out, const domino_adamw_conf
  * bf16 parameters without master, and 8-bit moments.  A block's scale is
  * max(largest |a| * (1 / 448), 2^-120); |a| / scale, at most 448, goes to one of
  * its two neighbours in e4m3, up with the probability of its place between them;
- * a v that is not 0 is never rounded to 0.  The random bits of position i in step
+ * a v of 2^-126 or more is never rounded to 0.  The random bits of position i in step
  * t are a function of (seed, t, i) alone, modulo 2^32:
  *   mix(h): h ^= h >> 15, h *= 0x6A09E667, h ^= h >> 13, h *= 0xBB67AE85, h ^ h >> 16
  *   key = mix(mix(t + 0x9E3779B9) + seed)

@@ -1,0 +1,76 @@
+// AdamW with moments in fp32.
+//
+// A thread has 8 consecutive elements; each is read and written once.
+#include "optim_adamw.cuh"
+
+namespace domino {
+namespace optim {
+
+namespace {
+
+constexpr int kE = 8;
+static_assert(kThreads * kE == kTile32, "a tile is one vector of every thread");
+
+template <int NT, typename K>
+__global__ void __launch_bounds__(kThreads, 4) k_adamw32(const __grid_constant__ Table<NT> w, AdamArgs a) {
+    typedef typename K::P P;
+    typedef typename K::G G;
+    const Coefficients k = coefficients(a);
+    int at = 0;
+    for (unsigned tile = blockIdx.x; !k.skip && tile < w.tiles; tile += gridDim.x) {
+        at = find(w, tile, at);
+        const Entry& e = w.e[at];
+        const long long n = e.n & kElements, i = (long long)(tile - e.tile) * kTile32 + threadIdx.x * kE;
+        const long long pos = (long long)e.block * kBlock + i;
+        if (i >= n) continue;
+        float* const m32 = static_cast<float*>(a.m) + (pos - i);
+        float* const v32 = static_cast<float*>(a.v) + (pos - i);
+        uint32_t rg[kE * sizeof(G) / 4], rp[kE * K::kFrom / 4], rm[kE], rv[kE];
+        load_elements<G, kE>(rg, static_cast<const G*>(e.g), i, n);
+        if (K::kMaster) load_elements<float, kE>(rp, a.master + (pos - i), i, n);
+        else load_elements<P, kE>(rp, static_cast<const P*>(e.p), i, n);
+        load_elements<float, kE>(rm, m32, i, n);
+        load_elements<float, kE>(rv, v32, i, n);
+        const unsigned h0 = (unsigned)pos * 0x9E3779B9u + (unsigned)(pos >> 32) * 0x3C6EF373u + k.key;
+#pragma unroll
+        for (int j = 0; j < kE / 2; ++j) {
+            const F2 g = mul2(f2(element<G>(rg, 2 * j), element<G>(rg, 2 * j + 1)), both(k.scale));
+            const F2 m = new_m(a, f2(element<float>(rm, 2 * j), element<float>(rm, 2 * j + 1)), g);
+            const F2 v = new_v(a, f2(element<float>(rv, 2 * j), element<float>(rv, 2 * j + 1)), g);
+            F2 p;
+            if (K::kFrom == 4) p = f2(element<float>(rp, 2 * j), element<float>(rp, 2 * j + 1));
+            else p = f2(element<P>(rp, 2 * j), element<P>(rp, 2 * j + 1));
+            const float2 mf = halves(m), vf = halves(v), q = halves(updated(a, k, p, m, v));
+            rm[2 * j] = __float_as_uint(mf.x);
+            rm[2 * j + 1] = __float_as_uint(mf.y);
+            rv[2 * j] = __float_as_uint(vf.x);
+            rv[2 * j + 1] = __float_as_uint(vf.y);
+            if (K::kLossy) {
+                rp[j] = lossy(q, mix(h0 + (2 * j) * 0x9E3779B9u), mix(h0 + (2 * j + 1) * 0x9E3779B9u));
+            } else {
+                rp[2 * j] = __float_as_uint(q.x);
+                rp[2 * j + 1] = __float_as_uint(q.y);
+            }
+        }
+        store_param<K, kE>(e, a.master, pos, i, n, rp);
+        store_elements<float, kE>(m32, i, n, rm);
+        store_elements<float, kE>(v32, i, n, rv);
+    }
+    done(a, k.skip);
+}
+
+template <int NT, typename K>
+cudaError_t launch_kind(const domino_adamw_ctx* c, const Work& w, const AdamArgs& a, cudaStream_t st) {
+    const unsigned most = (unsigned)c->num_sms * 4;
+    k_adamw32<NT, K><<<w.tiles < 1 ? 1 : w.tiles < most ? w.tiles : most, kThreads, 0, st>>>(table<NT>(w), a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_adamw32(const domino_adamw_ctx* c, const Work& w, const AdamArgs& a, cudaStream_t st) {
+    return of_kind(w, [&](auto nt, auto kind) { return launch_kind<decltype(nt)::value, decltype(kind)>(c, w, a, st); });
+}
+
+}  // namespace optim
+}  // namespace domino

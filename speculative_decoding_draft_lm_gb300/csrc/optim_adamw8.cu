@@ -1,0 +1,146 @@
+// AdamW with moments in e4m3, a scale for every 128 of them.
+//
+// A thread has 16 consecutive elements, eight threads a block: the largest
+// magnitudes of a block meet by shuffles, so each element is read and written once.
+#include "optim_adamw.cuh"
+
+namespace domino {
+namespace optim {
+
+namespace {
+
+constexpr int kE = 16, kLanes = kBlock / kE;
+static_assert(kThreads * kE == kTile8, "a tile is one vector of every thread");
+
+// four codes in the bytes of a word from words of places and their random bits, of m (signed) or of v
+__device__ __forceinline__ uint32_t codes_m(const uint32_t* x) {
+    constexpr uint32_t kMost = 0x07EF07EFu;  // the code 126, in bits 4 to 10 of a half
+    const uint32_t a = upper(x[0], x[1]), b = upper(x[2], x[3]);
+    const uint32_t lo = min16(a & 0x7FFF7FFFu, kMost) >> 4, hi = min16(b & 0x7FFF7FFFu, kMost) >> 4;
+    return (__byte_perm(lo, hi, 0x6420) & 0x7F7F7F7Fu) | (__byte_perm(a, b, 0x7531) & 0x80808080u);
+}
+__device__ __forceinline__ uint32_t codes_v(const uint32_t* x, const uint32_t* v) {
+    constexpr uint32_t kMost = 0x07EF07EFu, kLeast = 0x00100010u;
+    // a v that is not 0 does not become 0: its upper half is not 0 either, from 2^-126 on
+    const uint32_t a = max16(upper(x[0], x[1]), min16(upper(v[0], v[1]), kLeast));
+    const uint32_t b = max16(upper(x[2], x[3]), min16(upper(v[2], v[3]), kLeast));
+    return __byte_perm(min16(a, kMost) >> 4, min16(b, kMost) >> 4, 0x6420);
+}
+
+template <int NT, typename K>
+__global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ Table<NT> w, AdamArgs a) {
+    typedef typename K::P P;
+    typedef typename K::G G;
+    const Coefficients k = coefficients(a);
+    int at = 0;
+    for (unsigned tile = blockIdx.x; !k.skip && tile < w.tiles; tile += gridDim.x) {
+        at = find(w, tile, at);
+        const Entry& e = w.e[at];
+        const long long n = e.n & kElements, i = (long long)(tile - e.tile) * kTile8 + threadIdx.x * kE;
+        const long long block = (long long)e.block + i / kBlock, pos = (long long)e.block * kBlock + i;
+        uint32_t rg[kE * sizeof(G) / 4], rp[kE * K::kFrom / 4], rm[4], rv[4];
+        load_elements<G, kE>(rg, static_cast<const G*>(e.g), i, n);
+        if (K::kMaster) load_elements<float, kE>(rp, a.master + (pos - i), i, n);
+        else load_elements<P, kE>(rp, static_cast<const P*>(e.p), i, n);
+        uint8_t* const m8 = static_cast<uint8_t*>(a.m) + pos;
+        uint8_t* const v8 = static_cast<uint8_t*>(a.v) + pos;
+        float sm = 0.f, sv = 0.f;
+        if (i + kE <= n) {
+            load_words<4>(rm, m8, false);
+            load_words<4>(rv, v8, false);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) rm[j] = rv[j] = 0;
+#pragma unroll
+            for (int j = 0; j < kE; ++j) {
+                if (i + j >= n) continue;
+                rm[j / 4] |= (uint32_t)m8[j] << (j % 4 * 8);
+                rv[j / 4] |= (uint32_t)v8[j] << (j % 4 * 8);
+            }
+        }
+        if (i < n) {
+            sm = a.m_scale[block];
+            sv = a.v_scale[block];
+        }
+        const unsigned h0 = (unsigned)pos * 0x9E3779B9u + (unsigned)(pos >> 32) * 0x3C6EF373u + k.key;
+        F2 m[kE / 2], v[kE / 2];
+        float top_m = 0.f, top_v = 0.f;
+#pragma unroll
+        for (int j = 0; j < kE / 2; ++j) {
+            const F2 g = mul2(f2(element<G>(rg, 2 * j), element<G>(rg, 2 * j + 1)), both(k.scale));
+            const uint32_t cm = rm[j / 2] >> (j % 2 * 16), cv = rv[j / 2] >> (j % 2 * 16);
+            m[j] = new_m(a, mul2(e4m3_values(cm), both(sm)), g);
+            v[j] = new_v(a, mul2(e4m3_values(cv), both(sv)), g);
+            const float2 vf = halves(v[j]), mf = halves(m[j]);
+            top_m = top_nan(top_m, top_nan(mf.x, mf.y));
+            top_v = top_nan(top_v, top_nan(vf.x, vf.y));
+            F2 p;
+            if (K::kFrom == 4) p = f2(element<float>(rp, 2 * j), element<float>(rp, 2 * j + 1));
+            else p = f2(element<P>(rp, 2 * j), element<P>(rp, 2 * j + 1));
+            const float2 q = halves(updated(a, k, p, m[j], v[j]));
+            if (K::kLossy) {
+                rp[j] = lossy(q, mix(h0 + (2 * j) * 0x9E3779B9u), mix(h0 + (2 * j + 1) * 0x9E3779B9u));
+            } else {
+                rp[2 * j] = __float_as_uint(q.x);
+                rp[2 * j + 1] = __float_as_uint(q.y);
+            }
+        }
+        store_param<K, kE>(e, a.master, pos, i, n, rp);
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) {
+            top_m = top_nan(top_m, __shfl_xor_sync(0xffffffffu, top_m, o));
+            top_v = top_nan(top_v, __shfl_xor_sync(0xffffffffu, top_v, o));
+        }
+        const Scale zm = scale_of(top_m), zv = scale_of(top_v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t xm[4], xv[4], vw[4];
+#pragma unroll
+            for (int l = 0; l < 2; ++l) {
+                const uint2 ym = places(m[2 * j + l], both(zm.inv), both(-zm.s)), yv = places(v[2 * j + l], both(zv.inv), both(-zv.s));
+                const unsigned r0 = mix(h0 + (4 * j + 2 * l) * 0x9E3779B9u), r1 = mix(h0 + (4 * j + 2 * l + 1) * 0x9E3779B9u);
+                xm[2 * l] = ym.x + (r0 & 0xFFFFFu);
+                xm[2 * l + 1] = ym.y + (r1 & 0xFFFFFu);
+                xv[2 * l] = yv.x + (r0 >> 12);
+                xv[2 * l + 1] = yv.y + (r1 >> 12);
+                const float2 vf = halves(v[2 * j + l]);
+                vw[2 * l] = __float_as_uint(vf.x);
+                vw[2 * l + 1] = __float_as_uint(vf.y);
+            }
+            rm[j] = codes_m(xm);
+            rv[j] = codes_v(xv, vw);
+        }
+        if (i + kE <= n) {
+            store_words<4>(m8, rm, false);
+            store_words<4>(v8, rv, false);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kE; ++j) {
+                if (i + j >= n) continue;
+                m8[j] = (uint8_t)(rm[j / 4] >> (j % 4 * 8));
+                v8[j] = (uint8_t)(rv[j / 4] >> (j % 4 * 8));
+            }
+        }
+        if (threadIdx.x % kLanes == 0 && i < n) {
+            a.m_scale[block] = zm.s;
+            a.v_scale[block] = zv.s;
+        }
+    }
+    done(a, k.skip);
+}
+
+template <int NT, typename K>
+cudaError_t launch_kind(const domino_adamw_ctx* c, const Work& w, const AdamArgs& a, cudaStream_t st) {
+    const unsigned most = (unsigned)c->num_sms * 3;
+    k_adamw8<NT, K><<<w.tiles < 1 ? 1 : w.tiles < most ? w.tiles : most, kThreads, 0, st>>>(table<NT>(w), a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_adamw8(const domino_adamw_ctx* c, const Work& w, const AdamArgs& a, cudaStream_t st) {
+    return of_kind(w, [&](auto nt, auto kind) { return launch_kind<decltype(nt)::value, decltype(kind)>(c, w, a, st); });
+}
+
+}  // namespace optim
+}  // namespace domino

@@ -46,7 +46,7 @@ int check(const domino_adamw_config* g, long long* blocks) {
         if (*blocks > kMaxElements / DOMINO_ADAMW_BLOCK) return DOMINO_ERR_INVALID_ARG;
     }
     const bool narrow = g->state_bits == 8, empty = *blocks == 0;
-    const int align = 16;
+    const int align = 32;
     if (!g->count || !aligned(g->count, 8) || !aligned(g->m, align) || !aligned(g->v, align) ||
         !aligned(g->m_scale, 4) || !aligned(g->v_scale, 4) || !aligned(g->master, align))
         return DOMINO_ERR_INVALID_ARG;
@@ -86,30 +86,33 @@ int check_gradients(const domino_adamw_ctx* c, const void* const* grads, const i
     return DOMINO_OK;
 }
 
-// The tensors from *next on that one launch takes; *next becomes the one behind them.
-Work gather(domino_adamw_ctx* c, const void* const* grads, const int* dtypes, int* next) {
-    Work w = {0, 0, c->entry};
+// what a tensor and its gradient are, as in Entry::n
+unsigned long long kind_of(const domino_adamw_tensor& t, int grad_dtype) {
+    return (t.dtype == DOMINO_DTYPE_BF16 ? kParamBf16 : 0) | (t.master ? kMaster : 0) |
+           (grad_dtype == DOMINO_DTYPE_BF16 ? kGradBf16 : 0);
+}
+
+// The tensors from *next on that one launch takes, of one kind or (kAnyKind) of any; *next becomes the one behind them.
+constexpr unsigned long long kAnyKind = ~0ull;
+Work gather(domino_adamw_ctx* c, const void* const* grads, const int* dtypes, unsigned long long kind, int tile,
+            int* next) {
+    Work w = {0, 0, kind == kAnyKind ? 0 : kind, c->entry};
     int i = *next;
     for (; i < c->cfg.n_tensors && w.tensors < kMaxPerLaunch; ++i) {
         const domino_adamw_tensor& t = c->tensors[i];
         if (!grads[i] || t.n == 0) continue;
+        const unsigned long long its = kind_of(t, dtypes[i]);
+        if (kind != kAnyKind && its != kind) continue;
         Entry& e = w.entry[w.tensors++];
         e.p = t.param;
         e.g = grads[i];
-        e.n = (unsigned long long)t.n | (t.dtype == DOMINO_DTYPE_BF16 ? kParamBf16 : 0) | (t.master ? kMaster : 0) |
-              (dtypes[i] == DOMINO_DTYPE_BF16 ? kGradBf16 : 0);
+        e.n = (unsigned long long)t.n | its;
         e.tile = w.tiles;
         e.block = c->block[i];
-        w.tiles += (unsigned)((t.n + kTile - 1) / kTile);
+        w.tiles += (unsigned)((t.n + tile - 1) / tile);
     }
     *next = i;
     return w;
-}
-
-bool any_left(const domino_adamw_ctx* c, const void* const* grads, int i) {
-    for (; i < c->cfg.n_tensors; ++i)
-        if (grads[i] && c->tensors[i].n > 0) return true;
-    return false;
 }
 
 void release(domino_adamw_ctx* c) {  // on the context's device
@@ -200,19 +203,36 @@ int domino_adamw_step(domino_adamw_ctx* c, const void* const* grads, const int* 
     a.log_beta2 = (float)log(g.beta2);
     a.eps = (float)g.eps;
     a.decay = (float)g.weight_decay;
+    a.one = 1.f;
     a.seed = g.seed;
     DeviceGuard guard(c->device);
     const cudaStream_t st = (cudaStream_t)stream;
     WorkspaceOrder order(&c->use, st);
     if (order.error != cudaSuccess) return DOMINO_ERR_CUDA;
+    // a launch for every kind of tensors (mostly one), and for every kMaxPerLaunch of a kind
+    bool seen[8] = {};
+    int kinds = 0, launches = 0;
+    unsigned long long kind[8];
+    for (int i = 0; i < g.n_tensors; ++i) {
+        if (!grads[i] || c->tensors[i].n == 0) continue;
+        const unsigned long long its = kind_of(c->tensors[i], grad_dtypes[i]);
+        bool& known_kind = seen[its / kParamBf16];
+        if (!known_kind) kind[kinds++] = its;
+        known_kind = true;
+    }
+    if (kinds == 0) kind[kinds++] = 0;  // also without a gradient: the step counts
     cudaError_t launched = cudaSuccess;
-    int next = 0, launches = 0;
-    do {  // also without a gradient: the step counts
-        const Work w = gather(c, grads, grad_dtypes, &next);
-        a.last = !any_left(c, grads, next);
-        launched = launch_adamw(c, w, a, st);
-        ++launches;
-    } while (launched == cudaSuccess && !a.last);
+    for (int k = 0; launched == cudaSuccess && k < kinds; ++k) {
+        int next = 0;
+        do {
+            const Work w = gather(c, grads, grad_dtypes, kind[k], g.state_bits == 8 ? kTile8 : kTile32, &next);
+            for (; next < g.n_tensors; ++next)  // to the next one of this kind
+                if (grads[next] && c->tensors[next].n > 0 && kind_of(c->tensors[next], grad_dtypes[next]) == kind[k]) break;
+            a.last = k == kinds - 1 && next == g.n_tensors;
+            launched = g.state_bits == 8 ? launch_adamw8(c, w, a, st) : launch_adamw32(c, w, a, st);
+            ++launches;
+        } while (launched == cudaSuccess && next < g.n_tensors);
+    }
     const cudaError_t recorded = order.done();
     if (launched != cudaSuccess || recorded != cudaSuccess) return DOMINO_ERR_CUDA;
     c->last_launches = launches;
@@ -231,7 +251,8 @@ int domino_adamw_grad_norm(domino_adamw_ctx* c, const void* const* grads, const 
     a.max_norm = max_norm;
     a.norm = norm;
     a.scale = scale;
-    for (int next = 0; next < c->cfg.n_tensors;) a.ctas += norm_ctas(c, gather(c, grads, grad_dtypes, &next).tiles);
+    for (int next = 0; next < c->cfg.n_tensors;) 
+        a.ctas += norm_ctas(c, gather(c, grads, grad_dtypes, kAnyKind, kNormTile, &next).tiles);
     DeviceGuard guard(c->device);
     const cudaStream_t st = (cudaStream_t)stream;
     WorkspaceOrder order(&c->use, st);
@@ -241,10 +262,10 @@ int domino_adamw_grad_norm(domino_adamw_ctx* c, const void* const* grads, const 
     const bool none = a.ctas == 0;
     if (none) a.ctas = 1;
     for (int next = 0; launched == cudaSuccess && next < c->cfg.n_tensors;) {
-        const Work w = gather(c, grads, grad_dtypes, &next);
+        const Work w = gather(c, grads, grad_dtypes, kAnyKind, kNormTile, &next);
         const unsigned ctas = none ? 1 : norm_ctas(c, w.tiles);
         if (ctas == 0) continue;
-        launched = launch_norm(c, w, a, ctas, st);
+        launched = launch_norm(w, a, ctas, st);
         a.first += ctas;
         ++launches;
         if (none) break;

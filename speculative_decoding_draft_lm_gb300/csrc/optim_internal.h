@@ -9,7 +9,8 @@
 namespace domino {
 namespace optim {
 
-constexpr int kTile = 4096;          // elements that a CTA takes at once
+// elements that a CTA takes at once, in each kernel
+constexpr int kTile8 = 4096, kTile32 = 2048, kNormTile = 4096;
 constexpr int kMaxPerLaunch = 1000;  // tensors
 
 // A tensor of one launch, as the kernels' parameters hold it.
@@ -27,6 +28,7 @@ constexpr long long kMaxElements = 1ll << 38;  // of one context: tiles and bloc
 struct Work {
     int tensors;
     unsigned tiles;
+    unsigned long long kind;  // of all its tensors, as in Entry::n (0 for the norm)
     Entry* entry;  // host, [tensors]
 };
 
@@ -37,7 +39,7 @@ struct AdamArgs {
     const float* scale;
     const float* lr_factor;
     unsigned* ticket;
-    float lr, beta1, beta2, rest1, rest2, log_beta1, log_beta2, eps, decay;  // rest: 1 - beta
+    float lr, beta1, beta2, rest1, rest2, log_beta1, log_beta2, eps, decay, one;  // rest: 1 - beta; one: 1
     unsigned seed;
     int last;  // the step's last launch: the one that counts it
 };
@@ -70,8 +72,9 @@ namespace domino {
 namespace optim {
 
 unsigned norm_ctas(const domino_adamw_ctx* c, unsigned tiles);  // of a launch over so many tiles
-cudaError_t launch_adamw(domino_adamw_ctx* c, const Work& w, const AdamArgs& a, cudaStream_t st);
-cudaError_t launch_norm(domino_adamw_ctx* c, const Work& w, const NormArgs& a, unsigned ctas, cudaStream_t st);
+cudaError_t launch_adamw8(const domino_adamw_ctx* c, const Work& w, const AdamArgs& a, cudaStream_t st);
+cudaError_t launch_adamw32(const domino_adamw_ctx* c, const Work& w, const AdamArgs& a, cudaStream_t st);
+cudaError_t launch_norm(const Work& w, const NormArgs& a, unsigned ctas, cudaStream_t st);
 
 }  // namespace optim
 }  // namespace domino

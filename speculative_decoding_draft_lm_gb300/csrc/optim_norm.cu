@@ -1,0 +1,105 @@
+// The norm of the gradients of many tensors, and the factor that clips it.
+//
+// Every thread adds the squares of 16 consecutive elements in fp32 and keeps the
+// sum of such sums with what its additions round off; the CTAs' sums meet in fp64,
+// in an order that the sizes fix, at the CTA that is done last.
+#include "optim_table.cuh"
+
+namespace domino {
+namespace optim {
+
+namespace {
+
+constexpr int kE = 16;
+static_assert(kThreads * kE == kNormTile, "a tile is one vector of every thread");
+
+// A running sum s with what its additions rounded off, c.
+struct Sum {
+    float s = 0.f, c = 0.f;
+    __device__ __forceinline__ void add(float x) {
+        const float t = __fadd_rn(s, x), b = __fadd_rn(t, -s);
+        c += __fadd_rn(s, -__fadd_rn(t, -b)) + __fadd_rn(x, -b);
+        s = t;
+    }
+    __device__ __forceinline__ double value() const { return s < INFINITY ? (double)s + (double)c : (double)s; }
+};
+
+// The sum over a CTA's threads, in an order of its own; every thread gets it.
+__device__ __forceinline__ double block_sum(double s) {
+    __shared__ double part[kThreads / 32];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = s;
+    __syncthreads();
+    s = 0;
+    for (int i = 0; i < kThreads / 32; ++i) s += part[i];
+    return s;
+}
+
+template <typename G>
+__device__ __forceinline__ float squares(const uint32_t* w) {
+    float q = 0.f;
+#pragma unroll
+    for (int j = 0; j < kE; ++j) {
+        const float g = element<G>(w, j);
+        q = fmaf(g, g, q);
+    }
+    return q;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kThreads) k_norm(const __grid_constant__ Table<NT> w, NormArgs a) {
+    __shared__ bool is_last;
+    Sum sum;
+    int at = 0;
+#pragma unroll 2
+    for (unsigned tile = blockIdx.x; tile < w.tiles; tile += gridDim.x) {
+        at = find(w, tile, at);
+        const Entry& e = w.e[at];
+        const long long n = e.n & kElements, i = (long long)(tile - e.tile) * kNormTile + threadIdx.x * kE;
+        if (i >= n) continue;
+        uint32_t raw[kE];
+        if (e.n & kGradBf16) {
+            load_elements<__nv_bfloat16, kE>(raw, static_cast<const __nv_bfloat16*>(e.g), i, n);
+            sum.add(squares<__nv_bfloat16>(raw));
+        } else {
+            load_elements<float, kE>(raw, static_cast<const float*>(e.g), i, n);
+            sum.add(squares<float>(raw));
+        }
+    }
+    double s = block_sum(sum.value());
+    if (threadIdx.x == 0) {
+        a.part[a.first + blockIdx.x] = s;
+        __threadfence();
+        is_last = atomicInc(a.ticket, a.ctas - 1) == a.ctas - 1;
+    }
+    __syncthreads();
+    if (!is_last) return;
+    __threadfence();
+    s = 0;
+    for (unsigned i = threadIdx.x; i < a.ctas; i += kThreads) s += __ldcg(a.part + i);
+    s = block_sum(s);
+    if (threadIdx.x == 0) {
+        const double norm = sqrt(s);
+        *a.norm = (float)norm;
+        if (a.scale)
+            *a.scale = (float)norm < INFINITY ? (float)fmin(1.0, a.max_norm / (norm + 1e-6)) : __uint_as_float(0x7FC00000u);
+    }
+}
+
+}  // namespace
+
+unsigned norm_ctas(const domino_adamw_ctx* c, unsigned tiles) {
+    const unsigned most = (unsigned)c->num_sms * 6;
+    return tiles < most ? tiles : most;
+}
+
+cudaError_t launch_norm(const Work& w, const NormArgs& a, unsigned ctas, cudaStream_t st) {
+    if (w.tensors <= kFew) k_norm<kFew><<<ctas, kThreads, 0, st>>>(table<kFew>(w), a);
+    else k_norm<kMaxPerLaunch><<<ctas, kThreads, 0, st>>>(table<kMaxPerLaunch>(w), a);
+    return cudaGetLastError();
+}
+
+}  // namespace optim
+}  // namespace domino
