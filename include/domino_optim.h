@@ -92,7 +92,7 @@ DOMINO_API int domino_adamw_init(domino_adamw_ctx** out, const domino_adamw_conf
  * bf16 parameters without master, and 8-bit moments.  A block's scale is
  * max(largest |a| * (1 / 448), 2^-120); |a| / scale, at most 448, goes to one of
  * its two neighbours in e4m3, up with the probability of its place between them;
- * a v of 2^-126 or more is never rounded to 0.  The random bits of position i in step
+ * a v that is not 0 is never rounded to 0.  The random bits of position i in step
  * t are a function of (seed, t, i) alone, modulo 2^32:
  *   mix(h): h ^= h >> 15, h *= 0x6A09E667, h ^= h >> 13, h *= 0xBB67AE85, h ^ h >> 16
  *   key = mix(mix(t + 0x9E3779B9) + seed)

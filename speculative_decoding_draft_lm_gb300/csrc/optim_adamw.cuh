@@ -27,6 +27,7 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
     return r;
 }
 __device__ __forceinline__ F2 both(float x) { return f2(x, x); }
+__device__ __forceinline__ F2 both(float2 x) { return f2(x.x, x.y); }
 
 // The new moments, every product and sum rounded by itself.  The sums are written
 // as fma with a factor of 1 that the compiler does not know (AdamArgs::one): a
@@ -47,15 +48,11 @@ __device__ __forceinline__ float rcp_fast(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ bool either_nan(float a, float b) {
-    uint32_t r;
-    asm("{\n .reg .pred p;\n setp.nan.f32 p, %1, %2;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r) : "f"(a), "f"(b));
-    return r != 0;
-}
 // the largest magnitude, NaN if any is
-__device__ __forceinline__ float top_nan(float a, float b) {
+__device__ __forceinline__ float top_nan(float top, F2 v) {
+    const float2 h = halves(v);
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(top), "f"(fabsf(h.x)), "f"(fabsf(h.y)));
     return r;
 }
 
@@ -142,12 +139,6 @@ __device__ __forceinline__ uint32_t min16(uint32_t a, uint32_t b) {
     asm("min.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ uint32_t max16(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
 // what the kinds of a launch's tensors are
 template <typename P_, bool kMaster_, typename G_>
 struct Kind {
@@ -159,6 +150,13 @@ struct Kind {
     static constexpr int kFrom = kMaster ? 4 : (int)sizeof(P);  // bytes of an element of what is updated
 };
 
+// two of the parameters that the step starts from
+template <typename K>
+__device__ __forceinline__ F2 before(const uint32_t* w, int j) {
+    if (K::kFrom == 4) return f2(element<float>(w, 2 * j), element<float>(w, 2 * j + 1));
+    return f2(element<typename K::P>(w, 2 * j), element<typename K::P>(w, 2 * j + 1));
+}
+
 // p after the step, from the new m and v
 __device__ __forceinline__ F2 updated(const AdamArgs& a, const Coefficients& k, F2 p, F2 m, F2 v) {
     const float2 vf = halves(v);
@@ -166,14 +164,15 @@ __device__ __forceinline__ F2 updated(const AdamArgs& a, const Coefficients& k, 
     return fma2(both(-k.rate), mul2(m, f2(rcp_fast(d.x), rcp_fast(d.y))), mul2(p, both(k.decay)));
 }
 
-// two fp32 values rounded to bf16, up where the 16 lower bits and the random ones carry
+// Two fp32 values rounded to bf16, up where the 16 lower bits and the random ones
+// carry.  Not for NaN, whose bits may all be set: the carry would reach the sign.
 __device__ __forceinline__ uint32_t lossy(float2 q, unsigned r0, unsigned r1) {
-    uint32_t x0 = __float_as_uint(q.x) + (r0 >> 4 & 0xFFFFu), x1 = __float_as_uint(q.y) + (r1 >> 4 & 0xFFFFu);
-    if (either_nan(q.x, q.y)) {  // whose bits may all be set: the random ones would carry into the sign
-        if (q.x != q.x) x0 = 0x7FC00000u;
-        if (q.y != q.y) x1 = 0x7FC00000u;
-    }
-    return upper(x0, x1);
+    return upper(__float_as_uint(q.x) + (r0 * 4096u >> 16), __float_as_uint(q.y) + (r1 * 4096u >> 16));
+}
+// puts NaN in the places of the bf16 pairs w where q, element by element, is NaN
+__device__ __forceinline__ void set_nan(uint32_t& w, float2 q) {
+    if (q.x != q.x) w = (w & 0xFFFF0000u) | 0x7FC0u;
+    if (q.y != q.y) w = (w & 0xFFFFu) | 0x7FC00000u;
 }
 
 // a thread's new parameters to memory, the exact ones too where they are held

@@ -25,7 +25,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw32(const __grid_constant__
         if (i >= n) continue;
         float* const m32 = static_cast<float*>(a.m) + (pos - i);
         float* const v32 = static_cast<float*>(a.v) + (pos - i);
-        uint32_t rg[kE * sizeof(G) / 4], rp[kE * K::kFrom / 4], rm[kE], rv[kE];
+        uint32_t rg[kE * sizeof(G) / 4], rp[kE * K::kFrom / 4], rq[kE * K::kFrom / 4], rm[kE], rv[kE];
+        float top_p = 0.f;
         load_elements<G, kE>(rg, static_cast<const G*>(e.g), i, n);
         if (K::kMaster) load_elements<float, kE>(rp, a.master + (pos - i), i, n);
         else load_elements<P, kE>(rp, static_cast<const P*>(e.p), i, n);
@@ -37,22 +38,27 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw32(const __grid_constant__
             const F2 g = mul2(f2(element<G>(rg, 2 * j), element<G>(rg, 2 * j + 1)), both(k.scale));
             const F2 m = new_m(a, f2(element<float>(rm, 2 * j), element<float>(rm, 2 * j + 1)), g);
             const F2 v = new_v(a, f2(element<float>(rv, 2 * j), element<float>(rv, 2 * j + 1)), g);
-            F2 p;
-            if (K::kFrom == 4) p = f2(element<float>(rp, 2 * j), element<float>(rp, 2 * j + 1));
-            else p = f2(element<P>(rp, 2 * j), element<P>(rp, 2 * j + 1));
-            const float2 mf = halves(m), vf = halves(v), q = halves(updated(a, k, p, m, v));
+            const F2 q = updated(a, k, before<K>(rp, j), m, v);
+            const float2 mf = halves(m), vf = halves(v), qf = halves(q);
             rm[2 * j] = __float_as_uint(mf.x);
             rm[2 * j + 1] = __float_as_uint(mf.y);
             rv[2 * j] = __float_as_uint(vf.x);
             rv[2 * j + 1] = __float_as_uint(vf.y);
             if (K::kLossy) {
-                rp[j] = lossy(q, mix(h0 + (2 * j) * 0x9E3779B9u), mix(h0 + (2 * j + 1) * 0x9E3779B9u));
+                top_p = top_nan(top_p, q);
+                rq[j] = lossy(qf, mix(h0 + (2 * j) * 0x9E3779B9u), mix(h0 + (2 * j + 1) * 0x9E3779B9u));
             } else {
-                rp[2 * j] = __float_as_uint(q.x);
-                rp[2 * j + 1] = __float_as_uint(q.y);
+                rq[2 * j] = __float_as_uint(qf.x);
+                rq[2 * j + 1] = __float_as_uint(qf.y);
             }
         }
-        store_param<K, kE>(e, a.master, pos, i, n, rp);
+        if (K::kLossy && top_p != top_p) {
+#pragma unroll
+            for (int j = 0; j < kE / 2; ++j)
+                set_nan(rq[j], halves(updated(a, k, before<K>(rp, j), f2(element<float>(rm, 2 * j), element<float>(rm, 2 * j + 1)),
+                                              f2(element<float>(rv, 2 * j), element<float>(rv, 2 * j + 1)))));
+        }
+        store_param<K, kE>(e, a.master, pos, i, n, rq);
         store_elements<float, kE>(m32, i, n, rm);
         store_elements<float, kE>(v32, i, n, rv);
     }

@@ -12,19 +12,18 @@ namespace {
 constexpr int kE = 16, kLanes = kBlock / kE;
 static_assert(kThreads * kE == kTile8, "a tile is one vector of every thread");
 
-// four codes in the bytes of a word from words of places and their random bits, of m (signed) or of v
-__device__ __forceinline__ uint32_t codes_m(const uint32_t* x) {
-    constexpr uint32_t kMost = 0x07EF07EFu;  // the code 126, in bits 4 to 10 of a half
-    const uint32_t a = upper(x[0], x[1]), b = upper(x[2], x[3]);
-    const uint32_t lo = min16(a & 0x7FFF7FFFu, kMost) >> 4, hi = min16(b & 0x7FFF7FFFu, kMost) >> 4;
-    return (__byte_perm(lo, hi, 0x6420) & 0x7F7F7F7Fu) | (__byte_perm(a, b, 0x7531) & 0x80808080u);
+// Four codes in the bytes of a word, from words of places with their random bits
+// added: the code in bits 20 to 26, at most 126 (a quotient by a rounded scale can
+// pass the largest number by its last bits).  The halves are shifted by products,
+// which the pipe of the integer operations does not take.
+constexpr uint32_t kMost = 0x07EF07EFu;
+__device__ __forceinline__ uint32_t codes_v(const uint32_t* x) {
+    return __byte_perm(min16(upper(x[0], x[1]), kMost) * 16u, min16(upper(x[2], x[3]), kMost) * 16u, 0x7531);
 }
-__device__ __forceinline__ uint32_t codes_v(const uint32_t* x, const uint32_t* v) {
-    constexpr uint32_t kMost = 0x07EF07EFu, kLeast = 0x00100010u;
-    // a v that is not 0 does not become 0: its upper half is not 0 either, from 2^-126 on
-    const uint32_t a = max16(upper(x[0], x[1]), min16(upper(v[0], v[1]), kLeast));
-    const uint32_t b = max16(upper(x[2], x[3]), min16(upper(v[2], v[3]), kLeast));
-    return __byte_perm(min16(a, kMost) >> 4, min16(b, kMost) >> 4, 0x6420);
+__device__ __forceinline__ uint32_t codes_m(const uint32_t* x) {  // with the sign
+    const uint32_t a = upper(x[0], x[1]), b = upper(x[2], x[3]);
+    const uint32_t lo = min16(a & 0x7FFF7FFFu, kMost) * 16u, hi = min16(b & 0x7FFF7FFFu, kMost) * 16u;
+    return __byte_perm(lo, hi, 0x7531) | (__byte_perm(a, b, 0x7531) & 0x80808080u);
 }
 
 template <int NT, typename K>
@@ -38,7 +37,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ 
         const Entry& e = w.e[at];
         const long long n = e.n & kElements, i = (long long)(tile - e.tile) * kTile8 + threadIdx.x * kE;
         const long long block = (long long)e.block + i / kBlock, pos = (long long)e.block * kBlock + i;
-        uint32_t rg[kE * sizeof(G) / 4], rp[kE * K::kFrom / 4], rm[4], rv[4];
+        uint32_t rg[kE * sizeof(G) / 4], rp[kE * K::kFrom / 4], rq[kE * K::kFrom / 4], rm[4], rv[4];
         load_elements<G, kE>(rg, static_cast<const G*>(e.g), i, n);
         if (K::kMaster) load_elements<float, kE>(rp, a.master + (pos - i), i, n);
         else load_elements<P, kE>(rp, static_cast<const P*>(e.p), i, n);
@@ -64,51 +63,61 @@ __global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ 
         }
         const unsigned h0 = (unsigned)pos * 0x9E3779B9u + (unsigned)(pos >> 32) * 0x3C6EF373u + k.key;
         F2 m[kE / 2], v[kE / 2];
-        float top_m = 0.f, top_v = 0.f;
+        float top_m = 0.f, top_v = 0.f, top_p = 0.f;
 #pragma unroll
         for (int j = 0; j < kE / 2; ++j) {
             const F2 g = mul2(f2(element<G>(rg, 2 * j), element<G>(rg, 2 * j + 1)), both(k.scale));
             const uint32_t cm = rm[j / 2] >> (j % 2 * 16), cv = rv[j / 2] >> (j % 2 * 16);
             m[j] = new_m(a, mul2(e4m3_values(cm), both(sm)), g);
             v[j] = new_v(a, mul2(e4m3_values(cv), both(sv)), g);
-            const float2 vf = halves(v[j]), mf = halves(m[j]);
-            top_m = top_nan(top_m, top_nan(mf.x, mf.y));
-            top_v = top_nan(top_v, top_nan(vf.x, vf.y));
-            F2 p;
-            if (K::kFrom == 4) p = f2(element<float>(rp, 2 * j), element<float>(rp, 2 * j + 1));
-            else p = f2(element<P>(rp, 2 * j), element<P>(rp, 2 * j + 1));
-            const float2 q = halves(updated(a, k, p, m[j], v[j]));
+            top_m = top_nan(top_m, m[j]);
+            top_v = top_nan(top_v, v[j]);
+            const F2 q = updated(a, k, before<K>(rp, j), m[j], v[j]);
+            const float2 qf = halves(q);
             if (K::kLossy) {
-                rp[j] = lossy(q, mix(h0 + (2 * j) * 0x9E3779B9u), mix(h0 + (2 * j + 1) * 0x9E3779B9u));
+                top_p = top_nan(top_p, q);
+                rq[j] = lossy(qf, mix(h0 + (2 * j) * 0x9E3779B9u), mix(h0 + (2 * j + 1) * 0x9E3779B9u));
             } else {
-                rp[2 * j] = __float_as_uint(q.x);
-                rp[2 * j + 1] = __float_as_uint(q.y);
+                rq[2 * j] = __float_as_uint(qf.x);
+                rq[2 * j + 1] = __float_as_uint(qf.y);
             }
         }
-        store_param<K, kE>(e, a.master, pos, i, n, rp);
+        if (K::kLossy && top_p != top_p) {
+#pragma unroll
+            for (int j = 0; j < kE / 2; ++j) set_nan(rq[j], halves(updated(a, k, before<K>(rp, j), m[j], v[j])));
+        }
+        store_param<K, kE>(e, a.master, pos, i, n, rq);
 #pragma unroll
         for (int o = 1; o < kLanes; o <<= 1) {
-            top_m = top_nan(top_m, __shfl_xor_sync(0xffffffffu, top_m, o));
-            top_v = top_nan(top_v, __shfl_xor_sync(0xffffffffu, top_v, o));
+            const float om = __shfl_xor_sync(0xffffffffu, top_m, o), ov = __shfl_xor_sync(0xffffffffu, top_v, o);
+            top_m = top_nan(top_m, f2(om, om));
+            top_v = top_nan(top_v, f2(ov, ov));
         }
         const Scale zm = scale_of(top_m), zv = scale_of(top_v);
+        uint32_t any_zero = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            uint32_t xm[4], xv[4], vw[4];
+            uint32_t xm[4], xv[4];
 #pragma unroll
             for (int l = 0; l < 2; ++l) {
                 const uint2 ym = places(m[2 * j + l], both(zm.inv), both(-zm.s)), yv = places(v[2 * j + l], both(zv.inv), both(-zv.s));
                 const unsigned r0 = mix(h0 + (4 * j + 2 * l) * 0x9E3779B9u), r1 = mix(h0 + (4 * j + 2 * l + 1) * 0x9E3779B9u);
-                xm[2 * l] = ym.x + (r0 & 0xFFFFFu);
-                xm[2 * l + 1] = ym.y + (r1 & 0xFFFFFu);
+                xm[2 * l] = ym.x + (r0 * 4096u >> 12);
+                xm[2 * l + 1] = ym.y + (r1 * 4096u >> 12);
                 xv[2 * l] = yv.x + (r0 >> 12);
                 xv[2 * l + 1] = yv.y + (r1 >> 12);
-                const float2 vf = halves(v[2 * j + l]);
-                vw[2 * l] = __float_as_uint(vf.x);
-                vw[2 * l + 1] = __float_as_uint(vf.y);
             }
             rm[j] = codes_m(xm);
-            rv[j] = codes_v(xv, vw);
+            rv[j] = codes_v(xv);
+            any_zero |= (rv[j] - 0x01010101u) & 0x80808080u;
+        }
+        if (any_zero) {  // a v that is not 0 does not become 0
+#pragma unroll
+            for (int j = 0; j < kE; ++j) {
+                const float2 vf = halves(v[j / 2]);
+                const uint32_t one = 1u << (j % 4 * 8);
+                if ((j % 2 ? vf.y : vf.x) != 0.f && !(rv[j / 4] & 0x7Fu * one)) rv[j / 4] |= one;
+            }
         }
         if (i + kE <= n) {
             store_words<4>(m8, rm, false);

@@ -195,15 +195,16 @@ int domino_adamw_step(domino_adamw_ctx* c, const void* const* grads, const int* 
     a.lr_factor = lr_factor;
     a.ticket = c->ticket;
     a.lr = (float)lr;
-    a.beta1 = (float)g.beta1;
-    a.beta2 = (float)g.beta2;
-    a.rest1 = (float)(1 - g.beta1);
-    a.rest2 = (float)(1 - g.beta2);
+    const auto twice = [](double x) { return make_float2((float)x, (float)x); };
+    a.beta1 = twice(g.beta1);
+    a.beta2 = twice(g.beta2);
+    a.rest1 = twice(1 - g.beta1);
+    a.rest2 = twice(1 - g.beta2);
+    a.eps = twice(g.eps);
+    a.one = twice(1);
     a.log_beta1 = (float)log(g.beta1);
     a.log_beta2 = (float)log(g.beta2);
-    a.eps = (float)g.eps;
     a.decay = (float)g.weight_decay;
-    a.one = 1.f;
     a.seed = g.seed;
     DeviceGuard guard(c->device);
     const cudaStream_t st = (cudaStream_t)stream;

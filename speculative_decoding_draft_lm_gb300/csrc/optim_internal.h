@@ -39,7 +39,9 @@ struct AdamArgs {
     const float* scale;
     const float* lr_factor;
     unsigned* ticket;
-    float lr, beta1, beta2, rest1, rest2, log_beta1, log_beta2, eps, decay, one;  // rest: 1 - beta; one: 1
+    // twice each, as the packed operations take them; rest: 1 - beta; one: 1
+    float2 beta1, beta2, rest1, rest2, eps, one;
+    float lr, decay, log_beta1, log_beta2;
     unsigned seed;
     int last;  // the step's last launch: the one that counts it
 };

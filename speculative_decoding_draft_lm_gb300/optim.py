@@ -4,6 +4,7 @@ torch CUDA tensors and the current torch stream.  There is no CPU fallback.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 
 from . import rollout as _r
@@ -120,13 +121,13 @@ class DominoAdamW:
         self._current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                                        lambda i: torch.cuda.current_stream(i).cuda_stream)
         self._written = getattr(torch.autograd.graph, "increment_version", None)
-        self._f32, self._contiguous = torch.float32, torch.contiguous_format
+        self._f32 = torch.float32
         count = len(self.params)
         tensors = (domino_adamw_tensor * count)(*[
             domino_adamw_tensor(p.data_ptr(), p.numel(), self._codes[p.dtype],
                                 int(self.master and p.dtype is torch.bfloat16)) for p in self.params])
-        self._dtypes, self._dtype_codes = None, (ctypes.c_int * count)()
-        self._addresses = ctypes.c_void_p * count
+        self._dtypes = self._dtype_codes = None
+        self._devices, self._tensor = [device] * count, torch.Tensor
         address = {n: self.state[n].data_ptr() if n in self.state else None
                    for n in ("m", "v", "m_scale", "v_scale", "master", "count")}
         cfg = domino_adamw_config(count, tensors, state_bits, address["m"], address["v"], address["m_scale"],
@@ -139,27 +140,34 @@ class DominoAdamW:
     # -- checks (on every call's path) ----------------------------------------------
 
     def _gradients(self, grads):
-        """The C arrays of the gradients' addresses and types."""
+        """(addresses, types) of the gradients as C arrays, and what keeps them alive."""
         if grads is None:
             grads = [p.grad for p in self.params]
         elif len(grads) != len(self.params):
             raise ValueError(f"grads: want {len(self.params)} tensors (or None), got {len(grads)}")
-        index, codes, out, dtypes = self._index, self._codes, [], []
+        tensor = self._tensor
+        try:  # all at once, where all are given and as in the last call's types
+            if ([g.dtype for g in grads] == self._dtypes and [g.shape for g in grads] == self._shapes
+                    and list(map(tensor.get_device, grads)) == self._devices
+                    and all(map(tensor.is_contiguous, grads))):
+                held = array.array("Q", map(tensor.data_ptr, grads))
+                return held.buffer_info()[0], self._dtype_codes, held
+        except (AttributeError, TypeError):  # None among them
+            pass
+        codes, held, dtypes = self._codes, array.array("Q"), []
         for g, shape in zip(grads, self._shapes):
             if g is None:
-                out.append(None)
+                held.append(0)
                 dtypes.append(self._f32)
                 continue
             dtype = g.dtype
-            if g.shape != shape or dtype not in codes or g.get_device() != index or not g.is_contiguous():
-                raise ValueError(f"grads[{len(out)}]: want contiguous CUDA {tuple(shape)} bfloat16 or float32 on "
+            if g.shape != shape or dtype not in codes or g.get_device() != self._index or not g.is_contiguous():
+                raise ValueError(f"grads[{len(held)}]: want contiguous CUDA {tuple(shape)} bfloat16 or float32 on "
                                  f"{self.device}, got {tuple(g.shape)} {dtype} strides {g.stride()} on {g.device}")
-            out.append(g.data_ptr())
+            held.append(g.data_ptr())
             dtypes.append(dtype)
-        if dtypes != self._dtypes:
-            self._dtype_codes[:] = [codes[d] for d in dtypes]
-            self._dtypes = dtypes
-        return self._addresses(*out), self._dtype_codes
+        self._dtypes, self._dtype_codes = dtypes, (ctypes.c_int * len(dtypes))(*[codes[d] for d in dtypes])
+        return held.buffer_info()[0], self._dtype_codes, held
 
     def _scalar(self, t, name):
         """The address of one fp32 number on the device, or None."""
@@ -184,7 +192,7 @@ class DominoAdamW:
             import torch
             out = torch.empty((), device=self.device), torch.empty((), device=self.device)
         norm, scale = out
-        addresses, dtypes = self._gradients(grads)
+        addresses, dtypes, _held = self._gradients(grads)
         status = self._lib.domino_adamw_grad_norm(self.ctx, addresses, dtypes, max_norm, self._scalar(norm, "norm"),
                                                   self._scalar(scale, "scale"), self._stream(stream))
         if status:
@@ -196,7 +204,7 @@ class DominoAdamW:
         ``grad_norm`` gives; a step whose scale is not finite is left out).  ``grads`` as for
         ``grad_norm``; a parameter without one is left as it is.  ``lr`` replaces the constructor's;
         ``lr_factor`` (one float32 on the device) multiplies it, for schedules of captured steps."""
-        addresses, dtypes = self._gradients(grads)
+        addresses, dtypes, _held = self._gradients(grads)
         status = self._lib.domino_adamw_step(self.ctx, addresses, dtypes, self.lr if lr is None else lr,
                                              self._scalar(lr_factor, "lr_factor"), self._scalar(scale, "scale"),
                                              self._stream(stream))
