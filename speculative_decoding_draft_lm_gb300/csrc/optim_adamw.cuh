@@ -62,6 +62,21 @@ __device__ __forceinline__ unsigned mix(unsigned h) {
     return h ^ (h >> 16);
 }
 
+// The random words of consecutive positions, h0 the sum of the first one's.  Shifts
+// to the right are upper halves of products here: the multipliers have time where
+// the pipe of shifts and logic is what these kernels wait for.
+struct Mixer {
+    unsigned golden, right15, right13, right16;
+    __device__ __forceinline__ Mixer(const AdamArgs& a)
+        : golden(a.golden), right15(a.right15), right13(a.right13), right16(a.right16) {}
+    __device__ __forceinline__ unsigned operator()(unsigned h0, int j) const {
+        unsigned h = h0 + (unsigned)j * golden;
+        h = (h ^ __umulhi(h, right15)) * 0x6A09E667u;
+        h = (h ^ __umulhi(h, right13)) * 0xBB67AE85u;
+        return h ^ __umulhi(h, right16);
+    }
+};
+
 struct Coefficients {
     float scale, decay, rate, root;  // rate: of m; root: of sqrt(v)
     unsigned key;
@@ -166,8 +181,8 @@ __device__ __forceinline__ F2 updated(const AdamArgs& a, const Coefficients& k, 
 
 // Two fp32 values rounded to bf16, up where the 16 lower bits and the random ones
 // carry.  Not for NaN, whose bits may all be set: the carry would reach the sign.
-__device__ __forceinline__ uint32_t lossy(float2 q, unsigned r0, unsigned r1) {
-    return upper(__float_as_uint(q.x) + (r0 * 4096u >> 16), __float_as_uint(q.y) + (r1 * 4096u >> 16));
+__device__ __forceinline__ uint32_t lossy(float2 q, unsigned r0_up12, unsigned r1_up12) {
+    return upper(__float_as_uint(q.x) + (r0_up12 >> 16), __float_as_uint(q.y) + (r1_up12 >> 16));
 }
 // puts NaN in the places of the bf16 pairs w where q, element by element, is NaN
 __device__ __forceinline__ void set_nan(uint32_t& w, float2 q) {

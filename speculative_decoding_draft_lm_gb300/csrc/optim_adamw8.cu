@@ -13,24 +13,21 @@ constexpr int kE = 16, kLanes = kBlock / kE;
 static_assert(kThreads * kE == kTile8, "a tile is one vector of every thread");
 
 // Four codes in the bytes of a word, from words of places with their random bits
-// added: the code in bits 20 to 26, at most 126 (a quotient by a rounded scale can
-// pass the largest number by its last bits).  The halves are shifted by products,
-// which the pipe of the integer operations does not take.
-constexpr uint32_t kMost = 0x07EF07EFu;
-__device__ __forceinline__ uint32_t codes_v(const uint32_t* x) {
-    return __byte_perm(min16(upper(x[0], x[1]), kMost) * 16u, min16(upper(x[2], x[3]), kMost) * 16u, 0x7531);
-}
-__device__ __forceinline__ uint32_t codes_m(const uint32_t* x) {  // with the sign
+// added: the code is in bits 20 to 26.  The halves are shifted by products, which the
+// pipe of shifts and logic does not take.
+__device__ __forceinline__ uint32_t codes(const uint32_t* x, uint32_t* signs) {
     const uint32_t a = upper(x[0], x[1]), b = upper(x[2], x[3]);
-    const uint32_t lo = min16(a & 0x7FFF7FFFu, kMost) * 16u, hi = min16(b & 0x7FFF7FFFu, kMost) * 16u;
-    return __byte_perm(lo, hi, 0x7531) | (__byte_perm(a, b, 0x7531) & 0x80808080u);
+    *signs = __byte_perm(a, b, 0x7531);
+    return __byte_perm(a * 16u, b * 16u, 0x7531);
 }
+constexpr uint32_t kOnes = 0x01010101u, kTops = 0x80808080u;
 
 template <int NT, typename K>
 __global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ Table<NT> w, AdamArgs a) {
     typedef typename K::P P;
     typedef typename K::G G;
     const Coefficients k = coefficients(a);
+    const Mixer mixer(a);
     int at = 0;
     for (unsigned tile = blockIdx.x; !k.skip && tile < w.tiles; tile += gridDim.x) {
         at = find(w, tile, at);
@@ -76,7 +73,8 @@ __global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ 
             const float2 qf = halves(q);
             if (K::kLossy) {
                 top_p = top_nan(top_p, q);
-                rq[j] = lossy(qf, mix(h0 + (2 * j) * 0x9E3779B9u), mix(h0 + (2 * j + 1) * 0x9E3779B9u));
+                const unsigned r0 = mixer(h0, 2 * j) * a.up12, r1 = mixer(h0, 2 * j + 1) * a.up12;
+                rq[j] = lossy(qf, r0, r1);
             } else {
                 rq[2 * j] = __float_as_uint(qf.x);
                 rq[2 * j + 1] = __float_as_uint(qf.y);
@@ -94,28 +92,34 @@ __global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ 
             top_v = top_nan(top_v, f2(ov, ov));
         }
         const Scale zm = scale_of(top_m), zv = scale_of(top_v);
-        uint32_t any_zero = 0;
+        uint32_t odd = 0;  // a code of 127 or, of v, of 0
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            uint32_t xm[4], xv[4];
+            uint32_t xm[4], xv[4], signs, none;
 #pragma unroll
             for (int l = 0; l < 2; ++l) {
                 const uint2 ym = places(m[2 * j + l], both(zm.inv), both(-zm.s)), yv = places(v[2 * j + l], both(zv.inv), both(-zv.s));
-                const unsigned r0 = mix(h0 + (4 * j + 2 * l) * 0x9E3779B9u), r1 = mix(h0 + (4 * j + 2 * l + 1) * 0x9E3779B9u);
-                xm[2 * l] = ym.x + (r0 * 4096u >> 12);
-                xm[2 * l + 1] = ym.y + (r1 * 4096u >> 12);
+                const unsigned r0 = mixer(h0, 4 * j + 2 * l), r1 = mixer(h0, 4 * j + 2 * l + 1);
+                xm[2 * l] = ym.x + (r0 * a.up12 >> 12);
+                xm[2 * l + 1] = ym.y + (r1 * a.up12 >> 12);
                 xv[2 * l] = yv.x + (r0 >> 12);
                 xv[2 * l + 1] = yv.y + (r1 >> 12);
             }
-            rm[j] = codes_m(xm);
-            rv[j] = codes_v(xv);
-            any_zero |= (rv[j] - 0x01010101u) & 0x80808080u;
+            const uint32_t cm = codes(xm, &signs);
+            rv[j] = codes(xv, &none);
+            odd |= (cm + kOnes) | (rv[j] + kOnes);
+            odd |= rv[j] - kOnes;
+            rm[j] = cm | (signs & kTops);
         }
-        if (any_zero) {  // a v that is not 0 does not become 0
+        if (odd & kTops) {
+            // a quotient by a rounded scale can pass the largest number, 126, by its last bits;
+            // and a v that is not 0 does not become 0
 #pragma unroll
             for (int j = 0; j < kE; ++j) {
                 const float2 vf = halves(v[j / 2]);
                 const uint32_t one = 1u << (j % 4 * 8);
+                if ((rm[j / 4] & 0x7Fu * one) == 0x7Fu * one) rm[j / 4] -= one;
+                if ((rv[j / 4] & 0x7Fu * one) == 0x7Fu * one) rv[j / 4] -= one;
                 if ((j % 2 ? vf.y : vf.x) != 0.f && !(rv[j / 4] & 0x7Fu * one)) rv[j / 4] |= one;
             }
         }
@@ -140,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ 
 
 template <int NT, typename K>
 cudaError_t launch_kind(const domino_adamw_ctx* c, const Work& w, const AdamArgs& a, cudaStream_t st) {
-    const unsigned most = (unsigned)c->num_sms * 3;
+    const unsigned most = (unsigned)c->num_sms * 30;
     k_adamw8<NT, K><<<w.tiles < 1 ? 1 : w.tiles < most ? w.tiles : most, kThreads, 0, st>>>(table<NT>(w), a);
     return cudaGetLastError();
 }
