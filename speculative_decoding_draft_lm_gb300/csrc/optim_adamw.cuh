@@ -62,20 +62,12 @@ __device__ __forceinline__ unsigned mix(unsigned h) {
     return h ^ (h >> 16);
 }
 
-// The random words of consecutive positions, h0 the sum of the first one's.  Shifts
-// to the right are upper halves of products here: the multipliers have time where
-// the pipe of shifts and logic is what these kernels wait for.
-struct Mixer {
-    unsigned golden, right15, right13, right16;
-    __device__ __forceinline__ Mixer(const AdamArgs& a)
-        : golden(a.golden), right15(a.right15), right13(a.right13), right16(a.right16) {}
-    __device__ __forceinline__ unsigned operator()(unsigned h0, int j) const {
-        unsigned h = h0 + (unsigned)j * golden;
-        h = (h ^ __umulhi(h, right15)) * 0x6A09E667u;
-        h = (h ^ __umulhi(h, right13)) * 0xBB67AE85u;
-        return h ^ __umulhi(h, right16);
-    }
-};
+// The random word of the j-th position behind that whose sum is h0.  The factor is
+// one that the compiler does not know (AdamArgs::golden), so that a multiplier forms
+// the sum: the pipe of integer sums and logic is what these kernels wait for.
+__device__ __forceinline__ unsigned word_of(const AdamArgs& a, unsigned h0, int j) {
+    return mix(h0 + (unsigned)j * a.golden);
+}
 
 struct Coefficients {
     float scale, decay, rate, root;  // rate: of m; root: of sqrt(v)
@@ -113,10 +105,11 @@ __device__ __forceinline__ uint32_t nearest(float lo, float hi) {
 
 // ---- e4m3 ------------------------------------------------------------------------
 
-// two e4m3 codes (the low half of a word) as fp32
-__device__ __forceinline__ F2 e4m3_values(uint32_t codes) {
+// two e4m3 codes, in a word's low or high half, as fp32
+__device__ __forceinline__ F2 e4m3_values(uint32_t codes, bool high) {
     uint32_t h;
-    asm("{\n .reg .b16 c;\n cvt.u16.u32 c, %1;\n cvt.rn.f16x2.e4m3x2 %0, c;\n}" : "=r"(h) : "r"(codes));
+    if (high) asm("{\n .reg .b16 l, u;\n mov.b32 {l, u}, %1;\n cvt.rn.f16x2.e4m3x2 %0, u;\n}" : "=r"(h) : "r"(codes));
+    else asm("{\n .reg .b16 l, u;\n mov.b32 {l, u}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(h) : "r"(codes));
     F2 r;
     asm("{\n .reg .b16 l, u;\n .reg .f32 a, b;\n mov.b32 {l, u}, %1;\n cvt.f32.f16 a, l;\n cvt.f32.f16 b, u;\n"
         " mov.b64 %0, {a, b};\n}"

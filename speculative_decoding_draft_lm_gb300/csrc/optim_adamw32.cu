@@ -16,7 +16,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw32(const __grid_constant__
     typedef typename K::P P;
     typedef typename K::G G;
     const Coefficients k = coefficients(a);
-    const Mixer mixer(a);
     int at = 0;
     for (unsigned tile = blockIdx.x; !k.skip && tile < w.tiles; tile += gridDim.x) {
         at = find(w, tile, at);
@@ -47,7 +46,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw32(const __grid_constant__
             rv[2 * j + 1] = __float_as_uint(vf.y);
             if (K::kLossy) {
                 top_p = top_nan(top_p, q);
-                rq[j] = lossy(qf, mixer(h0, 2 * j) << 12, mixer(h0, 2 * j + 1) << 12);
+                rq[j] = lossy(qf, word_of(a, h0, 2 * j) << 12, word_of(a, h0, 2 * j + 1) << 12);
             } else {
                 rq[2 * j] = __float_as_uint(qf.x);
                 rq[2 * j + 1] = __float_as_uint(qf.y);

@@ -23,18 +23,17 @@ __device__ __forceinline__ uint32_t codes(const uint32_t* x, uint32_t* signs) {
 constexpr uint32_t kOnes = 0x01010101u, kTops = 0x80808080u;
 
 template <int NT, typename K>
-__global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ Table<NT> w, AdamArgs a) {
+__global__ void __launch_bounds__(kThreads, K::kFrom == 2 && sizeof(typename K::G) == 2 ? 4 : 3) k_adamw8(const __grid_constant__ Table<NT> w, AdamArgs a) {
     typedef typename K::P P;
     typedef typename K::G G;
     const Coefficients k = coefficients(a);
-    const Mixer mixer(a);
     int at = 0;
     for (unsigned tile = blockIdx.x; !k.skip && tile < w.tiles; tile += gridDim.x) {
         at = find(w, tile, at);
         const Entry& e = w.e[at];
         const long long n = e.n & kElements, i = (long long)(tile - e.tile) * kTile8 + threadIdx.x * kE;
         const long long block = (long long)e.block + i / kBlock, pos = (long long)e.block * kBlock + i;
-        uint32_t rg[kE * sizeof(G) / 4], rp[kE * K::kFrom / 4], rq[kE * K::kFrom / 4], rm[4], rv[4];
+        uint32_t rg[kE * sizeof(G) / 4], rp[kE * K::kFrom / 4], rm[4], rv[4];
         load_elements<G, kE>(rg, static_cast<const G*>(e.g), i, n);
         if (K::kMaster) load_elements<float, kE>(rp, a.master + (pos - i), i, n);
         else load_elements<P, kE>(rp, static_cast<const P*>(e.p), i, n);
@@ -64,27 +63,11 @@ __global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ 
 #pragma unroll
         for (int j = 0; j < kE / 2; ++j) {
             const F2 g = mul2(f2(element<G>(rg, 2 * j), element<G>(rg, 2 * j + 1)), both(k.scale));
-            const uint32_t cm = rm[j / 2] >> (j % 2 * 16), cv = rv[j / 2] >> (j % 2 * 16);
-            m[j] = new_m(a, mul2(e4m3_values(cm), both(sm)), g);
-            v[j] = new_v(a, mul2(e4m3_values(cv), both(sv)), g);
+            m[j] = new_m(a, mul2(e4m3_values(rm[j / 2], j % 2), both(sm)), g);
+            v[j] = new_v(a, mul2(e4m3_values(rv[j / 2], j % 2), both(sv)), g);
             top_m = top_nan(top_m, m[j]);
             top_v = top_nan(top_v, v[j]);
-            const F2 q = updated(a, k, before<K>(rp, j), m[j], v[j]);
-            const float2 qf = halves(q);
-            if (K::kLossy) {
-                top_p = top_nan(top_p, q);
-                const unsigned r0 = mixer(h0, 2 * j) * a.up12, r1 = mixer(h0, 2 * j + 1) * a.up12;
-                rq[j] = lossy(qf, r0, r1);
-            } else {
-                rq[2 * j] = __float_as_uint(qf.x);
-                rq[2 * j + 1] = __float_as_uint(qf.y);
-            }
         }
-        if (K::kLossy && top_p != top_p) {
-#pragma unroll
-            for (int j = 0; j < kE / 2; ++j) set_nan(rq[j], halves(updated(a, k, before<K>(rp, j), m[j], v[j])));
-        }
-        store_param<K, kE>(e, a.master, pos, i, n, rq);
 #pragma unroll
         for (int o = 1; o < kLanes; o <<= 1) {
             const float om = __shfl_xor_sync(0xffffffffu, top_m, o), ov = __shfl_xor_sync(0xffffffffu, top_v, o);
@@ -92,16 +75,28 @@ __global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ 
             top_v = top_nan(top_v, f2(ov, ov));
         }
         const Scale zm = scale_of(top_m), zv = scale_of(top_v);
+        // everything that takes an element's random word, so that it need not be held
         uint32_t odd = 0;  // a code of 127 or, of v, of 0
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint32_t xm[4], xv[4], signs, none;
 #pragma unroll
             for (int l = 0; l < 2; ++l) {
-                const uint2 ym = places(m[2 * j + l], both(zm.inv), both(-zm.s)), yv = places(v[2 * j + l], both(zv.inv), both(-zv.s));
-                const unsigned r0 = mixer(h0, 4 * j + 2 * l), r1 = mixer(h0, 4 * j + 2 * l + 1);
-                xm[2 * l] = ym.x + (r0 * a.up12 >> 12);
-                xm[2 * l + 1] = ym.y + (r1 * a.up12 >> 12);
+                const int at2 = 2 * j + l;
+                const unsigned r0 = word_of(a, h0, 2 * at2), r1 = word_of(a, h0, 2 * at2 + 1);
+                const unsigned u0 = r0 * a.up12, u1 = r1 * a.up12;
+                const F2 q = updated(a, k, before<K>(rp, at2), m[at2], v[at2]);
+                const float2 qf = halves(q);
+                if (K::kLossy) {
+                    top_p = top_nan(top_p, q);
+                    rp[at2] = lossy(qf, u0, u1);
+                } else {
+                    rp[2 * at2] = __float_as_uint(qf.x);
+                    rp[2 * at2 + 1] = __float_as_uint(qf.y);
+                }
+                const uint2 ym = places(m[at2], both(zm.inv), both(-zm.s)), yv = places(v[at2], both(zv.inv), both(-zv.s));
+                xm[2 * l] = ym.x + (u0 >> 12);
+                xm[2 * l + 1] = ym.y + (u1 >> 12);
                 xv[2 * l] = yv.x + (r0 >> 12);
                 xv[2 * l + 1] = yv.y + (r1 >> 12);
             }
@@ -111,6 +106,13 @@ __global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ 
             odd |= rv[j] - kOnes;
             rm[j] = cm | (signs & kTops);
         }
+        if (K::kLossy && top_p != top_p) {
+            uint32_t old[kE * K::kFrom / 4];
+            load_elements<P, kE>(old, static_cast<const P*>(e.p), i, n);
+#pragma unroll
+            for (int j = 0; j < kE / 2; ++j) set_nan(rp[j], halves(updated(a, k, before<K>(old, j), m[j], v[j])));
+        }
+        store_param<K, kE>(e, a.master, pos, i, n, rp);
         if (odd & kTops) {
             // a quotient by a rounded scale can pass the largest number, 126, by its last bits;
             // and a v that is not 0 does not become 0

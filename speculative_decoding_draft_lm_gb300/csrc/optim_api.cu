@@ -208,9 +208,6 @@ int domino_adamw_step(domino_adamw_ctx* c, const void* const* grads, const int* 
     a.seed = g.seed;
     a.golden = 0x9E3779B9u;
     a.up12 = 1u << 12;
-    a.right15 = 1u << 17;
-    a.right13 = 1u << 19;
-    a.right16 = 1u << 16;
     DeviceGuard guard(c->device);
     const cudaStream_t st = (cudaStream_t)stream;
     WorkspaceOrder order(&c->use, st);

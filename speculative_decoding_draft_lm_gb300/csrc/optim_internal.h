@@ -43,7 +43,7 @@ struct AdamArgs {
     float2 beta1, beta2, rest1, rest2, eps, one;
     float lr, decay, log_beta1, log_beta2;
     unsigned seed;
-    unsigned golden, up12, right15, right13, right16;  // factors that the compiler does not know (see Mixer)
+    unsigned golden, up12;  // factors that the compiler does not know
     int last;  // the step's last launch: the one that counts it
 };
 
