@@ -9,8 +9,8 @@ namespace optim {
 
 namespace {
 
-constexpr int kE = 16, kLanes = kBlock / kE;
-static_assert(kThreads * kE == kTile8, "a tile is one vector of every thread");
+constexpr int kThreads8 = kTile8 / 16, kE = 16, kLanes = kBlock / kE;
+static_assert(kThreads8 * kE == kTile8, "a tile is one vector of every thread");
 
 // Four codes in the bytes of a word, from words of places with their random bits
 // added: the code is in bits 20 to 26.  The halves are shifted by products, which the
@@ -23,7 +23,7 @@ __device__ __forceinline__ uint32_t codes(const uint32_t* x, uint32_t* signs) {
 constexpr uint32_t kOnes = 0x01010101u, kTops = 0x80808080u;
 
 template <int NT, typename K>
-__global__ void __launch_bounds__(kThreads, K::kFrom == 2 && sizeof(typename K::G) == 2 ? 4 : 3) k_adamw8(const __grid_constant__ Table<NT> w, AdamArgs a) {
+__global__ void __launch_bounds__(kThreads8, K::kFrom == 2 && sizeof(typename K::G) == 2 ? 4 : 3) k_adamw8(const __grid_constant__ Table<NT> w, AdamArgs a) {
     typedef typename K::P P;
     typedef typename K::G G;
     const Coefficients k = coefficients(a);
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, K::kFrom == 2 && sizeof(typename K::
 template <int NT, typename K>
 cudaError_t launch_kind(const domino_adamw_ctx* c, const Work& w, const AdamArgs& a, cudaStream_t st) {
     const unsigned most = (unsigned)c->num_sms * 30;
-    k_adamw8<NT, K><<<w.tiles < 1 ? 1 : w.tiles < most ? w.tiles : most, kThreads, 0, st>>>(table<NT>(w), a);
+    k_adamw8<NT, K><<<w.tiles < 1 ? 1 : w.tiles < most ? w.tiles : most, kThreads8, 0, st>>>(table<NT>(w), a);
     return cudaGetLastError();
 }
 
