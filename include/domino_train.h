@@ -137,7 +137,7 @@ DOMINO_API int domino_train_distill_step(domino_train_ctx* ctx, const void* logi
  *       (NULL: not written)
  * 0 <= n_alternatives <= min(V, DOMINO_TRAIN_MAX_ALTERNATIVES); at 0 the two
  * arrays may be NULL.  1e-3 <= temperature <= 1e3.
- * A row whose token is -1 takes no part, and its logits are not read: 0, 0 and
+ * A row whose token is -1 takes no part, whatever its logits: 0, 0 and
  * no alternatives.  A row without a logit above -inf has no distribution: -inf,
  * 0 and no alternatives.  A row with a NaN or +inf logit gets NaN for all its
  * floats.  What all logits of a row share cancels, up to the type's lowest value.

@@ -132,7 +132,8 @@ int domino_train_init(domino_train_ctx** out, const domino_train_config* cfg, in
     c->claim = (unsigned*)(base + o_claim);
     if (c->use.create() != cudaSuccess || cudaMemset(c->err, 0, sizeof(int)) != cudaSuccess ||
         train::prepare_embed_kernels() != cudaSuccess ||
-        train::prepare_distill_kernels() != cudaSuccess || train::prepare_top_kernels() != cudaSuccess ||
+        train::prepare_distill_kernels() != cudaSuccess ||
+        train::prepare_logprob_kernels() != cudaSuccess || train::prepare_top_kernels() != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
         release(c);
         return DOMINO_ERR_CUDA;

@@ -12,7 +12,8 @@ struct domino_train_ctx {
     int num_sms;
     int last_launches;
     int* err;             // device error word, and behind it the word that domino_train_status took
-    int step_clusters[17];  // clusters of each size that the GPU holds at once in distill_step (0: not asked yet)
+    // clusters of each size that the GPU holds at once in distill_step and in logprobs_step (0: not asked yet)
+    int step_clusters[17], score_clusters[17];
     // embed_grad workspace (max_tokens > 0)
     uint32_t* keys[2];    // [max_tokens] tokens between the passes of the sort
     int32_t* pos[2];      // [max_tokens] their positions
@@ -80,6 +81,7 @@ struct LogprobArgs {
     int* err;
 };
 
+cudaError_t prepare_logprob_kernels();
 cudaError_t launch_logprobs_forward(domino_train_ctx* c, int dtype, const LogprobArgs& a, cudaStream_t st);
 cudaError_t launch_logprobs_backward(domino_train_ctx* c, const LogprobArgs& a, cudaStream_t st);
 cudaError_t launch_logprobs_step(domino_train_ctx* c, const LogprobArgs& a, cudaStream_t st);
