@@ -234,46 +234,96 @@ struct ForwardShared {
     Scores part[kWarps];
     float top[kWarps];
     Scores of[kMaxCluster];              // every CTA's, at rank 0
-    Word best[kMaxCluster * kMaxK];      // every CTA's alternatives, at rank 0
-    Word bound;
+    alignas(16) Word best[kMaxCluster * kMaxK + 2];  // every CTA's alternatives, at rank 0
+    Word bound, nth[kWarps];
     int groups, words;
     int chosen[kMaxK];
 };
 // the lists of words lie in the ring, which is read by then: the threads' best groups,
 // the groups that may be chosen, the elements that may be
+static_assert(kMaxK * kAhead <= kThreads, "a thread for every vector of the chosen groups");
 constexpr int kListed = kMaxK * kMaxCalls, kElements = kMaxK * kAhead * 8 + 16;
-static_assert((kThreads + kListed + kElements) * sizeof(Word) <= kRingBytes, "the lists fit the ring");
+static_assert((kThreads + kListed + 2 + kElements + 2) * sizeof(Word) <= kRingBytes, "the lists fit the ring");
 
-// how many of n words are larger
+// how many of n words are larger, n even or followed by a 0
 __device__ __forceinline__ int rank_of(Word w, const Word* list, int n) {
     int r = 0;
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) r += list[i] > w ? 1 : 0;
+    for (int i = 0; i < n; i += 2) {
+        const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(list + i);
+        r += (two.x > w ? 1 : 0) + (two.y > w ? 1 : 0);
+    }
     return r;
+}
+
+// The n-th best of the lanes' words (0: there are fewer), n >= 1.
+__device__ __forceinline__ Word warp_nth(Word w, int n) {
+    unsigned hi = (unsigned)(w >> 32), lo = (unsigned)w, h = 0, l = 0;
+    for (int i = 0; i < n; ++i) {
+        h = __reduce_max_sync(0xffffffffu, hi);
+        l = __reduce_max_sync(0xffffffffu, hi == h ? lo : 0u);
+        if (hi == h && lo == l) hi = lo = 0;
+    }
+    return (Word)h << 32 | l;
 }
 
 // The k best elements of the CTA's slice to S.best[0 .. k), in order, 0 where there
 // are no more.  mine: the word of the thread's best group, side: its element beside
 // the vectors (0: none).
+//
+// The bound on groups: the worst of the warps' n-th best of their threads' best
+// groups, n = k / 8 upwards; k groups at least reach it.  Where many more do (all of
+// them in a few warps' places, as a mask can have it), the k-th best of the threads'
+// best groups, which k threads reach, each with as many groups as the stream had
+// calls.
 template <typename T>
 __device__ __forceinline__ void slice_best(ForwardShared& S, Word* lists, const Vectors<T>& x, const T* tops, int v0, int k,
                                            Word mine, Word side) {
-    const int t = threadIdx.x, groups = (x.last - x.first + kAhead - 1) / kAhead;
-    Word *firsts = lists, *listed = firsts + kThreads, *elements = listed + kListed;
-    firsts[t] = mine;
-    if (t == 0) S.bound = 0, S.groups = S.words = 0;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, groups = (x.last - x.first + kAhead - 1) / kAhead;
+    Word *firsts = lists, *listed = firsts + kThreads, *elements = listed + kListed + 2;
+    const Word nth = warp_nth(mine, (k + kWarps - 1) / kWarps);
+    if (lane == 0) S.nth[warp] = nth;
+    if (t == 0) S.groups = S.words = 0;
     for (int i = t; i < k; i += kThreads) S.best[i] = 0;
+    firsts[t] = mine;
     __syncthreads();
-    if (mine && rank_of(mine, firsts, kThreads) == k - 1) S.bound = mine;
+    Word bound = S.nth[0];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) bound = S.nth[i] < bound ? S.nth[i] : bound;
+    // a thread's groups are looked at by all lanes of its warp
+    const auto collect = [&] {
+        unsigned with = __ballot_sync(0xffffffffu, mine && mine >= bound);
+        while (with) {
+            const int l = __ffs(with) - 1;
+            with &= with - 1;
+            const int g = warp * 32 + l + lane * kThreads;
+            if (g < groups) {
+                const Word w = word_of(to_f32(tops[g]), g);
+                if (w && w >= bound) {
+                    const int at = atomicAdd(&S.groups, 1);
+                    if (at < kListed) listed[at] = w;
+                }
+            }
+        }
+    };
+    static_assert(kMaxCalls <= 32, "a lane for every call");
+    if (bound) collect();
     __syncthreads();
-    for (int g = t; mine >= S.bound && g < groups; g += kThreads) {
-        const Word w = word_of(to_f32(tops[g]), g);
-        if (w && w >= S.bound) listed[atomicAdd(&S.groups, 1)] = w;
+    int n = S.groups;
+    if (n == 0 || n > kListed) {  // the same for all threads
+        if (t == 0) S.bound = 0, S.groups = 0;
+        __syncthreads();
+        if (mine && rank_of(mine, firsts, kThreads) == k - 1) S.bound = mine;
+        __syncthreads();
+        bound = S.bound;
+        collect();
+        __syncthreads();
+        n = S.groups;
     }
-    __syncthreads();
-    const int n = S.groups;
-    __syncthreads();
-    if (t == 0) S.bound = 0;
+    if (t == 0) {
+        listed[n] = 0;
+        S.bound = 0;
+    }
     __syncthreads();
     for (int i = t; i < n; i += kThreads) {
         const Word w = listed[i];
@@ -286,18 +336,27 @@ __device__ __forceinline__ void slice_best(ForwardShared& S, Word* lists, const 
     const auto push = [&](Word w) {
         if (w && w >= least) elements[atomicAdd(&S.words, 1)] = w;
     };
-    for (int i = t; i < min(n, k) * kAhead; i += kThreads) {
-        const int at = x.first + S.chosen[i / kAhead] * kAhead + i % kAhead;
-        if (at >= x.last) continue;
-        const T* e = reinterpret_cast<const T*>(x.vec() + at);
-        const int id = v0 + at * Vectors<T>::kPer - x.phase;
+    if (t < min(n, k) * kAhead) {
+        const int at = x.first + S.chosen[t / kAhead] * kAhead + t % kAhead;
+        if (at < x.last) {
+            Vec16<T> v;
+            v.q = __ldg(x.vec() + at);
+            const int id = v0 + at * Vectors<T>::kPer - x.phase;
 #pragma unroll
-        for (int j = 0; j < Vectors<T>::kPer; ++j) push(word_of(to_f32(e[j]), id + j));
+            for (int j = 0; j < Vectors<T>::kPer / 2; ++j) {
+                const float2 h = halves(v.pair(j));
+                push(word_of(h.x, id + 2 * j));
+                push(word_of(h.y, id + 2 * j + 1));
+            }
+        }
     }
     push(side);
     __syncthreads();
-    for (int i = t; i < S.words; i += kThreads) {
-        const int r = rank_of(elements[i], elements, S.words);
+    const int m = S.words;
+    if (t == 0) elements[m] = 0;
+    __syncthreads();
+    for (int i = t; i < m; i += kThreads) {
+        const int r = rank_of(elements[i], elements, m);
         if (r < k) S.best[r] = elements[i];
     }
     __syncthreads();
@@ -415,22 +474,26 @@ __global__ void __launch_bounds__(kThreads, 4) k_scores(LogprobArgs p, int chunk
     if (kTop) {
         int* ids = p.alt_ids + (size_t)n * p.k;
         float* scores = p.alt_logprobs + (size_t)n * p.k;
+        const int words = size * p.k;
         int some = 0;
-        for (int i = t; i < size * p.k; i += kThreads) {
+        Word least = 1;
+        if (size > 1) {  // of what is worse than some CTA's k-th, nothing is among the best
+            for (int i = 0; i < size; ++i) least = max(least, S.best[i * p.k + p.k - 1]);
+            if (t == 0 && words % 2) S.best[words] = 0;
+        }
+        for (int i = 0; i < words; i += kThreads) some += __syncthreads_count(i + t < words && S.best[i + t] != 0);
+        for (int i = t; i < words; i += kThreads) {
             const Word w = S.best[i];
-            if (!w) continue;
-            const int at = size > 1 ? rank_of(w, S.best, size * p.k) : i;
+            if (w < least) continue;
+            const int at = size > 1 ? rank_of(w, S.best, words) : i;
             if (at >= p.k) continue;
             ids[at] = (int)~(unsigned)w;
             scores[at] = log_q(r.st, word_logit(w), p.temperature);
         }
         // places behind the last alternative
-        if (t < p.k) {
-            for (int i = 0; i < size * p.k; ++i) some += S.best[i] ? 1 : 0;
-            if (t >= some) {
-                ids[t] = -1;
-                scores[t] = -INFINITY;
-            }
+        if (t >= some && t < p.k) {
+            ids[t] = -1;
+            scores[t] = -INFINITY;
         }
     }
 }
