@@ -198,7 +198,8 @@ __device__ __forceinline__ float row_logprob(const RowScore& r, float x, float T
 // L2.  The k best groups are found the same way: among those at least as good as the
 // k-th best of the threads' best groups.
 //
-// A word orders both: the logit in orderable form over the inverted place, 0 for none.
+// A word orders both: the logit in orderable form over the inverted place.  What is
+// not above -inf is below kLeast.
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -209,8 +210,8 @@ constexpr int kMaxK = DOMINO_TRAIN_MAX_ALTERNATIVES;
 constexpr int kMaxCalls = 32;  // of the stream, in a CTA that looks for alternatives
 typedef unsigned long long Word;
 
+constexpr Word kLeast = (Word)0x00800000u << 32;
 __device__ __forceinline__ Word word_of(float x, int at) {
-    if (x == -INFINITY) return 0;
     return (Word)(x != x ? 0xFFFFFFFFu : ord_f32(x)) << 32 | (unsigned)~at;
 }
 __device__ __forceinline__ float word_logit(Word w) {
@@ -234,8 +235,8 @@ struct ForwardShared {
     Scores part[kWarps];
     float top[kWarps];
     Scores of[kMaxCluster];              // every CTA's, at rank 0
-    alignas(16) Word best[kMaxCluster * kMaxK + 2];  // every CTA's alternatives, at rank 0
-    Word bound, nth[kWarps];
+    alignas(16) Word best[kMaxCluster * kMaxK];  // every CTA's alternatives, at rank 0
+    Word bound, least, nth[kWarps];
     int groups, words;
     int chosen[kMaxK];
 };
@@ -243,17 +244,31 @@ struct ForwardShared {
 // the groups that may be chosen, the elements that may be
 static_assert(kMaxK * kAhead <= kThreads, "a thread for every vector of the chosen groups");
 constexpr int kListed = kMaxK * kMaxCalls, kElements = kMaxK * kAhead * 8 + 16;
-static_assert((kThreads + kListed + 2 + kElements + 2) * sizeof(Word) <= kRingBytes, "the lists fit the ring");
+static_assert((kThreads + kListed + kElements) * sizeof(Word) <= kRingBytes, "the lists fit the ring");
 
-// how many of n words are larger, n even or followed by a 0
-__device__ __forceinline__ int rank_of(Word w, const Word* list, int n) {
-    int r = 0;
+// The words that reach a bound to a list whose length is *count, in any order.
+// hit: a bit for each of the thread's words, of which get(j) is the j-th.
+template <typename Get>
+__device__ __forceinline__ void collect(unsigned hit, Word* list, int most, int* count, Get&& get) {
+    if (!hit) return;
+    int at = atomicAdd(count, __popc(hit));
+    for (; hit; hit &= hit - 1, ++at)
+        if (at < most) list[at] = get(__ffs(hit) - 1);
+}
+// f(word, rank) for the n words of a list (all different, or 0) that are in a rank
+// below k: four threads a word, which count what is larger.
+template <typename F>
+__device__ __forceinline__ void rank_words(const Word* list, int n, int k, F&& f) {
+    const int part = threadIdx.x & 3;
+    for (int i = threadIdx.x >> 2; i - (int)(threadIdx.x >> 2) < n; i += kThreads / 4) {
+        const Word w = i < n ? list[i] : 0;
+        int r = 0;
 #pragma unroll 4
-    for (int i = 0; i < n; i += 2) {
-        const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(list + i);
-        r += (two.x > w ? 1 : 0) + (two.y > w ? 1 : 0);
+        for (int j = part; j < n; j += 4) r += list[j] > w ? 1 : 0;
+        r += __shfl_xor_sync(0xffffffffu, r, 1);
+        r += __shfl_xor_sync(0xffffffffu, r, 2);
+        if (part == 0 && i < n && w && r < k) f(w, r);
     }
-    return r;
 }
 
 // The n-th best of the lanes' words (0: there are fewer), n >= 1.
@@ -280,85 +295,73 @@ template <typename T>
 __device__ __forceinline__ void slice_best(ForwardShared& S, Word* lists, const Vectors<T>& x, const T* tops, int v0, int k,
                                            Word mine, Word side) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, groups = (x.last - x.first + kAhead - 1) / kAhead;
-    Word *firsts = lists, *listed = firsts + kThreads, *elements = listed + kListed + 2;
+    Word *firsts = lists, *listed = firsts + kThreads, *elements = listed + kListed;
     const Word nth = warp_nth(mine, (k + kWarps - 1) / kWarps);
     if (lane == 0) S.nth[warp] = nth;
-    if (t == 0) S.groups = S.words = 0;
-    for (int i = t; i < k; i += kThreads) S.best[i] = 0;
+    if (t == 0) {
+        S.groups = S.words = 0;
+        S.bound = S.least = kLeast;
+    }
+    if (t < k) S.best[t] = 0;
     firsts[t] = mine;
     __syncthreads();
     Word bound = S.nth[0];
 #pragma unroll
     for (int i = 1; i < kWarps; ++i) bound = S.nth[i] < bound ? S.nth[i] : bound;
-    // a thread's groups are looked at by all lanes of its warp
-    const auto collect = [&] {
-        unsigned with = __ballot_sync(0xffffffffu, mine && mine >= bound);
-        while (with) {
-            const int l = __ffs(with) - 1;
-            with &= with - 1;
-            const int g = warp * 32 + l + lane * kThreads;
-            if (g < groups) {
-                const Word w = word_of(to_f32(tops[g]), g);
-                if (w && w >= bound) {
-                    const int at = atomicAdd(&S.groups, 1);
-                    if (at < kListed) listed[at] = w;
-                }
-            }
+    const auto group = [&](int call) { return word_of(to_f32(tops[t + call * kThreads]), t + call * kThreads); };
+    const auto collect_groups = [&] {
+        unsigned hit = 0;
+        if (mine >= bound) {
+#pragma unroll 4
+            for (int call = 0; t + call * kThreads < groups; ++call) hit |= group(call) >= bound ? 1u << call : 0u;
         }
+        collect(hit, listed, kListed, &S.groups, group);
     };
-    static_assert(kMaxCalls <= 32, "a lane for every call");
-    if (bound) collect();
+    static_assert(kMaxCalls <= 32, "a bit for every call");
+    if (bound) collect_groups();
     __syncthreads();
     int n = S.groups;
     if (n == 0 || n > kListed) {  // the same for all threads
-        if (t == 0) S.bound = 0, S.groups = 0;
-        __syncthreads();
-        if (mine && rank_of(mine, firsts, kThreads) == k - 1) S.bound = mine;
+        rank_words(firsts, kThreads, k, [&](Word w, int r) {
+            if (r == k - 1) S.bound = w;
+        });
         __syncthreads();
         bound = S.bound;
-        collect();
+        if (t == 0) S.groups = 0;
+        __syncthreads();
+        collect_groups();
         __syncthreads();
         n = S.groups;
     }
-    if (t == 0) {
-        listed[n] = 0;
-        S.bound = 0;
-    }
+    rank_words(listed, n, k, [&](Word w, int r) {
+        S.chosen[r] = (int)~(unsigned)w;
+        if (r == k - 1) S.least = w >> 32 << 32;
+    });
     __syncthreads();
-    for (int i = t; i < n; i += kThreads) {
-        const Word w = listed[i];
-        const int r = rank_of(w, listed, n);
-        if (r < k) S.chosen[r] = (int)~(unsigned)w;
-        if (r == k - 1) S.bound = w >> 32 << 32;
-    }
-    __syncthreads();
-    const Word least = S.bound;
-    const auto push = [&](Word w) {
-        if (w && w >= least) elements[atomicAdd(&S.words, 1)] = w;
-    };
+    const Word least = S.least;
     if (t < min(n, k) * kAhead) {
         const int at = x.first + S.chosen[t / kAhead] * kAhead + t % kAhead;
         if (at < x.last) {
             Vec16<T> v;
             v.q = __ldg(x.vec() + at);
             const int id = v0 + at * Vectors<T>::kPer - x.phase;
+            Word w[Vectors<T>::kPer];
+            unsigned hit = 0;
 #pragma unroll
-            for (int j = 0; j < Vectors<T>::kPer / 2; ++j) {
-                const float2 h = halves(v.pair(j));
-                push(word_of(h.x, id + 2 * j));
-                push(word_of(h.y, id + 2 * j + 1));
+            for (int j = 0; j < Vectors<T>::kPer; ++j) {
+                const float2 h = halves(v.pair(j / 2));
+                w[j] = word_of(j % 2 ? h.y : h.x, id + j);
+                hit |= w[j] >= least ? 1u << j : 0u;
             }
+            int to = hit ? atomicAdd(&S.words, __popc(hit)) : 0;
+#pragma unroll
+            for (int j = 0; j < Vectors<T>::kPer; ++j)
+                if (hit >> j & 1u) elements[to++] = w[j];
         }
     }
-    push(side);
+    if (side >= least) elements[atomicAdd(&S.words, 1)] = side;
     __syncthreads();
-    const int m = S.words;
-    if (t == 0) elements[m] = 0;
-    __syncthreads();
-    for (int i = t; i < m; i += kThreads) {
-        const int r = rank_of(elements[i], elements, m);
-        if (r < k) S.best[r] = elements[i];
-    }
+    rank_words(elements, S.words, k, [&](Word w, int r) { S.best[r] = w; });
     __syncthreads();
 }
 
@@ -429,13 +432,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_scores(LogprobArgs p, int chunk
         S.top[warp] = top;
     }
     __syncthreads();
-    float high = S.top[0];
-    u = S.part[0];
-#pragma unroll
-    for (int i = 1; i < kWarps; ++i) {
-        u = join(u, S.part[i], c);
-        high = fmaxf(high, S.top[i]);
-    }
+    const float high = warp_max(S.top[lane % kWarps]);
+    u = warp_join(lane < kWarps ? S.part[lane] : no_scores(), c);
     if (!plain_range(u.m)) {
         if (high == -INFINITY && u.s == 0.f) {
             u = no_scores();
@@ -446,13 +444,12 @@ __global__ void __launch_bounds__(kThreads, 4) k_scores(LogprobArgs p, int chunk
             __syncthreads();
             if (lane == 0) S.part[warp] = u;
             __syncthreads();
-            u = S.part[0];
-            for (int i = 1; i < kWarps; ++i) u = join(u, S.part[i], c);
+            u = warp_join(lane < kWarps ? S.part[lane] : no_scores(), c);
         }
     }
     if (kTop) {
-        const Word mine = word_of(word_logit((Word)best << 32), best_g);
-        slice_best<T>(S, reinterpret_cast<Word*>(ring), x, tops, v0, p.k, best ? mine : 0,
+        const Word mine = (Word)best << 32 | (unsigned)~best_g;
+        slice_best<T>(S, reinterpret_cast<Word*>(ring), x, tops, v0, p.k, mine >= kLeast ? mine : 0,
                       has_side ? word_of(to_f32(side), v0 + side_at) : 0);
     }
     if (size > 1) {
@@ -462,8 +459,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_scores(LogprobArgs p, int chunk
         if (kTop && rank > 0 && t < p.k) *cluster.map_shared_rank(&S.best[rank * p.k + t], 0) = S.best[t];
         cluster_barrier();
         if (rank != 0) return;
-        u = S.of[0];
-        for (int i = 1; i < size; ++i) u = join(u, S.of[i], c);
+        u = warp_join(lane < size ? S.of[lane] : no_scores(), c);
     }
     const RowScore r = finish(u);
     if (t == 0) {
@@ -474,21 +470,26 @@ __global__ void __launch_bounds__(kThreads, 4) k_scores(LogprobArgs p, int chunk
     if (kTop) {
         int* ids = p.alt_ids + (size_t)n * p.k;
         float* scores = p.alt_logprobs + (size_t)n * p.k;
-        const int words = size * p.k;
-        int some = 0;
-        Word least = 1;
-        if (size > 1) {  // of what is worse than some CTA's k-th, nothing is among the best
-            for (int i = 0; i < size; ++i) least = max(least, S.best[i * p.k + p.k - 1]);
-            if (t == 0 && words % 2) S.best[words] = 0;
-        }
-        for (int i = 0; i < words; i += kThreads) some += __syncthreads_count(i + t < words && S.best[i + t] != 0);
-        for (int i = t; i < words; i += kThreads) {
-            const Word w = S.best[i];
-            if (w < least) continue;
-            const int at = size > 1 ? rank_of(w, S.best, words) : i;
-            if (at >= p.k) continue;
+        int some = p.k;
+        const auto put = [&](Word w, int at) {
             ids[at] = (int)~(unsigned)w;
             scores[at] = log_q(r.st, word_logit(w), p.temperature);
+        };
+        if (size == 1) {
+            const Word w = t < p.k ? S.best[t] : 0;
+            if (w) put(w, t);
+            some = __syncthreads_count(w != 0);
+        } else {
+            // of what is worse than some CTA's k-th, nothing is among the best
+            Word *elements = reinterpret_cast<Word*>(ring), least = 1;
+            for (int i = 0; i < size; ++i) least = max(least, S.best[i * p.k + p.k - 1]);
+            if (t == 0) S.words = 0;
+            __syncthreads();
+            for (int i = t; i < size * p.k; i += kThreads)
+                if (S.best[i] >= least) elements[atomicAdd(&S.words, 1)] = S.best[i];
+            __syncthreads();
+            some = S.words;
+            rank_words(elements, some, p.k, put);
         }
         // places behind the last alternative
         if (t >= some && t < p.k) {
