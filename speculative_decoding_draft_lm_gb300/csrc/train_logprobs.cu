@@ -204,7 +204,7 @@ __device__ __forceinline__ float row_logprob(const RowScore& r, float x, float T
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kAhead = 4;
-constexpr int kStages = 2;
+constexpr int kStages = 3;
 constexpr size_t kRingBytes = (size_t)kThreads * kAhead * kStages * 16;
 constexpr int kMaxK = DOMINO_TRAIN_MAX_ALTERNATIVES;
 constexpr int kMaxCalls = 32;  // of the stream, in a CTA that looks for alternatives
@@ -366,7 +366,7 @@ __device__ __forceinline__ void slice_best(ForwardShared& S, Word* lists, const 
 }
 
 template <typename T, bool kTop>
-__global__ void __launch_bounds__(kThreads, 4) k_scores(LogprobArgs p, int chunk) {
+__global__ void __launch_bounds__(kThreads, 3) k_scores(LogprobArgs p, int chunk) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ ForwardShared S;
     cg::cluster_group cluster = cg::this_cluster();
@@ -777,7 +777,7 @@ int few_rows(const domino_train_ctx* ctx, int n, int V, int per_sm, int least, i
 template <typename T>
 cudaError_t launch_forward(domino_train_ctx* ctx, const LogprobArgs& a, cudaStream_t st) {
     constexpr int kCall = kThreads * kAhead * Vec16<T>::kElems;  // elements
-    int size = few_rows(ctx, a.n, a.V, 4, 4096, kMaxCluster);
+    int size = few_rows(ctx, a.n, a.V, 1, 4096, kMaxCluster);
     while (size < kMaxCluster && slice_of(a.V, size) > kMaxCalls * kCall) size *= 2;
     const int chunk = slice_of(a.V, size), calls = (chunk + kCall - 1) / kCall;
     const size_t smem = kRingBytes + (a.k > 0 ? (size_t)calls * kThreads * sizeof(T) : 0);
