@@ -219,17 +219,34 @@ __device__ __forceinline__ float word_logit(Word w) {
     return k == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : unord_f32(k);
 }
 
-// a group's largest logit as it is stored: the logits' own type
+// A group's largest logit as it is stored, in orderable form: 16 bits of it hold all
+// of a bf16.
 template <typename T>
-__device__ __forceinline__ void keep(T* to, float x);
+struct Stored;
 template <>
-__device__ __forceinline__ void keep<float>(float* to, float x) {
-    *to = x;
-}
+struct Stored<float> {
+    typedef uint32_t Key;
+    static __device__ __forceinline__ Key key(unsigned ord) { return ord; }
+    // whether group g with this key reaches the bound
+    static __device__ __forceinline__ bool reaches(Key k, int g, Word bound) {
+        return ((Word)k << 32 | (unsigned)~g) >= bound;
+    }
+    static __device__ __forceinline__ Word word(Key k, int g) { return (Word)k << 32 | (unsigned)~g; }
+};
 template <>
-__device__ __forceinline__ void keep<__nv_bfloat16>(__nv_bfloat16* to, float x) {
-    *reinterpret_cast<uint16_t*>(to) = (uint16_t)(__float_as_uint(x) >> 16);
-}
+struct Stored<__nv_bfloat16> {
+    typedef uint16_t Key;
+    static __device__ __forceinline__ Key key(unsigned ord) { return (Key)(ord >> 16); }
+    // the key's 16 bits and the place's in one word: both sides have 0 or all ones between them
+    static __device__ __forceinline__ bool reaches(Key k, int g, Word bound) {
+        return ((unsigned)k << 16 | (unsigned)(0xFFFF - g)) >= ((unsigned)(bound >> 48) << 16 | (unsigned)(bound & 0xFFFFu));
+    }
+    static __device__ __forceinline__ Word word(Key k, int g) {
+        // as word_of's of that logit: a negative one's lower bits are ones, and so are a NaN's
+        const unsigned low = k & 0x8000u && k != 0xFFFFu ? 0u : 0xFFFFu;
+        return (Word)((unsigned)k << 16 | low) << 32 | (unsigned)~g;
+    }
+};
 
 struct ForwardShared {
     Scores part[kWarps];
@@ -292,8 +309,8 @@ __device__ __forceinline__ Word warp_nth(Word w, int n) {
 // best groups, which k threads reach, each with as many groups as the stream had
 // calls.
 template <typename T>
-__device__ __forceinline__ void slice_best(ForwardShared& S, Word* lists, const Vectors<T>& x, const T* tops, int v0, int k,
-                                           Word mine, Word side) {
+__device__ __forceinline__ void slice_best(ForwardShared& S, Word* lists, const Vectors<T>& x,
+                                           const typename Stored<T>::Key* tops, int v0, int k, Word mine, Word side) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, groups = (x.last - x.first + kAhead - 1) / kAhead;
     Word *firsts = lists, *listed = firsts + kThreads, *elements = listed + kListed;
     const Word nth = warp_nth(mine, (k + kWarps - 1) / kWarps);
@@ -304,16 +321,17 @@ __device__ __forceinline__ void slice_best(ForwardShared& S, Word* lists, const 
     }
     if (t < k) S.best[t] = 0;
     firsts[t] = mine;
-    __syncthreads();
+    const bool any = __syncthreads_or(mine != 0);
     Word bound = S.nth[0];
 #pragma unroll
     for (int i = 1; i < kWarps; ++i) bound = S.nth[i] < bound ? S.nth[i] : bound;
-    const auto group = [&](int call) { return word_of(to_f32(tops[t + call * kThreads]), t + call * kThreads); };
+    const auto group = [&](int call) { return Stored<T>::word(tops[t + call * kThreads], t + call * kThreads); };
     const auto collect_groups = [&] {
         unsigned hit = 0;
         if (mine >= bound) {
 #pragma unroll 4
-            for (int call = 0; t + call * kThreads < groups; ++call) hit |= group(call) >= bound ? 1u << call : 0u;
+            for (int call = 0; t + call * kThreads < groups; ++call)
+                hit |= Stored<T>::reaches(tops[t + call * kThreads], t + call * kThreads, bound) ? 1u << call : 0u;
         }
         collect(hit, listed, kListed, &S.groups, group);
     };
@@ -321,7 +339,7 @@ __device__ __forceinline__ void slice_best(ForwardShared& S, Word* lists, const 
     if (bound) collect_groups();
     __syncthreads();
     int n = S.groups;
-    if (n == 0 || n > kListed) {  // the same for all threads
+    if (any && (n == 0 || n > kListed)) {  // the same for all threads
         rank_words(firsts, kThreads, k, [&](Word w, int r) {
             if (r == k - 1) S.bound = w;
         });
@@ -377,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_scores(LogprobArgs p, int chunk
     const T* row = static_cast<const T*>(p.x) + (size_t)n * p.ld;
     const Vectors<T> x(row + v0, min(p.V, v0 + chunk) - v0);
     uint4* ring = reinterpret_cast<uint4*>(smem);
-    T* tops = reinterpret_cast<T*>(smem + kRingBytes);
+    typename Stored<T>::Key* tops = reinterpret_cast<typename Stored<T>::Key*>(smem + kRingBytes);
     // the first vectors are on their way while the token is read
     Streamer<kThreads, kAhead, kStages, true, T> vectors(x, ring);
     const int tok = p.tokens[n];
@@ -412,8 +430,8 @@ __global__ void __launch_bounds__(kThreads, 3) k_scores(LogprobArgs p, int chunk
         const float high = top4(v);
         a.template add<kAhead>(v, high, c, cc);
         if (kTop) {
-            keep<T>(tops + g, high);
             const unsigned o = high != high ? 0xFFFFFFFFu : ord_f32(high);
+            tops[g] = Stored<T>::key(o);
             if (o > best) {
                 best = o;
                 best_g = g;
@@ -480,9 +498,12 @@ __global__ void __launch_bounds__(kThreads, 3) k_scores(LogprobArgs p, int chunk
             if (w) put(w, t);
             some = __syncthreads_count(w != 0);
         } else {
-            // of what is worse than some CTA's k-th, nothing is among the best
-            Word *elements = reinterpret_cast<Word*>(ring), least = 1;
-            for (int i = 0; i < size; ++i) least = max(least, S.best[i * p.k + p.k - 1]);
+            // nothing is among the best that is worse than some CTA's k-th, or than the n-th of
+            // half of them, n = k / half upwards
+            const int half = (size + 1) / 2;
+            Word *elements = reinterpret_cast<Word*>(ring);
+            Word least = warp_nth(lane < size ? S.best[lane * p.k + (p.k + half - 1) / half - 1] : 0, half);
+            least = max(max(least, (Word)1), warp_nth(lane < size ? S.best[lane * p.k + p.k - 1] : 0, 1));
             if (t == 0) S.words = 0;
             __syncthreads();
             for (int i = t; i < size * p.k; i += kThreads)
