@@ -1,0 +1,112 @@
+// The checks of the update's gradients, for Python: a step takes hundreds of tensors,
+// and four attributes of each read in Python cost 0.4 us a tensor (96 tensors: 43 us
+// a step, of which the GPU needs 7), here 5 ns.
+#include <Python.h>
+
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <cstdint>
+#include <exception>
+
+#include "domino_rollout.h"
+
+namespace {
+
+// the tensor of a list's entry; nullptr: none
+const at::Tensor* tensor_at(PyObject* fast, Py_ssize_t i) {
+    PyObject* o = PySequence_Fast_GET_ITEM(fast, i);
+    return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr;
+}
+
+// whether g is what the gradient of p has to be; *code: its type
+bool good(const at::Tensor& g, const at::Tensor& p, long device, int* code) {
+    if (g.layout() != c10::kStrided || g.get_device() != device) return false;
+    if (g.scalar_type() == at::kBFloat16) *code = DOMINO_DTYPE_BF16;
+    else if (g.scalar_type() == at::kFloat) *code = DOMINO_DTYPE_FP32;
+    else return false;
+    return g.sizes() == p.sizes() && g.is_contiguous();
+}
+
+// gradients(params, grads, device, addresses, dtypes) -> int
+//
+// params: list of tensors; grads: list of a tensor or None for each, or None for their .grad.  The gradients'
+// addresses (0: none) go to the uint64 array at `addresses`, their types to the int array at `dtypes`.  Returns -1,
+// or the place of the first gradient that is not contiguous, bf16 or fp32, of its parameter's shape and on `device`.
+PyObject* gradients(PyObject*, PyObject* args) {
+    PyObject *params, *grads;
+    long device;
+    unsigned long long addresses, dtypes;
+    if (!PyArg_ParseTuple(args, "O!OlKK", &PyList_Type, &params, &grads, &device, &addresses, &dtypes)) return nullptr;
+    const Py_ssize_t n = PyList_GET_SIZE(params);
+    uint64_t* to = reinterpret_cast<uint64_t*>(static_cast<uintptr_t>(addresses));
+    int* codes = reinterpret_cast<int*>(static_cast<uintptr_t>(dtypes));
+    PyObject* fast = nullptr;
+    if (grads != Py_None) {
+        fast = PySequence_Fast(grads, "grads: want a list of tensors");
+        if (!fast) return nullptr;
+        if (PySequence_Fast_GET_SIZE(fast) != n) {
+            Py_DECREF(fast);
+            PyErr_Format(PyExc_ValueError, "grads: want %zd tensors (or None)", n);
+            return nullptr;
+        }
+    }
+    Py_ssize_t bad = -1;
+    try {
+        for (Py_ssize_t i = 0; bad < 0 && i < n; ++i) {
+            const at::Tensor* p = tensor_at(params, i);
+            at::Tensor own;
+            const at::Tensor* g = nullptr;
+            bool none = false;
+            if (!p) {
+                bad = i;
+                break;
+            }
+            if (!fast) {
+                own = p->grad();
+                none = !own.defined();
+                g = &own;
+            } else {
+                none = PySequence_Fast_GET_ITEM(fast, i) == Py_None;
+                g = tensor_at(fast, i);
+            }
+            to[i] = 0;
+            codes[i] = DOMINO_DTYPE_FP32;
+            if (none) continue;
+            if (!g || !good(*g, *p, device, &codes[i])) bad = i;
+            else to[i] = static_cast<uint64_t>(reinterpret_cast<uintptr_t>(g->data_ptr()));
+        }
+    } catch (const std::exception& e) {
+        Py_XDECREF(fast);
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+    Py_XDECREF(fast);
+    return PyLong_FromSsize_t(bad);
+}
+
+// written(params, addresses): the parameters whose address is not 0 were changed in place
+PyObject* written(PyObject*, PyObject* args) {
+    PyObject* params;
+    unsigned long long addresses;
+    if (!PyArg_ParseTuple(args, "O!K", &PyList_Type, &params, &addresses)) return nullptr;
+    const uint64_t* at = reinterpret_cast<const uint64_t*>(static_cast<uintptr_t>(addresses));
+    try {
+        for (Py_ssize_t i = 0; i < PyList_GET_SIZE(params); ++i) {
+            const at::Tensor* p = tensor_at(params, i);
+            if (p && at[i] && !p->is_inference()) p->unsafeGetTensorImpl()->bump_version();
+        }
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+    Py_RETURN_NONE;
+}
+
+PyMethodDef methods[] = {{"gradients", gradients, METH_VARARGS, "addresses and types of a step's gradients"},
+                         {"written", written, METH_VARARGS, "counts the change of the parameters"},
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_optim_args", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__optim_args() { return PyModule_Create(&module); }

@@ -1,10 +1,10 @@
-"""Python binding of the weights' update in ``include/domino_optim.h`` (ctypes):
-argument marshalling and the flat buffers of the moments.  ``DominoAdamW`` takes
+"""Python binding of the weights' update in ``include/domino_optim.h`` (ctypes, and
+a C++ module that reads the tensors of a step): argument marshalling and the flat
+buffers of the moments.  ``DominoAdamW`` takes
 torch CUDA tensors and the current torch stream.  There is no CPU fallback.
 """
 from __future__ import annotations
 
-import array
 import ctypes
 
 from . import rollout as _r
@@ -55,6 +55,13 @@ def load_library() -> ctypes.CDLL:
     return lib
 
 
+def _load_args():
+    """The C++ module that reads a step's tensors (built beside the library)."""
+    import torch  # noqa: F401  its libraries first
+    from . import _optim_args
+    return _optim_args
+
+
 class DominoAdamW:
     """AdamW over a list of tensors (see the header for the formulas).
 
@@ -91,7 +98,6 @@ class DominoAdamW:
             if p.dtype not in self._codes or p.get_device() != device or not p.is_contiguous():
                 raise ValueError(f"params[{i}]: want contiguous CUDA bfloat16 or float32 on {self.device}, "
                                  f"got {tuple(p.shape)} {p.dtype} strides {p.stride()} on {p.device}")
-        self._shapes = [p.shape for p in self.params]
         self.offsets, total = [], 0
         for p in self.params:
             self.offsets.append(total)
@@ -120,54 +126,33 @@ class DominoAdamW:
         # the raw handle where torch gives it: a Stream object costs more than a launch
         self._current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                                        lambda i: torch.cuda.current_stream(i).cuda_stream)
-        self._written = getattr(torch.autograd.graph, "increment_version", None)
         self._f32 = torch.float32
         count = len(self.params)
         tensors = (domino_adamw_tensor * count)(*[
             domino_adamw_tensor(p.data_ptr(), p.numel(), self._codes[p.dtype],
                                 int(self.master and p.dtype is torch.bfloat16)) for p in self.params])
-        self._dtypes = self._dtype_codes = None
-        self._devices, self._tensor = [device] * count, torch.Tensor
+        self._addresses, self._dtypes = (ctypes.c_uint64 * count)(), (ctypes.c_int * count)()
+        self._addresses_at, self._dtypes_at = ctypes.addressof(self._addresses), ctypes.addressof(self._dtypes)
         address = {n: self.state[n].data_ptr() if n in self.state else None
                    for n in ("m", "v", "m_scale", "v_scale", "master", "count")}
         cfg = domino_adamw_config(count, tensors, state_bits, address["m"], address["v"], address["m_scale"],
                                   address["v_scale"], address["master"], address["count"], betas[0], betas[1], eps,
                                   weight_decay, seed)
-        self._lib = load_library()
+        self._lib, self._args = load_library(), _load_args()
         self.ctx = ctypes.c_void_p()
         _check(self._lib.domino_adamw_init(ctypes.byref(self.ctx), ctypes.byref(cfg), device), "domino_adamw_init")
 
     # -- checks (on every call's path) ----------------------------------------------
 
     def _gradients(self, grads):
-        """(addresses, types) of the gradients as C arrays, and what keeps them alive."""
-        if grads is None:
-            grads = [p.grad for p in self.params]
-        elif len(grads) != len(self.params):
-            raise ValueError(f"grads: want {len(self.params)} tensors (or None), got {len(grads)}")
-        tensor = self._tensor
-        try:  # all at once, where all are given and as in the last call's types
-            if ([g.dtype for g in grads] == self._dtypes and [g.shape for g in grads] == self._shapes
-                    and list(map(tensor.get_device, grads)) == self._devices
-                    and all(map(tensor.is_contiguous, grads))):
-                held = array.array("Q", map(tensor.data_ptr, grads))
-                return held.buffer_info()[0], self._dtype_codes, held
-        except (AttributeError, TypeError):  # None among them
-            pass
-        codes, held, dtypes = self._codes, array.array("Q"), []
-        for g, shape in zip(grads, self._shapes):
-            if g is None:
-                held.append(0)
-                dtypes.append(self._f32)
-                continue
-            dtype = g.dtype
-            if g.shape != shape or dtype not in codes or g.get_device() != self._index or not g.is_contiguous():
-                raise ValueError(f"grads[{len(held)}]: want contiguous CUDA {tuple(shape)} bfloat16 or float32 on "
-                                 f"{self.device}, got {tuple(g.shape)} {dtype} strides {g.stride()} on {g.device}")
-            held.append(g.data_ptr())
-            dtypes.append(dtype)
-        self._dtypes, self._dtype_codes = dtypes, (ctypes.c_int * len(dtypes))(*[codes[d] for d in dtypes])
-        return held.buffer_info()[0], self._dtype_codes, held
+        """Puts the gradients' addresses and types into this context's arrays."""
+        bad = self._args.gradients(self.params, grads, self._index, self._addresses_at, self._dtypes_at)
+        if bad >= 0:
+            g = self.params[bad].grad if grads is None else grads[bad]
+            if not hasattr(g, "dtype"):
+                raise ValueError(f"grads[{bad}]: want a tensor or None, got {type(g).__name__}")
+            raise ValueError(f"grads[{bad}]: want contiguous CUDA {tuple(self.params[bad].shape)} bfloat16 or float32 on "
+                             f"{self.device}, got {tuple(g.shape)} {g.dtype} strides {g.stride()} on {g.device}")
 
     def _scalar(self, t, name):
         """The address of one fp32 number on the device, or None."""
@@ -192,9 +177,10 @@ class DominoAdamW:
             import torch
             out = torch.empty((), device=self.device), torch.empty((), device=self.device)
         norm, scale = out
-        addresses, dtypes, _held = self._gradients(grads)
-        status = self._lib.domino_adamw_grad_norm(self.ctx, addresses, dtypes, max_norm, self._scalar(norm, "norm"),
-                                                  self._scalar(scale, "scale"), self._stream(stream))
+        self._gradients(grads)
+        status = self._lib.domino_adamw_grad_norm(self.ctx, self._addresses_at, self._dtypes_at, max_norm,
+                                                  self._scalar(norm, "norm"), self._scalar(scale, "scale"),
+                                                  self._stream(stream))
         if status:
             raise DominoError(status, "domino_adamw_grad_norm")
         return norm, scale
@@ -204,14 +190,13 @@ class DominoAdamW:
         ``grad_norm`` gives; a step whose scale is not finite is left out).  ``grads`` as for
         ``grad_norm``; a parameter without one is left as it is.  ``lr`` replaces the constructor's;
         ``lr_factor`` (one float32 on the device) multiplies it, for schedules of captured steps."""
-        addresses, dtypes, _held = self._gradients(grads)
-        status = self._lib.domino_adamw_step(self.ctx, addresses, dtypes, self.lr if lr is None else lr,
-                                             self._scalar(lr_factor, "lr_factor"), self._scalar(scale, "scale"),
-                                             self._stream(stream))
+        self._gradients(grads)
+        status = self._lib.domino_adamw_step(self.ctx, self._addresses_at, self._dtypes_at,
+                                             self.lr if lr is None else lr, self._scalar(lr_factor, "lr_factor"),
+                                             self._scalar(scale, "scale"), self._stream(stream))
         if status:
             raise DominoError(status, "domino_adamw_step")
-        if self._written is not None:
-            self._written(self.params)
+        self._args.written(self.params, self._addresses_at)
 
     # -- state ---------------------------------------------------------------------
 

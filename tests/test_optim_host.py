@@ -18,7 +18,7 @@ HEADER = open(os.path.join(ROOT, "include", "domino_optim.h")).read()
 @pytest.fixture(scope="module")
 def lib():
     from speculative_decoding_draft_lm_gb300 import build, optim, rollout
-    if not os.path.exists(rollout.LIB_PATH):
+    if not (os.path.exists(rollout.LIB_PATH) and os.path.exists(build.ARGS)):
         build.build()
     return optim.load_library()
 
@@ -98,6 +98,39 @@ def test_python_refusals():
             DominoAdamW([p], **kw)
     with pytest.raises(ValueError, match="1 to"):
         DominoAdamW([])
+
+
+def test_gradients_are_read(lib):
+    """The module that reads a step's tensors, on the CPU (device -1)."""
+    from speculative_decoding_draft_lm_gb300 import optim
+    args = optim._load_args()
+    params = [torch.zeros(4, 3), torch.zeros(5, dtype=torch.bfloat16), torch.zeros(0)]
+    at, codes = (ctypes.c_uint64 * 3)(), (ctypes.c_int * 3)()
+
+    def read(grads, device=-1):
+        return args.gradients(params, grads, device, ctypes.addressof(at), ctypes.addressof(codes))
+
+    g = [torch.ones(4, 3).bfloat16(), torch.ones(5), torch.ones(0)]
+    assert read(g) == -1 and list(at)[:2] == [t.data_ptr() for t in g[:2]] and list(codes) == [1, 0, 0]
+    assert read(tuple(g)) == -1
+    assert read([None, g[1], None]) == -1 and list(at) == [0, g[1].data_ptr(), 0]
+    assert read(None) == -1 and list(at) == [0, 0, 0]
+    params[0].grad = torch.ones(4, 3)
+    assert read(None) == -1 and at[0] == params[0].grad.data_ptr() and at[1] == 0
+    assert read(g, device=0) == 0
+    for place, wrong in ((0, torch.ones(3, 4)), (0, torch.ones(3, 4).t()), (0, torch.ones(12)), (1, torch.ones(5).half()),
+                         (1, torch.ones(5).double()), (1, torch.ones(10)[::2]), (0, 3.0), (1, torch.ones(5).to_sparse())):
+        bad = list(g)
+        bad[place] = wrong
+        assert read(bad) == place, wrong
+    with pytest.raises(ValueError, match="3 tensors"):
+        read(g[:2])
+    with pytest.raises(TypeError):
+        read(7)
+    read([None, g[1], None])
+    versions = [p._version for p in params]
+    args.written(params, ctypes.addressof(at))
+    assert [p._version for p in params] == [versions[0], versions[1] + 1, versions[2]]
 
 
 def test_narrow_against_torch():
