@@ -236,6 +236,7 @@ int domino_adamw_step(domino_adamw_ctx* c, const void* const* grads, const int* 
             ++launches;
         } while (launched == cudaSuccess && next < g.n_tensors);
     }
+    if (launched != cudaSuccess) cudaMemsetAsync(c->ws_base, 0, 256, st);  // a call cut short has not counted its CTAs out
     const cudaError_t recorded = order.done();
     if (launched != cudaSuccess || recorded != cudaSuccess) return DOMINO_ERR_CUDA;
     c->last_launches = launches;
@@ -273,6 +274,7 @@ int domino_adamw_grad_norm(domino_adamw_ctx* c, const void* const* grads, const 
         ++launches;
         if (none) break;
     }
+    if (launched != cudaSuccess) cudaMemsetAsync(c->ws_base, 0, 256, st);  // a call cut short has not counted its CTAs out
     const cudaError_t recorded = order.done();
     if (launched != cudaSuccess || recorded != cudaSuccess) return DOMINO_ERR_CUDA;
     c->last_launches = launches;

@@ -27,17 +27,20 @@ bool good(const at::Tensor& g, const at::Tensor& p, long device, int* code) {
     return g.sizes() == p.sizes() && g.is_contiguous();
 }
 
-// gradients(params, grads, device, addresses, dtypes) -> int
+// gradients(params, grads, device, held, addresses, dtypes) -> int
 //
 // params: list of tensors; grads: list of a tensor or None for each, or None for their .grad.  The gradients'
 // addresses (0: none) go to the uint64 array at `addresses`, their types to the int array at `dtypes`.  Returns -1,
-// or the place of the first gradient that is not contiguous, bf16 or fp32, of its parameter's shape and on `device`.
+// or the place of the first gradient that is not contiguous, bf16 or fp32, of its parameter's shape and on `device`,
+// or -2 - the place of the first parameter whose elements are not at its address in the uint64 array at `held`.
 PyObject* gradients(PyObject*, PyObject* args) {
     PyObject *params, *grads;
     long device;
-    unsigned long long addresses, dtypes;
-    if (!PyArg_ParseTuple(args, "O!OlKK", &PyList_Type, &params, &grads, &device, &addresses, &dtypes)) return nullptr;
+    unsigned long long held, addresses, dtypes;
+    if (!PyArg_ParseTuple(args, "O!OlKKK", &PyList_Type, &params, &grads, &device, &held, &addresses, &dtypes))
+        return nullptr;
     const Py_ssize_t n = PyList_GET_SIZE(params);
+    const uint64_t* at = reinterpret_cast<const uint64_t*>(static_cast<uintptr_t>(held));
     uint64_t* to = reinterpret_cast<uint64_t*>(static_cast<uintptr_t>(addresses));
     int* codes = reinterpret_cast<int*>(static_cast<uintptr_t>(dtypes));
     PyObject* fast = nullptr;
@@ -50,15 +53,15 @@ PyObject* gradients(PyObject*, PyObject* args) {
             return nullptr;
         }
     }
-    Py_ssize_t bad = -1;
+    Py_ssize_t bad = -1, moved = -1;
     try {
         for (Py_ssize_t i = 0; bad < 0 && i < n; ++i) {
             const at::Tensor* p = tensor_at(params, i);
             at::Tensor own;
             const at::Tensor* g = nullptr;
             bool none = false;
-            if (!p) {
-                bad = i;
+            if (!p || reinterpret_cast<uintptr_t>(p->data_ptr()) != at[i]) {
+                moved = i;
                 break;
             }
             if (!fast) {
@@ -81,7 +84,7 @@ PyObject* gradients(PyObject*, PyObject* args) {
         return nullptr;
     }
     Py_XDECREF(fast);
-    return PyLong_FromSsize_t(bad);
+    return PyLong_FromSsize_t(moved >= 0 ? -2 - moved : bad);
 }
 
 // written(params, addresses): the parameters whose address is not 0 were changed in place

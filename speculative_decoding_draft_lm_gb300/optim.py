@@ -77,6 +77,10 @@ class DominoAdamW:
     every 128 positions; ``master`` is float32; ``count`` int64 [1] holds the
     steps taken.
 
+    The tensors and buffers are updated where they are: a parameter whose ``.data`` is replaced
+    afterwards is refused.  A captured step reads the gradients at the capture's
+    addresses on every replay.
+
     Every method takes ``stream`` (a torch stream or raw handle; default: the
     current one).  With a stream other than the current one the caller orders the
     two, as for any kernel.
@@ -132,6 +136,8 @@ class DominoAdamW:
             domino_adamw_tensor(p.data_ptr(), p.numel(), self._codes[p.dtype],
                                 int(self.master and p.dtype is torch.bfloat16)) for p in self.params])
         self._addresses, self._dtypes = (ctypes.c_uint64 * count)(), (ctypes.c_int * count)()
+        self._held = (ctypes.c_uint64 * count)(*[p.data_ptr() for p in self.params])
+        self._held_at = ctypes.addressof(self._held)
         self._addresses_at, self._dtypes_at = ctypes.addressof(self._addresses), ctypes.addressof(self._dtypes)
         address = {n: self.state[n].data_ptr() if n in self.state else None
                    for n in ("m", "v", "m_scale", "v_scale", "master", "count")}
@@ -146,7 +152,10 @@ class DominoAdamW:
 
     def _gradients(self, grads):
         """Puts the gradients' addresses and types into this context's arrays."""
-        bad = self._args.gradients(self.params, grads, self._index, self._addresses_at, self._dtypes_at)
+        bad = self._args.gradients(self.params, grads, self._index, self._held_at, self._addresses_at, self._dtypes_at)
+        if bad < -1:
+            raise ValueError(f"params[{-2 - bad}]: its elements are no longer where they were when this optimizer was "
+                             "made (its .data was replaced): make a new one with state=state_dict()")
         if bad >= 0:
             g = self.params[bad].grad if grads is None else grads[bad]
             if not hasattr(g, "dtype"):

@@ -352,6 +352,21 @@ def test_refusals():
         _optim(p, state=dict(opt.state, v=opt.state["m"]))
 
 
+def test_a_parameter_that_moved_is_refused():
+    p = [torch.nn.Parameter(torch.randn(100, device="cuda")), torch.randn(50, device="cuda")]
+    opt = _optim(p)
+    g = [torch.randn_like(t) for t in p]
+    opt.step(grads=g)
+    p[0].data = p[0].data.clone()
+    for call in (opt.step, opt.grad_norm):
+        with pytest.raises(ValueError, match="params.0.*no longer"):
+            call(grads=g)
+    assert opt.steps() == 1
+    again = _optim(p, state=opt.state_dict())
+    again.step(grads=g)
+    assert again.steps() == 2
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_resume_from_a_state(bits):
     """A copy of the state and the parameters goes on as the original does, bit for bit."""

@@ -106,9 +106,10 @@ def test_gradients_are_read(lib):
     args = optim._load_args()
     params = [torch.zeros(4, 3), torch.zeros(5, dtype=torch.bfloat16), torch.zeros(0)]
     at, codes = (ctypes.c_uint64 * 3)(), (ctypes.c_int * 3)()
+    held = (ctypes.c_uint64 * 3)(*[p.data_ptr() for p in params])
 
     def read(grads, device=-1):
-        return args.gradients(params, grads, device, ctypes.addressof(at), ctypes.addressof(codes))
+        return args.gradients(params, grads, device, ctypes.addressof(held), ctypes.addressof(at), ctypes.addressof(codes))
 
     g = [torch.ones(4, 3).bfloat16(), torch.ones(5), torch.ones(0)]
     assert read(g) == -1 and list(at)[:2] == [t.data_ptr() for t in g[:2]] and list(codes) == [1, 0, 0]
@@ -127,6 +128,9 @@ def test_gradients_are_read(lib):
         read(g[:2])
     with pytest.raises(TypeError):
         read(7)
+    held[1] += 2  # a parameter that lies elsewhere by now
+    assert read(g) == -3
+    held[1] -= 2
     read([None, g[1], None])
     versions = [p._version for p in params]
     args.written(params, ctypes.addressof(at))
