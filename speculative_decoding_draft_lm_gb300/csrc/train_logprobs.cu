@@ -251,6 +251,7 @@ struct Stored<__nv_bfloat16> {
 struct ForwardShared {
     Scores part[kWarps];
     float top[kWarps];
+    float m, log_s;                      // of the whole row
     Scores of[kMaxCluster];              // every CTA's, at rank 0
     alignas(16) Word best[kMaxCluster * kMaxK];  // every CTA's alternatives, at rank 0
     Word bound, least, nth[kWarps];
@@ -308,20 +309,26 @@ __device__ __forceinline__ Word warp_nth(Word w, int n) {
 // them in a few warps' places, as a mask can have it), the k-th best of the threads'
 // best groups, which k threads reach, each with as many groups as the stream had
 // calls.
-template <typename T>
-__device__ __forceinline__ void slice_best(ForwardShared& S, Word* lists, const Vectors<T>& x,
-                                           const typename Stored<T>::Key* tops, int v0, int k, Word mine, Word side) {
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, groups = (x.last - x.first + kAhead - 1) / kAhead;
-    Word *firsts = lists, *listed = firsts + kThreads, *elements = listed + kListed;
+//
+// S.nth and the rest of S is set before the call's barrier (start_best); any: some
+// thread has a group above -inf.  meanwhile() is called by the last warp, while others
+// wait for the chosen groups.
+__device__ __forceinline__ void start_best(ForwardShared& S, int k, Word mine) {
+    const int t = threadIdx.x;
     const Word nth = warp_nth(mine, (k + kWarps - 1) / kWarps);
-    if (lane == 0) S.nth[warp] = nth;
+    if (t % 32 == 0) S.nth[t / 32] = nth;
     if (t == 0) {
         S.groups = S.words = 0;
         S.bound = S.least = kLeast;
     }
     if (t < k) S.best[t] = 0;
-    firsts[t] = mine;
-    const bool any = __syncthreads_or(mine != 0);
+}
+template <typename T, typename F>
+__device__ __forceinline__ void slice_best(ForwardShared& S, Word* lists, const Vectors<T>& x,
+                                           const typename Stored<T>::Key* tops, int v0, int k, bool any, Word mine,
+                                           Word side, F&& meanwhile) {
+    const int t = threadIdx.x, groups = (x.last - x.first + kAhead - 1) / kAhead;
+    Word *firsts = lists, *listed = firsts + kThreads, *elements = listed + kListed;
     Word bound = S.nth[0];
 #pragma unroll
     for (int i = 1; i < kWarps; ++i) bound = S.nth[i] < bound ? S.nth[i] : bound;
@@ -340,6 +347,8 @@ __device__ __forceinline__ void slice_best(ForwardShared& S, Word* lists, const 
     __syncthreads();
     int n = S.groups;
     if (any && (n == 0 || n > kListed)) {  // the same for all threads
+        firsts[t] = mine;
+        __syncthreads();
         rank_words(firsts, kThreads, k, [&](Word w, int r) {
             if (r == k - 1) S.bound = w;
         });
@@ -378,6 +387,7 @@ __device__ __forceinline__ void slice_best(ForwardShared& S, Word* lists, const 
         }
     }
     if (side >= least) elements[atomicAdd(&S.words, 1)] = side;
+    if (t / 32 == kWarps - 1) meanwhile();
     __syncthreads();
     rank_words(elements, S.words, k, [&](Word w, int r) { S.best[r] = w; });
     __syncthreads();
@@ -417,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_scores(LogprobArgs p, int chunk
         return;
     }
     if (size > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    const float said = rank == 0 && t == 0 ? to_f32(row[tok]) : 0.f;
+    const float said = to_f32(row[tok]);
     const int side_at = t < 2 * Vectors<T>::kPer ? x.beside(t) : x.n;
     const bool has_side = side_at < x.n;
     const T side = has_side ? x.src[side_at] : from_f32<T>(-INFINITY);
@@ -445,11 +455,17 @@ __global__ void __launch_bounds__(kThreads, 3) k_scores(LogprobArgs p, int chunk
     }
     Scores u = warp_join(a.scores(), c);
     const float top = warp_max(a.top);
+    Word mine = 0;
+    if (kTop) {
+        mine = (Word)best << 32 | (unsigned)~best_g;
+        if (mine < kLeast) mine = 0;
+        start_best(S, p.k, mine);
+    }
     if (lane == 0) {
         S.part[warp] = u;
         S.top[warp] = top;
     }
-    __syncthreads();
+    const bool any = __syncthreads_or(mine != 0);
     const float high = warp_max(S.top[lane % kWarps]);
     u = warp_join(lane < kWarps ? S.part[lane] : no_scores(), c);
     if (!plain_range(u.m)) {
@@ -465,10 +481,22 @@ __global__ void __launch_bounds__(kThreads, 3) k_scores(LogprobArgs p, int chunk
             u = warp_join(lane < kWarps ? S.part[lane] : no_scores(), c);
         }
     }
+    // the row's values, by one warp
+    const auto tell = [&] {
+        const RowScore r = finish(u);
+        if (lane == 0) {
+            p.logprob[n] = row_logprob(r, said, p.temperature);
+            if (p.entropy) p.entropy[n] = r.st.entropy;
+            if (p.stats) reinterpret_cast<LogprobStats*>(p.stats)[n] = r.st;
+            S.m = r.st.m;
+            S.log_s = r.st.log_s;
+        }
+    };
     if (kTop) {
-        const Word mine = (Word)best << 32 | (unsigned)~best_g;
-        slice_best<T>(S, reinterpret_cast<Word*>(ring), x, tops, v0, p.k, mine >= kLeast ? mine : 0,
-                      has_side ? word_of(to_f32(side), v0 + side_at) : 0);
+        slice_best<T>(S, reinterpret_cast<Word*>(ring), x, tops, v0, p.k, any, mine,
+                      has_side ? word_of(to_f32(side), v0 + side_at) : 0, [&] {
+                          if (size == 1) tell();
+                      });
     }
     if (size > 1) {
         __syncwarp();
@@ -479,19 +507,14 @@ __global__ void __launch_bounds__(kThreads, 3) k_scores(LogprobArgs p, int chunk
         if (rank != 0) return;
         u = warp_join(lane < size ? S.of[lane] : no_scores(), c);
     }
-    const RowScore r = finish(u);
-    if (t == 0) {
-        p.logprob[n] = row_logprob(r, said, p.temperature);
-        if (p.entropy) p.entropy[n] = r.st.entropy;
-        if (p.stats) reinterpret_cast<LogprobStats*>(p.stats)[n] = r.st;
-    }
+    if ((!kTop || size > 1) && warp == 0) tell();
     if (kTop) {
         int* ids = p.alt_ids + (size_t)n * p.k;
         float* scores = p.alt_logprobs + (size_t)n * p.k;
         int some = p.k;
         const auto put = [&](Word w, int at) {
             ids[at] = (int)~(unsigned)w;
-            scores[at] = log_q(r.st, word_logit(w), p.temperature);
+            scores[at] = (word_logit(w) - S.m) / p.temperature - S.log_s;
         };
         if (size == 1) {
             const Word w = t < p.k ? S.best[t] : 0;
