@@ -6,8 +6,6 @@
 // m and v are formed with every product and sum rounded by itself.
 #pragma once
 
-#include <type_traits>
-
 #include "optim_table.cuh"
 #include "train_math.cuh"
 
@@ -202,10 +200,7 @@ __device__ __forceinline__ void store_param(const Entry& e, float* master, long 
 // calls f(std::integral_constant of the table's size, Kind) for a launch
 template <typename F>
 cudaError_t of_kind(const Work& w, F&& f) {
-    const auto sized = [&](auto kind) {
-        return w.tensors <= kFew ? f(std::integral_constant<int, kFew>(), kind)
-                                 : f(std::integral_constant<int, kMaxPerLaunch>(), kind);
-    };
+    const auto sized = [&](auto kind) { return of_size(w.tensors, [&](auto nt) { return f(nt, kind); }); };
     const auto of = [&](auto grad) {
         typedef decltype(grad) G;
         if (w.kind & kMaster) return sized(Kind<__nv_bfloat16, true, G>());

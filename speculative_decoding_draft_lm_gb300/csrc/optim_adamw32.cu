@@ -1,6 +1,9 @@
 // AdamW with moments in fp32.
 //
-// A thread has 8 consecutive elements; each is read and written once.
+// A thread has 8 consecutive elements, 32 bytes of fp32 or 16 of bf16 a load; each is
+// read and written once.  Bound by HBM: 319 M bf16 parameters with a master copy, 28
+// bytes an element, 8.9 GB, in 1380 to 1417 us, 6.3 to 6.5 TB/s, 0.93 to 0.95 of the
+// measured copy rate (4 elements of a block a lane, one a load: 2790 us).
 #include "optim_adamw.cuh"
 
 namespace domino {

@@ -200,6 +200,16 @@ __device__ __forceinline__ float row_logprob(const RowScore& r, float x, float T
 //
 // A word orders both: the logit in orderable form over the inverted place.  What is
 // not above -inf is below kLeast.
+//
+// 960 rows of 151,936 bf16 logits, 0.29 GB: without alternatives 45.8 us, 6.4 TB/s, 0.94
+// of the measured copy rate; with 20 of them 51 us.  What they cost is the chain of small
+// steps behind a row's stream (bound, collection, two rankings, a second read from L2,
+// about 10 K cycles), which the two other CTAs of an SM hide but for the last rows.
+// Three CTAs an SM with three stages: four CTAs with two 56 us.  A CTA a row from as many
+// rows as SMs on: rows split over twice as many CTAs cost 300 rows 24 us instead of 19.
+// One row: 8.7 us with 20 alternatives, 3.5 without, over a cluster of 16.
+// Forms that were slower: every thread ranking its best group among all 256 (73 us for
+// the 960 rows), atomics in loops over a thread's groups and elements (65).
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -544,6 +554,9 @@ __global__ void __launch_bounds__(kThreads, 3) k_scores(LogprobArgs p, int chunk
 }
 
 // ---- gradient -----------------------------------------------------------------------
+//
+// By itself a stream as the forward's, each vector written where it was read: bound by
+// HBM, 960 rows of 151,936 bf16 logits, 0.58 GB, in 91 us, 6.4 TB/s.
 
 // What turns a logit into its gradient: e (a + b d) with e = 2^d, d = (x - m) c.
 struct Slope {
@@ -623,6 +636,11 @@ __global__ void __launch_bounds__(kThreads, 4) k_scores_backward(LogprobArgs p, 
 // other's shared memory, and a second pass writes the gradient.  So the logits are
 // read once and the gradient is written once.  One wave of clusters takes rows in
 // turn; a row's token and weights are read a row ahead.
+//
+// Bound by HBM: 3840 rows of 151,936 bf16 logits, 2.33 GB, in 368 us, 6.3 TB/s, 0.93 of
+// the measured copy rate.  1021 fp32 rows of 4097 take 8 us where L2 holds them, 12.3 us
+// else: one wave of CTAs that all load, sum and write at the same time.  With every
+// thread forming the row's statistics instead of one warp the 3840 rows took 424 us.
 
 constexpr int kSliceBytes = 40 * 1024;
 constexpr int kStepThreads = 128;
