@@ -162,13 +162,13 @@ int domino_adamw_init(domino_adamw_ctx** out, const domino_adamw_config* cfg, in
         return DOMINO_ERR_CUDA;
     }
     const size_t parts = (size_t)norm_ctas(c, ~0u) * ((n + kMaxPerLaunch - 1) / kMaxPerLaunch);
-    if (cudaMalloc(&c->ws_base, 256 + parts * sizeof(double)) != cudaSuccess) {
+    if (cudaMalloc(&c->ws_base, 256 + parts * sizeof(float2)) != cudaSuccess) {
         cudaGetLastError();
         release(c);
         return DOMINO_ERR_OOM;
     }
     c->ticket = (unsigned*)c->ws_base;
-    c->part = (double*)((char*)c->ws_base + 256);
+    c->part = (float2*)((char*)c->ws_base + 256);
     if (c->use.create() != cudaSuccess || cudaMemset(c->ws_base, 0, 256) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
         release(c);

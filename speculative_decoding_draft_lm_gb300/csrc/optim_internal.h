@@ -48,7 +48,7 @@ struct AdamArgs {
 };
 
 struct NormArgs {
-    double* part;      // a partial sum per CTA of the call
+    float2* part;      // a partial sum per CTA of the call
     unsigned* ticket;
     unsigned first, ctas;  // of this launch, and of the call
     double max_norm;
@@ -66,7 +66,7 @@ struct domino_adamw_ctx {
     unsigned* block;               // [n_tensors] first block of each
     domino::optim::Entry* entry;   // [kMaxPerLaunch] of the launch that is being put together
     unsigned* ticket;              // device: CTAs of a call that are done
-    double* part;                  // device
+    float2* part;                  // device
     void* ws_base;
     domino::WorkspaceUse use;
 };

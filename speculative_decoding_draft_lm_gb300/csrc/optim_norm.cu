@@ -1,14 +1,15 @@
 // The norm of the gradients of many tensors, and the factor that clips it.
 //
 // Every thread adds the squares of 16 consecutive elements in fp32 and keeps the
-// sum of such sums with what its additions round off; the CTAs' sums meet in fp64,
-// in an order that the sizes fix, at the CTA that is done last.  So the norm is as
+// sum of such sums with what its additions round off, and so do warps and CTAs, which
+// meet at the CTA that is done last, in an order that the sizes fix.  So the norm is as
 // good as rounded once: what it scales does not depend on how the sum was cut.
 //
-// Bound by HBM: 483 M bf16 gradients, 0.97 GB, in 148 us, 6.5 TB/s, 0.96 of the measured
-// copy rate (one element a load, summed plainly: 1506 us).  The tiny head's 1.2 M fp32
-// gradients take 6.9 us: the launch, the loads, and two small reductions with a counter
-// between them.
+// Bound by HBM: 483 M bf16 gradients, 0.97 GB, in 137 to 141 us, 6.9 to 7.1 TB/s, the
+// measured copy rate and a little more, for nothing is written (six CTAs an SM instead
+// of eight 146, four 171; one element a load 1506 us).  The tiny head's 1.2 M fp32
+// gradients take 5.2 us: the launch, the loads, and two small reductions with a counter
+// between them (in fp64 6.6 us).
 #include "optim_table.cuh"
 
 namespace domino {
@@ -19,7 +20,8 @@ namespace {
 constexpr int kE = 16;
 static_assert(kThreads * kE == kNormTile, "a tile is one vector of every thread");
 
-// A running sum s with what its additions rounded off, c.
+// A running sum s with what its additions rounded off, c (an infinite or NaN s: c is
+// not looked at).
 struct Sum {
     float s = 0.f, c = 0.f;
     __device__ __forceinline__ void add(float x) {
@@ -27,20 +29,30 @@ struct Sum {
         c += __fadd_rn(s, -__fadd_rn(t, -b)) + __fadd_rn(x, -b);
         s = t;
     }
+    __device__ __forceinline__ void add(float x, float xc) {
+        add(x);
+        c += xc;
+    }
     __device__ __forceinline__ double value() const { return s < INFINITY ? (double)s + (double)c : (double)s; }
 };
 
-// The sum over a CTA's threads, in an order of its own; every thread gets it.
-__device__ __forceinline__ double block_sum(double s) {
-    __shared__ double part[kThreads / 32];
+// The sum over the lanes' sums; lane 0 gets it.
+template <int kLanes>
+__device__ __forceinline__ Sum warp_sum(Sum a) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+        a.add(__shfl_down_sync(0xffffffffu, a.s, o), __shfl_down_sync(0xffffffffu, a.c, o));
+    return a;
+}
+// The sum over a CTA's threads; thread 0 gets it.
+__device__ __forceinline__ Sum block_sum(Sum a) {
+    __shared__ Sum part[kThreads / 32];
+    a = warp_sum<32>(a);
     __syncthreads();
-    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = s;
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = a;
     __syncthreads();
-    s = 0;
-    for (int i = 0; i < kThreads / 32; ++i) s += part[i];
-    return s;
+    if (threadIdx.x < 32) a = warp_sum<kThreads / 32>(threadIdx.x < kThreads / 32 ? part[threadIdx.x] : Sum());
+    return a;
 }
 
 template <typename G>
@@ -74,20 +86,23 @@ __global__ void __launch_bounds__(kThreads) k_norm(const __grid_constant__ Table
             sum.add(squares<float>(raw));
         }
     }
-    double s = block_sum(sum.value());
+    sum = block_sum(sum);
     if (threadIdx.x == 0) {
-        a.part[a.first + blockIdx.x] = s;
+        a.part[a.first + blockIdx.x] = make_float2(sum.s, sum.c);
         __threadfence();
         is_last = atomicInc(a.ticket, a.ctas - 1) == a.ctas - 1;
     }
     __syncthreads();
     if (!is_last) return;
     __threadfence();
-    s = 0;
-    for (unsigned i = threadIdx.x; i < a.ctas; i += kThreads) s += __ldcg(a.part + i);
-    s = block_sum(s);
+    sum = Sum();
+    for (unsigned i = threadIdx.x; i < a.ctas; i += kThreads) {
+        const float2 one = __ldcg(a.part + i);
+        sum.add(one.x, one.y);
+    }
+    sum = block_sum(sum);
     if (threadIdx.x == 0) {
-        const double norm = sqrt(s);
+        const double norm = sqrt(sum.value());
         *a.norm = (float)norm;
         if (a.scale)
             *a.scale = (float)norm < INFINITY ? (float)fmin(1.0, a.max_norm / (norm + 1e-6)) : __uint_as_float(0x7FC00000u);
@@ -97,7 +112,7 @@ __global__ void __launch_bounds__(kThreads) k_norm(const __grid_constant__ Table
 }  // namespace
 
 unsigned norm_ctas(const domino_adamw_ctx* c, unsigned tiles) {
-    const unsigned most = (unsigned)c->num_sms * 6;
+    const unsigned most = (unsigned)c->num_sms * 8;
     return tiles < most ? tiles : most;
 }
 
