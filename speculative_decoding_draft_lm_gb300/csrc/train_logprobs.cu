@@ -207,7 +207,7 @@ __device__ __forceinline__ float row_logprob(const RowScore& r, float x, float T
 // about 10 K cycles), which the two other CTAs of an SM hide but for the last rows.
 // Three CTAs an SM with three stages: four CTAs with two 56 us.  A CTA a row from as many
 // rows as SMs on: rows split over twice as many CTAs cost 300 rows 24 us instead of 19.
-// One row: 8.7 us with 20 alternatives, 3.5 without, over a cluster of 16.
+// One row: 7.1 us with 20 alternatives, 3.5 without, over a cluster of 16.
 // Forms that were slower: every thread ranking its best group among all 256 (73 us for
 // the 960 rows), atomics in loops over a thread's groups and elements (65).
 
@@ -264,7 +264,7 @@ struct ForwardShared {
     float m, log_s;                      // of the whole row
     Scores of[kMaxCluster];              // every CTA's, at rank 0
     alignas(16) Word best[kMaxCluster * kMaxK];  // every CTA's alternatives, at rank 0
-    Word bound, least, nth[kWarps];
+    Word bound, least, of8[kWarps], nth[kWarps];
     int groups, words;
     int chosen[kMaxK];
 };
@@ -299,34 +299,44 @@ __device__ __forceinline__ void rank_words(const Word* list, int n, int k, F&& f
     }
 }
 
-// The n-th best of the lanes' words (0: there are fewer), n >= 1.
-__device__ __forceinline__ Word warp_nth(Word w, int n) {
+// The n-th best of the lanes' words (0: there are fewer), n >= 1, and into *first the
+// early-th, early <= n.
+__device__ __forceinline__ Word warp_nth(Word w, int n, int early, Word* first) {
     unsigned hi = (unsigned)(w >> 32), lo = (unsigned)w, h = 0, l = 0;
     for (int i = 0; i < n; ++i) {
         h = __reduce_max_sync(0xffffffffu, hi);
         l = __reduce_max_sync(0xffffffffu, hi == h ? lo : 0u);
         if (hi == h && lo == l) hi = lo = 0;
+        if (i == early - 1) *first = (Word)h << 32 | l;
     }
     return (Word)h << 32 | l;
+}
+__device__ __forceinline__ Word warp_nth(Word w, int n) {
+    Word unused;
+    return warp_nth(w, n, 0, &unused);
 }
 
 // The k best elements of the CTA's slice to S.best[0 .. k), in order, 0 where there
 // are no more.  mine: the word of the thread's best group, side: its element beside
 // the vectors (0: none).
 //
-// The bound on groups: the worst of the warps' n-th best of their threads' best
-// groups, n = k / 8 upwards; k groups at least reach it.  Where many more do (all of
-// them in a few warps' places, as a mask can have it), the k-th best of the threads'
-// best groups, which k threads reach, each with as many groups as the stream had
-// calls.
+// The bound on groups: the h-th best of the warps' n-th best of their threads' best
+// groups, n = k / h upwards, which h n groups at least reach; the better one for h = 8, all
+// warps, and h = 4, or that for h = 2 or 1 where fewer warps have any (a mask can have it
+// so).  Where many more groups reach it, or no warp has k, the k-th best of the threads'
+// best groups, which k threads reach, each with as many groups as the stream had calls.
 //
 // S.nth and the rest of S is set before the call's barrier (start_best); any: some
 // thread has a group above -inf.  meanwhile() is called by the last warp, while others
 // wait for the chosen groups.
 __device__ __forceinline__ void start_best(ForwardShared& S, int k, Word mine) {
     const int t = threadIdx.x;
-    const Word nth = warp_nth(mine, (k + kWarps - 1) / kWarps);
-    if (t % 32 == 0) S.nth[t / 32] = nth;
+    Word of8 = 0;
+    const Word of4 = warp_nth(mine, (k + 3) / 4, (k + 7) / 8, &of8);
+    if (t % 32 == 0) {
+        S.of8[t / 32] = of8;
+        S.nth[t / 32] = of4;
+    }
     if (t == 0) {
         S.groups = S.words = 0;
         S.bound = S.least = kLeast;
@@ -337,11 +347,13 @@ template <typename T, typename F>
 __device__ __forceinline__ void slice_best(ForwardShared& S, Word* lists, const Vectors<T>& x,
                                            const typename Stored<T>::Key* tops, int v0, int k, bool any, Word mine,
                                            Word side, F&& meanwhile) {
-    const int t = threadIdx.x, groups = (x.last - x.first + kAhead - 1) / kAhead;
+    const int t = threadIdx.x, lane = t & 31, groups = (x.last - x.first + kAhead - 1) / kAhead;
     Word *firsts = lists, *listed = firsts + kThreads, *elements = listed + kListed;
-    Word bound = S.nth[0];
+    static_assert(kWarps == 8, "the bounds' warps");
+    Word bound = S.of8[0];
 #pragma unroll
-    for (int i = 1; i < kWarps; ++i) bound = S.nth[i] < bound ? S.nth[i] : bound;
+    for (int i = 1; i < kWarps; ++i) bound = min(bound, S.of8[i]);
+    bound = max(bound, warp_nth(lane < kWarps ? S.nth[lane] : 0, 4));
     const auto group = [&](int call) { return Stored<T>::word(tops[t + call * kThreads], t + call * kThreads); };
     const auto collect_groups = [&] {
         unsigned hit = 0;
@@ -353,6 +365,13 @@ __device__ __forceinline__ void slice_best(ForwardShared& S, Word* lists, const 
         collect(hit, listed, kListed, &S.groups, group);
     };
     static_assert(kMaxCalls <= 32, "a bit for every call");
+    for (int h = 2; any && !bound && h > 0; --h) {  // the same for all threads
+        const Word nth = warp_nth(mine, (k + h - 1) / h);
+        __syncthreads();  // S.nth is read
+        if (lane == 0) S.nth[t / 32] = nth;
+        __syncthreads();
+        bound = warp_nth(lane < kWarps ? S.nth[lane] : 0, h);
+    }
     if (bound) collect_groups();
     __syncthreads();
     int n = S.groups;
@@ -532,10 +551,10 @@ __global__ void __launch_bounds__(kThreads, 3) k_scores(LogprobArgs p, int chunk
             some = __syncthreads_count(w != 0);
         } else {
             // nothing is among the best that is worse than some CTA's k-th, or than the n-th of
-            // half of them, n = k / half upwards
-            const int half = (size + 1) / 2;
+            // h of them, n = k / h upwards
+            const int h = size < 4 ? size : 4;
             Word *elements = reinterpret_cast<Word*>(ring);
-            Word least = warp_nth(lane < size ? S.best[lane * p.k + (p.k + half - 1) / half - 1] : 0, half);
+            Word least = warp_nth(lane < size ? S.best[lane * p.k + (p.k + h - 1) / h - 1] : 0, h);
             least = max(max(least, (Word)1), warp_nth(lane < size ? S.best[lane * p.k + p.k - 1] : 0, 1));
             if (t == 0) S.words = 0;
             __syncthreads();
