@@ -83,7 +83,8 @@ DOMINO_API int domino_adamw_init(domino_adamw_ctx** out, const domino_adamw_conf
  *   p = p (1 - rate weight_decay)
  *       - rate / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  * in fp32, every product and sum of m and v rounded by itself (so that their codes
- * can be reproduced), p from m and v before they are narrowed; then *count = t.  Where *scale is
+ * can be reproduced), p from m and v before they are narrowed (the root of a v below
+ * 2^-126 counts as 0); then *count = t.  Where *scale is
  * not finite the whole step is left out, count included.  Gradients that are not
  * finite spoil their elements (with 8 bits: their blocks) for good.
  *

@@ -139,12 +139,6 @@ __device__ __forceinline__ uint2 places(F2 a, F2 inv, F2 minus_s) {
     return make_uint2(__float_as_uint(h.x), __float_as_uint(h.y));
 }
 
-// of each half
-__device__ __forceinline__ uint32_t min16(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("min.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 // what the kinds of a launch's tensors are
 template <typename P_, bool kMaster_, typename G_>
 struct Kind {

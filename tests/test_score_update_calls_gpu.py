@@ -207,3 +207,12 @@ def test_parameters_of_a_module():
             # the first step moves every element by lr towards its gradient's other side
             want = s - 1e-2 * t.grad.double() / (t.grad.double().abs() + 1e-8)
             assert (t.detach().double() - want).abs().max() < 1e-2 * 64 * 2.0 ** -24 + 2.0 ** -24 * s.abs().max() * 2
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_nothing_but_empty_tensors(bits):
+    p = [torch.zeros(0, device="cuda"), torch.zeros(3, 0, device="cuda")]
+    opt = _optim(p, state_bits=bits)
+    norm, scale = opt.grad_norm(grads=[torch.zeros_like(t) for t in p])
+    opt.step(grads=[torch.zeros_like(t) for t in p], scale=scale)
+    assert norm.item() == 0 and scale.item() == 1 and opt.steps() == 1
