@@ -887,7 +887,8 @@ cudaError_t launch_step(domino_train_ctx* ctx, const LogprobArgs& a, cudaStream_
     cudaLaunchAttribute attr;
     cudaLaunchConfig_t cfg = cluster_config(size, kStepThreads, size, smem, st, &attr);
     // one wave of clusters, each taking rows in turn; how many the GPU holds at once
-    // is asked once per context and cluster size
+    // is asked once per context and cluster size.  (Clusters of one CTA are launched as
+    // such too: the kernel's barriers and stores address a cluster.)
     int& most = ctx->score_clusters[size];
     if (most == 0) {
         const cudaError_t e = cudaOccupancyMaxActiveClusters(&most, k_scores_step<T>, &cfg);
