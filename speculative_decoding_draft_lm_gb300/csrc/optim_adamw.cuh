@@ -116,7 +116,7 @@ __device__ __forceinline__ F2 e4m3_values(uint32_t codes, bool high) {
     return r;
 }
 
-// A block's scale s, its reciprocal and what a quotient takes (see quotient).
+// A block's scale and its reciprocal.
 struct Scale {
     float s, inv;
 };

@@ -61,9 +61,11 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw32(const __grid_constant__
         }
         if (K::kLossy && top_p != top_p) {
 #pragma unroll
-            for (int j = 0; j < kE / 2; ++j)
-                set_nan(rq[j], halves(updated(a, k, before<K>(rp, j), f2(element<float>(rm, 2 * j), element<float>(rm, 2 * j + 1)),
-                                              f2(element<float>(rv, 2 * j), element<float>(rv, 2 * j + 1)))));
+            for (int j = 0; j < kE / 2; ++j) {
+                const F2 m = f2(element<float>(rm, 2 * j), element<float>(rm, 2 * j + 1));
+                const F2 v = f2(element<float>(rv, 2 * j), element<float>(rv, 2 * j + 1));
+                set_nan(rq[j], halves(updated(a, k, before<K>(rp, j), m, v)));
+            }
         }
         store_param<K, kE>(e, a.master, pos, i, n, rq);
         store_elements<float, kE>(m32, i, n, rm);
@@ -82,7 +84,8 @@ cudaError_t launch_kind(const domino_adamw_ctx* c, const Work& w, const AdamArgs
 }  // namespace
 
 cudaError_t launch_adamw32(const domino_adamw_ctx* c, const Work& w, const AdamArgs& a, cudaStream_t st) {
-    return of_kind(w, [&](auto nt, auto kind) { return launch_kind<decltype(nt)::value, decltype(kind)>(c, w, a, st); });
+    return of_kind(
+        w, [&](auto nt, auto kind) { return launch_kind<decltype(nt)::value, decltype(kind)>(c, w, a, st); });
 }
 
 }  // namespace optim

@@ -35,8 +35,12 @@ __device__ __forceinline__ uint32_t codes(const uint32_t* x, uint32_t* signs) {
 }
 constexpr uint32_t kOnes = 0x01010101u, kTops = 0x80808080u;
 
+// CTAs an SM: as many as leave the raw elements in registers
+template <typename K>
+constexpr int kPerSm = K::kFrom == 2 && sizeof(typename K::G) == 2 ? 4 : 3;
+
 template <int NT, typename K>
-__global__ void __launch_bounds__(kThreads8, K::kFrom == 2 && sizeof(typename K::G) == 2 ? 4 : 3) k_adamw8(const __grid_constant__ Table<NT> w, AdamArgs a) {
+__global__ void __launch_bounds__(kThreads8, kPerSm<K>) k_adamw8(const __grid_constant__ Table<NT> w, AdamArgs a) {
     typedef typename K::P P;
     typedef typename K::G G;
     const Coefficients k = coefficients(a);
@@ -107,7 +111,8 @@ __global__ void __launch_bounds__(kThreads8, K::kFrom == 2 && sizeof(typename K:
                     rp[2 * at2] = __float_as_uint(qf.x);
                     rp[2 * at2 + 1] = __float_as_uint(qf.y);
                 }
-                const uint2 ym = places(m[at2], both(zm.inv), both(-zm.s)), yv = places(v[at2], both(zv.inv), both(-zv.s));
+                const uint2 ym = places(m[at2], both(zm.inv), both(-zm.s));
+                const uint2 yv = places(v[at2], both(zv.inv), both(-zv.s));
                 xm[2 * l] = ym.x + (u0 >> 12);
                 xm[2 * l + 1] = ym.y + (u1 >> 12);
                 xv[2 * l] = yv.x + (r0 >> 12);
@@ -167,7 +172,8 @@ cudaError_t launch_kind(const domino_adamw_ctx* c, const Work& w, const AdamArgs
 }  // namespace
 
 cudaError_t launch_adamw8(const domino_adamw_ctx* c, const Work& w, const AdamArgs& a, cudaStream_t st) {
-    return of_kind(w, [&](auto nt, auto kind) { return launch_kind<decltype(nt)::value, decltype(kind)>(c, w, a, st); });
+    return of_kind(
+        w, [&](auto nt, auto kind) { return launch_kind<decltype(nt)::value, decltype(kind)>(c, w, a, st); });
 }
 
 }  // namespace optim

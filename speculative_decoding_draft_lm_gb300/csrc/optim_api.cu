@@ -230,13 +230,16 @@ int domino_adamw_step(domino_adamw_ctx* c, const void* const* grads, const int* 
         do {
             const Work w = gather(c, grads, grad_dtypes, kind[k], g.state_bits == 8 ? kTile8 : kTile32, &next);
             for (; next < g.n_tensors; ++next)  // to the next one of this kind
-                if (grads[next] && c->tensors[next].n > 0 && kind_of(c->tensors[next], grad_dtypes[next]) == kind[k]) break;
+                if (grads[next] && c->tensors[next].n > 0 &&
+                    kind_of(c->tensors[next], grad_dtypes[next]) == kind[k])
+                    break;
             a.last = k == kinds - 1 && next == g.n_tensors;
             launched = g.state_bits == 8 ? launch_adamw8(c, w, a, st) : launch_adamw32(c, w, a, st);
             ++launches;
         } while (launched == cudaSuccess && next < g.n_tensors);
     }
-    if (launched != cudaSuccess) cudaMemsetAsync(c->ws_base, 0, 256, st);  // a call cut short has not counted its CTAs out
+    // a call cut short has not counted its CTAs out
+    if (launched != cudaSuccess) cudaMemsetAsync(c->ws_base, 0, 256, st);
     const cudaError_t recorded = order.done();
     if (launched != cudaSuccess || recorded != cudaSuccess) return DOMINO_ERR_CUDA;
     c->last_launches = launches;
@@ -255,7 +258,7 @@ int domino_adamw_grad_norm(domino_adamw_ctx* c, const void* const* grads, const 
     a.max_norm = max_norm;
     a.norm = norm;
     a.scale = scale;
-    for (int next = 0; next < c->cfg.n_tensors;) 
+    for (int next = 0; next < c->cfg.n_tensors;)
         a.ctas += norm_ctas(c, gather(c, grads, grad_dtypes, kAnyKind, kNormTile, &next).tiles);
     DeviceGuard guard(c->device);
     const cudaStream_t st = (cudaStream_t)stream;
@@ -274,7 +277,8 @@ int domino_adamw_grad_norm(domino_adamw_ctx* c, const void* const* grads, const 
         ++launches;
         if (none) break;
     }
-    if (launched != cudaSuccess) cudaMemsetAsync(c->ws_base, 0, 256, st);  // a call cut short has not counted its CTAs out
+    // a call cut short has not counted its CTAs out
+    if (launched != cudaSuccess) cudaMemsetAsync(c->ws_base, 0, 256, st);
     const cudaError_t recorded = order.done();
     if (launched != cudaSuccess || recorded != cudaSuccess) return DOMINO_ERR_CUDA;
     c->last_launches = launches;

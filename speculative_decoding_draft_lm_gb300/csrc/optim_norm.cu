@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(kThreads) k_norm(const __grid_constant__ Table
         const double norm = sqrt(sum.value());
         *a.norm = (float)norm;
         if (a.scale)
-            *a.scale = (float)norm < INFINITY ? (float)fmin(1.0, a.max_norm / (norm + 1e-6)) : __uint_as_float(0x7FC00000u);
+            *a.scale = (float)norm < INFINITY ? (float)fmin(1.0, a.max_norm / (norm + 1e-6))
+                                              : __uint_as_float(0x7FC00000u);
     }
 }
 

@@ -723,10 +723,11 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_scores_step(LogprobArgs p, 
     __shared__ StepShared S;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, stride = gridDim.x / size;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const unsigned rows = p.n, stride = gridDim.x / size;  // a row's number and a stride fit 32 bits together
     const float c = kLog2e / p.temperature;
     const uint32_t bar = tc::smem_u32(&S.bar);
-    const auto slice = [&](int n) {
+    const auto slice = [&](unsigned n) {
         return Slice<T>(static_cast<const T*>(p.x) + (size_t)n * p.ld, p.V, chunk, rank, smem);
     };
     const auto request = [&](const Slice<T>& x) {  // one thread, after a barrier behind the buffer's last use
@@ -741,9 +742,9 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_scores_step(LogprobArgs p, 
         int tok;
         bool part;  // the row takes part
     };
-    const auto ahead = [&](int n) {
+    const auto ahead = [&](unsigned n) {
         Ahead a = {0.f, 0.f, -1, false};
-        if (n < p.n) {
+        if (n < rows) {
             if (p.dlogprob) a.g = p.dlogprob[n];
             if (p.dentropy) a.h = p.dentropy[n];
             a.tok = p.tokens[n];
@@ -753,7 +754,7 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_scores_step(LogprobArgs p, 
         }
         return a;
     };
-    int n = blockIdx.x / size;
+    unsigned n = blockIdx.x / size;
     Ahead now = ahead(n);
     if (t == 0) {
         tc::mbar_init(bar, 1);
@@ -765,7 +766,7 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_scores_step(LogprobArgs p, 
     if (now.part) slice(n).load_edges();
     cluster_barrier();  // every CTA of the cluster is running
     uint32_t turn = 0;  // rows so far that took part
-    for (; n < p.n; n += stride) {
+    for (; n < rows; n += stride) {
         const Ahead next = ahead(n + stride);
         const Slice<T> x = slice(n);
         T* dx = static_cast<T*>(p.dx) + (size_t)n * p.ld_d + x.v0;
@@ -851,7 +852,8 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_scores_step(LogprobArgs p, 
 // most CTAs a row of `n` rows takes until there are `per_sm` of them on every SM
 int few_rows(const domino_train_ctx* ctx, int n, int V, int per_sm, int least, int most) {
     int size = 1;
-    while (size < most && (long long)n * size < (long long)per_sm * ctx->num_sms && slice_of(V, 2 * size) >= least) size *= 2;
+    while (size < most && (long long)n * size < (long long)per_sm * ctx->num_sms && slice_of(V, 2 * size) >= least)
+        size *= 2;
     return size;
 }
 
@@ -865,7 +867,8 @@ cudaError_t launch_forward(domino_train_ctx* ctx, const LogprobArgs& a, cudaStre
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = cluster_config((unsigned)a.n * size, kThreads, size, smem, st, &attr);
     ctx->last_launches = 1;
-    return a.k > 0 ? cudaLaunchKernelEx(&cfg, k_scores<T, true>, a, chunk) : cudaLaunchKernelEx(&cfg, k_scores<T, false>, a, chunk);
+    return a.k > 0 ? cudaLaunchKernelEx(&cfg, k_scores<T, true>, a, chunk)
+                   : cudaLaunchKernelEx(&cfg, k_scores<T, false>, a, chunk);
 }
 
 template <typename T>
