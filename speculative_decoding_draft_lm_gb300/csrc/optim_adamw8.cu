@@ -43,6 +43,7 @@ template <int NT, typename K>
 __global__ void __launch_bounds__(kThreads8, kPerSm<K>) k_adamw8(const __grid_constant__ Table<NT> w, AdamArgs a) {
     typedef typename K::P P;
     typedef typename K::G G;
+    pdl_wait();
     const Coefficients k = coefficients(a);
     int at = 0;
     for (unsigned tile = blockIdx.x; !k.skip && tile < w.tiles; tile += gridDim.x) {
@@ -165,8 +166,8 @@ __global__ void __launch_bounds__(kThreads8, kPerSm<K>) k_adamw8(const __grid_co
 template <int NT, typename K>
 cudaError_t launch_kind(const domino_adamw_ctx* c, const Work& w, const AdamArgs& a, cudaStream_t st) {
     const unsigned most = (unsigned)c->num_sms * 30;
-    k_adamw8<NT, K><<<w.tiles < 1 ? 1 : w.tiles < most ? w.tiles : most, kThreads8, 0, st>>>(table<NT>(w), a);
-    return cudaGetLastError();
+    return launch_pdl(k_adamw8<NT, K>, dim3(w.tiles < 1 ? 1 : w.tiles < most ? w.tiles : most), dim3(kThreads8), 0, st,
+                      table<NT>(w), a);
 }
 
 }  // namespace

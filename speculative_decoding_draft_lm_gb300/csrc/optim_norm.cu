@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(kThreads) k_norm(const __grid_constant__ Table
     __shared__ bool is_last;
     Sum sum;
     int at = 0;
+    pdl_wait();
 #pragma unroll 2
     for (unsigned tile = blockIdx.x; tile < w.tiles; tile += gridDim.x) {
         at = find(w, tile, at);
@@ -120,8 +121,7 @@ unsigned norm_ctas(const domino_adamw_ctx* c, unsigned tiles) {
 cudaError_t launch_norm(const Work& w, const NormArgs& a, unsigned ctas, cudaStream_t st) {
     return of_size(w.tensors, [&](auto nt) {
         constexpr int kTensors = decltype(nt)::value;
-        k_norm<kTensors><<<ctas, kThreads, 0, st>>>(table<kTensors>(w), a);
-        return cudaGetLastError();
+        return launch_pdl(k_norm<kTensors>, dim3(ctas), dim3(kThreads), 0, st, table<kTensors>(w), a);
     });
 }
 

@@ -435,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_scores(LogprobArgs p, int chunk
     const Vectors<T> x(row + v0, min(p.V, v0 + chunk) - v0);
     uint4* ring = reinterpret_cast<uint4*>(smem);
     typename Stored<T>::Key* tops = reinterpret_cast<typename Stored<T>::Key*>(smem + kRingBytes);
+    pdl_wait();
     // the first vectors are on their way while the token is read
     Streamer<kThreads, kAhead, kStages, true, T> vectors(x, ring);
     const int tok = p.tokens[n];
@@ -621,6 +622,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_scores_backward(LogprobArgs p, 
     const float c = kLog2e / p.temperature;
     const Vectors<T> x(static_cast<const T*>(p.x) + (size_t)n * p.ld + v0, min(p.V, v0 + chunk) - v0);
     T* dx = static_cast<T*>(p.dx) + (size_t)n * p.ld_d + v0;
+    pdl_wait();
     const LogprobStats st = reinterpret_cast<const LogprobStats*>(p.stats)[n];
     const float g = p.dlogprob ? p.dlogprob[n] : 0.f, h = p.dentropy ? p.dentropy[n] : 0.f;
     const int tok = p.tokens[n] - v0;
@@ -755,6 +757,7 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_scores_step(LogprobArgs p, 
         return a;
     };
     unsigned n = blockIdx.x / size;
+    pdl_wait();
     Ahead now = ahead(n);
     if (t == 0) {
         tc::mbar_init(bar, 1);
@@ -849,6 +852,20 @@ __global__ void __launch_bounds__(kStepThreads, 8) k_scores_step(LogprobArgs p, 
     cluster_barrier();  // nobody leaves before all have their sums
 }
 
+// A launch in clusters of `size` CTAs that may be set up while the stream's last
+// kernel ends (every kernel here waits for that one before it reads memory): in
+// calls after one another a kernel of a few us comes 1 to 2 us earlier.
+struct Launch {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg;
+    Launch(unsigned blocks, int threads, int size, size_t smem, cudaStream_t st)
+        : cfg(cluster_config(blocks, threads, size, smem, st, attr)) {
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 2;
+    }
+};
+
 // most CTAs a row of `n` rows takes until there are `per_sm` of them on every SM
 int few_rows(const domino_train_ctx* ctx, int n, int V, int per_sm, int least, int most) {
     int size = 1;
@@ -863,21 +880,20 @@ cudaError_t launch_forward(domino_train_ctx* ctx, const LogprobArgs& a, cudaStre
     int size = few_rows(ctx, a.n, a.V, 1, 4096, kMaxCluster);
     while (size < kMaxCluster && slice_of(a.V, size) > kMaxCalls * kCall) size *= 2;
     const int chunk = slice_of(a.V, size), calls = (chunk + kCall - 1) / kCall;
-    const size_t smem = kRingBytes + (a.k > 0 ? (size_t)calls * kThreads * sizeof(T) : 0);
-    cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = cluster_config((unsigned)a.n * size, kThreads, size, smem, st, &attr);
+    const size_t smem = kRingBytes + (a.k > 0 ? (size_t)calls * kThreads * sizeof(typename Stored<T>::Key) : 0);
+    Launch l((unsigned)a.n * size, kThreads, size, smem, st);
     ctx->last_launches = 1;
-    return a.k > 0 ? cudaLaunchKernelEx(&cfg, k_scores<T, true>, a, chunk)
-                   : cudaLaunchKernelEx(&cfg, k_scores<T, false>, a, chunk);
+    return a.k > 0 ? cudaLaunchKernelEx(&l.cfg, k_scores<T, true>, a, chunk)
+                   : cudaLaunchKernelEx(&l.cfg, k_scores<T, false>, a, chunk);
 }
 
 template <typename T>
 cudaError_t launch_backward(domino_train_ctx* ctx, const LogprobArgs& a, cudaStream_t st) {
     int size = few_rows(ctx, a.n, a.V, 4, 2048, 64);
     while (slice_of(a.V, size) * (int)sizeof(T) > 160 * 1024) size *= 2;
-    k_scores_backward<T><<<(unsigned)a.n * size, kThreads, kRingBytes, st>>>(a, slice_of(a.V, size), size);
     ctx->last_launches = 1;
-    return cudaGetLastError();
+    return launch_pdl(k_scores_backward<T>, dim3((unsigned)a.n * size), dim3(kThreads), kRingBytes, st, a,
+                      slice_of(a.V, size), size);
 }
 
 template <typename T>
@@ -887,20 +903,19 @@ cudaError_t launch_step(domino_train_ctx* ctx, const LogprobArgs& a, cudaStream_
     while (size < kMaxCluster && (long long)a.n * size < 2 * ctx->num_sms && slice_of(a.V, 2 * size) >= 4096) size *= 2;
     const int chunk = slice_of(a.V, size);
     const size_t smem = (size_t)chunk * sizeof(T) + 32;
-    cudaLaunchAttribute attr;
-    cudaLaunchConfig_t cfg = cluster_config(size, kStepThreads, size, smem, st, &attr);
+    Launch l(size, kStepThreads, size, smem, st);
     // one wave of clusters, each taking rows in turn; how many the GPU holds at once
     // is asked once per context and cluster size.  (Clusters of one CTA are launched as
     // such too: the kernel's barriers and stores address a cluster.)
     int& most = ctx->score_clusters[size];
     if (most == 0) {
-        const cudaError_t e = cudaOccupancyMaxActiveClusters(&most, k_scores_step<T>, &cfg);
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&most, k_scores_step<T>, &l.cfg);
         if (e != cudaSuccess) return e;
         if (most < 1) most = 1;
     }
-    cfg.gridDim = dim3((unsigned)(a.n < most ? a.n : most) * size);
+    l.cfg.gridDim = dim3((unsigned)(a.n < most ? a.n : most) * size);
     ctx->last_launches = 1;
-    return cudaLaunchKernelEx(&cfg, k_scores_step<T>, a, chunk);
+    return cudaLaunchKernelEx(&l.cfg, k_scores_step<T>, a, chunk);
 }
 
 }  // namespace
