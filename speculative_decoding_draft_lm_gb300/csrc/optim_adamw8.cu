@@ -15,6 +15,8 @@
 // Tiles go to the CTAs in 30 shares an SM: with one share a resident CTA the SMs end
 // apart (654 against 632 when that was measured).  Prefetches of the next tile into L2,
 // threads by 128 or the random words' shifts as upper halves of products gained nothing.
+// A ring of asynchronous copies a tile ahead took 593: the issue slots were as full as
+// without it, with more instructions to issue.
 #include "optim_adamw.cuh"
 
 namespace domino {
