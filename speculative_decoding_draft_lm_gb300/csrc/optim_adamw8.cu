@@ -96,7 +96,6 @@ __global__ void __launch_bounds__(kThreads8, kPerSm<K>) k_adamw8(const __grid_co
         }
         const Scale zm = scale_of(top_m), zv = scale_of(top_v);
         // everything that takes an element's random word, so that it need not be held
-        uint32_t odd = 0;  // a code of 127 or, of v, of 0
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint32_t xm[4], xv[4], signs, none;
@@ -123,29 +122,35 @@ __global__ void __launch_bounds__(kThreads8, kPerSm<K>) k_adamw8(const __grid_co
             }
             const uint32_t cm = codes(xm, &signs);
             rv[j] = codes(xv, &none);
-            odd |= (cm + kOnes) | (rv[j] + kOnes);
-            odd |= rv[j] - kOnes;
             rm[j] = cm | (signs & kTops);
-        }
-        if (K::kLossy && top_p != top_p) {
-            uint32_t old[kE * K::kFrom / 4];
-            load_elements<P, kE>(old, static_cast<const P*>(e.p), i, n);
+            if (((cm + kOnes) | (rv[j] + kOnes) | (rv[j] - kOnes)) & kTops) {  // a code of 127 or, of v, of 0
+                // a quotient by a rounded scale can pass the largest number, 126, by its last bits;
+                // and a v that is not 0 does not become 0
 #pragma unroll
-            for (int j = 0; j < kE / 2; ++j) set_nan(rp[j], halves(updated(a, k, before<K>(old, j), m[j], v[j])));
-        }
-        store_param<K, kE>(e, a.master, pos, i, n, rp);
-        if (odd & kTops) {
-            // a quotient by a rounded scale can pass the largest number, 126, by its last bits;
-            // and a v that is not 0 does not become 0
-#pragma unroll
-            for (int j = 0; j < kE; ++j) {
-                const float2 vf = halves(v[j / 2]);
-                const uint32_t one = 1u << (j % 4 * 8);
-                if ((rm[j / 4] & 0x7Fu * one) == 0x7Fu * one) rm[j / 4] -= one;
-                if ((rv[j / 4] & 0x7Fu * one) == 0x7Fu * one) rv[j / 4] -= one;
-                if ((j % 2 ? vf.y : vf.x) != 0.f && !(rv[j / 4] & 0x7Fu * one)) rv[j / 4] |= one;
+                for (int l = 0; l < 4; ++l) {
+                    const float2 vf = halves(v[2 * j + l / 2]);
+                    const uint32_t one = 1u << (l * 8);
+                    if ((rm[j] & 0x7Fu * one) == 0x7Fu * one) rm[j] -= one;
+                    if ((rv[j] & 0x7Fu * one) == 0x7Fu * one) rv[j] -= one;
+                    if ((l % 2 ? vf.y : vf.x) != 0.f && !(rv[j] & 0x7Fu * one)) rv[j] |= one;
+                }
             }
         }
+        // (rare fixes hold nothing over the ordinary way: with one of all codes and one of all NaN from registers, here,
+        // 92 bytes a thread were spilled)
+        if (K::kLossy && top_p != top_p) {
+            // each element from memory once more, so that no register is held for this
+#pragma unroll
+            for (int j = 0; j < kE; ++j) {
+                if (i + j >= n) continue;
+                const F2 g = mul2(both(to_f32(static_cast<const G*>(e.g)[i + j])), both(k.scale));
+                const F2 m1 = new_m(a, mul2(e4m3_values(m8[j], false), both(a.m_scale[block])), g);
+                const F2 v1 = new_v(a, mul2(e4m3_values(v8[j], false), both(a.v_scale[block])), g);
+                const float q = halves(updated(a, k, both(to_f32(static_cast<const P*>(e.p)[i + j])), m1, v1)).x;
+                if (q != q) rp[j / 2] = (rp[j / 2] & (j % 2 ? 0xFFFFu : 0xFFFF0000u)) | 0x7FC0u << (j % 2 * 16);
+            }
+        }
+        store_param<K, kE>(e, a.master, pos, i, n, rp);
         if (i + kE <= n) {
             store_words<4>(m8, rm, false);
             store_words<4>(v8, rv, false);
