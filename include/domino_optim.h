@@ -105,9 +105,10 @@ DOMINO_API int domino_adamw_init(domino_adamw_ctx** out, const domino_adamw_conf
 DOMINO_API int domino_adamw_step(domino_adamw_ctx* ctx, const void* const* grads, const int* grad_dtypes, double lr,
                                  const float* lr_factor, const float* scale, void* cuda_stream);
 
-/* *norm = sqrt(sum of g^2 over the elements of all gradients), squares in fp32 (an
- * element past 1.8e19 makes the norm infinite, one below 4e-23 adds nothing), sums in
- * twice its precision, in an order that the sizes fix;
+/* *norm = sqrt(sum of g^2 over the elements of all gradients), squares and sums of up to
+ * four of them in fp32 (an element past 1.8e19 makes the norm infinite, one below 2e-23
+ * adds nothing), sums of those in twice its precision, in an order that the sizes fix:
+ * off by at most 2^-23 of itself;
  * *scale = min(1, max_norm / (*norm + 1e-6)), NaN where the norm is not finite (so
  * that a step with this scale is left out).  Both on the device; scale may be
  * NULL.  grads and grad_dtypes as in domino_adamw_step; max_norm > 0.

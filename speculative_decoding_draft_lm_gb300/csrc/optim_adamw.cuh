@@ -18,16 +18,12 @@ namespace optim {
 
 using train::F2;
 using train::f2;
+using train::fma2;
 using train::halves;
 using train::mul2;
 
 constexpr int kBlock = DOMINO_ADAMW_BLOCK;
 
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
 __device__ __forceinline__ F2 both(float x) { return f2(x, x); }
 __device__ __forceinline__ F2 both(float2 x) { return f2(x.x, x.y); }
 

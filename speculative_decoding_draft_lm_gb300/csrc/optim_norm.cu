@@ -1,9 +1,11 @@
 // The norm of the gradients of many tensors, and the factor that clips it.
 //
-// Every thread adds the squares of 16 consecutive elements in fp32 and keeps the
-// sum of such sums with what its additions round off, and so do warps and CTAs, which
-// meet at the CTA that is done last, in an order that the sizes fix.  So the norm is as
-// good as rounded once: what it scales does not depend on how the sum was cut.
+// Every thread adds two or four squares in fp32 and keeps the sum of such sums with what
+// its additions round off, and so do warps and CTAs, which meet at the CTA that is done
+// last, in an order that the sizes fix.  So the norm is off by two units of 2^-24 at most,
+// one of them its own rounding.  (With 16 squares in a plain sum it was off by up to 7, for
+// a large element beside small ones, and as fast from 0.5 GB of gradients on.  Every square
+// by itself into the sum with its rest took 170 us for the gradients below.)
 //
 // Bound by HBM: 483 M bf16 gradients, 0.97 GB, in 137 to 141 us, 6.9 to 7.1 TB/s, the
 // measured copy rate and a little more, for nothing is written (six CTAs an SM instead
@@ -11,11 +13,19 @@
 // gradients take 5.2 us: the launch, the loads, and two small reductions with a counter
 // between them (in fp64 6.6 us).
 #include "optim_table.cuh"
+#include "train_math.cuh"
 
 namespace domino {
 namespace optim {
 
 namespace {
+
+using train::add2;
+using train::F2;
+using train::f2;
+using train::fma2;
+using train::halves;
+using train::mul2;
 
 constexpr int kE = 16;
 static_assert(kThreads * kE == kNormTile, "a tile is one vector of every thread");
@@ -55,24 +65,43 @@ __device__ __forceinline__ Sum block_sum(Sum a) {
     return a;
 }
 
-template <typename G>
-__device__ __forceinline__ float squares(const uint32_t* w) {
-    float q = 0.f;
-#pragma unroll
-    for (int j = 0; j < kE; ++j) {
-        const float g = element<G>(w, j);
-        q = fmaf(g, g, q);
+// A thread's sum of squares with what its additions round off: two of them, in packed
+// operations.  Two (fp32) or four (bf16, whose squares are exact) squares are added
+// before, with two roundings: 2^-23 of them at most, half of which is the norm's.
+struct Squares {
+    F2 s = f2(0.f, 0.f), c = f2(0.f, 0.f);
+    __device__ __forceinline__ void add(F2 x) {
+        const F2 minus = f2(-1.f, -1.f), t = add2(s, x), b = fma2(t, minus, s);  // b: minus what s grew by
+        c = add2(c, add2(fma2(add2(t, b), minus, s), add2(x, b)));
+        s = t;
     }
-    return q;
-}
+    template <typename G>
+    __device__ __forceinline__ void add(const uint32_t* w) {
+        const auto two = [&](int j) {
+            const F2 g = f2(element<G>(w, j), element<G>(w, j + 1)), h = f2(element<G>(w, j + 2), element<G>(w, j + 3));
+            return fma2(g, g, mul2(h, h));
+        };
+        constexpr int kStep = sizeof(G) == 2 ? 8 : 4;
+#pragma unroll
+        for (int j = 0; j < kE; j += kStep) add(kStep == 8 ? add2(two(j), two(j + 4)) : two(j));
+    }
+    __device__ __forceinline__ Sum sum() const {
+        const float2 hs = halves(s), hc = halves(c);
+        Sum r;
+        r.s = hs.x;
+        r.c = hc.x;
+        r.add(hs.y, hc.y);
+        return r;
+    }
+};
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads) k_norm(const __grid_constant__ Table<NT> w, NormArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) k_norm(const __grid_constant__ Table<NT> w, NormArgs a) {
     __shared__ bool is_last;
-    Sum sum;
+    Squares squares;
     int at = 0;
     pdl_wait();
-#pragma unroll 2
+#pragma unroll 1
     for (unsigned tile = blockIdx.x; tile < w.tiles; tile += gridDim.x) {
         at = find(w, tile, at);
         const Entry& e = w.e[at];
@@ -81,13 +110,13 @@ __global__ void __launch_bounds__(kThreads) k_norm(const __grid_constant__ Table
         uint32_t raw[kE];
         if (e.n & kGradBf16) {
             load_elements<__nv_bfloat16, kE>(raw, static_cast<const __nv_bfloat16*>(e.g), i, n);
-            sum.add(squares<__nv_bfloat16>(raw));
+            squares.template add<__nv_bfloat16>(raw);
         } else {
             load_elements<float, kE>(raw, static_cast<const float*>(e.g), i, n);
-            sum.add(squares<float>(raw));
+            squares.template add<float>(raw);
         }
     }
-    sum = block_sum(sum);
+    Sum sum = block_sum(squares.sum());
     if (threadIdx.x == 0) {
         a.part[a.first + blockIdx.x] = make_float2(sum.s, sum.c);
         __threadfence();

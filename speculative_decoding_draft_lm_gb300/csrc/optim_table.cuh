@@ -40,6 +40,7 @@ Table<NT> table(const Work& w) {
 template <int NT>
 __device__ __forceinline__ int find(const Table<NT>& w, unsigned tile, int lo) {
     int hi = w.tensors;
+    if (lo + 1 >= hi || w.e[lo + 1].tile > tile) return lo;  // mostly that of the CTA's last tile
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
         if (w.e[mid].tile <= tile) lo = mid;

@@ -72,11 +72,6 @@ __device__ __forceinline__ Scores warp_join(Scores a, float c) {
 constexpr float kLow = -1e30f, kFloor = -1e29f;
 __device__ __forceinline__ bool plain_range(float m) { return m > kFloor && m <= -kFloor; }
 
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
