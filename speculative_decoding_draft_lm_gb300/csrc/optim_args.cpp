@@ -18,31 +18,46 @@ const at::Tensor* tensor_at(PyObject* fast, Py_ssize_t i) {
     return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr;
 }
 
-// whether g is what the gradient of p has to be; *code: its type
-bool good(const at::Tensor& g, const at::Tensor& p, long device, int* code) {
-    if (g.layout() != c10::kStrided || g.get_device() != device) return false;
-    if (g.scalar_type() == at::kBFloat16) *code = DOMINO_DTYPE_BF16;
-    else if (g.scalar_type() == at::kFloat) *code = DOMINO_DTYPE_FP32;
+// the library's name of a tensor's type; false: it has none
+bool type_code(const at::Tensor& t, int* code) {
+    if (t.scalar_type() == at::kBFloat16) *code = DOMINO_DTYPE_BF16;
+    else if (t.scalar_type() == at::kFloat) *code = DOMINO_DTYPE_FP32;
     else return false;
-    return g.sizes() == p.sizes() && g.is_contiguous();
+    return true;
 }
 
-// gradients(params, grads, device, held, addresses, dtypes) -> int
+// whether g is what the gradient of p has to be; *code: its type
+bool good(const at::Tensor& g, const at::Tensor& p, long device, int* code) {
+    return g.layout() == c10::kStrided && g.get_device() == device && type_code(g, code) && g.sizes() == p.sizes() &&
+           g.is_contiguous();
+}
+
+// whether p still is `n` elements in a row, of type `code`
+bool same(const at::Tensor& p, int64_t n, int code) {
+    int its;
+    return p.numel() == n && type_code(p, &its) && its == code && p.is_contiguous();
+}
+
+// gradients(params, grads, device, held, addresses, dtypes, sizes = 0, types = 0) -> int
 //
 // params: list of tensors; grads: list of a tensor or None for each, or None for their .grad.  The gradients'
 // addresses (0: none) go to the uint64 array at `addresses`, their types to the int array at `dtypes`.  Returns -1,
 // or the place of the first gradient that is not contiguous, bf16 or fp32, of its parameter's shape and on `device`,
-// or -2 - the place of the first parameter whose elements are not at its address in the uint64 array at `held`.
+// or -2 - the place of the first parameter whose elements are not at its address in the uint64 array at `held`, or
+// not as many as the int64 array at `sizes` has it, of the type in the int array at `types` and contiguous.
 PyObject* gradients(PyObject*, PyObject* args) {
     PyObject *params, *grads;
     long device;
-    unsigned long long held, addresses, dtypes;
-    if (!PyArg_ParseTuple(args, "O!OlKKK", &PyList_Type, &params, &grads, &device, &held, &addresses, &dtypes))
+    unsigned long long held, addresses, dtypes, sizes = 0, types = 0;
+    if (!PyArg_ParseTuple(args, "O!OlKKK|KK", &PyList_Type, &params, &grads, &device, &held, &addresses, &dtypes, &sizes,
+                          &types))
         return nullptr;
     const Py_ssize_t n = PyList_GET_SIZE(params);
     const uint64_t* at = reinterpret_cast<const uint64_t*>(static_cast<uintptr_t>(held));
     uint64_t* to = reinterpret_cast<uint64_t*>(static_cast<uintptr_t>(addresses));
     int* codes = reinterpret_cast<int*>(static_cast<uintptr_t>(dtypes));
+    const int64_t* n_of = reinterpret_cast<const int64_t*>(static_cast<uintptr_t>(sizes));
+    const int* type_of = reinterpret_cast<const int*>(static_cast<uintptr_t>(types));
     PyObject* fast = nullptr;
     if (grads != Py_None) {
         fast = PySequence_Fast(grads, "grads: want a list of tensors");
@@ -60,7 +75,8 @@ PyObject* gradients(PyObject*, PyObject* args) {
             at::Tensor own;
             const at::Tensor* g = nullptr;
             bool none = false;
-            if (!p || reinterpret_cast<uintptr_t>(p->data_ptr()) != at[i]) {
+            if (!p || reinterpret_cast<uintptr_t>(p->data_ptr()) != at[i] ||
+                (n_of && type_of && !same(*p, n_of[i], type_of[i]))) {
                 moved = i;
                 break;
             }

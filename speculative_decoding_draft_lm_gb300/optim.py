@@ -137,7 +137,9 @@ class DominoAdamW:
                                 int(self.master and p.dtype is torch.bfloat16)) for p in self.params])
         self._addresses, self._dtypes = (ctypes.c_uint64 * count)(), (ctypes.c_int * count)()
         self._held = (ctypes.c_uint64 * count)(*[p.data_ptr() for p in self.params])
-        self._held_at = ctypes.addressof(self._held)
+        self._sizes = (ctypes.c_int64 * count)(*[p.numel() for p in self.params])
+        self._types = (ctypes.c_int * count)(*[self._codes[p.dtype] for p in self.params])
+        self._held_at, self._sizes_at, self._types_at = map(ctypes.addressof, (self._held, self._sizes, self._types))
         self._addresses_at, self._dtypes_at = ctypes.addressof(self._addresses), ctypes.addressof(self._dtypes)
         address = {n: self.state[n].data_ptr() if n in self.state else None
                    for n in ("m", "v", "m_scale", "v_scale", "master", "count")}
@@ -152,10 +154,11 @@ class DominoAdamW:
 
     def _gradients(self, grads):
         """Puts the gradients' addresses and types into this context's arrays."""
-        bad = self._args.gradients(self.params, grads, self._index, self._held_at, self._addresses_at, self._dtypes_at)
+        bad = self._args.gradients(self.params, grads, self._index, self._held_at, self._addresses_at, self._dtypes_at,
+                                   self._sizes_at, self._types_at)
         if bad < -1:
-            raise ValueError(f"params[{-2 - bad}]: its elements are no longer where they were when this optimizer was "
-                             "made (its .data was replaced): make a new one with state=state_dict()")
+            raise ValueError(f"params[{-2 - bad}]: its elements are no longer what and where they were when this "
+                             "optimizer was made (its .data was replaced): make a new one with state=state_dict()")
         if bad >= 0:
             g = self.params[bad].grad if grads is None else grads[bad]
             if not hasattr(g, "dtype"):

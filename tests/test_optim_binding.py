@@ -1,0 +1,101 @@
+"""The update's Python binding without a GPU: a stand-in library, tensors on the CPU."""
+import ctypes
+import os
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+class Library:
+    """Takes calls and notes the gradients' addresses as they are at the time."""
+
+    def __init__(self, count):
+        self.count, self.calls, self.during = count, [], lambda: None
+
+    def domino_adamw_init(self, ctx, cfg, device):
+        return 0
+
+    def _call(self, name, at):
+        self.calls.append((name, list((ctypes.c_uint64 * self.count).from_address(at))))
+        self.during()
+        return 0
+
+    def domino_adamw_step(self, ctx, addresses, dtypes, lr, lr_factor, scale, stream):
+        return self._call("step", addresses)
+
+    def domino_adamw_grad_norm(self, ctx, addresses, dtypes, most, norm, scale, stream):
+        return self._call("norm", addresses)
+
+
+@pytest.fixture
+def make(monkeypatch):
+    from speculative_decoding_draft_lm_gb300 import build, optim
+    if not os.path.exists(build.ARGS):
+        build.build()
+    device = torch.device
+
+    def make(params, **kw):
+        params = list(params)
+        lib = Library(len(params))
+        with monkeypatch.context() as m:
+            m.setattr(optim, "load_library", lambda: lib)
+            m.setattr(torch, "device", lambda *a: device("cpu"))
+            opt = optim.DominoAdamW(params, device=-1, **kw)
+        opt._current_stream = lambda i: 0
+        return opt, lib
+
+    return make
+
+
+def _both(opt, match, **kw):
+    for call in (opt.step, opt.grad_norm):
+        with pytest.raises(ValueError, match=match):
+            call(**kw)
+
+
+def test_calls_reach_the_library(make):
+    p = [torch.zeros(4, 3), torch.zeros(5, dtype=torch.bfloat16), torch.zeros(0)]
+    opt, lib = make(p)
+    g = [torch.ones(4, 3), None, torch.ones(0)]
+    opt.step(grads=g)
+    opt.grad_norm(grads=g)
+    assert lib.calls == [(n, [g[0].data_ptr(), 0, 0]) for n in ("step", "norm")]
+
+
+def test_a_parameter_that_became_another_is_refused(make):
+    """Fewer elements, another type or another order at the same address: the context holds what was there first."""
+    def half(t):
+        t.data = t.data[:2]
+
+    def typed(t):
+        t.data = t.data.view(torch.bfloat16)
+
+    def turned(t):
+        t.data = t.data.t()
+
+    def larger(t):
+        t.data = t.data.as_strided((8, 3), (0, 1))
+
+    def moved(t):
+        t.data = t.data.clone()
+
+    for change in (half, typed, turned, larger, moved):
+        p = [torch.zeros(7), torch.zeros(4, 3)]
+        opt, lib = make(p)
+        at = p[1].data_ptr()
+        opt.step(grads=[torch.ones(7), torch.ones(4, 3)])
+        change(p[1])
+        assert change is moved or p[1].data_ptr() == at
+        g = [torch.ones(7), torch.ones(p[1].shape).to(p[1].dtype)]
+        _both(opt, "params.1.*no longer", grads=g)
+        _both(opt, "params.1.*no longer", grads=[g[0], None])
+        p[1].grad = g[1]
+        _both(opt, "params.1.*no longer")
+        assert len(lib.calls) == 1
+    # the same elements in another shape are the same
+    p = [torch.zeros(4, 3)]
+    opt, lib = make(p)
+    p[0].data = p[0].data.view(12)
+    opt.step(grads=[torch.ones(12)])
+    assert len(lib.calls) == 1
