@@ -38,19 +38,22 @@ bool same(const at::Tensor& p, int64_t n, int code) {
     return p.numel() == n && type_code(p, &its) && its == code && p.is_contiguous();
 }
 
-// gradients(params, grads, device, held, addresses, dtypes, sizes = 0, types = 0) -> int
+// gradients(params, grads, device, held, addresses, dtypes, sizes = 0, types = 0, buffers = None, buffers_held = 0) -> int
 //
 // params: list of tensors; grads: list of a tensor or None for each, or None for their .grad.  The gradients'
 // addresses (0: none) go to the uint64 array at `addresses`, their types to the int array at `dtypes`.  Returns -1,
 // or the place of the first gradient that is not contiguous, bf16 or fp32, of its parameter's shape and on `device`,
 // or -2 - the place of the first parameter whose elements are not at its address in the uint64 array at `held`, or
-// not as many as the int64 array at `sizes` has it, of the type in the int array at `types` and contiguous.
+// not as many as the int64 array at `sizes` has it, of the type in the int array at `types` and contiguous.  After the
+// parameters come the tensors of the list `buffers`: address and bytes of each in the uint64 array at `buffers_held`.
 PyObject* gradients(PyObject*, PyObject* args) {
     PyObject *params, *grads;
     long device;
     unsigned long long held, addresses, dtypes, sizes = 0, types = 0;
-    if (!PyArg_ParseTuple(args, "O!OlKKK|KK", &PyList_Type, &params, &grads, &device, &held, &addresses, &dtypes, &sizes,
-                          &types))
+    unsigned long long buffers_held = 0;
+    PyObject* buffers = Py_None;
+    if (!PyArg_ParseTuple(args, "O!OlKKK|KKOK", &PyList_Type, &params, &grads, &device, &held, &addresses, &dtypes, &sizes,
+                          &types, &buffers, &buffers_held))
         return nullptr;
     const Py_ssize_t n = PyList_GET_SIZE(params);
     const uint64_t* at = reinterpret_cast<const uint64_t*>(static_cast<uintptr_t>(held));
@@ -58,6 +61,7 @@ PyObject* gradients(PyObject*, PyObject* args) {
     int* codes = reinterpret_cast<int*>(static_cast<uintptr_t>(dtypes));
     const int64_t* n_of = reinterpret_cast<const int64_t*>(static_cast<uintptr_t>(sizes));
     const int* type_of = reinterpret_cast<const int*>(static_cast<uintptr_t>(types));
+    const uint64_t* buffer_at = reinterpret_cast<const uint64_t*>(static_cast<uintptr_t>(buffers_held));
     PyObject* fast = nullptr;
     if (grads != Py_None) {
         fast = PySequence_Fast(grads, "grads: want a list of tensors");
@@ -93,6 +97,12 @@ PyObject* gradients(PyObject*, PyObject* args) {
             if (none) continue;
             if (!g || !good(*g, *p, device, &codes[i])) bad = i;
             else to[i] = static_cast<uint64_t>(reinterpret_cast<uintptr_t>(g->data_ptr()));
+        }
+        for (Py_ssize_t i = 0; bad < 0 && moved < 0 && PyList_Check(buffers) && i < PyList_GET_SIZE(buffers); ++i) {
+            const at::Tensor* b = tensor_at(buffers, i);
+            if (!b || reinterpret_cast<uintptr_t>(b->data_ptr()) != buffer_at[2 * i] || b->nbytes() != buffer_at[2 * i + 1] ||
+                !b->is_contiguous())
+                moved = n + i;
         }
     } catch (const std::exception& e) {
         Py_XDECREF(fast);

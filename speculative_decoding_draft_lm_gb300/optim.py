@@ -62,6 +62,18 @@ def _load_args():
     return _optim_args
 
 
+class _Buffers(dict):
+    """A dict whose entries are settled; copied and pickled as an ordinary one."""
+
+    def _refuse(self, *a, **kw):
+        raise TypeError("the buffers of an optimizer are settled: copy into them, or make a new one with state=")
+
+    __setitem__ = __delitem__ = __ior__ = update = setdefault = pop = popitem = clear = _refuse
+
+    def __reduce__(self):
+        return dict, (dict(self),)
+
+
 class DominoAdamW:
     """AdamW over a list of tensors (see the header for the formulas).
 
@@ -77,9 +89,9 @@ class DominoAdamW:
     every 128 positions; ``master`` is float32; ``count`` int64 [1] holds the
     steps taken.
 
-    The tensors and buffers are updated where they are: a parameter whose ``.data`` is replaced
-    afterwards is refused.  A captured step reads the gradients at the capture's
-    addresses on every replay.
+    The tensors and buffers are updated where they are: which ones is settled, and calls with one
+    whose ``.data`` was replaced are refused.  A captured step reads the gradients at the
+    capture's addresses on every replay.
 
     Every method takes ``stream`` (a torch stream or raw handle; default: the
     current one).  With a stream other than the current one the caller orders the
@@ -94,19 +106,19 @@ class DominoAdamW:
         if not isinstance(seed, int) or not 0 <= seed < 2 ** 32:
             raise ValueError(f"seed: want an integer in [0, 2^32), got {seed!r}")
         self._codes = {torch.bfloat16: DOMINO_DTYPE_BF16, torch.float32: DOMINO_DTYPE_FP32}
-        self.params, self.lr, self.state_bits = list(params), lr, state_bits
+        self._params, self.lr, self.state_bits = list(params), lr, state_bits
         self.device, self._index = torch.device("cuda", device), device
-        if not 1 <= len(self.params) <= DOMINO_ADAMW_MAX_TENSORS:
-            raise ValueError(f"params: want 1 to {DOMINO_ADAMW_MAX_TENSORS} tensors, got {len(self.params)}")
-        for i, p in enumerate(self.params):
+        if not 1 <= len(self._params) <= DOMINO_ADAMW_MAX_TENSORS:
+            raise ValueError(f"params: want 1 to {DOMINO_ADAMW_MAX_TENSORS} tensors, got {len(self._params)}")
+        for i, p in enumerate(self._params):
             if p.dtype not in self._codes or p.get_device() != device or not p.is_contiguous():
                 raise ValueError(f"params[{i}]: want contiguous CUDA bfloat16 or float32 on {self.device}, "
                                  f"got {tuple(p.shape)} {p.dtype} strides {p.stride()} on {p.device}")
         self.offsets, total = [], 0
-        for p in self.params:
+        for p in self._params:
             self.offsets.append(total)
             total += -(-p.numel() // DOMINO_ADAMW_BLOCK) * DOMINO_ADAMW_BLOCK
-        self.master = bool(master) and any(p.dtype is torch.bfloat16 for p in self.params)
+        self.master = bool(master) and any(p.dtype is torch.bfloat16 for p in self._params)
         narrow, blocks = state_bits == 8, total // DOMINO_ADAMW_BLOCK
         moment = torch.float8_e4m3fn if narrow else torch.float32
         want = {"m": ((total,), moment), "v": ((total,), moment), "count": ((1,), torch.int64)}
@@ -117,7 +129,7 @@ class DominoAdamW:
         if state is None:
             state = {n: torch.zeros(shape, dtype=dtype, device=self.device) for n, (shape, dtype) in want.items()}
             if self.master:
-                for p, at in zip(self.params, self.offsets):
+                for p, at in zip(self._params, self.offsets):
                     state["master"][at:at + p.numel()].copy_(p.detach().reshape(-1))
         if set(state) != set(want):
             raise ValueError(f"state: want {sorted(want)}, got {sorted(state)}")
@@ -126,22 +138,26 @@ class DominoAdamW:
             if tuple(t.shape) != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
                 raise ValueError(f"state[{n!r}]: want contiguous CUDA {shape} {dtype} on {self.device}, "
                                  f"got {tuple(t.shape)} {t.dtype} on {t.device}")
-        self.state = dict(state)
+        self._state = _Buffers((n, state[n]) for n in want)
         # the raw handle where torch gives it: a Stream object costs more than a launch
         self._current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                                        lambda i: torch.cuda.current_stream(i).cuda_stream)
         self._f32 = torch.float32
-        count = len(self.params)
+        count = len(self._params)
         tensors = (domino_adamw_tensor * count)(*[
             domino_adamw_tensor(p.data_ptr(), p.numel(), self._codes[p.dtype],
-                                int(self.master and p.dtype is torch.bfloat16)) for p in self.params])
+                                int(self.master and p.dtype is torch.bfloat16)) for p in self._params])
         self._addresses, self._dtypes = (ctypes.c_uint64 * count)(), (ctypes.c_int * count)()
-        self._held = (ctypes.c_uint64 * count)(*[p.data_ptr() for p in self.params])
-        self._sizes = (ctypes.c_int64 * count)(*[p.numel() for p in self.params])
-        self._types = (ctypes.c_int * count)(*[self._codes[p.dtype] for p in self.params])
-        self._held_at, self._sizes_at, self._types_at = map(ctypes.addressof, (self._held, self._sizes, self._types))
+        self._held = (ctypes.c_uint64 * count)(*[p.data_ptr() for p in self._params])
+        self._sizes = (ctypes.c_int64 * count)(*[p.numel() for p in self._params])
+        self._types = (ctypes.c_int * count)(*[self._codes[p.dtype] for p in self._params])
+        self._buffers = list(self._state.values())
+        self._buffers_held = (ctypes.c_uint64 * (2 * len(self._buffers)))(
+            *[x for t in self._buffers for x in (t.data_ptr(), t.numel() * t.element_size())])
+        self._held_at, self._sizes_at, self._types_at, self._buffers_at = map(
+            ctypes.addressof, (self._held, self._sizes, self._types, self._buffers_held))
         self._addresses_at, self._dtypes_at = ctypes.addressof(self._addresses), ctypes.addressof(self._dtypes)
-        address = {n: self.state[n].data_ptr() if n in self.state else None
+        address = {n: self._state[n].data_ptr() if n in want else None
                    for n in ("m", "v", "m_scale", "v_scale", "master", "count")}
         cfg = domino_adamw_config(count, tensors, state_bits, address["m"], address["v"], address["m_scale"],
                                   address["v_scale"], address["master"], address["count"], betas[0], betas[1], eps,
@@ -150,20 +166,32 @@ class DominoAdamW:
         self.ctx = ctypes.c_void_p()
         _check(self._lib.domino_adamw_init(ctypes.byref(self.ctx), ctypes.byref(cfg), device), "domino_adamw_init")
 
+    @property
+    def params(self):
+        """The tensors, as a tuple: which ones they are is settled."""
+        return tuple(self._params)
+
+    @property
+    def state(self):
+        """The flat buffers by name, to read and to fill, not to replace."""
+        return self._state
+
     # -- checks (on every call's path) ----------------------------------------------
 
     def _gradients(self, grads):
         """Puts the gradients' addresses and types into this context's arrays."""
-        bad = self._args.gradients(self.params, grads, self._index, self._held_at, self._addresses_at, self._dtypes_at,
-                                   self._sizes_at, self._types_at)
+        bad = self._args.gradients(self._params, grads, self._index, self._held_at, self._addresses_at, self._dtypes_at,
+                                   self._sizes_at, self._types_at, self._buffers, self._buffers_at)
         if bad < -1:
-            raise ValueError(f"params[{-2 - bad}]: its elements are no longer what and where they were when this "
-                             "optimizer was made (its .data was replaced): make a new one with state=state_dict()")
+            i, n = -2 - bad, len(self._params)
+            name = f"params[{i}]" if i < n else f"state[{list(self._state)[i - n]!r}]"
+            raise ValueError(f"{name}: its elements are no longer what and where they were when this optimizer was made "
+                             "(its .data was replaced): make a new one with state=state_dict()")
         if bad >= 0:
-            g = self.params[bad].grad if grads is None else grads[bad]
+            g = self._params[bad].grad if grads is None else grads[bad]
             if not hasattr(g, "dtype"):
                 raise ValueError(f"grads[{bad}]: want a tensor or None, got {type(g).__name__}")
-            raise ValueError(f"grads[{bad}]: want contiguous CUDA {tuple(self.params[bad].shape)} bfloat16 or float32 on "
+            raise ValueError(f"grads[{bad}]: want contiguous CUDA {tuple(self._params[bad].shape)} bfloat16 or float32 on "
                              f"{self.device}, got {tuple(g.shape)} {g.dtype} strides {g.stride()} on {g.device}")
 
     def _scalar(self, t, name):
@@ -208,7 +236,7 @@ class DominoAdamW:
                                              self._scalar(scale, "scale"), self._stream(stream))
         if status:
             raise DominoError(status, "domino_adamw_step")
-        self._args.written(self.params, self._addresses_at)
+        self._args.written(self._params, self._addresses_at)
 
     # -- state ---------------------------------------------------------------------
 
@@ -218,23 +246,23 @@ class DominoAdamW:
 
     def moments(self, i):
         """(m, v) of parameter i in float32, in its shape."""
-        p, at = self.params[i], self.offsets[i]
+        p, at = self._params[i], self.offsets[i]
         n, out = p.numel(), []
         for name in ("m", "v"):
-            a = self.state[name][at:at + n].float()
+            a = self._state[name][at:at + n].float()
             if self.state_bits == 8:
                 j = at // DOMINO_ADAMW_BLOCK
-                s = self.state[name + "_scale"][j:j + -(-n // DOMINO_ADAMW_BLOCK)]
+                s = self._state[name + "_scale"][j:j + -(-n // DOMINO_ADAMW_BLOCK)]
                 a = a * s.repeat_interleave(DOMINO_ADAMW_BLOCK)[:n]
             out.append(a.view(p.shape))
         return tuple(out)
 
     def state_dict(self):
         """The flat buffers themselves; ``state=`` of a new optimizer over tensors of the same sizes."""
-        return dict(self.state)
+        return dict(self._state)
 
     def zero_grad(self):
-        for p in self.params:
+        for p in self._params:
             p.grad = None
 
     def last_launch_count(self) -> int:

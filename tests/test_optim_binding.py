@@ -1,6 +1,8 @@
 """The update's Python binding without a GPU: a stand-in library, tensors on the CPU."""
 import ctypes
 import os
+import pickle
+from copy import deepcopy
 
 import pytest
 
@@ -99,3 +101,53 @@ def test_a_parameter_that_became_another_is_refused(make):
     p[0].data = p[0].data.view(12)
     opt.step(grads=[torch.ones(12)])
     assert len(lib.calls) == 1
+
+
+def test_what_the_context_holds_cannot_be_swapped(make):
+    """The list of parameters and the dict of buffers are views to read: the context goes by what it was made with."""
+    p = [torch.zeros(40), torch.zeros(50)]
+    given = list(p)
+    opt, lib = make(given)
+    given.append(torch.zeros(3))
+    given[0] = torch.zeros(2)
+    assert len(opt.params) == 2 and all(a is b for a, b in zip(opt.params, p))
+    for change in (lambda: opt.params.append(p[0]), lambda: opt.params.pop(), lambda: opt.params.clear()):
+        with pytest.raises(AttributeError):
+            change()
+    with pytest.raises(TypeError):
+        opt.params[0] = torch.zeros(40)
+    with pytest.raises(AttributeError):
+        opt.params = p[:1]
+    for change in (lambda: opt.state.update(m=opt.state["v"]), lambda: opt.state.pop("m"), lambda: opt.state.clear()):
+        with pytest.raises(TypeError, match="settled"):
+            change()
+    with pytest.raises(TypeError, match="settled"):
+        opt.state["m"] = torch.zeros_like(opt.state["m"])
+    with pytest.raises(TypeError):
+        del opt.state["m"]
+    with pytest.raises(AttributeError):
+        opt.state = opt.state_dict()
+    copy = opt.state_dict()
+    copy["m"] = copy.pop("v")
+    for other in (pickle.loads(pickle.dumps(opt.state)), deepcopy(opt.state)):  # ordinary dicts, of tensors of their own
+        assert type(other) is dict and torch.equal(other["m"], opt.state["m"])
+        other["m"] = other["m"] + 1
+    assert set(opt.state) == {"m", "v", "count"} and opt.state["m"] is not copy["m"]
+    opt.step(grads=[torch.ones(40), torch.ones(50)])
+    assert len(lib.calls) == 1
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_buffer_that_became_another_is_refused(make, bits):
+    names = ["m", "v", "master", "count"] + (["m_scale", "v_scale"] if bits == 8 else [])
+    for name in names:
+        opt, lib = make([torch.zeros(300, dtype=torch.bfloat16)], state_bits=bits, master=True)
+        assert sorted(opt.state) == sorted(names)
+        g = [torch.ones(300)]
+        opt.step(grads=g)
+        opt.state[name].data = opt.state[name].data.clone()
+        _both(opt, f"state.'{name}'.*no longer", grads=g)
+        opt, lib = make([torch.zeros(300, dtype=torch.bfloat16)], state_bits=bits, master=True)
+        opt.state[name].data = opt.state[name].data[:0]
+        _both(opt, f"state.'{name}'.*no longer", grads=g)
+        assert lib.calls == []
