@@ -178,8 +178,13 @@ class DominoAdamW:
 
     # -- checks (on every call's path) ----------------------------------------------
 
-    def _gradients(self, grads):
-        """Puts the gradients' addresses and types into this context's arrays."""
+    def _gradients(self, grads, stream):
+        """Puts the gradients' addresses and types into this context's arrays.  Returns what has to live until the
+        launch is enqueued."""
+        if not (grads is None or isinstance(grads, (list, tuple))):
+            if stream is not None and hasattr(grads, "__next__"):
+                raise ValueError("grads: want a list of tensors, which the caller keeps, where a stream is given")
+            grads = list(grads)
         bad = self._args.gradients(self._params, grads, self._index, self._held_at, self._addresses_at, self._dtypes_at,
                                    self._sizes_at, self._types_at, self._buffers, self._buffers_at)
         if bad < -1:
@@ -193,6 +198,7 @@ class DominoAdamW:
                 raise ValueError(f"grads[{bad}]: want a tensor or None, got {type(g).__name__}")
             raise ValueError(f"grads[{bad}]: want contiguous CUDA {tuple(self._params[bad].shape)} bfloat16 or float32 on "
                              f"{self.device}, got {tuple(g.shape)} {g.dtype} strides {g.stride()} on {g.device}")
+        return grads
 
     def _scalar(self, t, name):
         """The address of one fp32 number on the device, or None."""
@@ -217,7 +223,7 @@ class DominoAdamW:
             import torch
             out = torch.empty((), device=self.device), torch.empty((), device=self.device)
         norm, scale = out
-        self._gradients(grads)
+        grads = self._gradients(grads, stream)
         status = self._lib.domino_adamw_grad_norm(self.ctx, self._addresses_at, self._dtypes_at, max_norm,
                                                   self._scalar(norm, "norm"), self._scalar(scale, "scale"),
                                                   self._stream(stream))
@@ -230,7 +236,7 @@ class DominoAdamW:
         ``grad_norm`` gives; a step whose scale is not finite is left out).  ``grads`` as for
         ``grad_norm``; a parameter without one is left as it is.  ``lr`` replaces the constructor's;
         ``lr_factor`` (one float32 on the device) multiplies it, for schedules of captured steps."""
-        self._gradients(grads)
+        grads = self._gradients(grads, stream)
         status = self._lib.domino_adamw_step(self.ctx, self._addresses_at, self._dtypes_at,
                                              self.lr if lr is None else lr, self._scalar(lr_factor, "lr_factor"),
                                              self._scalar(scale, "scale"), self._stream(stream))

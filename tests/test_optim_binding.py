@@ -2,6 +2,7 @@
 import ctypes
 import os
 import pickle
+import weakref
 from copy import deepcopy
 
 import pytest
@@ -151,3 +152,35 @@ def test_a_buffer_that_became_another_is_refused(make, bits):
         opt.state[name].data = opt.state[name].data[:0]
         _both(opt, f"state.'{name}'.*no longer", grads=g)
         assert lib.calls == []
+
+
+def test_gradients_of_a_generator(make):
+    """Tensors that nobody else holds live until the launch is enqueued; a bad one is named; an iterator's tensors on a
+    stream of the caller's, whom nothing lets keep them, are refused."""
+    p = [torch.zeros(40), torch.zeros(50)]
+    opt, lib = make(p)
+    for call in (opt.step, opt.grad_norm):
+        held = []
+
+        def gradients():
+            for t in p:
+                g = torch.ones_like(t)
+                held.append((weakref.ref(g), g.data_ptr()))
+                yield g
+
+        alive = []
+        lib.during = lambda: alive.extend(r() is not None for r, _ in held)
+        call(grads=gradients())
+        assert alive == [True, True] and lib.calls[-1][1] == [at for _, at in held]
+        lib.during = lambda: None
+        with pytest.raises(ValueError, match="grads.1.*float64"):
+            call(grads=(g for g in [torch.ones(40), torch.ones(50).double()]))
+        with pytest.raises(ValueError, match="grads.0.*want a tensor or None"):
+            call(grads=(g for g in [3.0, None]))
+        with pytest.raises(ValueError, match="2 tensors"):
+            call(grads=(g for g in [None]))
+        with pytest.raises(TypeError):
+            call(grads=5)
+        with pytest.raises(ValueError, match="list"):
+            call(grads=gradients(), stream=7)
+        call(grads=dict(enumerate(map(torch.ones_like, p))).values(), stream=7)
