@@ -221,7 +221,7 @@ class DominoAdamW:
         parameter (default: their ``.grad``)."""
         if out is None:
             import torch
-            out = torch.empty((), device=self.device), torch.empty((), device=self.device)
+            out = [torch.empty((), dtype=self._f32, device=self.device) for _ in range(2)]
         norm, scale = out
         grads = self._gradients(grads, stream)
         status = self._lib.domino_adamw_grad_norm(self.ctx, self._addresses_at, self._dtypes_at, max_norm,

@@ -184,3 +184,21 @@ def test_gradients_of_a_generator(make):
         with pytest.raises(ValueError, match="list"):
             call(grads=gradients(), stream=7)
         call(grads=dict(enumerate(map(torch.ones_like, p))).values(), stream=7)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float64])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_another_default_type(make, dtype, bits):
+    """What the binding makes itself is of its own types, whatever torch's default."""
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(dtype)
+    try:
+        opt, lib = make([torch.zeros(40, dtype=torch.float32), torch.zeros(50, dtype=torch.bfloat16)], state_bits=bits,
+                        master=True)
+        g = [torch.ones(40, dtype=torch.float32), None]
+        norm, scale = opt.grad_norm(grads=g)
+        opt.step(grads=g, scale=scale)
+        m, v = opt.moments(1)
+    finally:
+        torch.set_default_dtype(before)
+    assert all(t.dtype is torch.float32 for t in (norm, scale, m, v)) and len(lib.calls) == 2
