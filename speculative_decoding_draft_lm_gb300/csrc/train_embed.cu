@@ -402,8 +402,7 @@ __global__ void __launch_bounds__(kMarkThreads) k_mark(const int32_t* __restrict
 // Zeros to the rows that no token names.  One wave of blocks that claims 32
 // rows at a time: an SM that also sorts, or meets many named rows, takes fewer.
 template <typename G, bool VEC16>
-__global__ void __launch_bounds__(kFillThreads) k_fill(const unsigned* __restrict__ named, unsigned* __restrict__ claim,
-                                                       int V, int E, G* __restrict__ dtable) {
+__global__ void __launch_bounds__(kFillThreads) k_fill(const unsigned* named, unsigned* claim, int V, int E, G* dtable) {
     __shared__ unsigned next[2];
     pdl_trigger();
     pdl_wait();
@@ -413,7 +412,7 @@ __global__ void __launch_bounds__(kFillThreads) k_fill(const unsigned* __restric
         __syncthreads();
         const unsigned w = next[turn];
         if (w >= (unsigned)words) return;
-        const unsigned bits = named[w];
+        const unsigned bits = __ldcg(named + w);
         for (int r = warp; r < kFillRows; r += kFillThreads / 32) {
             const int v = (int)w * 32 + r;
             if (v >= V || (bits >> r & 1u)) continue;
