@@ -394,7 +394,7 @@ __device__ __forceinline__ void slice_best(ForwardShared& S, Word* lists, const 
         const int at = x.first + S.chosen[t / kAhead] * kAhead + t % kAhead;
         if (at < x.last) {
             Vec16<T> v;
-            v.q = __ldg(x.vec() + at);
+            v.q = __ldcg(x.vec() + at);
             const int id = v0 + at * Vectors<T>::kPer - x.phase;
             Word w[Vectors<T>::kPer];
             unsigned hit = 0;

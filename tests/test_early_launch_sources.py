@@ -29,3 +29,9 @@ def test_nothing_is_promised_that_the_kernel_before_may_write():
     for path, name, head, _ in _kernels():
         promised = set(re.findall(r"\bconst\s+\w+\s*\*\s*__restrict__\s+(\w+)", head))
         assert not {(name, p) for p in promised} - COMPLETE, (path, name, promised)
+
+
+def test_no_read_only_loads():
+    for path in sorted({k[0] for k in _kernels()}):
+        text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, path)).read())
+        assert not re.search(r"\b__ldg\(|\bld\.global\S*\.nc\b", text), path
