@@ -4,7 +4,8 @@
 ``__graft_entry__.build()``.  Each translation unit compiles in parallel to
 an object file under ``_build/``; the objects link into
 ``speculative_decoding_draft_lm_gb300/libdomino_rollout.so``.  Beside it lies
-``_optim_args.so``, the Python module that reads a step's tensors (C++, no CUDA).
+``_optim_args``, the Python module that reads a step's tensors (C++, no CUDA), under
+the name of this Python's extensions; without torch it is left out.
 """
 from __future__ import annotations
 
@@ -20,7 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdomino_rollout.so")
-ARGS = os.path.join(PKG, "_optim_args.so")
+ARGS = os.path.join(PKG, "_optim_args" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "--expt-relaxed-constexpr",
@@ -47,12 +48,17 @@ def _compile(src: str, extra: list) -> str:
     return obj
 
 
-def _compile_args() -> str:
-    import torch
+def _compile_args() -> str | None:
+    try:
+        import torch
+    except ImportError:
+        print("torch is not installed: _optim_args, which DominoAdamW needs, is not built")
+        return None
     root = os.path.dirname(torch.__file__)
     tmp = ARGS + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + INCLUDE,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DDOMINO_TORCH_VERSION="{torch.__version__}"', "-I" + INCLUDE,
            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(root, "include"),
            "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(CSRC, "optim_args.cpp"),
            "-o", tmp, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
@@ -70,13 +76,13 @@ def build(verbose: bool = False, extra: list | None = None) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         args = ex.submit(_compile_args)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
-        args.result()
     tmp = LIB + ".tmp"
     cmd = [_nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
+    args.result()
     if verbose:
         print("built", LIB)
     return LIB

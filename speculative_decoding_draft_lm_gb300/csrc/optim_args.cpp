@@ -138,4 +138,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_optim_args", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__optim_args() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__optim_args() {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", DOMINO_TORCH_VERSION) < 0) Py_CLEAR(m);
+    return m;
+}

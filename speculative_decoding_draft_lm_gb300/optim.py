@@ -57,8 +57,16 @@ def load_library() -> ctypes.CDLL:
 
 def _load_args():
     """The C++ module that reads a step's tensors (built beside the library)."""
-    import torch  # noqa: F401  its libraries first
-    from . import _optim_args
+    import torch  # its libraries first
+    build = "python -m speculative_decoding_draft_lm_gb300.build"
+    try:
+        from . import _optim_args
+    except ImportError as e:
+        raise ImportError(f"the module that reads a step's tensors is not built for this Python and torch: {build}") from e
+    built_for = getattr(_optim_args, "torch_version", None)
+    if built_for != torch.__version__:
+        raise ImportError(f"the module that reads a step's tensors was built for torch {built_for}, this is "
+                          f"{torch.__version__}: {build}")
     return _optim_args
 
 
