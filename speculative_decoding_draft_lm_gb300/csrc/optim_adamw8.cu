@@ -136,16 +136,14 @@ __global__ void __launch_bounds__(kThreads8, kPerSm<K>) k_adamw8(const __grid_co
                 }
             }
         }
-        // (rare fixes hold nothing over the ordinary way: with one of all codes and one of all NaN from registers, here,
-        // 92 bytes a thread were spilled)
         if (K::kLossy && top_p != top_p) {
             // each element from memory once more, so that no register is held for this
 #pragma unroll
             for (int j = 0; j < kE; ++j) {
                 if (i + j >= n) continue;
                 const F2 g = mul2(both(to_f32(static_cast<const G*>(e.g)[i + j])), both(k.scale));
-                const F2 m1 = new_m(a, mul2(e4m3_values(m8[j], false), both(a.m_scale[block])), g);
-                const F2 v1 = new_v(a, mul2(e4m3_values(v8[j], false), both(a.v_scale[block])), g);
+                const F2 m1 = new_m(a, mul2(e4m3_values(m8[j], false), both(sm)), g);
+                const F2 v1 = new_v(a, mul2(e4m3_values(v8[j], false), both(sv)), g);
                 const float q = halves(updated(a, k, both(to_f32(static_cast<const P*>(e.p)[i + j])), m1, v1)).x;
                 if (q != q) rp[j / 2] = (rp[j / 2] & (j % 2 ? 0xFFFFu : 0xFFFF0000u)) | 0x7FC0u << (j % 2 * 16);
             }
