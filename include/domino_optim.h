@@ -86,7 +86,8 @@ DOMINO_API int domino_adamw_init(domino_adamw_ctx** out, const domino_adamw_conf
  * can be reproduced), p from m and v before they are narrowed (the root of a v below
  * 2^-126 counts as 0); then *count = t.  What is taken from p, decay and update together,
  * is formed by itself and subtracted with one rounding to fp32: it is as good as fp32
- * holds it at its own size, and lost only where it is below 2^-25 |p|.  Where *scale is
+ * holds it at its own size, and lost only where it is below 2^-25 |p|.  An infinite p stays
+ * as it is.  Where *scale is
  * not finite the whole step is left out, count included.  Gradients that are not
  * finite spoil their elements (with 8 bits: their blocks) for good.
  *

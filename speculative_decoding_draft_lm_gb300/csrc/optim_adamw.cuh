@@ -164,16 +164,22 @@ __device__ __forceinline__ F2 updated(const AdamArgs& a, const Coefficients& k, 
     const float2 d = halves(fma2(f2(sqrt_fast(vf.x), sqrt_fast(vf.y)), both(k.root), both(a.eps)));
     return fma2(both(-k.rate), fma2(p, both(k.decay), mul2(m, f2(rcp_fast(d.x), rcp_fast(d.y)))), p);
 }
+// The word of what an element p becomes that `updated` makes NaN: an infinite one minus its
+// infinite decay stays as it is, as long as m and v are finite.
+__device__ __forceinline__ uint32_t of_nan(float p, float m, float v) {
+    return fabsf(p) == INFINITY && fabsf(m) < INFINITY && v < INFINITY ? __float_as_uint(p) : 0x7FC00000u;
+}
 
 // Two fp32 values rounded to bf16, up where the 16 lower bits and the random ones
 // carry.  Not for NaN, whose bits may all be set: the carry would reach the sign.
 __device__ __forceinline__ uint32_t lossy(float2 q, unsigned r0_up12, unsigned r1_up12) {
     return upper(__float_as_uint(q.x) + (r0_up12 >> 16), __float_as_uint(q.y) + (r1_up12 >> 16));
 }
-// puts NaN in the places of the bf16 pairs w where q, element by element, is NaN
-__device__ __forceinline__ void set_nan(uint32_t& w, float2 q) {
-    if (q.x != q.x) w = (w & 0xFFFF0000u) | 0x7FC0u;
-    if (q.y != q.y) w = (w & 0xFFFFu) | 0x7FC00000u;
+// the fp32 number of the word x, NaN or infinite, as element j of the words w
+template <typename K>
+__device__ __forceinline__ void set_word(uint32_t* w, int j, uint32_t x) {
+    if (K::kLossy) w[j / 2] = (w[j / 2] & (j % 2 ? 0xFFFFu : 0xFFFF0000u)) | x >> 16 << (j % 2 * 16);
+    else w[j] = x;
 }
 
 // a thread's new parameters to memory, the exact ones too where they are held

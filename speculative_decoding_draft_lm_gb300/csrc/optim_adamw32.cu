@@ -52,20 +52,21 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw32(const __grid_constant__
             rm[2 * j + 1] = __float_as_uint(mf.y);
             rv[2 * j] = __float_as_uint(vf.x);
             rv[2 * j + 1] = __float_as_uint(vf.y);
+            top_p = top_nan(top_p, q);
             if (K::kLossy) {
-                top_p = top_nan(top_p, q);
                 rq[j] = lossy(qf, word_of(a, h0, 2 * j) << 12, word_of(a, h0, 2 * j + 1) << 12);
             } else {
                 rq[2 * j] = __float_as_uint(qf.x);
                 rq[2 * j + 1] = __float_as_uint(qf.y);
             }
         }
-        if (K::kLossy && top_p != top_p) {
+        if (top_p != top_p) {
 #pragma unroll
-            for (int j = 0; j < kE / 2; ++j) {
-                const F2 m = f2(element<float>(rm, 2 * j), element<float>(rm, 2 * j + 1));
-                const F2 v = f2(element<float>(rv, 2 * j), element<float>(rv, 2 * j + 1));
-                set_nan(rq[j], halves(updated(a, k, before<K>(rp, j), m, v)));
+            for (int j = 0; j < kE; ++j) {
+                const float2 ps = halves(before<K>(rp, j / 2));
+                const float p = j % 2 ? ps.y : ps.x, m = element<float>(rm, j), v = element<float>(rv, j);
+                const float q = halves(updated(a, k, both(p), both(m), both(v))).x;
+                if (q != q) set_word<K>(rq, j, of_nan(p, m, v));
             }
         }
         store_param<K, kE>(e, a.master, pos, i, n, rq);

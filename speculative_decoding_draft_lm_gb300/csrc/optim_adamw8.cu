@@ -106,8 +106,8 @@ __global__ void __launch_bounds__(kThreads8, kPerSm<K>) k_adamw8(const __grid_co
                 const unsigned u0 = r0 * a.up12, u1 = r1 * a.up12;
                 const F2 q = updated(a, k, before<K>(rp, at2), m[at2], v[at2]);
                 const float2 qf = halves(q);
+                top_p = top_nan(top_p, q);
                 if (K::kLossy) {
-                    top_p = top_nan(top_p, q);
                     rp[at2] = lossy(qf, u0, u1);
                 } else {
                     rp[2 * at2] = __float_as_uint(qf.x);
@@ -136,16 +136,18 @@ __global__ void __launch_bounds__(kThreads8, kPerSm<K>) k_adamw8(const __grid_co
                 }
             }
         }
-        if (K::kLossy && top_p != top_p) {
-            // each element from memory once more, so that no register is held for this
+        if (top_p != top_p) {
+            // each element from memory once more, so that no register is held for this (from registers, and with the
+            // codes' fix behind all of them, 92 bytes a thread were spilled)
 #pragma unroll
             for (int j = 0; j < kE; ++j) {
                 if (i + j >= n) continue;
                 const F2 g = mul2(both(to_f32(static_cast<const G*>(e.g)[i + j])), both(k.scale));
                 const F2 m1 = new_m(a, mul2(e4m3_values(m8[j], false), both(sm)), g);
                 const F2 v1 = new_v(a, mul2(e4m3_values(v8[j], false), both(sv)), g);
-                const float q = halves(updated(a, k, both(to_f32(static_cast<const P*>(e.p)[i + j])), m1, v1)).x;
-                if (q != q) rp[j / 2] = (rp[j / 2] & (j % 2 ? 0xFFFFu : 0xFFFF0000u)) | 0x7FC0u << (j % 2 * 16);
+                const float p = K::kMaster ? a.master[pos + j] : to_f32(static_cast<const P*>(e.p)[i + j]);
+                const float q = halves(updated(a, k, both(p), m1, v1)).x;
+                if (q != q) set_word<K>(rp, j, of_nan(p, halves(m1).x, halves(v1).x));
             }
         }
         store_param<K, kE>(e, a.master, pos, i, n, rp);
