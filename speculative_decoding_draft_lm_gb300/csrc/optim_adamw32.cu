@@ -4,10 +4,10 @@
 // read and written once.  Bound by HBM: 319 M bf16 parameters with a master copy, 28
 // bytes an element, 8.9 GB, in 1270 us, 7.0 TB/s, a little above the measured copy rate.
 //
-// Tiles go to the CTAs in up to 400 shares an SM, nearly a CTA a tile: CTAs that each
-// take a tile in turn drift apart and with them the places of memory that are open at
-// one time (4 shares an SM, the resident CTAs', 1409 us, 30 1314, 100 1294).  One element
-// a load, a warp a block of 128: 2790 us.
+// Tiles go to the CTAs in up to 400 shares an SM, two or three tiles a CTA here: CTAs that
+// take many tiles in turn drift apart and with them the places of memory that are open at
+// one time (4 shares an SM, the resident CTAs', 1409 us, 30 1314, 100 1294, 150 1285, a
+// CTA a tile 1274).  One element a load, a warp a block of 128: 2790 us.
 #include "optim_adamw.cuh"
 
 namespace domino {

@@ -3,14 +3,15 @@
 // A thread has 16 consecutive elements, eight threads a block: the largest
 // magnitudes of a block meet by shuffles, so each element is read and written once.
 //
-// At 10 bytes an element (bf16) the instructions weigh as much as the bytes: 55 an
-// element, which alone would take 480 us for 319 M elements where the bytes take 475
-// at the measured copy rate.  They take 572 us, 5.6 TB/s, 0.83 of that rate.  What
+// At 10 bytes an element (bf16) the instructions weigh as much as the bytes: 54 an
+// element, which alone would take 470 us for 319 M elements where the bytes take 475
+// at the measured copy rate.  They take 562 us, 5.7 TB/s, 0.85 of that rate.  What
 // brought it there, in us: one element a load, branches in the conversions 4949;
 // vectors, codes by integer places 839; constants in pairs, no branch an element 726;
 // the ends of the codes' range looked at once a thread 657; the parameter's update
 // behind the block's maxima, so that a random word is used as soon as it is formed
-// and four CTAs fit an SM, 572 (three: 605, five: 688 with spills).
+// and four CTAs fit an SM, 572 (three: 605, five: 688 with spills); nothing held over a
+// thread's four words of codes for what is rare (their ends, NaN) 562.
 //
 // Tiles go to the CTAs in 30 shares an SM: with one share a resident CTA the SMs end
 // apart (654 against 632 when that was measured).  Prefetches of the next tile into L2,
@@ -37,7 +38,7 @@ __device__ __forceinline__ uint32_t codes(const uint32_t* x, uint32_t* signs) {
 }
 constexpr uint32_t kOnes = 0x01010101u, kTops = 0x80808080u;
 
-// CTAs an SM: as many as leave the raw elements in registers
+// CTAs an SM: as many as leave the raw elements in registers, none of them spilled
 template <typename K>
 constexpr int kPerSm = K::kFrom == 2 && sizeof(typename K::G) == 2 ? 4 : 3;
 

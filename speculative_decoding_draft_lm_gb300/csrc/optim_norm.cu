@@ -7,11 +7,10 @@
 // a large element beside small ones, and as fast from 0.5 GB of gradients on.  Every square
 // by itself into the sum with its rest took 170 us for the gradients below.)
 //
-// Bound by HBM: 483 M bf16 gradients, 0.97 GB, in 137 to 141 us, 6.9 to 7.1 TB/s, the
-// measured copy rate and a little more, for nothing is written (six CTAs an SM instead
-// of eight 146, four 171; one element a load 1506 us).  The tiny head's 1.2 M fp32
-// gradients take 5.2 us: the launch, the loads, and two small reductions with a counter
-// between them (in fp64 6.6 us).
+// Bound by HBM: 483 M bf16 gradients, 0.97 GB, in 142.6 us, 6.8 TB/s, the measured copy
+// rate (with plain sums of 16: six CTAs an SM instead of eight 3 % more, four 20 %; one
+// element a load 1506 us).  The tiny head's 1.2 M fp32 gradients take 5.2 us: the launch,
+// the loads, and two small reductions with a counter between them (in fp64 6.6 us).
 #include "optim_table.cuh"
 #include "train_math.cuh"
 
