@@ -87,9 +87,8 @@ DOMINO_API int domino_adamw_init(domino_adamw_ctx** out, const domino_adamw_conf
  * 2^-126 counts as 0); then *count = t.  What is taken from p, decay and update together,
  * is formed by itself and subtracted with one rounding to fp32: it is as good as fp32
  * holds it at its own size, and lost only where it is below 2^-25 |p|.  An infinite p stays
- * as it is.  Where *scale is
- * not finite the whole step is left out, count included.  Gradients that are not
- * finite spoil their elements (with 8 bits: their blocks) for good.
+ * as it is.  Where *scale is not finite the whole step is left out, count included.
+ * Gradients that are not finite spoil their elements (with 8 bits: their blocks) for good.
  *
  * What is held in fewer than 32 bits, and has no exact copy, is rounded
  * stochastically, so that changes below a rounding step add up over the steps:
@@ -109,7 +108,8 @@ DOMINO_API int domino_adamw_step(domino_adamw_ctx* ctx, const void* const* grads
 /* *norm = sqrt(sum of g^2 over the elements of all gradients), squares and sums of up to
  * four of them in fp32 (an element past 1.8e19 makes the norm infinite, one below 2e-23
  * adds nothing), sums of those in twice its precision, in an order that the sizes fix:
- * off by at most 2^-23 of itself;
+ * off by at most 2^-23 of itself where elements above 1.1e-19, whose squares are normal
+ * numbers, make it up;
  * *scale = min(1, max_norm / (*norm + 1e-6)), NaN where the norm is not finite (so
  * that a step with this scale is left out).  Both on the device; scale may be
  * NULL.  grads and grad_dtypes as in domino_adamw_step; max_norm > 0.
