@@ -162,15 +162,18 @@ class DominoAdamW:
         self._buffers = list(self._state.values())
         self._buffers_held = (ctypes.c_uint64 * (2 * len(self._buffers)))(
             *[x for t in self._buffers for x in (t.data_ptr(), t.numel() * t.element_size())])
-        self._held_at, self._sizes_at, self._types_at, self._buffers_at = map(
-            ctypes.addressof, (self._held, self._sizes, self._types, self._buffers_held))
         self._addresses_at, self._dtypes_at = ctypes.addressof(self._addresses), ctypes.addressof(self._dtypes)
         address = {n: self._state[n].data_ptr() if n in want else None
                    for n in ("m", "v", "m_scale", "v_scale", "master", "count")}
         cfg = domino_adamw_config(count, tensors, state_bits, address["m"], address["v"], address["m_scale"],
                                   address["v_scale"], address["master"], address["count"], betas[0], betas[1], eps,
                                   weight_decay, seed)
-        self._lib, self._args = load_library(), _load_args()
+        self._lib = load_library()
+        # reads a step's gradients, and counts its change of the parameters; the arrays and lists are this object's
+        self._read, self._written = _load_args().plan(
+            self._params, device, ctypes.addressof(self._held), self._addresses_at, self._dtypes_at,
+            ctypes.addressof(self._sizes), ctypes.addressof(self._types), self._buffers,
+            ctypes.addressof(self._buffers_held))
         self.ctx = ctypes.c_void_p()
         _check(self._lib.domino_adamw_init(ctypes.byref(self.ctx), ctypes.byref(cfg), device), "domino_adamw_init")
 
@@ -189,12 +192,11 @@ class DominoAdamW:
     def _gradients(self, grads, stream):
         """Puts the gradients' addresses and types into this context's arrays.  Returns what has to live until the
         launch is enqueued."""
-        if not (grads is None or isinstance(grads, (list, tuple))):
+        if grads.__class__ is not list and not (grads is None or isinstance(grads, (list, tuple))):
             if stream is not None and hasattr(grads, "__next__"):
                 raise ValueError("grads: want a list of tensors, which the caller keeps, where a stream is given")
             grads = list(grads)
-        bad = self._args.gradients(self._params, grads, self._index, self._held_at, self._addresses_at, self._dtypes_at,
-                                   self._sizes_at, self._types_at, self._buffers, self._buffers_at)
+        bad = self._read(grads)
         if bad < -1:
             i, n = -2 - bad, len(self._params)
             name = f"params[{i}]" if i < n else f"state[{list(self._state)[i - n]!r}]"
@@ -250,7 +252,7 @@ class DominoAdamW:
                                              self._scalar(scale, "scale"), self._stream(stream))
         if status:
             raise DominoError(status, "domino_adamw_step")
-        self._args.written(self._params, self._addresses_at)
+        self._written()
 
     # -- state ---------------------------------------------------------------------
 
