@@ -103,7 +103,7 @@ class DominoAdamW:
 
     Every method takes ``stream`` (a torch stream or raw handle; default: the
     current one).  With a stream other than the current one the caller orders the
-    two, as for any kernel.
+    two, as for any kernel, keeps the gradients until the call is done, and gives ``out``.
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, state_bits=32, master=False,
